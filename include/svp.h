@@ -74,7 +74,11 @@ typedef enum {
 #define SVP_DEV_WORKSPACE   0x8   /* workspace last used with another head_dim or tile mode:
                                      nothing was computed; run svp_workspace_init first     */
 
-typedef enum { SVP_F32 = 0, SVP_BF16 = 1 } svp_dtype;
+typedef enum {
+    SVP_F32 = 0,
+    SVP_BF16 = 1,
+    SVP_E4M3 = 2             /* paged caches only (svp_cache): 8-bit rows with an exponent byte */
+} svp_dtype;
 
 /* Query-row tile of the verification attention (DScale SIII-B, path-aware tile router). */
 typedef enum {
@@ -406,6 +410,98 @@ svp_status svp_draft_features(const void *logits, int64_t row_stride, int32_t ro
 /* workspace.                                                                             */
 svp_status svp_act_truncate(const float *margins, int64_t stride, int32_t n, int32_t w,
                             float threshold, int32_t *k_out, void *stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* The paged cache's own calls: writing new key / value rows into the pages (the rows of */
+/* a prompt, of a decode step, or the accepted candidates after a verification), reading */
+/* cached positions back to contiguous rows, and attention of a chunk of new tokens      */
+/* whose keys and values are already in the pages.                                       */
+/*                                                                                      */
+/* 8-bit rows (SVP_E4M3): the d elements of one token and head are e4m3 codes with one   */
+/* exponent byte b; an element is code * 2^(b - 127).  svp_cache_write picks the smallest */
+/* power of two that takes the row's largest magnitude to 448 or less (b >= 15; an        */
+/* element below 2^-9 of that power rounds to a multiple of it), so scaling is exact and  */
+/* each element is rounded once, to nearest even: at most 2^-4 relative for elements down */
+/* to 2^-15 of the row's largest.  A row with an infinite or NaN element gets b = 255 and */
+/* codes 0: every element of it reads as NaN.  Readers take any byte; codes 0x7f and 0xff */
+/* (which svp_cache_write never stores) read as +-480 * 2^(b - 127) in svp_chunk_attn and */
+/* svp_cache_read, and b = 0 as 0.                                                       */
+typedef struct {
+    void *k, *v;                /* page pools, [num_pages] pages of page_size tokens; 16-byte
+                                   aligned                                                 */
+    uint8_t *k_exp, *v_exp;     /* SVP_E4M3: exponent bytes [num_pages, hkv, page_size],
+                                   16-byte aligned; else NULL                              */
+    const int32_t *block_table; /* device [n, max_pages] page ids, row-major               */
+    int32_t max_pages;          /* columns of block_table                                  */
+    int32_t page_size;          /* tokens per page: 16, 32, 64 or 128                      */
+    int64_t num_pages;          /* pages in the pool, < 2^31                               */
+    int64_t stride_page;        /* element strides of both pools, multiples of 16 bytes;   */
+    int64_t stride_head;        /*   the last dim (d) is contiguous, and no two (page,      */
+    int64_t stride_tok;         /*   head, token) rows overlap                             */
+    svp_dtype dtype;            /* SVP_F32, SVP_BF16 or SVP_E4M3                           */
+} svp_cache;
+
+/*
+ * Row j of request i (packed row cu_slots[i] + j of k and v) goes to position ctx_len[i] + j
+ * of the request, i.e. to page block_table[i][pos / page_size], token pos % page_size.
+ * k, v      rows [m_cap, hkv, d] (dtype SVP_F32 or SVP_BF16), row r at element r * row_stride
+ *           (row_stride >= hkv * d, so both may be slices of a fused projection's output);
+ *           16-byte aligned, row_stride a multiple of 16 bytes
+ * ctx_len   [n] int32; cu_slots [n+1] int32
+ * take      [n] int32 or NULL: only rows j < take[i] are written (clamped to 0..k_i), e.g. the
+ *           accept_len of svp_greedy_accept / svp_margin_accept / svp_stochastic_accept
+ * ws        at least 256 bytes, zeroed once by svp_workspace_init (status word only)
+ * Rows >= cu_slots[n] may be read but are not used.  An SVP_F32 row is rounded to nearest
+ * even for an SVP_BF16 cache.  A request whose rows leave [0, m_cap) or run backwards is
+ * skipped (SVP_DEV_BAD_SLOTS); one with ctx_len < 0 or positions past max_pages * page_size is
+ * skipped, and a row whose page id is outside [0, num_pages) is not written
+ * (SVP_DEV_BAD_CONTEXT).  Two rows of one call must not share a (page, token).
+ */
+svp_status svp_cache_write(const void *k, const void *v, int64_t row_stride, svp_dtype dtype,
+                           const svp_cache *cache, const int32_t *ctx_len,
+                           const int32_t *cu_slots, const int32_t *take, int32_t n,
+                           int32_t m_cap, int32_t hkv, int32_t d, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/*
+ * The inverse: row cu_rows[i] + j of k_out / v_out [rows, hkv, d] (dtype SVP_F32 or SVP_BF16,
+ * contiguous, 16-byte aligned) = position start[i] + j of request i, 0 <= j < cu_rows[i+1] -
+ * cu_rows[i].  start [n] int32, or NULL for 0.  Values of an 8-bit row are exact in both types
+ * (bf16: while the product is a normal bf16 number).  Other rows of the outputs are left as
+ * they were.  Errors, status bits and ws as for svp_cache_write; a row whose page id is
+ * invalid is not written.  The output is the contiguous context of svp_verify_attn_packed.
+ */
+svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const int32_t *cu_rows,
+                          int32_t n, int32_t rows, int32_t hkv, int32_t d, svp_dtype dtype,
+                          void *k_out, void *v_out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of new tokens over the pages: row j of request i (packed row cu_slots[i] + j) sees
+ * positions 0 .. ctx_len[i] + j of its request, all of them in the cache (svp_cache_write puts
+ * the rows' own keys and values there first).  One call serves decode tokens (k_i = 1),
+ * candidate blocks and prompt chunks of thousands of rows together.
+ *   out = softmax(scale q K^T) V, lse = natural-log softmax normaliser (may be NULL)
+ * q      [m_cap, hq, d], row r at element r * q_row_stride (>= hq * d; 16-byte aligned, a
+ *        multiple of 16 bytes); out [m_cap, hq, d] contiguous, lse [m_cap, hq] fp32
+ * w      largest allowed k_i (host; 1 <= w); a request with k_i > w is skipped
+ * dtype  of q and out: SVP_BF16 with an SVP_BF16 or SVP_E4M3 cache (tcgen05 kernel, fp32
+ *        accumulation, probabilities rounded to bf16), SVP_F32 with an SVP_F32 cache (FFMA)
+ * ws     at least svp_chunk_attn_workspace_size bytes (it depends on d and dtype only),
+ *        zeroed once by svp_workspace_init; every call leaves it ready for the next one of
+ *        any size.
+ * 0 <= n <= 1024, hq / hkv <= 128, d = 64, 128 or 256 (SVP_EUNSUPPORTED otherwise).
+ * Rows >= cu_slots[n] and rows of skipped requests are not written.  Device checks as for
+ * svp_cache_write, for positions 0 .. ctx_len[i] + k_i - 1; a page id outside the pool reads
+ * as a page of zeros (SVP_DEV_BAD_CONTEXT).  Cache positions past a request's last row (the
+ * rest of its last page) may hold anything, NaN included; a NaN or infinity in the value row
+ * of a position that some row of the request may not see yet can reach that row.
+ */
+svp_status svp_chunk_attn_workspace_size(const svp_heads *heads, svp_dtype dtype, size_t *bytes);
+
+svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *cache,
+                          const int32_t *ctx_len, const int32_t *cu_slots, int32_t n,
+                          int32_t m_cap, int32_t w, const svp_heads *heads, svp_dtype dtype,
+                          void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,11 @@ Entry points (same names as the C ABI, without the ``svp_`` prefix):
   draft_margin         per-row top-1 index/value, top-2 value and fp32 margin
   greedy_accept        longest matching draft prefix and successor token per request
   margin_accept        draft_margin over packed target rows fused with greedy_accept
+  cache_write          new key / value rows (or their accepted prefixes) into the pages of a
+                       cache in fp32, bf16 or 8 bits with an exponent per row (make_cache)
+  cache_read           cached positions back to contiguous rows
+  chunk_attn           attention of decode tokens, candidate blocks and prompt chunks whose
+                       keys and values are in the cache already
 """
 from __future__ import annotations
 
@@ -27,7 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsvp.so")
 
 SVP_OK, SVP_EINVAL, SVP_EUNSUPPORTED, SVP_EWORKSPACE, SVP_ECUDA = 0, 1, 2, 3, 4
-SVP_F32, SVP_BF16 = 0, 1
+SVP_F32, SVP_BF16, SVP_E4M3 = 0, 1, 2
 TILE_AUTO, TILE_SHORT, TILE_FIXED128, TILE_WIDE, TILE_SHORT_UNPACKED = 0, 1, 2, 3, 4
 DEV_BAD_SLOTS, DEV_BAD_CONTEXT, DEV_TIMEOUT, DEV_WORKSPACE = 0x1, 0x2, 0x4, 0x8
 
@@ -57,6 +62,16 @@ class svp_kv(ctypes.Structure):
 class svp_gather_field(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("src_rows", ctypes.c_int64),
                 ("row_bytes", ctypes.c_int64), ("dst", ctypes.c_void_p)]
+
+
+class svp_cache(ctypes.Structure):
+    """A paged cache for cache_write / cache_read / chunk_attn; see make_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("stride_tok", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 GATHER_MAX_FIELDS = 8
@@ -127,6 +142,21 @@ _SIGS = {
     "svp_act_truncate": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
         ctypes.c_void_p, ctypes.c_void_p]),
+    "svp_cache_write": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(svp_cache),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_cache_read": (ctypes.c_int, [
+        ctypes.POINTER(svp_cache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_chunk_attn_workspace_size": (ctypes.c_int, [
+        ctypes.POINTER(svp_heads), ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "svp_chunk_attn": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(svp_cache), ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(svp_heads),
+        ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_void_p]),
     "svp_margin_accept": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
@@ -557,3 +587,169 @@ def act_truncate(margins, *, n: int, w: int, threshold: float, stride: int = 1, 
                                   float(threshold), _dev(out, "k", torch.int32), _stream(stream)),
            "svp_act_truncate")
     return out
+
+
+# ----------------------------------------------------------------- paged cache
+_CACHE_DTYPES = {torch.float32: SVP_F32, torch.bfloat16: SVP_BF16, torch.float8_e4m3fn: SVP_E4M3}
+
+
+def make_cache(k_cache, v_cache, block_table, *, k_exp=None, v_exp=None) -> svp_cache:
+    """svp_cache over page pools k_cache / v_cache [pages, hkv, page_size, d] (fp32, bf16 or
+    float8_e4m3fn; any strides with the last dim contiguous, so pools laid out [pages,
+    page_size, hkv, d] are given as their transpose(1, 2)) and block_table [n, max_pages] int32.
+    float8_e4m3fn pools need k_exp / v_exp [pages, hkv, page_size] uint8: an element is its
+    code times 2^(byte - 127).  The struct keeps the tensors alive."""
+    for name, x in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+        if x.dim() != 4 or x.dtype not in _CACHE_DTYPES:
+            raise TypeError(f"{name} must be [pages, hkv, page_size, d] in fp32, bf16 or float8_e4m3fn")
+    if (k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype
+            or k_cache.stride() != v_cache.stride() or k_cache.stride(-1) != 1):
+        raise ValueError("k_cache and v_cache need one shape, type and strides, last dim contiguous")
+    c = svp_cache()
+    c.k, c.v, c.dtype = k_cache.data_ptr(), v_cache.data_ptr(), _CACHE_DTYPES[k_cache.dtype]
+    c.num_pages, c.hkv, c.page_size, c.d = k_cache.shape
+    c.stride_page, c.stride_head, c.stride_tok = k_cache.stride()[:3]
+    c.block_table = _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n, max_pages]")
+    c.max_n, c.max_pages = block_table.shape
+    if c.dtype == SVP_E4M3:
+        for name, x in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if x is None or tuple(x.shape) != tuple(k_cache.shape[:3]):
+                raise ValueError(f"an 8-bit cache needs {name} [pages, hkv, page_size]")
+        c.k_exp, c.v_exp = _dev(k_exp, "k_exp", torch.uint8), _dev(v_exp, "v_exp", torch.uint8)
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("exponent bytes belong to float8_e4m3fn pools")
+    c.device = k_cache.device
+    c.keep = (k_cache, v_cache, k_exp, v_exp, block_table)
+    for x in c.keep:
+        if x is not None and x.device != c.device:
+            raise ValueError("the cache's tensors must be on one device")
+    c.ref = ctypes.byref(c)
+    return c
+
+
+def _rows(t, name: str, heads: int, cache: svp_cache) -> int:
+    """Row stride of rows [m, heads, d] whose heads and elements are contiguous."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.d:
+        raise ValueError(f"{name} must be [rows, {heads}, {cache.d}]")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != cache.d):
+        raise ValueError(f"{name} needs contiguous rows (any row stride)")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * cache.d)
+
+
+def _requests(cu, ctx, cache: svp_cache, name: str) -> int:
+    """Number of requests of cu [n+1]; checks it, the per-request array and the block table."""
+    n = cu.shape[0] - 1
+    _dev(cu, name, torch.int32)
+    if n < 0 or n > cache.max_n:
+        raise ValueError(f"{name} must have 1..{cache.max_n + 1} entries (rows of the block table)")
+    if ctx is not None and ctx.shape[0] < n:
+        raise ValueError("one cached length is needed for each request")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current CUDA device")
+    return n
+
+
+def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
+                ws: Optional[Workspace] = None, stream=None) -> None:
+    """Store packed rows k, v [m_cap, hkv, d] (bf16 or fp32; slices of a fused projection are
+    fine) at positions ctx_len[i] + j of their requests (svp_cache_write).  take [n] int32:
+    only the first take[i] rows of request i, e.g. the accept_len of margin_accept."""
+    n = _requests(cu_slots, ctx_len, cache, "cu_slots")
+    stride = _rows(k, "k", cache.hkv, cache)
+    if k.shape != v.shape or k.dtype != v.dtype or _rows(v, "v", cache.hkv, cache) != stride:
+        raise ValueError("k and v need one shape, type and row stride")
+    if take is not None and take.shape[0] < n:
+        raise ValueError("take needs one count for each request")
+    if ws is None:
+        ws = _workspace(("cache",), 256, cache.device, stream)
+    _check(lib().svp_cache_write(
+        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref,
+        _dev(ctx_len, "ctx_len", torch.int32), cu_slots.data_ptr(), _dev(take, "take", torch.int32),
+        n, k.shape[0], cache.hkv, cache.d, ws.ptr, ws.nbytes, _stream(stream)), "svp_cache_write")
+
+
+def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
+               dtype: torch.dtype = torch.bfloat16, k_out=None, v_out=None,
+               ws: Optional[Workspace] = None, stream=None):
+    """Positions start[i].. (0.. for None) of each request as contiguous rows
+    cu_rows[i]..cu_rows[i+1]-1 of (k_out, v_out) [rows, hkv, d] (svp_cache_read).  Outputs that
+    are not given are made with ``rows`` rows of ``dtype``, zeros where nothing is read."""
+    n = _requests(cu_rows, start, cache, "cu_rows")
+    if k_out is None or v_out is None:
+        if rows is None or k_out is not None or v_out is not None:
+            raise ValueError("give both k_out and v_out, or rows")
+        k_out = torch.zeros(rows, cache.hkv, cache.d, dtype=dtype, device=cache.device)
+        v_out = torch.zeros_like(k_out)
+    for name, x in (("k_out", k_out), ("v_out", v_out)):
+        _rows(x, name, cache.hkv, cache)
+        _dev(x, name, k_out.dtype)
+    if k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out need one shape")
+    if ws is None:
+        ws = _workspace(("cache",), 256, cache.device, stream)
+    _check(lib().svp_cache_read(
+        cache.ref, _dev(start, "start", torch.int32), cu_rows.data_ptr(), n, k_out.shape[0],
+        cache.hkv, cache.d, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.ptr,
+        ws.nbytes, _stream(stream)), "svp_cache_read")
+    return k_out, v_out
+
+
+def chunk_attn_workspace_size(hq: int, hkv: int, d: int, dtype=torch.bfloat16) -> int:
+    nb = ctypes.c_size_t(0)
+    h = _heads(hq, hkv, d, 0.0)
+    _check(lib().svp_chunk_attn_workspace_size(ctypes.byref(h), SVP_BF16 if dtype == torch.bfloat16 else SVP_F32,
+                                               ctypes.byref(nb)), "svp_chunk_attn_workspace_size")
+    return int(nb.value)
+
+
+def _chunk_workspace(hq: int, cache: svp_cache, dtype, stream) -> Workspace:
+    """The scratch of chunk_attn calls that bring none: one for each stream, as calls on two
+    streams may overlap; a call that is being captured gets its own, which lives in the graph's
+    memory, as graphs may be replayed on any stream."""
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, stream)
+    key = (("chunk", cache.d, dtype, _stream(stream)), cache.device)
+    ws = _ws_cache.get(key)
+    if ws is None:
+        ws = _ws_cache[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
+                                        cache.device, stream)
+    return ws
+
+
+def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = None, out=None,
+               lse=None, want_lse: bool = True, scale: float = 0.0, ws: Optional[Workspace] = None,
+               stream=None):
+    """Attention of packed new rows q [m_cap, hq, d] over the cache; row j of request i sees
+    positions 0..ctx_len[i]+j, its own (written by cache_write before) included.  w: largest
+    row count of a request (default m_cap).  Returns (out [m_cap, hq, d], lse [m_cap, hq] or
+    None); rows past cu_slots[n] are left as they were (zeros in outputs made here).  A call
+    captured on a stream that is not torch's current one needs its own ``ws``."""
+    n = _requests(cu_slots, ctx_len, cache, "cu_slots")
+    hq = q.shape[1]
+    if hq < 1 or hq % cache.hkv:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    stride = _rows(q, "q", hq, cache)
+    m_cap = q.shape[0]
+    if out is None:
+        out = torch.zeros(m_cap, hq, cache.d, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None and want_lse:
+        lse = torch.zeros(m_cap, hq, dtype=torch.float32, device=q.device)
+    elif lse is not None and tuple(lse.shape) != (m_cap, hq):
+        raise ValueError("lse must be [m_cap, hq]")
+    if ws is None:
+        ws = _chunk_workspace(hq, cache, q.dtype, stream)
+    h = _heads(hq, cache.hkv, cache.d, scale)
+    _check(lib().svp_chunk_attn(
+        q.data_ptr(), stride, cache.ref, _dev(ctx_len, "ctx_len", torch.int32), cu_slots.data_ptr(),
+        n, m_cap, max(m_cap, 1) if w is None else int(w), ctypes.byref(h), _dtype_code(q),
+        _dev(out, "out", q.dtype), _dev(lse, "lse", torch.float32), ws.ptr, ws.nbytes,
+        _stream(stream)), "svp_chunk_attn")
+    return out, lse
