@@ -68,8 +68,8 @@ static EncodeTiledFn encode_fn()
     return fn;
 }
 
-static bool encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                        const uint64_t *strides_bytes, const uint32_t *box)
+bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *base, int rank,
+                  const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn)
@@ -83,10 +83,17 @@ static bool encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64
         if (r + 1 < rank)
             gs[r] = strides_bytes[r];
     }
-    CUresult rc = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
-                     gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    CUresult rc = fn(m, type, (cuuint32_t)rank, const_cast<void *>(base),
+                     gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return rc == CUDA_SUCCESS;
+}
+
+static bool encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+                        const uint64_t *strides_bytes, const uint32_t *box)
+{
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims,
+                        strides_bytes, box);
 }
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

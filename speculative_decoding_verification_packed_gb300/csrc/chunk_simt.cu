@@ -1,9 +1,12 @@
-// chunk_simt.cu -- attention of new tokens over the paged cache on CUDA cores, fp32 throughout.
+// chunk_simt.cu -- svp_chunk_attn's checks, and its fp32 form on CUDA cores (fp32 throughout; tf32
+// tensor cores would round the scores to 11 bits).  bf16 queries go to chunk_tc.cu.
 //
 // Row j of request i (packed row cu_slots[i] + j) sees cache positions 0 .. ctx_len[i] + j:
 // o = softmax(scale q K^T) V.  One CTA of 128 threads per (packed row, query head): each thread
 // scores one key of a 128-key tile against the query row in shared memory, the tile's maximum
 // and sum update the running softmax, and each thread accumulates d / 128 output columns.
+#include <cmath>
+
 #include "svp_cache.cuh"
 
 namespace svp {
@@ -12,47 +15,25 @@ constexpr int kCsThreads = 128;
 
 struct ChunkSimtParams {
     CacheParams c;
-    const void *q;
+    const float *q;
     int64_t q_stride;
     const int32_t *ctx_len, *cu;
     int32_t n, m_cap, w, hq, d;
     float scale;
-    void *out;
-    float *lse;
+    float *out, *lse;
     int32_t *status;
 };
 
-template <int T>
-__device__ __forceinline__ float cs_elem(const void *base, int64_t e)
-{
-    if constexpr (T == SVP_F32)
-        return __ldg(static_cast<const float *>(base) + e);
-    else if constexpr (T == SVP_BF16)
-        return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(base) + e) << 16);
-    else {
-        float f[4];
-        e4m3x4_to_f32(__ldg(static_cast<const uint8_t *>(base) + e), f);
-        return f[0];
-    }
-}
-
-// Element offset of position t's row of head g, and its scale (8-bit rows); false: page invalid.
-template <int T>
-__device__ __forceinline__ bool cs_row(const ChunkSimtParams &p, int32_t i, int32_t g, int32_t t,
-                                       const uint8_t *exps, int64_t &at, float &scale)
+// Element offset of position t's row of head g; false: the page is invalid.
+__device__ __forceinline__ bool cs_row(const ChunkSimtParams &p, int32_t i, int32_t g, int32_t t, int64_t &at)
 {
     const int32_t page = __ldg(p.c.block_table + (int64_t)i * p.c.max_pages + (t >> p.c.page_shift));
     if (page < 0 || page >= p.c.num_pages)
         return false;
-    const int32_t tok = t & ((1 << p.c.page_shift) - 1);
-    at = page * p.c.s_page + g * p.c.s_head + tok * p.c.s_tok;
-    scale = 1.0f;
-    if constexpr (T == SVP_E4M3)
-        scale = exp_byte_scale(__ldg(exps + ((((int64_t)page * p.c.hkv + g) << p.c.page_shift) + tok)));
+    at = page * p.c.s_page + g * p.c.s_head + (t & ((1 << p.c.page_shift) - 1)) * p.c.s_tok;
     return true;
 }
 
-template <int TQ, int TC>
 __global__ void __launch_bounds__(kCsThreads) chunk_simt_kernel(const __grid_constant__ ChunkSimtParams p)
 {
     __shared__ float qs[256];
@@ -87,7 +68,7 @@ __global__ void __launch_bounds__(kCsThreads) chunk_simt_kernel(const __grid_con
     const int64_t qrow = (int64_t)row * p.q_stride + (int64_t)h * D;
     const int64_t orow = ((int64_t)row * p.hq + h) * D;
     for (int e = tid; e < D; e += kCsThreads)
-        qs[e] = cs_elem<TQ>(p.q, qrow + e);
+        qs[e] = __ldg(p.q + qrow + e);
     __syncthreads();
     const int32_t nkeys = __ldg(p.ctx_len + i) + (row - __ldg(p.cu + i)) + 1;
     float m_run = -INFINITY, l_run = 0.0f;
@@ -97,12 +78,11 @@ __global__ void __launch_bounds__(kCsThreads) chunk_simt_kernel(const __grid_con
         float s = -INFINITY;
         if (t < nkeys) {
             int64_t at;
-            float sc;
             float dot = 0.0f;
-            if (cs_row<TC>(p, i, g, t, p.c.k_exp, at, sc)) {
+            if (cs_row(p, i, g, t, at)) {
+                const float *kr = static_cast<const float *>(p.c.k) + at;
                 for (int e = 0; e < D; ++e)
-                    dot = fmaf(qs[e], cs_elem<TC>(p.c.k, at + e), dot);
-                dot *= sc;
+                    dot = fmaf(qs[e], __ldg(kr + e), dot);
             } else {
                 set_status(p.status, SVP_DEV_BAD_CONTEXT);   // a page of zeros
             }
@@ -134,31 +114,30 @@ __global__ void __launch_bounds__(kCsThreads) chunk_simt_kernel(const __grid_con
         const int32_t cnt = min(kCsThreads, nkeys - t0);
         for (int32_t kk = 0; kk < cnt; ++kk) {
             int64_t at;
-            float sc;
-            if (!cs_row<TC>(p, i, g, t0 + kk, p.c.v_exp, at, sc))
+            if (!cs_row(p, i, g, t0 + kk, at))
                 continue;
-            const float pw = ps[kk] * sc;
+            const float pw = ps[kk];
+            const float *vr = static_cast<const float *>(p.c.v) + at;
             if (tid < D)
-                acc0 = fmaf(pw, cs_elem<TC>(p.c.v, at + tid), acc0);
+                acc0 = fmaf(pw, __ldg(vr + tid), acc0);
             if (tid + kCsThreads < D)
-                acc1 = fmaf(pw, cs_elem<TC>(p.c.v, at + tid + kCsThreads), acc1);
+                acc1 = fmaf(pw, __ldg(vr + tid + kCsThreads), acc1);
         }
         __syncthreads();
     }
     const float inv = 1.0f / l_run;
-    auto put = [&](int32_t e, float x) {
-        if constexpr (TQ == SVP_F32)
-            static_cast<float *>(p.out)[orow + e] = x;
-        else
-            static_cast<uint16_t *>(p.out)[orow + e] = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xffffu);
-    };
     if (tid < D)
-        put(tid, acc0 * inv);
+        p.out[orow + tid] = acc0 * inv;
     if (tid + kCsThreads < D)
-        put(tid + kCsThreads, acc1 * inv);
+        p.out[orow + tid + kCsThreads] = acc1 * inv;
     if (tid == 0 && p.lse)
         p.lse[(int64_t)row * p.hq + h] = m_run + logf(l_run);
 }
+
+size_t chunk_tc_workspace(int32_t d);
+svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const CacheParams &c, const int32_t *ctx_len,
+                           const int32_t *cu, int32_t n, int32_t m_cap, int32_t w, int32_t hq, int32_t d, float scale,
+                           void *out, float *lse, void *ws, cudaStream_t stream);
 
 static bool al16(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
 
@@ -176,7 +155,7 @@ svp_status svp_chunk_attn_workspace_size(const svp_heads *heads, svp_dtype dtype
         return SVP_EUNSUPPORTED;
     if ((dtype != SVP_F32 && dtype != SVP_BF16) || heads->hq / heads->hkv > 128)
         return SVP_EUNSUPPORTED;
-    *bytes = kWsHeader;
+    *bytes = dtype == SVP_F32 ? kWsHeader : chunk_tc_workspace(heads->d);
     return SVP_OK;
 }
 
@@ -193,8 +172,11 @@ svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *
         return SVP_EINVAL;
     if (n > 1024)
         return SVP_EUNSUPPORTED;
-    ChunkSimtParams p{};
-    st = cache_params(cache, heads->hkv, heads->d, p.c);
+    const float scale = heads->scale != 0.0f ? heads->scale : 1.0f / sqrtf((float)heads->d);
+    if (!(scale > 0.0f) || !std::isfinite(scale))
+        return SVP_EINVAL;
+    CacheParams c{};
+    st = cache_params(cache, heads->hkv, heads->d, c);
     if (st != SVP_OK)
         return st;
     if ((dtype == SVP_F32) != (cache->dtype == SVP_F32))
@@ -207,7 +189,12 @@ svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *
         return SVP_OK;
     if (!q || !ctx_len || !cu_slots || !out || !al16(q) || !al16(out))
         return SVP_EINVAL;
-    p.q = q;
+    if (dtype == SVP_BF16)
+        return chunk_tc_launch(q, q_row_stride, cache->dtype, c, ctx_len, cu_slots, n, m_cap, w, heads->hq, heads->d,
+                               scale, out, lse, ws, (cudaStream_t)stream);
+    ChunkSimtParams p{};
+    p.c = c;
+    p.q = static_cast<const float *>(q);
     p.q_stride = q_row_stride;
     p.ctx_len = ctx_len;
     p.cu = cu_slots;
@@ -216,18 +203,11 @@ svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *
     p.w = w;
     p.hq = heads->hq;
     p.d = heads->d;
-    p.scale = heads->scale != 0.0f ? heads->scale : 1.0f / sqrtf((float)heads->d);
-    p.out = out;
+    p.scale = scale;
+    p.out = static_cast<float *>(out);
     p.lse = lse;
     p.status = static_cast<int32_t *>(ws);
-    const dim3 grid((unsigned)m_cap, (unsigned)heads->hq);
-    cudaStream_t s = (cudaStream_t)stream;
-    if (cache->dtype == SVP_F32)
-        chunk_simt_kernel<SVP_F32, SVP_F32><<<grid, kCsThreads, 0, s>>>(p);
-    else if (cache->dtype == SVP_BF16)
-        chunk_simt_kernel<SVP_BF16, SVP_BF16><<<grid, kCsThreads, 0, s>>>(p);
-    else
-        chunk_simt_kernel<SVP_BF16, SVP_E4M3><<<grid, kCsThreads, 0, s>>>(p);
+    chunk_simt_kernel<<<dim3((unsigned)m_cap, (unsigned)heads->hq), kCsThreads, 0, (cudaStream_t)stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? SVP_OK : SVP_ECUDA;
 }
 

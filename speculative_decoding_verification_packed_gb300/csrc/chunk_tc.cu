@@ -1,0 +1,1134 @@
+// chunk_tc.cu -- attention of new tokens over the paged cache on tcgen05, bf16 and 8-bit pages.
+//
+// Row j of request i sees cache positions 0 .. ctx_len[i] + j: o = softmax(scale q K^T) V.
+//
+// Tiles.  The G query heads that share a KV head are packed with R = 128 / G tokens into a
+// 128-row query tile (row = token * G + head), so a key / value tile of 128 positions serves
+// all of them:  S = Q K^T (TMEM, 128 x 128 fp32), P = 2^(S c - m) in bf16 over the first
+// half of S's columns, O += P V with P taken straight from TMEM.  One thread owns one row.
+//   * long pieces (more than R tokens, d <= 128): two query tiles share one K / V stream; the
+//     softmax of one runs while the tensor pipe works on the other.
+//   * short pieces (decode tokens, candidate blocks): one query tile, and the two softmax
+//     warpgroups take alternate KV tiles with an accumulator and a running (m, l) each; the
+//     first joins them in TMEM at the end.
+//   * d = 256: O fills the TMEM that a second tile would need, so one warpgroup works through
+//     one query tile with two S buffers (its MMAs take twice as long a tile).
+// The exponent reference m is the row's maximum over the piece's first tile; it moves (and O is
+// rescaled) only when a later tile's sum exceeds 2^32, so ordinary tiles need no maximum.
+//
+// 8-bit rows.  Four more warps turn the raw tile (e4m3 codes and exponent bytes, by TMA) into
+// the bf16 tile that the MMAs read.  Since the scale is a power of two the bf16 values are
+// exact: a code's fields are moved to those of a bf16 number and multiplied by 2^(120 + e).
+//
+// Split.  Work is the sequence of pairs (request, KV head, token block); a pair costs its
+// keys plus kStartKeys, and every CTA (one per SM) takes an equal share of the total, so long
+// prompts, blocks and single tokens balance in one launch.  All bounds follow in closed form
+// from per-request prefix sums; the first and last piece of a CTA may be parts of a pair, whose
+// (O, m, l) go to the workspace and are joined by a second kernel in the pieces' order.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "svp_cache.cuh"
+
+namespace svp {
+
+constexpr int kCkKeys = 128;          // keys a KV tile
+constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
+constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
+constexpr int kShareKeys = 512;       // smallest share of a CTA, in keys
+constexpr float kCkSumLimit = 4294967296.0f;
+
+struct ChunkDesc {                    // a pair that was split: read by the joining kernel
+    int32_t np, row0, ntok, g;        // pieces (0: none), first packed row, tokens, KV head
+};
+
+struct ChunkParams {
+    CUtensorMap tm_q, tm_k, tm_v;
+    CacheParams c;
+    const int32_t *ctx_len, *cu;
+    int32_t n, m_cap, w, hq, G, R;
+    float scale_log2;
+    void *out;
+    float *lse;
+    int32_t *status;
+    ChunkDesc *desc;                  // [grid]
+    float2 *part_ml;                  // [2 * grid][rows]
+    float *part_o;                    // [2 * grid][rows][d]; rows = 256 (d <= 128) or 128
+    int32_t nslot, nraw;              // bf16 tile slots, raw slots (8-bit pages)
+    int32_t off_ring, off_raw, off_misc;
+};
+
+template <int D, bool Q8>
+struct ChunkCfg {
+    static constexpr int NT = D == 256 ? 1 : 2;            // query tiles of a long piece
+    static constexpr int NH = D == 256 ? 2 : 1;            // 128-column halves of d
+    static constexpr int DH = D / NH;
+    static constexpr int kSlot = (DH / 64) * kCkSub;       // a half tile in bf16
+    static constexpr int kRaw = kCkKeys * DH;              // and in codes
+    static constexpr int kRawSlot = kRaw + 128;            // + exponent bytes
+    static constexpr int kQTile = (D / 64) * kCkSub;
+    static constexpr int kSoftWarp0 = Q8 ? 4 : 2;          // (setmaxnreg is by warpgroup)
+    static constexpr int kConvWarp0 = kSoftWarp0 + 4 * NT;
+    static constexpr int kThreads = 32 * (kConvWarp0 + (Q8 ? 4 : 0));
+    static constexpr int kPartRows = 128 * NT;
+};
+
+struct ChunkMisc {
+    uint64_t bars[48];
+    uint32_t tmem;
+    int32_t abort_flag;
+    int64_t warp_tot[16];
+    float2 ml[128];                   // (m, l) of the second warpgroup's half of a short piece
+    int64_t prefix[1];                // [n + 1]: cost before request i
+};
+
+// ------------------------------------------------------------------ the sequence of pairs
+struct ChunkPiece {
+    int32_t i, g, b, nb;              // request, KV head, token block, blocks of the request
+    int32_t off, k, L;                // the request's first packed row, rows, cached tokens
+    int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
+    int32_t nt, t0, t1;               // its KV tiles, and those of this piece
+    int64_t base;                     // cost before the pair
+};
+
+__device__ __forceinline__ int64_t ck_before(int64_t a, int64_t B, int64_t b)   // cost of blocks 0..b-1
+{
+    return b * a + B * (b * (b + 1) / 2);
+}
+
+// Cost of one KV head of a request: block b costs kStartKeys + L + (keys of its own tokens).
+__device__ __forceinline__ int64_t ck_head_cost(int32_t L, int32_t k, int32_t B)
+{
+    const int64_t nb = (k + B - 1) / B, a = (int64_t)kStartKeys + L;
+    return nb == 0 ? 0 : ck_before(a, B, nb - 1) + a + k;
+}
+
+__device__ __forceinline__ int32_t ck_tile_at(int64_t x)   // first tile at or after cost x of a pair
+{
+    return x <= kStartKeys ? 0 : (int32_t)((x - kStartKeys + kCkKeys - 1) / kCkKeys);
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int64_t v1, int32_t t0)
+{
+    const int32_t B = NT * p.R;
+    s.tb0 = s.b * B;
+    s.ntok = min(B, s.k - s.tb0);
+    s.len = s.L + s.tb0 + s.ntok;
+    s.nt = (s.len + kCkKeys - 1) / kCkKeys;
+    s.t0 = t0;
+    const int64_t y = v1 - s.base;
+    s.t1 = y >= (int64_t)kStartKeys + s.len ? s.nt : min(s.nt, ck_tile_at(y));
+    return s.t0 < s.t1;
+}
+
+__device__ __forceinline__ void ck_request(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int32_t B)
+{
+    s.off = __ldg(p.cu + s.i);
+    s.k = __ldg(p.cu + s.i + 1) - s.off;
+    s.L = __ldg(p.ctx_len + s.i);
+    s.nb = (s.k + B - 1) / B;
+}
+
+// The next pair before cost v1, from its first tile.
+template <int NT>
+__device__ __forceinline__ bool ck_next(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int64_t v1)
+{
+    s.base += (int64_t)kStartKeys + s.len;
+    if (s.base >= v1)
+        return false;
+    if (++s.b == s.nb) {
+        s.b = 0;
+        if (++s.g == p.c.hkv) {
+            s.g = 0;
+            do
+                ++s.i;
+            while (m->prefix[s.i + 1] == m->prefix[s.i]);   // (base < v1 <= the total: there is one)
+            ck_request(p, m, s, NT * p.R);
+        }
+    }
+    return ck_set<NT>(p, s, v1, 0);
+}
+
+// The first piece of the share [v0, v1).
+template <int NT>
+__device__ __forceinline__ bool ck_first(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int64_t v0,
+                                         int64_t v1)
+{
+    if (v0 >= v1)
+        return false;
+    const int32_t B = NT * p.R;
+    int32_t lo = 0, hi = p.n;
+    while (hi - lo > 1) {             // last request with prefix <= v0 (it has a cost: v0 < total)
+        const int32_t mid = (lo + hi) >> 1;
+        if (m->prefix[mid] <= v0)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    s.i = lo;
+    ck_request(p, m, s, B);
+    const int64_t H = ck_head_cost(s.L, s.k, B);
+    int64_t rem = v0 - m->prefix[lo];
+    s.g = (int32_t)(rem / H);
+    rem -= s.g * H;
+    // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem, put right
+    const int64_t a = (int64_t)kStartKeys + s.L;
+    const float h = (float)a + 0.5f * B;
+    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * (float)rem) - h) / B);
+    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
+    while (b + 1 < s.nb && ck_before(a, B, b + 1) <= rem)
+        ++b;
+    while (b > 0 && ck_before(a, B, b) > rem)
+        --b;
+    s.b = (int32_t)b;
+    s.base = m->prefix[lo] + s.g * H + ck_before(a, B, b);
+    const int32_t t0 = ck_tile_at(v0 - s.base);
+    const bool have = ck_set<NT>(p, s, v1, t0);
+    // a share that begins behind the pair's last tile begins with the next pair
+    return have || (t0 >= s.nt && ck_next<NT>(p, m, s, v1));
+}
+
+__device__ __forceinline__ int64_t ck_bound(int64_t total, int32_t c, int32_t ncta)
+{
+    return total * c / ncta;
+}
+
+// The CTA that owns the tile that starts at cost u: the last c with ck_bound(c) <= u.
+__device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t u)
+{
+    int32_t c = (int32_t)min((int64_t)ncta - 1, ((u + 1) * ncta + total - 1) / total - 1);
+    return c < 0 ? 0 : c;
+}
+
+// ------------------------------------------------------------------ small device helpers
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 bytes global -> shared on the async proxy, completing on an mbarrier.
+__device__ __forceinline__ void ck_bulk16(uint32_t dst, const void *src, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+        "l"(src), "r"(bar)
+        : "memory");
+}
+
+// Two codes to bf16 times 2^-120: sel 0x9180 takes bytes 0, 1 of w, 0xb3a2 bytes 2, 3, each
+// with its sign spread over the byte above; then s eeee mmm sits at sign, exponent, mantissa.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t ck_codes(uint32_t w)
+{
+    uint32_t y;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(SEL));
+    return (y << 4) & 0x87f087f0u;
+}
+
+__device__ __forceinline__ uint32_t ck_mul2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Largest raw score of this thread's row in one S tile; with kMasked, keys past kmax are hidden.
+template <bool kMasked>
+__device__ __forceinline__ float ck_row_max(uint32_t ts, int32_t kmax)
+{
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t sa[32], sb[32];
+        tmem_ld32(ts + half * 64, sa);
+        tmem_ld32(ts + half * 64 + 32, sb);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+            const float v = __uint_as_float(e < 32 ? sa[e] : sb[e - 32]);
+            mx[e & 3] = fmaxf(mx[e & 3], (!kMasked || half * 64 + e <= kmax) ? v : -INFINITY);
+        }
+    }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// P = 2^(s * cl2 - m) of this thread's row as 64 bf16 pairs, and its sum in fp32.
+template <bool kMasked>
+__device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2, float m, uint32_t (&pk)[64])
+{
+    const uint64_t c2 = f32x2_pack(cl2, cl2), nm2 = f32x2_pack(-m, -m);
+    uint64_t acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        acc[i] = f32x2_pack(0.0f, 0.0f);
+    uint32_t sv[4][32];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        tmem_ld32(ts + q * 32, sv[q]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 64; ++e) {
+        const int k0 = 2 * e;
+        float s0 = __uint_as_float(sv[k0 >> 5][k0 & 31]);
+        float s1 = __uint_as_float(sv[k0 >> 5][(k0 & 31) + 1]);
+        if (kMasked) {
+            s0 = k0 <= kmax ? s0 : -INFINITY;
+            s1 = k0 + 1 <= kmax ? s1 : -INFINITY;
+        }
+        float y0, y1;
+        f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), c2, nm2), y0, y1);
+        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+        pk[e] = pack_bf16x2(p0, p1);
+        acc[e & 3] = f32x2_add(acc[e & 3], f32x2_pack(p0, p1));
+    }
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f32x2_unpack(acc[i], s[2 * i], s[2 * i + 1]);
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int D, bool Q8>
+__global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p)
+{
+    using Cfg = ChunkCfg<D, Q8>;
+    constexpr int NT = Cfg::NT, NH = Cfg::NH, DH = Cfg::DH;
+    constexpr bool kMono = NT == 1;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    ChunkMisc *m = reinterpret_cast<ChunkMisc *>(smem + p.off_misc);
+    const uint32_t bar0 = smem_u32(m->bars);
+    // bf16 tile slots (filled by TMA, or by the converting warps), raw slots
+    auto bar_full = [&](int s) { return bar0 + 8u * s; };
+    auto bar_empty = [&](int s) { return bar0 + 8u * (8 + s); };
+    auto bar_rfull = [&](int s) { return bar0 + 8u * (16 + s); };
+    auto bar_rempty = [&](int s) { return bar0 + 8u * (24 + s); };
+    const uint32_t bar_q = bar0 + 8u * 32;
+    auto bar_s = [&](int a) { return bar0 + 8u * (33 + a); };        // S buffer a is complete
+    auto bar_p = [&](int a) { return bar0 + 8u * (35 + a); };        // P buffer a is written
+    auto bar_o = [&](int a) { return bar0 + 8u * (37 + a); };        // O_a of the piece is complete
+    auto bar_ofree = [&](int a) { return bar0 + 8u * (39 + a); };    // and has been read
+    const uint32_t bar_pv = bar0 + 8u * 41;                          // kMono: PV of a tile is done
+    const uint32_t bar_ml = bar0 + 8u * 42, bar_mlfree = bar0 + 8u * 43, bar_drain = bar0 + 8u * 44;
+    volatile int *abort_flag = &m->abort_flag;
+    const int32_t nslot = p.nslot, nraw = p.nraw;
+
+    if (tid == 0) {
+        for (int s = 0; s < 8; ++s) {
+            mbar_init(bar_full(s), Q8 ? 4 : 1);
+            mbar_init(bar_empty(s), 1);
+            mbar_init(bar_rfull(s), 1);
+            mbar_init(bar_rempty(s), 4);
+        }
+        mbar_init(bar_q, 1);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar_s(a), 1);
+            mbar_init(bar_p(a), 4);
+            mbar_init(bar_o(a), 1);
+            mbar_init(bar_ofree(a), 4);
+        }
+        mbar_init(bar_pv, 1);
+        mbar_init(bar_ml, 4);
+        mbar_init(bar_mlfree, 4);
+        mbar_init(bar_drain, 1);
+        mbar_fence_init();
+        m->abort_flag = 0;
+        m->prefix[0] = 0;
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&m->tmem), 512);
+        tmem_relinquish();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    if (tid == 0)
+        p.desc[blockIdx.x].np = 0;
+    // cost before each request; a request that breaks the contract costs nothing (status bit)
+    int64_t running = 0;
+    for (int32_t base = 0; base < p.n; base += Cfg::kThreads) {
+        const int32_t i = base + tid;
+        int64_t cost = 0;
+        if (i < p.n) {
+            const int32_t off = __ldg(p.cu + i), end = __ldg(p.cu + i + 1), L = __ldg(p.ctx_len + i);
+            int32_t bad = 0;
+            if (off < 0 || end < off || end - off > p.w || end > p.m_cap)
+                bad = SVP_DEV_BAD_SLOTS;
+            else if (end > off && (L < 0 || (int64_t)L + (end - off) > ((int64_t)p.c.max_pages << p.c.page_shift)))
+                bad = SVP_DEV_BAD_CONTEXT;
+            if (bad && blockIdx.x == 0)
+                set_status(p.status, bad);
+            if (!bad)
+                cost = ck_head_cost(L, end - off, NT * p.R) * p.c.hkv;
+        }
+        int64_t incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            m->warp_tot[warp] = incl;
+        __syncthreads();
+        int64_t before = running;
+        for (int w2 = 0; w2 < Cfg::kThreads / 32; ++w2) {
+            const int64_t t = m->warp_tot[w2];
+            if (w2 < warp)
+                before += t;
+            running += t;
+        }
+        if (i < p.n)
+            m->prefix[i + 1] = before + incl;
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    const int64_t total = m->prefix[p.n];
+    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareKeys));
+    const int32_t cta = blockIdx.x;
+    const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
+    const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
+    ChunkPiece s;
+    auto is_long = [&](const ChunkPiece &x) { return !kMono && x.ntok > p.R; };
+
+    if constexpr (Q8 && !kMono) {
+        // 512 threads of 128 registers at launch: 72 + 2 * 176 + 88 = 4 * 128
+        if (warp < Cfg::kSoftWarp0)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else if (warp < Cfg::kConvWarp0)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    }
+
+    if (warp == 0) {
+        // ============================================================ K / V producer
+        // The warp runs the loop together: lane u < 8 looks after positions 16 u .. 16 u + 15 of a
+        // tile, which lie in one page.  Positions past the block's last visible key, and pages
+        // whose id is outside the pool, are loaded from a page past the pool: TMA fills zeros.
+        uint32_t pos = 0;             // half tiles loaded so far
+        bool ok = true;
+        const int32_t nring = Q8 ? nraw : nslot;
+        uint32_t slot = 0, phase = 0;
+        const uint64_t pol_once = l2_policy_evict_first();
+        for (bool have = ck_first<NT>(p, m, s, v0, v1); have && ok; have = ck_next<NT>(p, m, s, v1)) {
+            const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
+            auto page_of = [&](int32_t t) -> int32_t {
+                const int32_t at = t * kCkKeys + lane * 16;
+                if (lane >= 8 || t >= s.t1 || at >= s.len)
+                    return -2;
+                return __ldg(bt + (at >> p.c.page_shift));
+            };
+            const bool once = s.nb == 1;      // no other block of the request reads these keys
+            int32_t id_next = page_of(s.t0);
+            for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
+                int32_t id = id_next;
+                id_next = page_of(t + 1);
+                if (id != -2 && (id < 0 || id >= p.c.num_pages)) {
+                    set_status(p.status, SVP_DEV_BAD_CONTEXT);
+                    id = -2;
+                }
+                const int32_t tok = (t * kCkKeys + lane * 16) & ((1 << p.c.page_shift) - 1);
+                const int32_t page = id < 0 ? max(p.c.num_pages, 1) : id;
+                const int32_t nvalid = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    const CUtensorMap *tm = kv ? &p.tm_v : &p.tm_k;
+                    for (int h = 0; h < NH; ++h, ++pos) {
+                        const uint32_t full = Q8 ? bar_rfull(slot) : bar_full(slot);
+                        int got = 1;
+                        if (lane == 0)
+                            got = mbar_wait(Q8 ? bar_rempty(slot) : bar_empty(slot), phase ^ 1u, abort_flag);
+                        if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0))
+                            break;
+                        if constexpr (Q8) {
+                            const uint32_t dst = sbase + p.off_raw + slot * Cfg::kRawSlot;
+                            if (lane < 8 && id < 0)   // the codes are zeros: any finite scale will do
+                                st_shared_v4(dst + Cfg::kRaw + lane * 16, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu,
+                                             0x7f7f7f7fu);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(full, (uint32_t)(Cfg::kRaw + 16 * nvalid));
+                            __syncwarp();
+                            if (lane < 8) {
+                                if (once)
+                                    tma_load_4d_hint(dst + lane * 16 * DH, tm, full, h * DH, tok, s.g, page, pol_once);
+                                else
+                                    tma_load_4d(dst + lane * 16 * DH, tm, full, h * DH, tok, s.g, page);
+                                if (id >= 0)
+                                    ck_bulk16(dst + Cfg::kRaw + lane * 16,
+                                              (kv ? p.c.v_exp : p.c.k_exp) +
+                                                  ((((int64_t)id * p.c.hkv + s.g) << p.c.page_shift) + tok),
+                                              full);
+                            }
+                        } else {
+                            const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(full, (uint32_t)Cfg::kSlot);
+                            __syncwarp();
+                            if (lane < 8) {
+#pragma unroll
+                                for (int c = 0; c < DH / 64; ++c) {
+                                    if (once)
+                                        tma_load_4d_hint(dst + c * kCkSub + lane * 2048, tm, full, h * DH + c * 64, tok,
+                                                         s.g, page, pol_once);
+                                    else
+                                        tma_load_4d(dst + c * kCkSub + lane * 2048, tm, full, h * DH + c * 64, tok, s.g,
+                                                    page);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        if (++slot == (uint32_t)nring) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        }
+        // every load lands (and, of the bf16 ring, every release by the tensor core) before the
+        // CTA's shared memory is given back
+        if (lane == 0) {
+            volatile int drain = 0;
+            const uint32_t first = pos > (uint32_t)nring ? pos - nring : 0u;
+            for (uint32_t k = first; k < pos; ++k) {
+                mbar_wait(Q8 ? bar_rfull((int)(k % nring)) : bar_full((int)(k % nring)), (k / nring) & 1u, &drain);
+                if (!Q8 && ok)
+                    mbar_wait(bar_empty((int)(k % nring)), (k / nring) & 1u, abort_flag);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ============================================================ MMA issuer
+        // The warp runs the loop together (it clears V rows together); lane 0 issues.
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_o = idesc_bf16_f32(128, DH, false, true);
+        uint32_t tile0 = 0, npiece = 0;       // KV tiles and pieces before this one
+        uint32_t np_[2] = {0, 0}, no_[2] = {0, 0};   // uses of P / S buffer a and of O_a so far
+        bool ok = true;
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        };
+        auto load_q = [&](const ChunkPiece &x) {
+            if (lane == 0) {
+                const int tiles = is_long(x) ? 2 : 1;
+                mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles * (D / 64) * 128 * p.G * p.R));
+                for (int a = 0; a < tiles; ++a)
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(sbase + a * Cfg::kQTile + c * kCkSub, &p.tm_q, bar_q, c * 64, x.g * p.G,
+                                    x.off + x.tb0 + a * p.R);
+            }
+            __syncwarp();
+        };
+        bool have = ck_first<NT>(p, m, s, v0, v1);
+        if (have)
+            load_q(s);
+        uint32_t q_loads = have ? 1 : 0;
+        while (have && ok) {
+            const bool lng = is_long(s);
+            const int32_t nt = s.t1 - s.t0, nj = lng ? 2 * nt : nt;
+            auto pos_of = [&](int32_t t, int kv, int h) { return (tile0 + t) * (2u * NH) + kv * NH + h; };
+            auto issue_s = [&](int32_t j) -> bool {
+                const int32_t t = lng ? j >> 1 : j;
+                const int a = j & 1;
+                for (int h = 0; h < NH; ++h) {
+                    const uint32_t ps = pos_of(t, 0, h);
+                    const int sl = (int)(ps % nslot);
+                    if ((!lng || a == 0) && !wait_all(bar_full(sl), (ps / nslot) & 1u))
+                        return false;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t qd = sw128_desc(sbase + (lng ? a : 0) * Cfg::kQTile + h * 2 * kCkSub, 16, 1024);
+                        const uint64_t kd = sw128_desc(sbase + p.off_ring + sl * Cfg::kSlot, 16, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < DH / 16; ++ks)
+                            tc_mma_ss(tmem + a * 128, qd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2),
+                                      kd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2), idesc_s,
+                                      (h | ks) ? 1u : 0u);
+                        if (!lng || a == 1)
+                            tc_commit(bar_empty(sl));
+                    }
+                }
+                if (lane == 0)
+                    tc_commit(bar_s(a));
+                __syncwarp();
+                return true;
+            };
+            if (!(ok = wait_all(bar_q, npiece & 1u)))
+                break;
+            if (!(ok = issue_s(0)) || (nj > 1 && !(ok = issue_s(1))))
+                break;
+            ChunkPiece nx = s;
+            bool have_next = false;
+            for (int32_t j = 0; j < nj; ++j) {
+                const int32_t t = lng ? j >> 1 : j;
+                const int a = j & 1, ob = kMono ? 0 : a;
+                if (!(ok = wait_all(bar_p(a), np_[a] & 1u)))
+                    break;
+                ++np_[a];
+                const bool first = kMono ? j == 0 : j < 2;
+                if (first && no_[ob] > 0 && !(ok = wait_all(bar_ofree(ob), (no_[ob] - 1) & 1u)))
+                    break;
+                if (j == nj - 1) {
+                    // every S of this piece is done (its last P is written): Q may be replaced
+                    have_next = ck_next<NT>(p, m, nx, v1);
+                    if (have_next) {
+                        load_q(nx);
+                        ++q_loads;
+                    }
+                }
+                for (int h = 0; h < NH; ++h) {
+                    const uint32_t ps = pos_of(t, 1, h);
+                    const int sl = (int)(ps % nslot);
+                    const uint32_t va = sbase + p.off_ring + sl * Cfg::kSlot;
+                    if (!lng || a == 0) {
+                        if (!(ok = wait_all(bar_full(sl), (ps / nslot) & 1u)))
+                            break;
+                        // rows of the last page past the last visible key may hold anything, and
+                        // P = 0 does not hide a NaN: they are cleared (whole pages past it are zeros
+                        // already, and the converting warps clear theirs)
+                        const int32_t kvalid = s.len - (s.t0 + t) * kCkKeys;
+                        if (!Q8 && kvalid < kCkKeys && (kvalid & 15)) {
+                            const int32_t rows = 16 - (kvalid & 15);
+                            for (int32_t x = lane; x < rows * (DH / 8); x += 32) {
+                                const int32_t r = kvalid + x / (DH / 8), c = x % (DH / 8);
+                                st_shared_v4(va + (c >> 3) * kCkSub + r * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t vd = sw128_desc(va, kCkSub, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)   // 16 keys = 8 TMEM columns of P a step
+                            ck_mma_ts(tmem + 256 + ob * D + h * DH, tmem + a * 128 + ks * 8, vd + (uint64_t)(ks * 128),
+                                      idesc_o, (!first || ks) ? 1u : 0u);
+                        if (!lng || a == 1)
+                            tc_commit(bar_empty(sl));
+                    }
+                }
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    if (kMono)
+                        tc_commit(bar_pv);
+                    if (kMono ? j == nj - 1 : j + 2 >= nj)
+                        tc_commit(bar_o(ob));
+                }
+                __syncwarp();
+                if (j + 2 < nj && !(ok = issue_s(j + 2)))
+                    break;
+            }
+            if (!ok)
+                break;
+            ++no_[0];
+            if (!kMono && nj > 1)
+                ++no_[1];
+            tile0 += (uint32_t)nt;
+            ++npiece;
+            s = nx;
+            have = have_next;
+        }
+        if (lane == 0) {
+            volatile int drain = 0;
+            if (kMono && tile0 > 0 && ok)
+                mbar_wait(bar_pv, (tile0 - 1) & 1u, &drain);
+            tc_commit(bar_drain);
+            mbar_wait(bar_drain, 0, &drain);
+            for (uint32_t k = npiece; k < q_loads; ++k)   // query tiles on their way when a wait gave up
+                mbar_wait(bar_q, k & 1u, &drain);
+        }
+        __syncwarp();
+    } else if (warp >= Cfg::kSoftWarp0 && warp < Cfg::kConvWarp0) {
+        // ============================================================ softmax, one row a thread
+        const int a = (warp - Cfg::kSoftWarp0) >> 2;
+        const int r = (warp & 3) * 32 + lane;             // row of the tile = TMEM lane
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t to0 = tmem + lane_off + 256;
+        const float cl2 = p.scale_log2;
+        uint32_t ns_[2] = {0, 0}, no_[2] = {0, 0}, nml = 0, npv = 0;
+        bool ok = true, owe = false;
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        };
+        for (bool have = ck_first<NT>(p, m, s, v0, v1); have; have = ck_next<NT>(p, m, s, v1)) {
+            const bool lng = is_long(s);
+            const int32_t nt = s.t1 - s.t0;
+            const int32_t tok = (lng ? a * p.R : 0) + r / p.G;      // token of the block
+            const bool live = r < p.G * p.R && tok < s.ntok;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int32_t last = live ? s.L + s.tb0 + tok : -1;      // last visible key
+            const int32_t all = s.L + s.tb0 + (lng ? a * p.R : 0);   // last key that every row sees
+            const uint32_t to = to0 + (kMono ? 0 : a * D);
+            float m_ref = -INFINITY, l = 0.0f;
+            int32_t done = 0;                                        // tiles of this warpgroup so far
+            for (int32_t t = (lng || kMono) ? 0 : a; t < nt; t += (lng || kMono) ? 1 : 2, ++done) {
+                const int buf = kMono ? (t & 1) : a;
+                const uint32_t ts = tmem + lane_off + buf * 128;
+                if (!(ok = wait_all(bar_s(buf), ns_[buf] & 1u)))
+                    break;
+                ++ns_[buf];
+                // Barriers are waited for by parity, so no phase may be skipped, nor waited for when the
+                // next may have completed.  O_1 of an earlier short piece, which the first warpgroup
+                // read: no later phase can complete before the arrival below.
+                if (owe && !(ok = wait_all(bar_o(1), (no_[1] - 1) & 1u)))
+                    break;
+                owe = false;
+                // PV of the tile before (one accumulator for all tiles): waited for in every tile before
+                // the arrival below, which its successor needs; the tensor pipe has S of the next tile to
+                // go on with.
+                bool pv_seen = !kMono || npv == 0;
+                tc_fence_after();
+                if (warp_live) {
+                    const int32_t k0 = (s.t0 + t) * kCkKeys;
+                    const bool masked = k0 + kCkKeys - 1 > all;
+                    const int32_t kmax = last - k0;
+                    uint32_t pk[64];
+                    float tsum;
+                    // (a row that has seen no score yet has no reference)
+                    bool move = done == 0 || __any_sync(0xffffffffu, live && m_ref == -INFINITY);
+#pragma unroll 1
+                    for (;;) {
+                        if (move) {
+                            const float tmax = fmaxf(m_ref, (masked ? ck_row_max<true>(ts, kmax)
+                                                                    : ck_row_max<false>(ts, kmax)) * cl2);
+                            if (done > 0) {
+                                const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - tmax);
+                                if (!pv_seen && !(ok = wait_all(bar_pv, (npv - 1) & 1u)))
+                                    break;
+                                pv_seen = true;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int cc = 0; cc < D / 32; ++cc) {
+                                    uint32_t ov[32];
+                                    tmem_ld32(to + cc * 32, ov);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                    tmem_st32(to + cc * 32, ov);
+                                }
+                                l *= alpha;
+                            }
+                            m_ref = tmax;
+                        }
+                        const float mm = m_ref == -INFINITY ? 0.0f : m_ref;
+                        tsum = masked ? ck_row_exp<true>(ts, kmax, cl2, mm, pk) : ck_row_exp<false>(ts, kmax, cl2, mm, pk);
+                        if (move || !__any_sync(0xffffffffu, live && !(tsum <= kCkSumLimit)))
+                            break;
+                        move = true;
+                    }
+                    if (!ok)
+                        break;
+                    tmem_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+                    tmem_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+                    l += tsum;
+                    tmem_wait_st();
+                }
+                if (!pv_seen && !(ok = wait_all(bar_pv, (npv - 1) & 1u)))
+                    break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_p(buf));
+                ++npv;
+            }
+            if (!ok)
+                break;
+            const bool both = !kMono && !lng && nt > 1;   // two accumulators of one query tile
+            if (both && a == 1) {
+                // (m, l) to the first warpgroup, which joins the two halves
+                if (nml > 0 && !(ok = wait_all(bar_mlfree, (nml - 1) & 1u)))
+                    break;
+                m->ml[r] = make_float2(m_ref, l);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_ml);
+                owe = true;
+            }
+            if (a == 0 || lng) {
+                if (!(ok = wait_all(bar_o(a), no_[a] & 1u)) || (both && !(ok = wait_all(bar_o(1), no_[1] & 1u))))
+                    break;
+                tc_fence_after();
+                float f0 = 1.0f, f1 = 0.0f;
+                if (both) {
+                    if (!(ok = wait_all(bar_ml, nml & 1u)))
+                        break;
+                    const float2 o = m->ml[r];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar_mlfree);
+                    // a half without a visible key has l = 0 and is left out whatever its O holds
+                    if (o.y != 0.0f) {
+                        const float mx = fmaxf(m_ref, o.x);
+                        f0 = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - mx);
+                        f1 = fast_exp2(o.x - mx);
+                        l = l * f0 + o.y * f1;
+                        m_ref = mx;
+                    }
+                }
+                const bool whole = s.t0 == 0 && s.t1 == s.nt;
+                const int32_t row = s.off + s.tb0 + tok, head = s.g * p.G + r % p.G;
+                const int32_t slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
+                const int64_t prow = (int64_t)slot * Cfg::kPartRows + (lng ? a * 128 : 0) + r;
+                const float inv = 1.0f / l;
+                if (warp_live) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t ov[32];
+                        tmem_ld32(to + cc * 32, ov);
+                        if (both) {
+                            uint32_t ow[32];
+                            tmem_ld32(to + D + cc * 32, ow);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0 +
+                                                        (f1 != 0.0f ? __uint_as_float(ow[e]) * f1 : 0.0f));
+                        } else {
+                            tmem_wait_ld();
+                        }
+                        if (!live)
+                            continue;
+                        if (whole) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                pk[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
+                            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) +
+                                                                   ((int64_t)row * p.hq + head) * D + cc * 32);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + prow * D + cc * 32);
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                dst[v] = make_uint4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+                        }
+                    }
+                    if (live) {
+                        if (!whole)
+                            p.part_ml[prow] = make_float2(m_ref, l);
+                        else if (p.lse)
+                            p.lse[(int64_t)row * p.hq + head] = (m_ref + __log2f(l)) * 0.69314718055994531f;
+                    }
+                }
+                if (!whole && s.t0 == 0 && a == 0 && r == 0) {
+                    // this CTA has the pair's first piece: CTAs up to the owner of its last tile have the rest
+                    ChunkDesc d;
+                    d.np = ck_owner(total, ncta, s.base + kStartKeys + (int64_t)kCkKeys * (s.nt - 1)) - cta + 1;
+                    d.row0 = s.off + s.tb0;
+                    d.ntok = s.ntok;
+                    d.g = s.g;
+                    p.desc[cta] = d;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_ofree(a));
+                    if (both)
+                        mbar_arrive(bar_ofree(1));
+                }
+            }
+            // uses of the accumulators, as the issuer counts them
+            ++no_[0];
+            if (!kMono && (lng || nt > 1))
+                ++no_[1];
+            if (both)
+                ++nml;
+        }
+    } else if (Q8 && warp >= Cfg::kConvWarp0) {
+        // ============================================================ codes -> bf16 tiles
+        // A thread takes 16 codes of one row at a time (neighbours take the rest of the row): reads
+        // and writes of a quarter warp fall on different banks, the odd half of the row writing its
+        // second 16 bytes first.
+        if constexpr (Q8) {
+            constexpr int CPR = DH / 16;                  // 16-code chunks a row
+            const int ct = tid - Cfg::kConvWarp0 * 32;
+            const int c = ct % CPR, row0 = ct / CPR;
+            uint32_t pos = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
+            bool ok = true;
+            for (bool have = ck_first<NT>(p, m, s, v0, v1); have && ok; have = ck_next<NT>(p, m, s, v1)) {
+                for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
+                    const int32_t kvalid = s.len - t * kCkKeys;
+                    for (int half = 0; half < 2 * NH; ++half, ++pos) {
+                        const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
+                                         mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
+                        if (!(ok = __all_sync(0xffffffffu, got)))
+                            break;
+                        const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
+                        const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
+#pragma unroll 4
+                        for (int it = 0; it < CPR; ++it) {
+                            const int row = it * (128 / CPR) + row0;
+                            const uint4 w = *reinterpret_cast<const uint4 *>(raw + row * DH + c * 16);
+                            const uint32_t b = raw[Cfg::kRaw + row];
+                            // 2^(120 + b - 127) as bf16; exponents above 2^7 in a second product
+                            uint32_t mul = b == 255u ? 0x7fc0u : (min(b, 134u) + 120u) << 7;
+                            mul = row < kvalid ? mul : 0u;
+                            mul |= mul << 16;
+                            uint32_t x[8] = {ck_codes<0x9180>(w.x), ck_codes<0xb3a2>(w.x), ck_codes<0x9180>(w.y),
+                                             ck_codes<0xb3a2>(w.y), ck_codes<0x9180>(w.z), ck_codes<0xb3a2>(w.z),
+                                             ck_codes<0x9180>(w.w), ck_codes<0xb3a2>(w.w)};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                x[e] = ck_mul2(x[e], mul);
+                            if (b > 134u && b < 255u) {
+                                const uint32_t more = ((b - 134u + 127u) << 7) * 0x10001u;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    x[e] = ck_mul2(x[e], more);
+                            }
+                            const int odd = (c >> 2) & 1;
+                            const uint32_t line = dst + (c >> 2) * kCkSub + row * 128;
+                            const int ch = 2 * (c & 3);
+                            const uint32_t a0 = line + (((ch + odd) ^ (row & 7)) << 4);
+                            const uint32_t a1 = line + (((ch + (odd ^ 1)) ^ (row & 7)) << 4);
+                            st_shared_v4(a0, odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
+                            st_shared_v4(a1, odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar_rempty(rslot));
+                            mbar_arrive(bar_full(slot));
+                        }
+                        if (++slot == (uint32_t)nslot) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                        if (++rslot == (uint32_t)nraw) {
+                            rslot = 0;
+                            rphase ^= 1u;
+                        }
+                    }
+                }
+            }
+            // the tensor core's releases land before the CTA's shared memory is given back
+            if (lane == 0 && ok) {
+                const uint32_t first = pos > (uint32_t)nslot ? pos - nslot : 0u;
+                for (uint32_t k = first; k < pos; ++k)
+                    mbar_wait(bar_empty((int)(k % nslot)), (k / nslot) & 1u, abort_flag);
+            }
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag && tid == 0)
+        set_status(p.status, SVP_DEV_TIMEOUT);
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ joining split pairs
+// Block (c, y): rows of the pair whose first piece CTA c had, one row a warp: o = sum_q 2^(m_q - M)
+// O_q / L over the pieces in their order, L = sum_q 2^(m_q - M) l_q.  Launched behind the kernel above
+// as its dependent; most blocks find nothing to do.
+constexpr int kJoinWarps = 4, kJoinY = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p, int32_t part_rows)
+{
+    constexpr int E = D / 32;                             // columns a lane
+    griddep_launch_dependents();
+    griddep_wait();
+    const int32_t c = blockIdx.x, lane = threadIdx.x & 31;
+    const ChunkDesc d = p.desc[c];
+    if (d.np < 2)
+        return;
+    for (int32_t rho = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); rho < d.ntok * p.G; rho += kJoinWarps * kJoinY) {
+        const int32_t tok = rho / p.G, h = rho - tok * p.G;
+        const bool second = tok >= p.R;                   // token of the second query tile
+        const int32_t pr = (second ? 128 : 0) + (tok - (second ? p.R : 0)) * p.G + h;
+        auto at = [&](int32_t q) { return (int64_t)(q == 0 ? 2 * c + 1 : 2 * (c + q)) * part_rows + pr; };
+        float M = -INFINITY;
+        for (int32_t q = lane; q < d.np; q += 32) {
+            const float2 ml = __ldcg(p.part_ml + at(q));
+            M = fmaxf(M, ml.y != 0.0f ? ml.x : -INFINITY);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float acc[E], L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.0f;
+        for (int32_t q0 = 0; q0 < d.np; q0 += 32) {
+            float w = 0.0f, wl = 0.0f;
+            if (q0 + lane < d.np) {
+                const float2 ml = __ldcg(p.part_ml + at(q0 + lane));
+                // a piece without a visible key of this row (l = 0) is left out whatever its O holds
+                w = ml.y != 0.0f ? fast_exp2(ml.x - M) : 0.0f;
+                wl = ml.y != 0.0f ? w * ml.y : 0.0f;
+            }
+            const int32_t cnt = min(32, d.np - q0);
+#pragma unroll 4
+            for (int32_t q = 0; q < cnt; ++q) {
+                const float wq = __shfl_sync(0xffffffffu, w, q);
+                L += __shfl_sync(0xffffffffu, wl, q);
+                const float *o = p.part_o + at(q0 + q) * D + lane * E;
+                float x[E];
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(o + e));
+                    x[e] = v.x;
+                    x[e + 1] = v.y;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] = wq != 0.0f ? fmaf(wq, x[e], acc[e]) : acc[e];
+            }
+        }
+        const float inv = 1.0f / L;
+        const int64_t orow = (int64_t)(d.row0 + tok) * p.hq + d.g * p.G + h;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && p.lse)
+            p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+int sm_count();
+bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *base, int rank,
+                  const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box);
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct ChunkWs {
+    size_t desc, ml, o, bytes;
+};
+
+static ChunkWs chunk_ws(int32_t d)
+{
+    const size_t g = (size_t)sm_count(), rows = d == 256 ? 128 : 256;
+    ChunkWs w;
+    w.desc = kWsHeader;
+    w.ml = up256(w.desc + g * sizeof(ChunkDesc));
+    w.o = up256(w.ml + 2 * g * rows * sizeof(float2));
+    w.bytes = up256(w.o + 2 * g * rows * (size_t)d * sizeof(float));
+    return w;
+}
+
+size_t chunk_tc_workspace(int32_t d) { return chunk_ws(d).bytes; }
+
+template <int D, bool Q8>
+static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
+{
+    using Cfg = ChunkCfg<D, Q8>;
+    constexpr int kBudget = 227 * 1024;
+    // one query tile is enough when no request can have a long piece
+    const int qbytes = ((Cfg::NT == 2 && p.w > p.R) ? 2 : 1) * Cfg::kQTile;
+    const int misc = (int)(sizeof(ChunkMisc) + (size_t)p.n * sizeof(int64_t) + 127) / 128 * 128;
+    p.off_ring = qbytes;
+    const int room = kBudget - qbytes - misc;
+    if (Q8) {
+        // as many raw as bf16 slots, and a fourth bf16 slot before a fourth raw one: S of the next
+        // tile but one is issued before V of this tile is released
+        p.nraw = std::min(8, std::max(2, (room - 4 * Cfg::kSlot) / Cfg::kRawSlot));
+        p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
+    } else {
+        p.nraw = 1;
+        p.nslot = std::min(8, room / Cfg::kSlot);
+    }
+    if (p.nslot < (D == 256 ? 4 : 3))
+        return SVP_EUNSUPPORTED;
+    p.off_raw = p.off_ring + p.nslot * Cfg::kSlot;
+    p.off_misc = p.off_raw + (Q8 ? p.nraw * Cfg::kRawSlot : 0);
+    const int smem = p.off_misc + misc;
+    static std::atomic<uint64_t> configured{0};
+    if (set_smem_limit_once(chunk_tc_kernel<D, Q8>, kBudget, configured) != cudaSuccess)
+        return SVP_ECUDA;
+    const int grid = sm_count();
+    if (launch_pdl(chunk_tc_kernel<D, Q8>, dim3(grid), dim3(Cfg::kThreads), (size_t)smem, stream, p) != cudaSuccess)
+        return SVP_ECUDA;
+    return launch_pdl(chunk_join_kernel<D>, dim3(grid, kJoinY), dim3(kJoinWarps * 32), 0, stream, p,
+                      (int32_t)Cfg::kPartRows) == cudaSuccess
+               ? SVP_OK
+               : SVP_ECUDA;
+}
+
+svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const CacheParams &c, const int32_t *ctx_len,
+                           const int32_t *cu, int32_t n, int32_t m_cap, int32_t w, int32_t hq, int32_t d, float scale,
+                           void *out, float *lse, void *ws, cudaStream_t stream)
+{
+    ChunkParams p;
+    std::memset(&p, 0, sizeof p);
+    p.c = c;
+    p.ctx_len = ctx_len;
+    p.cu = cu;
+    p.n = n;
+    p.m_cap = m_cap;
+    p.w = w;
+    p.hq = hq;
+    p.G = hq / c.hkv;
+    p.R = 128 / p.G;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out;
+    p.lse = lse;
+    const ChunkWs o = chunk_ws(d);
+    uint8_t *wsb = static_cast<uint8_t *>(ws);
+    p.status = reinterpret_cast<int32_t *>(wsb);
+    p.desc = reinterpret_cast<ChunkDesc *>(wsb + o.desc);
+    p.part_ml = reinterpret_cast<float2 *>(wsb + o.ml);
+    p.part_o = reinterpret_cast<float *>(wsb + o.o);
+    {
+        const uint64_t dims[3] = {(uint64_t)d, (uint64_t)hq, (uint64_t)m_cap};
+        const uint64_t str[2] = {(uint64_t)d * 2, (uint64_t)q_stride * 2};
+        const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)p.R};
+        if (!encode_tiled(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, q, 3, dims, str, box))
+            return SVP_EUNSUPPORTED;
+    }
+    {
+        const bool q8 = kv == SVP_E4M3;
+        const uint64_t esz = q8 ? 1 : 2;
+        const uint64_t dims[4] = {(uint64_t)d, (uint64_t)1 << c.page_shift, (uint64_t)c.hkv,
+                                  (uint64_t)std::max(c.num_pages, 1)};
+        const uint64_t str[3] = {(uint64_t)c.s_tok * esz, (uint64_t)c.s_head * esz, (uint64_t)c.s_page * esz};
+        const uint32_t box[4] = {q8 ? (uint32_t)std::min(d, 128) : 64u, 16, 1, 1};
+        const CUtensorMapDataType type = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const CUtensorMapSwizzle sw = q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+        if (!encode_tiled(&p.tm_k, type, sw, c.k, 4, dims, str, box) ||
+            !encode_tiled(&p.tm_v, type, sw, c.v, 4, dims, str, box))
+            return SVP_EUNSUPPORTED;
+    }
+    if (kv == SVP_E4M3) {
+        switch (d) {
+        case 64: return chunk_run<64, true>(p, stream);
+        case 128: return chunk_run<128, true>(p, stream);
+        default: return chunk_run<256, true>(p, stream);
+        }
+    }
+    switch (d) {
+    case 64: return chunk_run<64, false>(p, stream);
+    case 128: return chunk_run<128, false>(p, stream);
+    default: return chunk_run<256, false>(p, stream);
+    }
+}
+
+}  // namespace svp
