@@ -14,7 +14,7 @@
 //   * d = 256: O fills the TMEM that a second tile would need, so one warpgroup works through
 //     one query tile with two S buffers (its MMAs take twice as long a tile).
 // The exponent reference m is the row's maximum over the piece's first tile; it moves (and O is
-// rescaled) only when a later tile's sum exceeds 2^32, so ordinary tiles need no maximum.
+// rescaled) only when a later score lies more than 2^8 above it.
 //
 // 8-bit rows.  Four more warps turn the raw tile (e4m3 codes and exponent bytes, by TMA) into
 // the bf16 tile that the MMAs read.  Since the scale is a power of two the bf16 values are
@@ -37,7 +37,7 @@ constexpr int kCkKeys = 128;          // keys a KV tile
 constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
 constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
 constexpr int kShareKeys = 512;       // smallest share of a CTA, in keys
-constexpr float kCkSumLimit = 4294967296.0f;
+constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
 
 struct ChunkDesc {                    // a pair that was split: read by the joining kernel
     int32_t np, row0, ntok, g;        // pieces (0: none), first packed row, tokens, KV head
@@ -57,6 +57,7 @@ struct ChunkParams {
     float *part_o;                    // [2 * grid][rows][d]; rows = 256 (d <= 128) or 128
     int32_t nslot, nraw;              // bf16 tile slots, raw slots (8-bit pages)
     int32_t off_ring, off_raw, off_misc;
+    int32_t Rb, qsub;                 // tokens of a query box: min(R, w); bytes of its [rows][64] blocks
 };
 
 template <int D, bool Q8>
@@ -66,19 +67,21 @@ struct ChunkCfg {
     static constexpr int DH = D / NH;
     static constexpr int kSlot = (DH / 64) * kCkSub;       // a half tile in bf16
     static constexpr int kRaw = kCkKeys * DH;              // and in codes
-    static constexpr int kRawSlot = kRaw + 128;            // + exponent bytes
-    static constexpr int kQTile = (D / 64) * kCkSub;
-    static constexpr int kSoftWarp0 = Q8 ? 4 : 2;          // (setmaxnreg is by warpgroup)
+    static constexpr int kRawSlot = kRaw + 4 * kCkKeys;    // + the rows' multipliers
+    // warps: 0 K loader, 1 and 2 MMA issuers, 3 V loader, then warpgroups of softmax and converting warps
+    static constexpr int kSoftWarp0 = 4;
     static constexpr int kConvWarp0 = kSoftWarp0 + 4 * NT;
-    static constexpr int kThreads = 32 * (kConvWarp0 + (Q8 ? 4 : 0));
+    static constexpr int kConvWarps = Q8 ? 8 : 0;
+    static constexpr bool kTwoLoad = !(Q8 && NH == 2);     // (there the raw ring has no room for two tiles)
+    static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
     static constexpr int kPartRows = 128 * NT;
 };
 
 struct ChunkMisc {
-    uint64_t bars[48];
+    uint64_t bars[52];
     uint32_t tmem;
     int32_t abort_flag;
-    int64_t warp_tot[16];
+    int64_t warp_tot[20];
     float2 ml[128];                   // (m, l) of the second warpgroup's half of a short piece
     int64_t prefix[1];                // [n + 1]: cost before request i
 };
@@ -215,15 +218,6 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// 16 bytes global -> shared on the async proxy, completing on an mbarrier.
-__device__ __forceinline__ void ck_bulk16(uint32_t dst, const void *src, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
-        "l"(src), "r"(bar)
-        : "memory");
-}
-
 // Two codes to bf16 times 2^-120: sel 0x9180 takes bytes 0, 1 of w, 0xb3a2 bytes 2, 3, each
 // with its sign spread over the byte above; then s eeee mmm sits at sign, exponent, mantissa.
 template <uint32_t SEL>
@@ -241,60 +235,85 @@ __device__ __forceinline__ uint32_t ck_mul2(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Largest raw score of this thread's row in one S tile; with kMasked, keys past kmax are hidden.
+// The softmax of one S tile in this thread's row, 64 columns a turn: its instructions are kept few, as
+// seven kinds of warps share the instruction cache (whole rows unrolled took twice as long).
+
+// 32 columns of this thread's TMEM lane, and the largest of them.
+__device__ __forceinline__ float ck_ld32_max(uint32_t taddr, uint32_t (&r)[32])
+{
+    float mx;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31]), "=f"(mx)
+        : "r"(taddr));
+    return mx;
+}
+
+// Largest raw score; with kMasked, keys past kmax are hidden.
 template <bool kMasked>
 __device__ __forceinline__ float ck_row_max(uint32_t ts, int32_t kmax)
 {
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+    float mx = -INFINITY;
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         uint32_t sa[32], sb[32];
-        tmem_ld32(ts + half * 64, sa);
-        tmem_ld32(ts + half * 64 + 32, sb);
+        const float ma = ck_ld32_max(ts + half * 64, sa), mb = ck_ld32_max(ts + half * 64 + 32, sb);
         tmem_wait_ld();
+        if (!kMasked) {
+            mx = fmaxf(mx, fmaxf(ma, mb));
+        } else {
+            const int32_t left = kmax - half * 64;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-            const float v = __uint_as_float(e < 32 ? sa[e] : sb[e - 32]);
-            mx[e & 3] = fmaxf(mx[e & 3], (!kMasked || half * 64 + e <= kmax) ? v : -INFINITY);
+            for (int e = 0; e < 32; ++e) {
+                mx = fmaxf(mx, e <= left ? __uint_as_float(sa[e]) : -INFINITY);
+                mx = fmaxf(mx, e + 32 <= left ? __uint_as_float(sb[e]) : -INFINITY);
+            }
         }
     }
-    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    return mx;
 }
 
-// P = 2^(s * cl2 - m) of this thread's row as 64 bf16 pairs, and its sum in fp32.
+// P = 2^(s * cl2 - m) in bf16 over the first half of S's columns (a turn's P lies over scores that it or
+// an earlier turn has read); returns its sum in fp32.
 template <bool kMasked>
-__device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2, float m, uint32_t (&pk)[64])
+__device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2, float m)
 {
     const uint64_t c2 = f32x2_pack(cl2, cl2), nm2 = f32x2_pack(-m, -m);
-    uint64_t acc[4];
+    uint64_t acc[2] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f)};
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t sv[2][32], pk[32];
+        tmem_ld32(ts + half * 64, sv[0]);
+        tmem_ld32(ts + half * 64 + 32, sv[1]);
+        tmem_wait_ld();
+        const int32_t left = kmax - half * 64;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        acc[i] = f32x2_pack(0.0f, 0.0f);
-    uint32_t sv[4][32];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        tmem_ld32(ts + q * 32, sv[q]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 64; ++e) {
-        const int k0 = 2 * e;
-        float s0 = __uint_as_float(sv[k0 >> 5][k0 & 31]);
-        float s1 = __uint_as_float(sv[k0 >> 5][(k0 & 31) + 1]);
-        if (kMasked) {
-            s0 = k0 <= kmax ? s0 : -INFINITY;
-            s1 = k0 + 1 <= kmax ? s1 : -INFINITY;
+        for (int e = 0; e < 32; ++e) {
+            const int k0 = 2 * e;
+            float s0 = __uint_as_float(sv[k0 >> 5][k0 & 31]);
+            float s1 = __uint_as_float(sv[k0 >> 5][(k0 & 31) + 1]);
+            if (kMasked) {
+                s0 = k0 <= left ? s0 : -INFINITY;
+                s1 = k0 + 1 <= left ? s1 : -INFINITY;
+            }
+            float y0, y1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), c2, nm2), y0, y1);
+            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+            pk[e] = pack_bf16x2(p0, p1);
+            acc[e & 1] = f32x2_add(acc[e & 1], f32x2_pack(p0, p1));
         }
-        float y0, y1;
-        f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), c2, nm2), y0, y1);
-        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-        pk[e] = pack_bf16x2(p0, p1);
-        acc[e & 3] = f32x2_add(acc[e & 3], f32x2_pack(p0, p1));
+        tmem_st32(ts + half * 32, pk);
     }
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f32x2_unpack(acc[i], s[2 * i], s[2 * i + 1]);
-    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    float s[4];
+    f32x2_unpack(acc[0], s[0], s[1]);
+    f32x2_unpack(acc[1], s[2], s[3]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -314,34 +333,39 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     auto bar_empty = [&](int s) { return bar0 + 8u * (8 + s); };
     auto bar_rfull = [&](int s) { return bar0 + 8u * (16 + s); };
     auto bar_rempty = [&](int s) { return bar0 + 8u * (24 + s); };
-    const uint32_t bar_q = bar0 + 8u * 32;
-    auto bar_s = [&](int a) { return bar0 + 8u * (33 + a); };        // S buffer a is complete
-    auto bar_p = [&](int a) { return bar0 + 8u * (35 + a); };        // P buffer a is written
-    auto bar_o = [&](int a) { return bar0 + 8u * (37 + a); };        // O_a of the piece is complete
-    auto bar_ofree = [&](int a) { return bar0 + 8u * (39 + a); };    // and has been read
-    const uint32_t bar_pv = bar0 + 8u * 41;                          // kMono: PV of a tile is done
-    const uint32_t bar_ml = bar0 + 8u * 42, bar_mlfree = bar0 + 8u * 43, bar_drain = bar0 + 8u * 44;
+    auto bar_q = [&](int a) { return bar0 + 8u * (32 + a); };        // query tile a is loaded
+    auto bar_s = [&](int a) { return bar0 + 8u * (34 + a); };        // S buffer a is complete
+    auto bar_p = [&](int a) { return bar0 + 8u * (36 + a); };        // P buffer a is written
+    auto bar_o = [&](int a) { return bar0 + 8u * (38 + a); };        // O_a of the piece is complete
+    auto bar_ofree = [&](int a) { return bar0 + 8u * (40 + a); };    // and has been read
+    auto bar_pv = [&](int a) { return bar0 + 8u * (42 + a); };       // d = 256: P buffer a has been read
+    const uint32_t bar_ml = bar0 + 8u * 44, bar_mlfree = bar0 + 8u * 45;
+    auto bar_drain = [&](int a) { return bar0 + 8u * (46 + a); };
+    const uint32_t bar_sdone = bar0 + 8u * 48;                       // d = 256: every S of a piece is done
+    auto bar_turn = [&](int a) { return bar0 + 8u * (49 + a); };     // long pieces: issuer a's turn
     volatile int *abort_flag = &m->abort_flag;
     const int32_t nslot = p.nslot, nraw = p.nraw;
 
     if (tid == 0) {
         for (int s = 0; s < 8; ++s) {
-            mbar_init(bar_full(s), Q8 ? 4 : 1);
-            mbar_init(bar_empty(s), 1);
+            mbar_init(bar_full(s), Q8 ? Cfg::kConvWarps : 1);
+            mbar_init(bar_empty(s), 2);                              // one release from each issuer
             mbar_init(bar_rfull(s), 1);
-            mbar_init(bar_rempty(s), 4);
+            mbar_init(bar_rempty(s), Q8 ? Cfg::kConvWarps : 1);
         }
-        mbar_init(bar_q, 1);
         for (int a = 0; a < 2; ++a) {
+            mbar_init(bar_q(a), 1);
+            mbar_init(bar_turn(a), 1);
+            mbar_init(bar_pv(a), 1);
+            mbar_init(bar_drain(a), 1);
             mbar_init(bar_s(a), 1);
             mbar_init(bar_p(a), 4);
             mbar_init(bar_o(a), 1);
             mbar_init(bar_ofree(a), 4);
         }
-        mbar_init(bar_pv, 1);
         mbar_init(bar_ml, 4);
         mbar_init(bar_mlfree, 4);
-        mbar_init(bar_drain, 1);
+        mbar_init(bar_sdone, 1);
         mbar_fence_init();
         m->abort_flag = 0;
         m->prefix[0] = 0;
@@ -407,49 +431,71 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     ChunkPiece s;
     auto is_long = [&](const ChunkPiece &x) { return !kMono && x.ntok > p.R; };
 
-    if constexpr (Q8 && !kMono) {
-        // 512 threads of 128 registers at launch: 72 + 2 * 176 + 88 = 4 * 128
+    if constexpr (Q8) {
+        // the registers of 640 threads (96 at launch; 512 and 128 for d = 256) by warpgroup:
+        // 96 + 2 * 128 + 2 * 64 = 5 * 96, and 96 + 160 + 2 * 64 < 4 * 128
         if (warp < Cfg::kSoftWarp0)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         else if (warp < Cfg::kConvWarp0)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMono ? 160 : 128));
         else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     }
 
-    if (warp == 0) {
-        // ============================================================ K / V producer
-        // The warp runs the loop together: lane u < 8 looks after positions 16 u .. 16 u + 15 of a
-        // tile, which lie in one page.  Positions past the block's last visible key, and pages
-        // whose id is outside the pool, are loaded from a page past the pool: TMA fills zeros.
-        uint32_t pos = 0;             // half tiles loaded so far
+    if (warp == 0 || (Cfg::kTwoLoad && warp == 3)) {
+        // ============================================================ K / V producers
+        // One warp loads K and one V (issuing the copies of 16-token pages is what bounds a single one);
+        // the ring holds whole tiles, so each has its own slots.  A warp runs its loop together: lane u
+        // looks after positions 4 u .. 4 u + 3 of a tile, which lie in one page, and the lane of a
+        // page's first positions loads the page.  What lies past the block's last visible key, and
+        // pages whose id is outside the pool, is loaded from a page past the pool: TMA fills zeros.
+        // Exponent bytes come by ordinary loads one tile ahead (page ids two), as copies of their own
+        // would double the TMA's requests, and go to shared memory as the multipliers that the
+        // converting warps need.
+        const int kv0 = Cfg::kTwoLoad ? (warp == 0 ? 0 : 1) : 0, kv1 = Cfg::kTwoLoad ? kv0 + 1 : 2;
         bool ok = true;
         const int32_t nring = Q8 ? nraw : nslot;
-        uint32_t slot = 0, phase = 0;
+        uint32_t done = 0;            // tiles loaded
+        uint32_t slot = kv0 * NH, phase = 0;
         const uint64_t pol_once = l2_policy_evict_first();
+        const int32_t in_page = (1 << p.c.page_shift) - 1;
+        const bool loads = ((lane * 4) & in_page) == 0;
         for (bool have = ck_first<NT>(p, m, s, v0, v1); have && ok; have = ck_next<NT>(p, m, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
+            constexpr int32_t kNone = INT32_MIN;             // nothing of the tile needs a page here
             auto page_of = [&](int32_t t) -> int32_t {
-                const int32_t at = t * kCkKeys + lane * 16;
-                if (lane >= 8 || t >= s.t1 || at >= s.len)
-                    return -2;
+                const int32_t at = t * kCkKeys + lane * 4;
+                if (t >= s.t1 || (at & ~in_page) >= s.len)
+                    return kNone;
                 return __ldg(bt + (at >> p.c.page_shift));
             };
-            const bool once = s.nb == 1;      // no other block of the request reads these keys
-            int32_t id_next = page_of(s.t0);
-            for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
-                int32_t id = id_next;
-                id_next = page_of(t + 1);
-                if (id != -2 && (id < 0 || id >= p.c.num_pages)) {
+            auto checked = [&](int32_t id) -> int32_t {      // -1: none, or none in the pool
+                if (id >= 0 && id < p.c.num_pages)
+                    return id;
+                if (id != kNone)
                     set_status(p.status, SVP_DEV_BAD_CONTEXT);
-                    id = -2;
-                }
-                const int32_t tok = (t * kCkKeys + lane * 16) & ((1 << p.c.page_shift) - 1);
+                return -1;
+            };
+            auto exps_of = [&](int kv, int32_t t, int32_t id) -> uint32_t {   // of this lane's four rows
+                if (!Q8 || id < 0)
+                    return 0;
+                const int64_t at = (((int64_t)id * p.c.hkv + s.g) << p.c.page_shift) + ((t * kCkKeys + lane * 4) & in_page);
+                return __ldg(reinterpret_cast<const uint32_t *>((kv ? p.c.v_exp : p.c.k_exp) + at));
+            };
+            const bool once = s.nb == 1;      // no other block of the request reads these keys
+            int32_t id = checked(page_of(s.t0)), id1 = page_of(s.t0 + 1);
+            uint32_t e[2] = {0, 0}, e1[2] = {0, 0};
+            for (int kv = kv0; kv < kv1; ++kv)
+                e[kv] = exps_of(kv, s.t0, id);
+            for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++done) {
+                id1 = checked(id1);
+                const int32_t id2 = page_of(t + 2);
+                for (int kv = kv0; kv < kv1; ++kv)
+                    e1[kv] = exps_of(kv, t + 1, id1);
                 const int32_t page = id < 0 ? max(p.c.num_pages, 1) : id;
-                const int32_t nvalid = __popc(__ballot_sync(0xffffffffu, id >= 0));
-                for (int kv = 0; kv < 2 && ok; ++kv) {
+                for (int kv = kv0; kv < kv1 && ok; ++kv) {
                     const CUtensorMap *tm = kv ? &p.tm_v : &p.tm_k;
-                    for (int h = 0; h < NH; ++h, ++pos) {
+                    for (int h = 0; h < NH; ++h) {
                         const uint32_t full = Q8 ? bar_rfull(slot) : bar_full(slot);
                         int got = 1;
                         if (lane == 0)
@@ -458,39 +504,40 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                             break;
                         if constexpr (Q8) {
                             const uint32_t dst = sbase + p.off_raw + slot * Cfg::kRawSlot;
-                            if (lane < 8 && id < 0)   // the codes are zeros: any finite scale will do
-                                st_shared_v4(dst + Cfg::kRaw + lane * 16, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu,
-                                             0x7f7f7f7fu);
-                            fence_proxy_async_smem();
+                            if (loads) {
+                                if (once)
+                                    tma_load_4d_hint(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page, pol_once);
+                                else
+                                    tma_load_4d(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page);
+                            }
+                            // low half: 2^(120 + b - 127) in bf16 (NaN for 255, 0 past the last visible
+                            // key); high half: the rest of exponents above 2^7, else 1
+                            uint32_t mul[4];
+                            const int32_t left = s.len - t * kCkKeys - lane * 4;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t b = (e[kv] >> (8 * x)) & 0xffu;
+                                const uint32_t lo = b == 255u ? 0x7fc0u : (min(b, 134u) + 120u) << 7;
+                                const uint32_t hi = b == 255u ? 0x3f80u : (max(b, 134u) - 134u + 127u) << 7;
+                                mul[x] = x < left ? lo | (hi << 16) : 0x3f800000u;
+                            }
+                            st_shared_v4(dst + Cfg::kRaw + lane * 16, mul[0], mul[1], mul[2], mul[3]);
                             __syncwarp();
                             if (lane == 0)
-                                mbar_arrive_expect_tx(full, (uint32_t)(Cfg::kRaw + 16 * nvalid));
-                            __syncwarp();
-                            if (lane < 8) {
-                                if (once)
-                                    tma_load_4d_hint(dst + lane * 16 * DH, tm, full, h * DH, tok, s.g, page, pol_once);
-                                else
-                                    tma_load_4d(dst + lane * 16 * DH, tm, full, h * DH, tok, s.g, page);
-                                if (id >= 0)
-                                    ck_bulk16(dst + Cfg::kRaw + lane * 16,
-                                              (kv ? p.c.v_exp : p.c.k_exp) +
-                                                  ((((int64_t)id * p.c.hkv + s.g) << p.c.page_shift) + tok),
-                                              full);
-                            }
+                                mbar_arrive_expect_tx(full, (uint32_t)Cfg::kRaw);
                         } else {
                             const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
                             if (lane == 0)
                                 mbar_arrive_expect_tx(full, (uint32_t)Cfg::kSlot);
                             __syncwarp();
-                            if (lane < 8) {
+                            if (loads) {
 #pragma unroll
                                 for (int c = 0; c < DH / 64; ++c) {
+                                    const uint32_t at = dst + c * kCkSub + lane * 512;
                                     if (once)
-                                        tma_load_4d_hint(dst + c * kCkSub + lane * 2048, tm, full, h * DH + c * 64, tok,
-                                                         s.g, page, pol_once);
+                                        tma_load_4d_hint(at, tm, full, h * DH + c * 64, 0, s.g, page, pol_once);
                                     else
-                                        tma_load_4d(dst + c * kCkSub + lane * 2048, tm, full, h * DH + c * 64, tok, s.g,
-                                                    page);
+                                        tma_load_4d(at, tm, full, h * DH + c * 64, 0, s.g, page);
                                 }
                             }
                         }
@@ -500,162 +547,241 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                             phase ^= 1u;
                         }
                     }
+                    if (Cfg::kTwoLoad && (slot += NH) >= (uint32_t)nring) {   // past the other warp's
+                        slot -= nring;
+                        phase ^= 1u;
+                    }
                 }
+                e[0] = e1[0];
+                e[1] = e1[1];
+                id = id1;
+                id1 = id2;
             }
         }
         // every load lands (and, of the bf16 ring, every release by the tensor core) before the
-        // CTA's shared memory is given back
+        // CTA's shared memory is given back; a fill that did not happen is not waited for
         if (lane == 0) {
             volatile int drain = 0;
-            const uint32_t first = pos > (uint32_t)nring ? pos - nring : 0u;
-            for (uint32_t k = first; k < pos; ++k) {
-                mbar_wait(Q8 ? bar_rfull((int)(k % nring)) : bar_full((int)(k % nring)), (k / nring) & 1u, &drain);
-                if (!Q8 && ok)
-                    mbar_wait(bar_empty((int)(k % nring)), (k / nring) & 1u, abort_flag);
-            }
+            const uint32_t back = nring / (2 * NH) + 1;
+            for (uint32_t x = done > back ? done - back : 0u; x < done; ++x)
+                for (int kv = kv0; kv < kv1; ++kv)
+                    for (int h = 0; h < NH; ++h) {
+                        const uint32_t k = x * 2 * NH + kv * NH + h;
+                        if (k + nring < done * 2 * NH)
+                            continue;         // filled again later
+                        mbar_wait(Q8 ? bar_rfull(k % nring) : bar_full(k % nring), (k / nring) & 1u, &drain);
+                        if (!Q8 && ok)
+                            mbar_wait(bar_empty(k % nring), (k / nring) & 1u, abort_flag);
+                    }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ============================================================ MMA issuer
-        // The warp runs the loop together (it clears V rows together); lane 0 issues.
+    } else if (warp == 1 || warp == 2) {
+        // ============================================================ MMA issuers
+        // A thread's waits queue behind the MMAs it has issued, so one issuer alone leaves the tensor
+        // pipe idle between them: two warps issue.  d <= 128: warp 1 + a issues S_a and PV_a (its own
+        // next wait, for the P that follows that S, could not end earlier anyway), and in short pieces
+        // only looks after every other tile.  d = 256: warp 1 issues S, warp 2 PV.  Both warps see every
+        // ring slot filled and both release it (a parity wait may not skip a phase).  The warps run
+        // their loops together (they clear V rows together); lane 0 issues.
+        const int me = warp - 1;
         const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
         const uint32_t idesc_o = idesc_bf16_f32(128, DH, false, true);
-        uint32_t tile0 = 0, npiece = 0;       // KV tiles and pieces before this one
-        uint32_t np_[2] = {0, 0}, no_[2] = {0, 0};   // uses of P / S buffer a and of O_a so far
+        uint32_t nq = 0, q_loads = 0;         // query tiles used and loaded
+        uint32_t npiece = 0, nturn = 0;
+        uint32_t nsp[2] = {0, 0}, no = 0;     // uses of S / P buffer a, and of this warp's O, so far
         bool ok = true;
+        uint32_t slot = 0, phase = 0;         // ring position
+        auto step = [&]() {
+            if (++slot == (uint32_t)nslot) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         };
+        // Long pieces: the two issuers take turns, PV of a tile and S of the next at a time, warp 1 first.
+        // Left to share the pipe they keep in step: both tiles' MMAs at once, then both softmaxes.
+        auto turn = [&]() -> bool {
+            const uint32_t n = nturn++;
+            return me == 0 ? n == 0 || wait_all(bar_turn(0), (n - 1) & 1u) : wait_all(bar_turn(1), n & 1u);
+        };
+        auto yield = [&]() {
+            if (lane == 0)
+                mbar_arrive(bar_turn(me ^ 1));
+            __syncwarp();
+        };
+        // NH slots of the other warp's: seen and released
+        auto pass = [&]() -> bool {
+            for (int h = 0; h < NH; ++h) {
+                if (!wait_all(bar_full(slot), phase))
+                    return false;
+                if (lane == 0)
+                    mbar_arrive(bar_empty(slot));
+                step();
+            }
+            return true;
+        };
+        auto my_jobs = [&](const ChunkPiece &x) -> int32_t {   // tiles of the piece that this warp works on
+            const int32_t nt = x.t1 - x.t0;
+            return kMono || is_long(x) ? nt : (nt + 1 - me) >> 1;
+        };
         auto load_q = [&](const ChunkPiece &x) {
+            if (kMono ? me != 0 : my_jobs(x) == 0)
+                return;
             if (lane == 0) {
-                const int tiles = is_long(x) ? 2 : 1;
-                mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles * (D / 64) * 128 * p.G * p.R));
-                for (int a = 0; a < tiles; ++a)
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(sbase + a * Cfg::kQTile + c * kCkSub, &p.tm_q, bar_q, c * 64, x.g * p.G,
-                                    x.off + x.tb0 + a * p.R);
+                mbar_arrive_expect_tx(bar_q(me), (uint32_t)((D / 64) * 128 * p.G * p.Rb));
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(sbase + (me * (D / 64) + c) * p.qsub, &p.tm_q, bar_q(me), c * 64, x.g * p.G,
+                                x.off + x.tb0 + (is_long(x) ? me * p.R : 0));
             }
             __syncwarp();
+            ++q_loads;
+        };
+        auto issue_s = [&](int buf) -> bool {                  // S of the tile at the ring position
+            for (int h = 0; h < NH; ++h) {
+                if (!wait_all(bar_full(slot), phase))
+                    return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t qd = sw128_desc(sbase + (me * (D / 64) + h * 2) * p.qsub, 16, 1024);
+                    const uint64_t kd = sw128_desc(sbase + p.off_ring + slot * Cfg::kSlot, 16, 1024);
+                    const uint32_t qs16 = (uint32_t)p.qsub >> 4;
+#pragma unroll
+                    for (int ks = 0; ks < DH / 16; ++ks)
+                        tc_mma_ss(tmem + buf * 128, qd + (uint64_t)((ks >> 2) * qs16 + (ks & 3) * 2),
+                                  kd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2), idesc_s,
+                                  (h | ks) ? 1u : 0u);
+                    if (h == NH - 1)
+                        tc_commit(bar_s(buf));
+                    tc_commit(bar_empty(slot));
+                }
+                step();
+            }
+            __syncwarp();
+            return true;
+        };
+        bool have_next = false;
+        auto issue_pv = [&](int buf, int ob, int32_t kvalid, bool first, bool last, bool lng) -> bool {
+            uint32_t sl[NH];
+            for (int h = 0; h < NH; ++h) {
+                if (!wait_all(bar_full(slot), phase))
+                    return false;
+                sl[h] = slot;
+                step();
+            }
+            // rows of the last page past the last visible key may hold anything, and P = 0 does not hide
+            // a NaN: they are cleared (whole pages past it are zeros already, and the converting warps'
+            // multipliers clear theirs)
+            const int32_t rest = kvalid & ((1 << p.c.page_shift) - 1);
+            if (!Q8 && kvalid < kCkKeys && rest) {
+                const int32_t rows = (1 << p.c.page_shift) - rest;
+                for (int h = 0; h < NH; ++h)
+                    for (int32_t x = lane; x < rows * (DH / 8); x += 32) {
+                        const int32_t r = kvalid + x / (DH / 8), c = x % (DH / 8);
+                        st_shared_v4(sbase + p.off_ring + sl[h] * Cfg::kSlot + (c >> 3) * kCkSub + r * 128 +
+                                         (c & 7) * 16, 0u, 0u, 0u, 0u);
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (first && no > 0 && !wait_all(bar_ofree(ob), (no - 1) & 1u))
+                return false;
+            if (!wait_all(bar_p(buf), nsp[buf] & 1u))
+                return false;
+            ++nsp[buf];
+            if (!kMono && last) {
+                // this warp's last P of the piece: all its S are done and its query tile may be replaced
+                have_next = ck_next<NT>(p, m, s, v1);
+                if (have_next)
+                    load_q(s);
+            }
+            if (lng && !turn())
+                return false;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const uint64_t vd = sw128_desc(sbase + p.off_ring + sl[h] * Cfg::kSlot, kCkSub, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)   // 16 keys = 8 TMEM columns of P a step
+                        ck_mma_ts(tmem + 256 + ob * D + h * DH, tmem + buf * 128 + ks * 8, vd + (uint64_t)(ks * 128),
+                                  idesc_o, (!first || ks) ? 1u : 0u);
+                    tc_commit(bar_empty(sl[h]));
+                }
+                if (kMono)
+                    tc_commit(bar_pv(buf));
+                if (last)
+                    tc_commit(bar_o(ob));
+            }
+            __syncwarp();
+            return true;
         };
         bool have = ck_first<NT>(p, m, s, v0, v1);
         if (have)
             load_q(s);
-        uint32_t q_loads = have ? 1 : 0;
         while (have && ok) {
+            const int32_t nt = s.t1 - s.t0, mine = my_jobs(s);
             const bool lng = is_long(s);
-            const int32_t nt = s.t1 - s.t0, nj = lng ? 2 * nt : nt;
-            auto pos_of = [&](int32_t t, int kv, int h) { return (tile0 + t) * (2u * NH) + kv * NH + h; };
-            auto issue_s = [&](int32_t j) -> bool {
-                const int32_t t = lng ? j >> 1 : j;
-                const int a = j & 1;
-                for (int h = 0; h < NH; ++h) {
-                    const uint32_t ps = pos_of(t, 0, h);
-                    const int sl = (int)(ps % nslot);
-                    if ((!lng || a == 0) && !wait_all(bar_full(sl), (ps / nslot) & 1u))
-                        return false;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t qd = sw128_desc(sbase + (lng ? a : 0) * Cfg::kQTile + h * 2 * kCkSub, 16, 1024);
-                        const uint64_t kd = sw128_desc(sbase + p.off_ring + sl * Cfg::kSlot, 16, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < DH / 16; ++ks)
-                            tc_mma_ss(tmem + a * 128, qd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2),
-                                      kd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2), idesc_s,
-                                      (h | ks) ? 1u : 0u);
-                        if (!lng || a == 1)
-                            tc_commit(bar_empty(sl));
-                    }
-                }
-                if (lane == 0)
-                    tc_commit(bar_s(a));
-                __syncwarp();
-                return true;
-            };
-            if (!(ok = wait_all(bar_q, npiece & 1u)))
-                break;
-            if (!(ok = issue_s(0)) || (nj > 1 && !(ok = issue_s(1))))
-                break;
-            ChunkPiece nx = s;
-            bool have_next = false;
-            for (int32_t j = 0; j < nj; ++j) {
-                const int32_t t = lng ? j >> 1 : j;
-                const int a = j & 1, ob = kMono ? 0 : a;
-                if (!(ok = wait_all(bar_p(a), np_[a] & 1u)))
+            if (mine > 0 && (!kMono || me == 0)) {
+                if (!(ok = wait_all(bar_q(me), nq & 1u)))
                     break;
-                ++np_[a];
-                const bool first = kMono ? j == 0 : j < 2;
-                if (first && no_[ob] > 0 && !(ok = wait_all(bar_ofree(ob), (no_[ob] - 1) & 1u)))
-                    break;
-                if (j == nj - 1) {
-                    // every S of this piece is done (its last P is written): Q may be replaced
-                    have_next = ck_next<NT>(p, m, nx, v1);
-                    if (have_next) {
-                        load_q(nx);
-                        ++q_loads;
-                    }
-                }
-                for (int h = 0; h < NH; ++h) {
-                    const uint32_t ps = pos_of(t, 1, h);
-                    const int sl = (int)(ps % nslot);
-                    const uint32_t va = sbase + p.off_ring + sl * Cfg::kSlot;
-                    if (!lng || a == 0) {
-                        if (!(ok = wait_all(bar_full(sl), (ps / nslot) & 1u)))
+                ++nq;
+            }
+            // (from the last P on, s is the next piece: what the loop needs of this one is kept here)
+            int32_t kvalid = s.len - s.t0 * kCkKeys;      // keys of tile t that the block sees
+            for (int32_t t = 0; t < nt; ++t, kvalid -= kCkKeys) {
+                if (kMono) {
+                    const int buf = t & 1;
+                    if (me == 0) {
+                        // the buffer's last P has been read
+                        if (!(ok = nsp[buf] == 0 || wait_all(bar_pv(buf), (nsp[buf] - 1) & 1u)) ||
+                            !(ok = issue_s(buf)))
                             break;
-                        // rows of the last page past the last visible key may hold anything, and
-                        // P = 0 does not hide a NaN: they are cleared (whole pages past it are zeros
-                        // already, and the converting warps clear theirs)
-                        const int32_t kvalid = s.len - (s.t0 + t) * kCkKeys;
-                        if (!Q8 && kvalid < kCkKeys && (kvalid & 15)) {
-                            const int32_t rows = 16 - (kvalid & 15);
-                            for (int32_t x = lane; x < rows * (DH / 8); x += 32) {
-                                const int32_t r = kvalid + x / (DH / 8), c = x % (DH / 8);
-                                st_shared_v4(va + (c >> 3) * kCkSub + r * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
+                        ++nsp[buf];
+                        if (t == nt - 1 && lane == 0)
+                            tc_commit(bar_sdone);
+                        if (!(ok = pass()))
+                            break;
+                    } else if (!(ok = pass()) || !(ok = issue_pv(buf, 0, kvalid, t == 0, t == nt - 1, false))) {
+                        break;
                     }
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t vd = sw128_desc(va, kCkSub, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)   // 16 keys = 8 TMEM columns of P a step
-                            ck_mma_ts(tmem + 256 + ob * D + h * DH, tmem + a * 128 + ks * 8, vd + (uint64_t)(ks * 128),
-                                      idesc_o, (!first || ks) ? 1u : 0u);
-                        if (!lng || a == 1)
-                            tc_commit(bar_empty(sl));
-                    }
-                }
-                if (!ok)
+                } else if (lng) {
+                    // (the K wait is inside the turn: the other issuer needs the same tile)
+                    if ((t == 0 && !(ok = turn())) || !(ok = issue_s(me)))
+                        break;
+                    yield();
+                    if (!(ok = issue_pv(me, me, kvalid, t == 0, t == nt - 1, true)))
+                        break;
+                    if (t == nt - 1)
+                        yield();
+                } else if ((t & 1) == me) {
+                    if (!(ok = issue_s(me)) || !(ok = issue_pv(me, me, kvalid, t < 2, t + 2 >= nt, false)))
+                        break;
+                } else if (!(ok = pass()) || !(ok = pass())) {
                     break;
-                if (lane == 0) {
-                    if (kMono)
-                        tc_commit(bar_pv);
-                    if (kMono ? j == nj - 1 : j + 2 >= nj)
-                        tc_commit(bar_o(ob));
                 }
-                __syncwarp();
-                if (j + 2 < nj && !(ok = issue_s(j + 2)))
-                    break;
             }
             if (!ok)
                 break;
-            ++no_[0];
-            if (!kMono && nj > 1)
-                ++no_[1];
-            tile0 += (uint32_t)nt;
+            if (mine > 0)
+                ++no;
+            if (kMono || mine == 0) {
+                have_next = ck_next<NT>(p, m, s, v1);
+                if (kMono && me == 0 && !(ok = wait_all(bar_sdone, npiece & 1u)))
+                    break;
+                if (have_next)
+                    load_q(s);
+            }
             ++npiece;
-            s = nx;
             have = have_next;
         }
         if (lane == 0) {
             volatile int drain = 0;
-            if (kMono && tile0 > 0 && ok)
-                mbar_wait(bar_pv, (tile0 - 1) & 1u, &drain);
-            tc_commit(bar_drain);
-            mbar_wait(bar_drain, 0, &drain);
-            for (uint32_t k = npiece; k < q_loads; ++k)   // query tiles on their way when a wait gave up
-                mbar_wait(bar_q, k & 1u, &drain);
+            tc_commit(bar_drain(me));
+            mbar_wait(bar_drain(me), 0, &drain);
+            for (uint32_t k = nq; k < q_loads; ++k)   // a query tile on its way when a wait gave up
+                mbar_wait(bar_q(me), k & 1u, &drain);
         }
         __syncwarp();
     } else if (warp >= Cfg::kSoftWarp0 && warp < Cfg::kConvWarp0) {
@@ -665,7 +791,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t to0 = tmem + lane_off + 256;
         const float cl2 = p.scale_log2;
-        uint32_t ns_[2] = {0, 0}, no_[2] = {0, 0}, nml = 0, npv = 0;
+        uint32_t ns_[2] = {0, 0}, no_[2] = {0, 0}, nml = 0;
         bool ok = true, owe = false;
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
@@ -693,64 +819,48 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (owe && !(ok = wait_all(bar_o(1), (no_[1] - 1) & 1u)))
                     break;
                 owe = false;
-                // PV of the tile before (one accumulator for all tiles): waited for in every tile before
-                // the arrival below, which its successor needs; the tensor pipe has S of the next tile to
-                // go on with.
-                bool pv_seen = !kMono || npv == 0;
+                // d = 256: PV of the tile before, into the same O, is waited for before a rescale and before
+                // the arrival below (which PV of this tile needs; the pipe has S of the next to go on with)
+                bool pv_seen = !kMono || t == 0;
                 tc_fence_after();
                 if (warp_live) {
                     const int32_t k0 = (s.t0 + t) * kCkKeys;
                     const bool masked = k0 + kCkKeys - 1 > all;
                     const int32_t kmax = last - k0;
-                    uint32_t pk[64];
-                    float tsum;
-                    // (a row that has seen no score yet has no reference)
-                    bool move = done == 0 || __any_sync(0xffffffffu, live && m_ref == -INFINITY);
+                    const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * cl2;
+                    // the reference moves when a score lies more than 2^8 above it (or there is none yet)
+                    if (__any_sync(0xffffffffu, live && (tmax > m_ref + kCkSlack || (m_ref == -INFINITY && tmax != m_ref)))) {
+                        const float m_new = fmaxf(m_ref, tmax);
+                        if (done > 0) {
+                            const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - m_new);
+                            if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
+                                break;
+                            pv_seen = true;
+                            tc_fence_after();
 #pragma unroll 1
-                    for (;;) {
-                        if (move) {
-                            const float tmax = fmaxf(m_ref, (masked ? ck_row_max<true>(ts, kmax)
-                                                                    : ck_row_max<false>(ts, kmax)) * cl2);
-                            if (done > 0) {
-                                const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - tmax);
-                                if (!pv_seen && !(ok = wait_all(bar_pv, (npv - 1) & 1u)))
-                                    break;
-                                pv_seen = true;
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int cc = 0; cc < D / 32; ++cc) {
-                                    uint32_t ov[32];
-                                    tmem_ld32(to + cc * 32, ov);
-                                    tmem_wait_ld();
+                            for (int cc = 0; cc < D / 32; ++cc) {
+                                uint32_t ov[32];
+                                tmem_ld32(to + cc * 32, ov);
+                                tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                    tmem_st32(to + cc * 32, ov);
-                                }
-                                l *= alpha;
+                                for (int e = 0; e < 32; ++e)
+                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                tmem_st32(to + cc * 32, ov);
                             }
-                            m_ref = tmax;
+                            l *= alpha;
                         }
-                        const float mm = m_ref == -INFINITY ? 0.0f : m_ref;
-                        tsum = masked ? ck_row_exp<true>(ts, kmax, cl2, mm, pk) : ck_row_exp<false>(ts, kmax, cl2, mm, pk);
-                        if (move || !__any_sync(0xffffffffu, live && !(tsum <= kCkSumLimit)))
-                            break;
-                        move = true;
+                        m_ref = m_new;
                     }
-                    if (!ok)
-                        break;
-                    tmem_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-                    tmem_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
-                    l += tsum;
+                    const float mm = m_ref == -INFINITY ? 0.0f : m_ref;
+                    l += masked ? ck_row_exp<true>(ts, kmax, cl2, mm) : ck_row_exp<false>(ts, kmax, cl2, mm);
                     tmem_wait_st();
                 }
-                if (!pv_seen && !(ok = wait_all(bar_pv, (npv - 1) & 1u)))
+                if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
                     break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_p(buf));
-                ++npv;
             }
             if (!ok)
                 break;
@@ -859,68 +969,66 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         }
     } else if (Q8 && warp >= Cfg::kConvWarp0) {
         // ============================================================ codes -> bf16 tiles
-        // A thread takes 16 codes of one row at a time (neighbours take the rest of the row): reads
-        // and writes of a quarter warp fall on different banks, the odd half of the row writing its
-        // second 16 bytes first.
+        // A thread takes 16 codes of one row at a time, its neighbours the rest of the row.
         if constexpr (Q8) {
             constexpr int CPR = DH / 16;                  // 16-code chunks a row
+            constexpr int RPI = 32 * Cfg::kConvWarps / CPR;   // rows a turn
             const int ct = tid - Cfg::kConvWarp0 * 32;
             const int c = ct % CPR, row0 = ct / CPR;
+            // which half of its 16 codes a thread takes first: the lanes of one access then cover all banks,
+            // in the raw rows as in the swizzled ones
+            const int odd = (DH == 128 ? (c >> 2) ^ row0 : row0 >> 1) & 1;
+            const uint32_t src = row0 * DH + c * 16 + odd * 8, src2 = row0 * DH + c * 16 + (odd ^ 1) * 8;
+            const uint32_t line = (c >> 2) * kCkSub + row0 * 128;
+            const uint32_t out = line + (((2 * (c & 3) + odd) ^ (row0 & 7)) << 4);
+            const uint32_t out2 = line + (((2 * (c & 3) + (odd ^ 1)) ^ (row0 & 7)) << 4);
             uint32_t pos = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
             bool ok = true;
-            for (bool have = ck_first<NT>(p, m, s, v0, v1); have && ok; have = ck_next<NT>(p, m, s, v1)) {
-                for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
-                    const int32_t kvalid = s.len - t * kCkKeys;
-                    for (int half = 0; half < 2 * NH; ++half, ++pos) {
-                        const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
-                                         mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
-                        if (!(ok = __all_sync(0xffffffffu, got)))
-                            break;
-                        const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
-                        const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
-#pragma unroll 4
-                        for (int it = 0; it < CPR; ++it) {
-                            const int row = it * (128 / CPR) + row0;
-                            const uint4 w = *reinterpret_cast<const uint4 *>(raw + row * DH + c * 16);
-                            const uint32_t b = raw[Cfg::kRaw + row];
-                            // 2^(120 + b - 127) as bf16; exponents above 2^7 in a second product
-                            uint32_t mul = b == 255u ? 0x7fc0u : (min(b, 134u) + 120u) << 7;
-                            mul = row < kvalid ? mul : 0u;
-                            mul |= mul << 16;
-                            uint32_t x[8] = {ck_codes<0x9180>(w.x), ck_codes<0xb3a2>(w.x), ck_codes<0x9180>(w.y),
-                                             ck_codes<0xb3a2>(w.y), ck_codes<0x9180>(w.z), ck_codes<0xb3a2>(w.z),
-                                             ck_codes<0x9180>(w.w), ck_codes<0xb3a2>(w.w)};
+            uint32_t halves = 0;                          // of all pieces
+            for (bool have = ck_first<NT>(p, m, s, v0, v1); have; have = ck_next<NT>(p, m, s, v1))
+                halves += (uint32_t)(s.t1 - s.t0) * 2 * NH;
+            {
+                for (; pos < halves; ++pos) {
+                    const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
+                                     mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, got)))
+                        break;
+                    const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
+                    const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
+#pragma unroll 2
+                    for (int it = 0; it < 128 / RPI; ++it) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
+                        const uint2 w2 = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
+                        const uint32_t mw = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
+                        const uint32_t mul = __byte_perm(mw, 0, 0x1010);
+                        uint32_t x[8] = {ck_codes<0x9180>(w.x), ck_codes<0xb3a2>(w.x), ck_codes<0x9180>(w.y),
+                                         ck_codes<0xb3a2>(w.y), ck_codes<0x9180>(w2.x), ck_codes<0xb3a2>(w2.x),
+                                         ck_codes<0x9180>(w2.y), ck_codes<0xb3a2>(w2.y)};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = ck_mul2(x[e], mul);
+                        if ((mw >> 16) != 0x3f80u) {      // an exponent above 2^7: the rest of it
+                            const uint32_t more = __byte_perm(mw, 0, 0x3232);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                x[e] = ck_mul2(x[e], mul);
-                            if (b > 134u && b < 255u) {
-                                const uint32_t more = ((b - 134u + 127u) << 7) * 0x10001u;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    x[e] = ck_mul2(x[e], more);
-                            }
-                            const int odd = (c >> 2) & 1;
-                            const uint32_t line = dst + (c >> 2) * kCkSub + row * 128;
-                            const int ch = 2 * (c & 3);
-                            const uint32_t a0 = line + (((ch + odd) ^ (row & 7)) << 4);
-                            const uint32_t a1 = line + (((ch + (odd ^ 1)) ^ (row & 7)) << 4);
-                            st_shared_v4(a0, odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
-                            st_shared_v4(a1, odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
+                                x[e] = ck_mul2(x[e], more);
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(bar_rempty(rslot));
-                            mbar_arrive(bar_full(slot));
-                        }
-                        if (++slot == (uint32_t)nslot) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
-                        if (++rslot == (uint32_t)nraw) {
-                            rslot = 0;
-                            rphase ^= 1u;
-                        }
+                        st_shared_v4(dst + out + it * (RPI * 128), x[0], x[1], x[2], x[3]);
+                        st_shared_v4(dst + out2 + it * (RPI * 128), x[4], x[5], x[6], x[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar_rempty(rslot));
+                        mbar_arrive(bar_full(slot));
+                    }
+                    if (++slot == (uint32_t)nslot) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    if (++rslot == (uint32_t)nraw) {
+                        rslot = 0;
+                        rphase ^= 1u;
                     }
                 }
             }
@@ -1042,21 +1150,30 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
 {
     using Cfg = ChunkCfg<D, Q8>;
     constexpr int kBudget = 227 * 1024;
-    // one query tile is enough when no request can have a long piece
-    const int qbytes = ((Cfg::NT == 2 && p.w > p.R) ? 2 : 1) * Cfg::kQTile;
+    // query blocks hold the rows that a piece can have; the MMA reads 128 rows whatever they are (the
+    // rows behind belong to no query and their results to no output)
+    p.Rb = std::min(p.R, p.w);
+    p.qsub = (p.G * p.Rb + 7) / 8 * 1024;
+    const int qbytes = Cfg::NT * (D / 64) * p.qsub;
     const int misc = (int)(sizeof(ChunkMisc) + (size_t)p.n * sizeof(int64_t) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
+    // rings that a K and a V loader share hold whole tiles (2 NH slots); the bf16 ring of 8-bit pages is
+    // filled by the converting warps in order and needs 3 slots (4 for d = 256: S of the next tile is
+    // issued before V of this one is released)
+    constexpr int kTile = 2 * Cfg::NH, kLeast = Cfg::NH == 2 ? 4 : 3;
     if (Q8) {
-        // as many raw as bf16 slots, and a fourth bf16 slot before a fourth raw one: S of the next
-        // tile but one is issued before V of this tile is released
-        p.nraw = std::min(8, std::max(2, (room - 4 * Cfg::kSlot) / Cfg::kRawSlot));
-        p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
+        p.nslot = 4;
+        p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot);
+        if (Cfg::kTwoLoad)
+            p.nraw = p.nraw / kTile * kTile;
+        if (p.nraw >= 2)
+            p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
     } else {
-        p.nraw = 1;
-        p.nslot = std::min(8, room / Cfg::kSlot);
+        p.nraw = kTile;
+        p.nslot = std::min(8, room / Cfg::kSlot) / kTile * kTile;
     }
-    if (p.nslot < (D == 256 ? 4 : 3))
+    if (p.nslot < kLeast || p.nraw < 2)
         return SVP_EUNSUPPORTED;
     p.off_raw = p.off_ring + p.nslot * Cfg::kSlot;
     p.off_misc = p.off_raw + (Q8 ? p.nraw * Cfg::kRawSlot : 0);
@@ -1100,7 +1217,7 @@ svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const 
     {
         const uint64_t dims[3] = {(uint64_t)d, (uint64_t)hq, (uint64_t)m_cap};
         const uint64_t str[2] = {(uint64_t)d * 2, (uint64_t)q_stride * 2};
-        const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)p.R};
+        const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)std::min(p.R, w)};
         if (!encode_tiled(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, q, 3, dims, str, box))
             return SVP_EUNSUPPORTED;
     }
@@ -1110,7 +1227,7 @@ svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const 
         const uint64_t dims[4] = {(uint64_t)d, (uint64_t)1 << c.page_shift, (uint64_t)c.hkv,
                                   (uint64_t)std::max(c.num_pages, 1)};
         const uint64_t str[3] = {(uint64_t)c.s_tok * esz, (uint64_t)c.s_head * esz, (uint64_t)c.s_page * esz};
-        const uint32_t box[4] = {q8 ? (uint32_t)std::min(d, 128) : 64u, 16, 1, 1};
+        const uint32_t box[4] = {q8 ? (uint32_t)std::min(d, 128) : 64u, 1u << c.page_shift, 1, 1};   // a page of one head
         const CUtensorMapDataType type = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         const CUtensorMapSwizzle sw = q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
         if (!encode_tiled(&p.tm_k, type, sw, c.k, 4, dims, str, box) ||
