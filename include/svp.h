@@ -423,9 +423,8 @@ svp_status svp_act_truncate(const float *margins, int64_t stride, int32_t n, int
 /* element below 2^-9 of that power rounds to a multiple of it), so scaling is exact and  */
 /* each element is rounded once, to nearest even: at most 2^-4 relative for elements down */
 /* to 2^-15 of the row's largest.  A row with an infinite or NaN element gets b = 255 and */
-/* codes 0: every element of it reads as NaN.  Readers take any byte; codes 0x7f and 0xff */
-/* (which svp_cache_write never stores) read as +-480 * 2^(b - 127) in svp_chunk_attn and */
-/* svp_cache_read, and b = 0 as 0.                                                       */
+/* codes 0: every element of it reads as NaN, as do codes 0x7f and 0xff.  Readers take    */
+/* any byte (b = 0 as 0).                                                                 */
 typedef struct {
     void *k, *v;                /* page pools, [num_pages] pages of page_size tokens; 16-byte
                                    aligned                                                 */

@@ -71,18 +71,20 @@ struct ChunkCfg {
     // warps: 0 K loader, 1 and 2 MMA issuers, 3 V loader, then warpgroups of softmax and converting warps
     static constexpr int kSoftWarp0 = 4;
     static constexpr int kConvWarp0 = kSoftWarp0 + 4 * NT;
-    static constexpr int kConvWarps = Q8 ? 8 : 0;
+    static constexpr int kConvWarps = Q8 ? 4 : 0;
     static constexpr bool kTwoLoad = !(Q8 && NH == 2);     // (there the raw ring has no room for two tiles)
     static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
     static constexpr int kPartRows = 128 * NT;
 };
 
 struct ChunkMisc {
-    uint64_t bars[52];
+    uint64_t bars[54];
     uint32_t tmem;
     int32_t abort_flag;
     int64_t warp_tot[20];
     float2 ml[128];                   // (m, l) of the second warpgroup's half of a short piece
+    float o_scale;                    // and what its O is to be multiplied with
+    float2 scales[16];                // 8-bit pages: (2^E of K, E of V) of a KV tile, by tile mod 16
     int64_t prefix[1];                // [n + 1]: cost before request i
 };
 
@@ -218,21 +220,29 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// Two codes to bf16 times 2^-120: sel 0x9180 takes bytes 0, 1 of w, 0xb3a2 bytes 2, 3, each
-// with its sign spread over the byte above; then s eeee mmm sits at sign, exponent, mantissa.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t ck_codes(uint32_t w)
+// Four codes to fp16, times the row's power of two (both halves of mul).
+__device__ __forceinline__ void ck_codes(uint32_t w, uint32_t mul, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t y;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w), "n"(SEL));
-    return (y << 4) & 0x87f087f0u;
+    asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 x, y;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 y, b;\n\t"
+        "mul.rn.f16x2 %0, x, %3;\n\t"
+        "mul.rn.f16x2 %1, y, %3;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w), "r"(mul));
 }
 
-__device__ __forceinline__ uint32_t ck_mul2(uint32_t a, uint32_t b)
+__device__ __forceinline__ uint32_t ck_pack_f16x2(float lo, float hi)
 {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float ck_pow2(int32_t e)      // 2^e, e clamped to the normal range
+{
+    return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23);
 }
 
 // The softmax of one S tile in this thread's row, 64 columns a turn: its instructions are kept few, as
@@ -279,9 +289,9 @@ __device__ __forceinline__ float ck_row_max(uint32_t ts, int32_t kmax)
     return mx;
 }
 
-// P = 2^(s * cl2 - m) in bf16 over the first half of S's columns (a turn's P lies over scores that it or
+// P = 2^(s * cl2 - m) in 16 bits over the first half of S's columns (a turn's P lies over scores that it or
 // an earlier turn has read); returns its sum in fp32.
-template <bool kMasked>
+template <bool kMasked, bool F16>
 __device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2, float m)
 {
     const uint64_t c2 = f32x2_pack(cl2, cl2), nm2 = f32x2_pack(-m, -m);
@@ -305,7 +315,7 @@ __device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2
             float y0, y1;
             f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), c2, nm2), y0, y1);
             const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-            pk[e] = pack_bf16x2(p0, p1);
+            pk[e] = F16 ? ck_pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
             acc[e & 1] = f32x2_add(acc[e & 1], f32x2_pack(p0, p1));
         }
         tmem_st32(ts + half * 32, pk);
@@ -343,6 +353,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     auto bar_drain = [&](int a) { return bar0 + 8u * (46 + a); };
     const uint32_t bar_sdone = bar0 + 8u * 48;                       // d = 256: every S of a piece is done
     auto bar_turn = [&](int a) { return bar0 + 8u * (49 + a); };     // long pieces: issuer a's turn
+    auto bar_qc = [&](int a) { return bar0 + 8u * (51 + a); };       // 8-bit pages: query tile a is in fp16
     volatile int *abort_flag = &m->abort_flag;
     const int32_t nslot = p.nslot, nraw = p.nraw;
 
@@ -356,6 +367,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar_q(a), 1);
             mbar_init(bar_turn(a), 1);
+            mbar_init(bar_qc(a), 4);
             mbar_init(bar_pv(a), 1);
             mbar_init(bar_drain(a), 1);
             mbar_init(bar_s(a), 1);
@@ -431,17 +443,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     ChunkPiece s;
     auto is_long = [&](const ChunkPiece &x) { return !kMono && x.ntok > p.R; };
 
-    if constexpr (Q8) {
-        // the registers of 640 threads (96 at launch; 512 and 128 for d = 256) by warpgroup:
-        // 96 + 2 * 128 + 2 * 64 = 5 * 96, and 96 + 160 + 2 * 64 < 4 * 128
-        if (warp < Cfg::kSoftWarp0)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        else if (warp < Cfg::kConvWarp0)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMono ? 160 : 128));
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    }
-
     if (warp == 0 || (Cfg::kTwoLoad && warp == 3)) {
         // ============================================================ K / V producers
         // One warp loads K and one V (issuing the copies of 16-token pages is what bounds a single one);
@@ -485,13 +486,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const bool once = s.nb == 1;      // no other block of the request reads these keys
             int32_t id = checked(page_of(s.t0)), id1 = page_of(s.t0 + 1);
             uint32_t e[2] = {0, 0}, e1[2] = {0, 0};
-            for (int kv = kv0; kv < kv1; ++kv)
+            for (int kv = kv0; kv < 2; ++kv)                 // (the K loader tells the softmax of V's too)
                 e[kv] = exps_of(kv, s.t0, id);
             for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++done) {
                 id1 = checked(id1);
                 const int32_t id2 = page_of(t + 2);
-                for (int kv = kv0; kv < kv1; ++kv)
+                for (int kv = kv0; kv < 2; ++kv)
                     e1[kv] = exps_of(kv, t + 1, id1);
+                // the largest exponent of the tile's visible rows, at least 2^-60 (NaN rows apart)
+                uint32_t top[2] = {67, 67};
+                const int32_t left = s.len - t * kCkKeys - lane * 4;   // of this lane's rows, the visible
+                if constexpr (Q8) {
+                    for (int kv = kv0; kv < 2; ++kv) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t b = (e[kv] >> (8 * x)) & 0xffu;
+                            top[kv] = max(top[kv], x < left && b != 255u ? b : 0u);
+                        }
+                        top[kv] = __reduce_max_sync(0xffffffffu, top[kv]);
+                    }
+                    if (kv0 == 0 && lane == 0)
+                        m->scales[done & 15] = make_float2(__uint_as_float(top[0] << 23), (float)((int32_t)top[1] - 127));
+                }
                 const int32_t page = id < 0 ? max(p.c.num_pages, 1) : id;
                 for (int kv = kv0; kv < kv1 && ok; ++kv) {
                     const CUtensorMap *tm = kv ? &p.tm_v : &p.tm_k;
@@ -510,16 +526,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                                 else
                                     tma_load_4d(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page);
                             }
-                            // low half: 2^(120 + b - 127) in bf16 (NaN for 255, 0 past the last visible
-                            // key); high half: the rest of exponents above 2^7, else 1
+                            // 2^(b - top) twice in fp16 (NaN for byte 255, 0 past the last visible key)
                             uint32_t mul[4];
-                            const int32_t left = s.len - t * kCkKeys - lane * 4;
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const uint32_t b = (e[kv] >> (8 * x)) & 0xffu;
-                                const uint32_t lo = b == 255u ? 0x7fc0u : (min(b, 134u) + 120u) << 7;
-                                const uint32_t hi = b == 255u ? 0x3f80u : (max(b, 134u) - 134u + 127u) << 7;
-                                mul[x] = x < left ? lo | (hi << 16) : 0x3f800000u;
+                                const int32_t down = (int32_t)top[kv] - (int32_t)b;
+                                const uint32_t f = b == 255u ? 0x7e00u
+                                                   : down <= 14 ? (uint32_t)(15 - down) << 10
+                                                   : down <= 24 ? 1u << (24 - down) : 0u;
+                                mul[x] = x < left ? f * 0x10001u : 0u;
                             }
                             st_shared_v4(dst + Cfg::kRaw + lane * 16, mul[0], mul[1], mul[2], mul[3]);
                             __syncwarp();
@@ -584,8 +600,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         // ring slot filled and both release it (a parity wait may not skip a phase).  The warps run
         // their loops together (they clear V rows together); lane 0 issues.
         const int me = warp - 1;
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-        const uint32_t idesc_o = idesc_bf16_f32(128, DH, false, true);
+        // bf16 operands, or fp16 ones (type bits 0) made from 8-bit pages
+        const uint32_t types = Q8 ? ~((1u << 7) | (1u << 10)) : ~0u;
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false) & types;
+        const uint32_t idesc_o = idesc_bf16_f32(128, DH, false, true) & types;
         uint32_t nq = 0, q_loads = 0;         // query tiles used and loaded
         uint32_t npiece = 0, nturn = 0;
         uint32_t nsp[2] = {0, 0}, no = 0;     // uses of S / P buffer a, and of this warp's O, so far
@@ -724,7 +742,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const int32_t nt = s.t1 - s.t0, mine = my_jobs(s);
             const bool lng = is_long(s);
             if (mine > 0 && (!kMono || me == 0)) {
-                if (!(ok = wait_all(bar_q(me), nq & 1u)))
+                // (8-bit pages: until the softmax warps have made it fp16)
+                if (!(ok = wait_all(Q8 ? bar_qc(me) : bar_q(me), nq & 1u)))
                     break;
                 ++nq;
             }
@@ -790,7 +809,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         const int r = (warp & 3) * 32 + lane;             // row of the tile = TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t to0 = tmem + lane_off + 256;
-        const float cl2 = p.scale_log2;
+        uint32_t ntile = 0, nq = 0;                       // KV tiles and query tiles of earlier pieces
         uint32_t ns_[2] = {0, 0}, no_[2] = {0, 0}, nml = 0;
         bool ok = true, owe = false;
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
@@ -807,6 +826,49 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const uint32_t to = to0 + (kMono ? 0 : a * D);
             float m_ref = -INFINITY, l = 0.0f;
             int32_t done = 0;                                        // tiles of this warpgroup so far
+            float cl2 = p.scale_log2;
+            float e_first = 0.0f;                                    // 8-bit pages: E of V in its first tile
+            if (Q8 && (lng || kMono || a < nt)) {
+                // This row of the query in fp16, times the power of two that takes its largest magnitude
+                // to 2^14 or more: 8 bits of mantissa fit, and what falls under fp16's range is less than
+                // 2^-38 of the largest.
+                if (!(ok = wait_all(bar_q(a), nq & 1u)))
+                    break;
+                ++nq;
+                if (live) {
+                    const uint32_t line = sbase + a * (D / 64) * p.qsub + r * 128;
+                    uint32_t top = 0;
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {
+                        const int32_t up = 141 - (int32_t)(top >> 7);    // 2^14 over the largest (bf16 bits in top)
+                        const int32_t shift = top < 128u ? 0 : max(-100, min(up, 100));
+                        const float f = ck_pow2(shift);
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint32_t at = line + (x >> 3) * p.qsub + (((x & 7) ^ (r & 7)) << 4);
+                            const int4 w = ld_shared_i4(at);
+                            const uint32_t v[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+                            if (pass == 0) {
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    top = max(top, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
+                            } else {
+                                uint32_t u[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    u[y] = ck_pack_f16x2(bf16_lo(v[y]) * f, bf16_hi(v[y]) * f);
+                                st_shared_v4(at, u[0], u[1], u[2], u[3]);
+                            }
+                        }
+                        if (pass == 1)
+                            cl2 *= ck_pow2(-shift);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_qc(a));
+            }
             for (int32_t t = (lng || kMono) ? 0 : a; t < nt; t += (lng || kMono) ? 1 : 2, ++done) {
                 const int buf = kMono ? (t & 1) : a;
                 const uint32_t ts = tmem + lane_off + buf * 128;
@@ -827,7 +889,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     const int32_t k0 = (s.t0 + t) * kCkKeys;
                     const bool masked = k0 + kCkKeys - 1 > all;
                     const int32_t kmax = last - k0;
-                    const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * cl2;
+                    // 8-bit pages: K and V of the tile are in units of 2^E; the probabilities take over V's
+                    // (P 2^E V, against a reference of s c + E, so the accumulator needs no other), and
+                    // the sum gives it back, relative to the first tile's
+                    float ct = cl2, ev = 0.0f;
+                    if constexpr (Q8) {
+                        const float2 sc = m->scales[(ntile + t) & 15];
+                        ct *= sc.x;
+                        ev = sc.y;
+                        if (done == 0)
+                            e_first = ev;
+                    }
+                    const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * ct + ev;
                     // the reference moves when a score lies more than 2^8 above it (or there is none yet)
                     if (__any_sync(0xffffffffu, live && (tmax > m_ref + kCkSlack || (m_ref == -INFINITY && tmax != m_ref)))) {
                         const float m_new = fmaxf(m_ref, tmax);
@@ -851,8 +924,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                         }
                         m_ref = m_new;
                     }
-                    const float mm = m_ref == -INFINITY ? 0.0f : m_ref;
-                    l += masked ? ck_row_exp<true>(ts, kmax, cl2, mm) : ck_row_exp<false>(ts, kmax, cl2, mm);
+                    const float mm = (m_ref == -INFINITY ? 0.0f : m_ref) - ev;
+                    const float sum = masked ? ck_row_exp<true, Q8>(ts, kmax, ct, mm) : ck_row_exp<false, Q8>(ts, kmax, ct, mm);
+                    l += Q8 ? sum * ck_pow2((int32_t)(e_first - ev)) : sum;
                     tmem_wait_st();
                 }
                 if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
@@ -865,11 +939,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             if (!ok)
                 break;
             const bool both = !kMono && !lng && nt > 1;   // two accumulators of one query tile
+            float o_scale = 1.0f;                         // O and m in units of 1 from here on
+            if constexpr (Q8) {
+                o_scale = ck_pow2((int32_t)e_first);
+                m_ref -= e_first;
+                ntile += (uint32_t)nt;
+            }
             if (both && a == 1) {
                 // (m, l) to the first warpgroup, which joins the two halves
                 if (nml > 0 && !(ok = wait_all(bar_mlfree, (nml - 1) & 1u)))
                     break;
                 m->ml[r] = make_float2(m_ref, l);
+                if (Q8 && r == 0)
+                    m->o_scale = o_scale;          // (of all its live rows; row 0 is one)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_ml);
@@ -884,6 +966,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     if (!(ok = wait_all(bar_ml, nml & 1u)))
                         break;
                     const float2 o = m->ml[r];
+                    const float o1_scale = Q8 ? m->o_scale : 1.0f;
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar_mlfree);
@@ -894,8 +977,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                         f1 = fast_exp2(o.x - mx);
                         l = l * f0 + o.y * f1;
                         m_ref = mx;
+                        f1 *= o1_scale;
                     }
                 }
+                f0 *= o_scale;
                 const bool whole = s.t0 == 0 && s.t1 == s.nt;
                 const int32_t row = s.off + s.tb0 + tok, head = s.g * p.G + r % p.G;
                 const int32_t slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
@@ -916,6 +1001,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                                                         (f1 != 0.0f ? __uint_as_float(ow[e]) * f1 : 0.0f));
                         } else {
                             tmem_wait_ld();
+                            if (Q8) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0);
+                            }
                         }
                         if (!live)
                             continue;
@@ -997,22 +1087,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
 #pragma unroll 2
                     for (int it = 0; it < 128 / RPI; ++it) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
-                        const uint2 w2 = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
-                        const uint32_t mw = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
-                        const uint32_t mul = __byte_perm(mw, 0, 0x1010);
-                        uint32_t x[8] = {ck_codes<0x9180>(w.x), ck_codes<0xb3a2>(w.x), ck_codes<0x9180>(w.y),
-                                         ck_codes<0xb3a2>(w.y), ck_codes<0x9180>(w2.x), ck_codes<0xb3a2>(w2.x),
-                                         ck_codes<0x9180>(w2.y), ck_codes<0xb3a2>(w2.y)};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x[e] = ck_mul2(x[e], mul);
-                        if ((mw >> 16) != 0x3f80u) {      // an exponent above 2^7: the rest of it
-                            const uint32_t more = __byte_perm(mw, 0, 0x3232);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                x[e] = ck_mul2(x[e], more);
-                        }
+                        uint2 w = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
+                        uint2 w2 = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
+                        const uint32_t mul = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
+                        if (mul == 0u)                    // (the codes may be NaN, which 0 would not hide)
+                            w = w2 = make_uint2(0u, 0u);
+                        uint32_t x[8];
+                        ck_codes(w.x, mul, x[0], x[1]);
+                        ck_codes(w.y, mul, x[2], x[3]);
+                        ck_codes(w2.x, mul, x[4], x[5]);
+                        ck_codes(w2.y, mul, x[6], x[7]);
                         st_shared_v4(dst + out + it * (RPI * 128), x[0], x[1], x[2], x[3]);
                         st_shared_v4(dst + out2 + it * (RPI * 128), x[4], x[5], x[6], x[7]);
                     }

@@ -22,16 +22,21 @@ __device__ __forceinline__ float exp_byte_scale(uint32_t b)
     return __uint_as_float(b == 255u ? 0x7fc00000u : b << 23);
 }
 
-// Four e4m3 codes (bytes 0..3 of w) as fp32: the byte's sign, exponent and mantissa fields are
-// put at those of a bf16 number, which is the code's value times 2^-120 (e4m3 subnormals become
-// bf16 subnormals), and the product with 2^120 is exact.
+// Four e4m3 codes (bytes 0..3 of w) as fp32 (through fp16, which holds every code).
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&f)[4])
 {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t b = (w >> (8 * e)) & 0xffu;
-        f[e] = __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7fu) << 20)) * 0x1p120f;
-    }
+    asm("{\n\t.reg .b16 a, b, c, d;\n\t.reg .b32 x;\n\t"
+        "mov.b32 {a, b}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, a;\n\t"
+        "mov.b32 {c, d}, x;\n\t"
+        "cvt.f32.f16 %0, c;\n\t"
+        "cvt.f32.f16 %1, d;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, b;\n\t"
+        "mov.b32 {c, d}, x;\n\t"
+        "cvt.f32.f16 %2, c;\n\t"
+        "cvt.f32.f16 %3, d;\n\t}"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+        : "r"(w));
 }
 
 // Byte of the smallest power of two that takes magnitude bits `amax` (fp32, finite) to 448 =

@@ -17,10 +17,12 @@ BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 # ------------------------------------------------------------------ plain 64-bit forms
 def e4m3_values(codes):
-    """Values of e4m3 codes (uint8) in 64 bits, from the format: bias 7, 3 mantissa bits."""
+    """Values of e4m3 codes (uint8) in 64 bits, from the format: bias 7, 3 mantissa bits, the
+    last code of each sign NaN."""
     c = codes.astype(np.int64)
     e, m = (c >> 3) & 15, c & 7
     v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v = np.where(c & 127 == 127, np.nan, v)
     return np.where(c & 128, -v, v)
 
 
@@ -243,7 +245,7 @@ def test_read_every_code_and_byte():
     want = vals[None] * 2.0 ** (np.array(bytes_[:-1], np.float64) - 127)[:, None]
     with np.errstate(over="ignore"):
         want = want.astype(np.float32)
-    assert np.array_equal(k[:-1].astype(np.float32), want)
+    assert np.array_equal(k[:-1].astype(np.float32), want, equal_nan=True)
 
 
 # ------------------------------------------------------------------ attention
