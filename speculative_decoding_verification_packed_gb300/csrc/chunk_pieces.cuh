@@ -1,0 +1,218 @@
+// chunk_pieces.cuh -- how the work of svp_chunk_attn is cut: shared by its tcgen05 kernel, its short
+// kernel for 8-bit pages and the kernel that joins split pairs.
+#pragma once
+
+#include "svp_cache.cuh"
+
+namespace svp {
+
+constexpr int kCkKeys = 128;          // keys a KV tile
+constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
+constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
+constexpr int kShareKeys = 512;       // smallest share of a CTA, in keys
+constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
+
+constexpr int kShortRows = 16;        // query rows of a KV head up to which 8-bit pages take chunk_short.cu
+
+struct ChunkDesc {                    // a pair that was split: read by the joining kernel
+    int32_t np, row0, ntok, g;        // pieces (0: none), first packed row, tokens, KV head
+};
+
+struct ChunkParams {
+    CUtensorMap tm_q, tm_k, tm_v;
+    CacheParams c;
+    const int32_t *ctx_len, *cu;
+    const void *q;                    // [m_cap, hq, d] bf16, rows q_stride apart
+    int64_t q_stride;
+    int32_t n, m_cap, w, hq, G, R;    // R: tokens of a query tile
+    float scale_log2;
+    void *out;
+    float *lse;
+    int32_t *status;
+    ChunkDesc *desc;                  // [grid]
+    float2 *part_ml;                  // [2 * grid][rows]
+    float *part_o;                    // [2 * grid][rows][d]; rows = 256 (d <= 128) or 128
+    int32_t nslot, nraw;              // bf16 tile slots, raw slots (8-bit pages)
+    int32_t off_ring, off_raw, off_misc;
+    int32_t Rb, qsub;                 // tokens of a query box: min(R, w); bytes of its [rows][64] blocks
+};
+
+// ------------------------------------------------------------------ the sequence of pairs
+struct ChunkPiece {
+    int32_t i, g, b, nb;              // request, KV head, token block, blocks of the request
+    int32_t off, k, L;                // the request's first packed row, rows, cached tokens
+    int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
+    int32_t nt, t0, t1;               // its KV tiles, and those of this piece
+    int64_t base;                     // cost before the pair
+};
+
+__device__ __forceinline__ int64_t ck_before(int64_t a, int64_t B, int64_t b)   // cost of blocks 0..b-1
+{
+    return b * a + B * (b * (b + 1) / 2);
+}
+
+// Cost of one KV head of a request: block b costs kStartKeys + L + (keys of its own tokens).
+__device__ __forceinline__ int64_t ck_head_cost(int32_t L, int32_t k, int32_t B)
+{
+    const int64_t nb = (k + B - 1) / B, a = (int64_t)kStartKeys + L;
+    return nb == 0 ? 0 : ck_before(a, B, nb - 1) + a + k;
+}
+
+__device__ __forceinline__ int32_t ck_tile_at(int64_t x)   // first tile at or after cost x of a pair
+{
+    return x <= kStartKeys ? 0 : (int32_t)((x - kStartKeys + kCkKeys - 1) / kCkKeys);
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int64_t v1, int32_t t0)
+{
+    const int32_t B = NT * p.R;
+    s.tb0 = s.b * B;
+    s.ntok = min(B, s.k - s.tb0);
+    s.len = s.L + s.tb0 + s.ntok;
+    s.nt = (s.len + kCkKeys - 1) / kCkKeys;
+    s.t0 = t0;
+    const int64_t y = v1 - s.base;
+    s.t1 = y >= (int64_t)kStartKeys + s.len ? s.nt : min(s.nt, ck_tile_at(y));
+    return s.t0 < s.t1;
+}
+
+__device__ __forceinline__ void ck_request(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int32_t B)
+{
+    s.off = __ldg(p.cu + s.i);
+    s.k = __ldg(p.cu + s.i + 1) - s.off;
+    s.L = __ldg(p.ctx_len + s.i);
+    s.nb = (s.k + B - 1) / B;
+}
+
+// The next pair before cost v1, from its first tile.
+template <int NT>
+__device__ __forceinline__ bool ck_next(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int64_t v1)
+{
+    s.base += (int64_t)kStartKeys + s.len;
+    if (s.base >= v1)
+        return false;
+    if (++s.b == s.nb) {
+        s.b = 0;
+        if (++s.g == p.c.hkv) {
+            s.g = 0;
+            do
+                ++s.i;
+            while (prefix[s.i + 1] == prefix[s.i]);   // (base < v1 <= the total: there is one)
+            ck_request(p, prefix, s, NT * p.R);
+        }
+    }
+    return ck_set<NT>(p, s, v1, 0);
+}
+
+// The first piece of the share [v0, v1).
+template <int NT>
+__device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int64_t v0,
+                                         int64_t v1)
+{
+    if (v0 >= v1)
+        return false;
+    const int32_t B = NT * p.R;
+    int32_t lo = 0, hi = p.n;
+    while (hi - lo > 1) {             // last request with prefix <= v0 (it has a cost: v0 < total)
+        const int32_t mid = (lo + hi) >> 1;
+        if (prefix[mid] <= v0)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    s.i = lo;
+    ck_request(p, prefix, s, B);
+    const int64_t H = ck_head_cost(s.L, s.k, B);
+    int64_t rem = v0 - prefix[lo];
+    s.g = (int32_t)(rem / H);
+    rem -= s.g * H;
+    // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem, put right
+    const int64_t a = (int64_t)kStartKeys + s.L;
+    const float h = (float)a + 0.5f * B;
+    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * (float)rem) - h) / B);
+    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
+    while (b + 1 < s.nb && ck_before(a, B, b + 1) <= rem)
+        ++b;
+    while (b > 0 && ck_before(a, B, b) > rem)
+        --b;
+    s.b = (int32_t)b;
+    s.base = prefix[lo] + s.g * H + ck_before(a, B, b);
+    const int32_t t0 = ck_tile_at(v0 - s.base);
+    const bool have = ck_set<NT>(p, s, v1, t0);
+    // a share that begins behind the pair's last tile begins with the next pair
+    return have || (t0 >= s.nt && ck_next<NT>(p, prefix, s, v1));
+}
+
+__device__ __forceinline__ int64_t ck_bound(int64_t total, int32_t c, int32_t ncta)
+{
+    return total * c / ncta;
+}
+
+// The CTA that owns the tile that starts at cost u: the last c with ck_bound(c) <= u.
+__device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t u)
+{
+    int32_t c = (int32_t)min((int64_t)ncta - 1, ((u + 1) * ncta + total - 1) / total - 1);
+    return c < 0 ? 0 : c;
+}
+
+// Cost before each request into prefix[0..n] (shared memory; every thread of the block, tot: one entry
+// a warp).  A request that breaks the contract costs nothing, and sets a status bit.  Ends in a barrier.
+__device__ __forceinline__ void ck_prologue(const ChunkParams &p, int32_t B, int64_t *prefix, int64_t *tot)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+    if (tid == 0)
+        prefix[0] = 0;
+    int64_t running = 0;
+    for (int32_t base = 0; base < p.n; base += (int32_t)blockDim.x) {
+        const int32_t i = base + tid;
+        int64_t cost = 0;
+        if (i < p.n) {
+            const int32_t off = __ldg(p.cu + i), end = __ldg(p.cu + i + 1), L = __ldg(p.ctx_len + i);
+            int32_t bad = 0;
+            if (off < 0 || end < off || end - off > p.w || end > p.m_cap)
+                bad = SVP_DEV_BAD_SLOTS;
+            else if (end > off && (L < 0 || (int64_t)L + (end - off) > ((int64_t)p.c.max_pages << p.c.page_shift)))
+                bad = SVP_DEV_BAD_CONTEXT;
+            if (bad && blockIdx.x == 0)
+                set_status(p.status, bad);
+            if (!bad)
+                cost = ck_head_cost(L, end - off, B) * p.c.hkv;
+        }
+        int64_t incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            tot[warp] = incl;
+        __syncthreads();
+        int64_t before = running;
+        for (int w2 = 0; w2 < nwarp; ++w2) {
+            const int64_t x = tot[w2];
+            if (w2 < warp)
+                before += x;
+            running += x;
+        }
+        if (i < p.n)
+            prefix[i + 1] = before + incl;
+        __syncthreads();
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float ck_pow2(int32_t e)      // 2^e, e clamped to the normal range
+{
+    return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23);
+}
+
+__device__ __forceinline__ uint32_t ck_pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace svp

@@ -29,36 +29,9 @@
 #include <cmath>
 #include <cstring>
 
-#include "svp_cache.cuh"
+#include "chunk_pieces.cuh"
 
 namespace svp {
-
-constexpr int kCkKeys = 128;          // keys a KV tile
-constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
-constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
-constexpr int kShareKeys = 512;       // smallest share of a CTA, in keys
-constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
-
-struct ChunkDesc {                    // a pair that was split: read by the joining kernel
-    int32_t np, row0, ntok, g;        // pieces (0: none), first packed row, tokens, KV head
-};
-
-struct ChunkParams {
-    CUtensorMap tm_q, tm_k, tm_v;
-    CacheParams c;
-    const int32_t *ctx_len, *cu;
-    int32_t n, m_cap, w, hq, G, R;
-    float scale_log2;
-    void *out;
-    float *lse;
-    int32_t *status;
-    ChunkDesc *desc;                  // [grid]
-    float2 *part_ml;                  // [2 * grid][rows]
-    float *part_o;                    // [2 * grid][rows][d]; rows = 256 (d <= 128) or 128
-    int32_t nslot, nraw;              // bf16 tile slots, raw slots (8-bit pages)
-    int32_t off_ring, off_raw, off_misc;
-    int32_t Rb, qsub;                 // tokens of a query box: min(R, w); bytes of its [rows][64] blocks
-};
 
 template <int D, bool Q8>
 struct ChunkCfg {
@@ -88,125 +61,6 @@ struct ChunkMisc {
     int64_t prefix[1];                // [n + 1]: cost before request i
 };
 
-// ------------------------------------------------------------------ the sequence of pairs
-struct ChunkPiece {
-    int32_t i, g, b, nb;              // request, KV head, token block, blocks of the request
-    int32_t off, k, L;                // the request's first packed row, rows, cached tokens
-    int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
-    int32_t nt, t0, t1;               // its KV tiles, and those of this piece
-    int64_t base;                     // cost before the pair
-};
-
-__device__ __forceinline__ int64_t ck_before(int64_t a, int64_t B, int64_t b)   // cost of blocks 0..b-1
-{
-    return b * a + B * (b * (b + 1) / 2);
-}
-
-// Cost of one KV head of a request: block b costs kStartKeys + L + (keys of its own tokens).
-__device__ __forceinline__ int64_t ck_head_cost(int32_t L, int32_t k, int32_t B)
-{
-    const int64_t nb = (k + B - 1) / B, a = (int64_t)kStartKeys + L;
-    return nb == 0 ? 0 : ck_before(a, B, nb - 1) + a + k;
-}
-
-__device__ __forceinline__ int32_t ck_tile_at(int64_t x)   // first tile at or after cost x of a pair
-{
-    return x <= kStartKeys ? 0 : (int32_t)((x - kStartKeys + kCkKeys - 1) / kCkKeys);
-}
-
-template <int NT>
-__device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int64_t v1, int32_t t0)
-{
-    const int32_t B = NT * p.R;
-    s.tb0 = s.b * B;
-    s.ntok = min(B, s.k - s.tb0);
-    s.len = s.L + s.tb0 + s.ntok;
-    s.nt = (s.len + kCkKeys - 1) / kCkKeys;
-    s.t0 = t0;
-    const int64_t y = v1 - s.base;
-    s.t1 = y >= (int64_t)kStartKeys + s.len ? s.nt : min(s.nt, ck_tile_at(y));
-    return s.t0 < s.t1;
-}
-
-__device__ __forceinline__ void ck_request(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int32_t B)
-{
-    s.off = __ldg(p.cu + s.i);
-    s.k = __ldg(p.cu + s.i + 1) - s.off;
-    s.L = __ldg(p.ctx_len + s.i);
-    s.nb = (s.k + B - 1) / B;
-}
-
-// The next pair before cost v1, from its first tile.
-template <int NT>
-__device__ __forceinline__ bool ck_next(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int64_t v1)
-{
-    s.base += (int64_t)kStartKeys + s.len;
-    if (s.base >= v1)
-        return false;
-    if (++s.b == s.nb) {
-        s.b = 0;
-        if (++s.g == p.c.hkv) {
-            s.g = 0;
-            do
-                ++s.i;
-            while (m->prefix[s.i + 1] == m->prefix[s.i]);   // (base < v1 <= the total: there is one)
-            ck_request(p, m, s, NT * p.R);
-        }
-    }
-    return ck_set<NT>(p, s, v1, 0);
-}
-
-// The first piece of the share [v0, v1).
-template <int NT>
-__device__ __forceinline__ bool ck_first(const ChunkParams &p, const ChunkMisc *m, ChunkPiece &s, int64_t v0,
-                                         int64_t v1)
-{
-    if (v0 >= v1)
-        return false;
-    const int32_t B = NT * p.R;
-    int32_t lo = 0, hi = p.n;
-    while (hi - lo > 1) {             // last request with prefix <= v0 (it has a cost: v0 < total)
-        const int32_t mid = (lo + hi) >> 1;
-        if (m->prefix[mid] <= v0)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    s.i = lo;
-    ck_request(p, m, s, B);
-    const int64_t H = ck_head_cost(s.L, s.k, B);
-    int64_t rem = v0 - m->prefix[lo];
-    s.g = (int32_t)(rem / H);
-    rem -= s.g * H;
-    // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem, put right
-    const int64_t a = (int64_t)kStartKeys + s.L;
-    const float h = (float)a + 0.5f * B;
-    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * (float)rem) - h) / B);
-    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
-    while (b + 1 < s.nb && ck_before(a, B, b + 1) <= rem)
-        ++b;
-    while (b > 0 && ck_before(a, B, b) > rem)
-        --b;
-    s.b = (int32_t)b;
-    s.base = m->prefix[lo] + s.g * H + ck_before(a, B, b);
-    const int32_t t0 = ck_tile_at(v0 - s.base);
-    const bool have = ck_set<NT>(p, s, v1, t0);
-    // a share that begins behind the pair's last tile begins with the next pair
-    return have || (t0 >= s.nt && ck_next<NT>(p, m, s, v1));
-}
-
-__device__ __forceinline__ int64_t ck_bound(int64_t total, int32_t c, int32_t ncta)
-{
-    return total * c / ncta;
-}
-
-// The CTA that owns the tile that starts at cost u: the last c with ck_bound(c) <= u.
-__device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t u)
-{
-    int32_t c = (int32_t)min((int64_t)ncta - 1, ((u + 1) * ncta + total - 1) / total - 1);
-    return c < 0 ? 0 : c;
-}
-
 // ------------------------------------------------------------------ small device helpers
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -231,18 +85,6 @@ __device__ __forceinline__ void ck_codes(uint32_t w, uint32_t mul, uint32_t &lo,
         "mul.rn.f16x2 %1, y, %3;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w), "r"(mul));
-}
-
-__device__ __forceinline__ uint32_t ck_pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float ck_pow2(int32_t e)      // 2^e, e clamped to the normal range
-{
-    return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23);
 }
 
 // The softmax of one S tile in this thread's row, 64 columns a turn: its instructions are kept few, as
@@ -380,7 +222,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         mbar_init(bar_sdone, 1);
         mbar_fence_init();
         m->abort_flag = 0;
-        m->prefix[0] = 0;
         tma_prefetch_desc(&p.tm_q);
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
@@ -393,44 +234,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     griddep_wait();
     if (tid == 0)
         p.desc[blockIdx.x].np = 0;
-    // cost before each request; a request that breaks the contract costs nothing (status bit)
-    int64_t running = 0;
-    for (int32_t base = 0; base < p.n; base += Cfg::kThreads) {
-        const int32_t i = base + tid;
-        int64_t cost = 0;
-        if (i < p.n) {
-            const int32_t off = __ldg(p.cu + i), end = __ldg(p.cu + i + 1), L = __ldg(p.ctx_len + i);
-            int32_t bad = 0;
-            if (off < 0 || end < off || end - off > p.w || end > p.m_cap)
-                bad = SVP_DEV_BAD_SLOTS;
-            else if (end > off && (L < 0 || (int64_t)L + (end - off) > ((int64_t)p.c.max_pages << p.c.page_shift)))
-                bad = SVP_DEV_BAD_CONTEXT;
-            if (bad && blockIdx.x == 0)
-                set_status(p.status, bad);
-            if (!bad)
-                cost = ck_head_cost(L, end - off, NT * p.R) * p.c.hkv;
-        }
-        int64_t incl = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += v;
-        }
-        if (lane == 31)
-            m->warp_tot[warp] = incl;
-        __syncthreads();
-        int64_t before = running;
-        for (int w2 = 0; w2 < Cfg::kThreads / 32; ++w2) {
-            const int64_t t = m->warp_tot[w2];
-            if (w2 < warp)
-                before += t;
-            running += t;
-        }
-        if (i < p.n)
-            m->prefix[i + 1] = before + incl;
-        __syncthreads();
-    }
+    ck_prologue(p, NT * p.R, m->prefix, m->warp_tot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -461,7 +265,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         const uint64_t pol_once = l2_policy_evict_first();
         const int32_t in_page = (1 << p.c.page_shift) - 1;
         const bool loads = ((lane * 4) & in_page) == 0;
-        for (bool have = ck_first<NT>(p, m, s, v0, v1); have && ok; have = ck_next<NT>(p, m, s, v1)) {
+        for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have && ok; have = ck_next<NT>(p, m->prefix, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
             constexpr int32_t kNone = INT32_MIN;             // nothing of the tile needs a page here
             auto page_of = [&](int32_t t) -> int32_t {
@@ -710,7 +514,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             ++nsp[buf];
             if (!kMono && last) {
                 // this warp's last P of the piece: all its S are done and its query tile may be replaced
-                have_next = ck_next<NT>(p, m, s, v1);
+                have_next = ck_next<NT>(p, m->prefix, s, v1);
                 if (have_next)
                     load_q(s);
             }
@@ -735,7 +539,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             __syncwarp();
             return true;
         };
-        bool have = ck_first<NT>(p, m, s, v0, v1);
+        bool have = ck_first<NT>(p, m->prefix, s, v0, v1);
         if (have)
             load_q(s);
         while (have && ok) {
@@ -786,7 +590,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             if (mine > 0)
                 ++no;
             if (kMono || mine == 0) {
-                have_next = ck_next<NT>(p, m, s, v1);
+                have_next = ck_next<NT>(p, m->prefix, s, v1);
                 if (kMono && me == 0 && !(ok = wait_all(bar_sdone, npiece & 1u)))
                     break;
                 if (have_next)
@@ -815,7 +619,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         };
-        for (bool have = ck_first<NT>(p, m, s, v0, v1); have; have = ck_next<NT>(p, m, s, v1)) {
+        for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have; have = ck_next<NT>(p, m->prefix, s, v1)) {
             const bool lng = is_long(s);
             const int32_t nt = s.t1 - s.t0;
             const int32_t tok = (lng ? a * p.R : 0) + r / p.G;      // token of the block
@@ -1075,7 +879,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             uint32_t pos = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
             bool ok = true;
             uint32_t halves = 0;                          // of all pieces
-            for (bool have = ck_first<NT>(p, m, s, v0, v1); have; have = ck_next<NT>(p, m, s, v1))
+            for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have; have = ck_next<NT>(p, m->prefix, s, v1))
                 halves += (uint32_t)(s.t1 - s.t0) * 2 * NH;
             {
                 for (; pos < halves; ++pos) {
@@ -1229,6 +1033,17 @@ static ChunkWs chunk_ws(int32_t d)
 
 size_t chunk_tc_workspace(int32_t d) { return chunk_ws(d).bytes; }
 
+svp_status chunk_short_run(ChunkParams &p, int32_t d, cudaStream_t stream);
+
+template <int D>
+static svp_status chunk_join(const ChunkParams &p, int32_t part_rows, cudaStream_t stream)
+{
+    return launch_pdl(chunk_join_kernel<D>, dim3(sm_count(), kJoinY), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
+                   cudaSuccess
+               ? SVP_OK
+               : SVP_ECUDA;
+}
+
 template <int D, bool Q8>
 static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
 {
@@ -1268,10 +1083,7 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     const int grid = sm_count();
     if (launch_pdl(chunk_tc_kernel<D, Q8>, dim3(grid), dim3(Cfg::kThreads), (size_t)smem, stream, p) != cudaSuccess)
         return SVP_ECUDA;
-    return launch_pdl(chunk_join_kernel<D>, dim3(grid, kJoinY), dim3(kJoinWarps * 32), 0, stream, p,
-                      (int32_t)Cfg::kPartRows) == cudaSuccess
-               ? SVP_OK
-               : SVP_ECUDA;
+    return chunk_join<D>(p, Cfg::kPartRows, stream);
 }
 
 svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const CacheParams &c, const int32_t *ctx_len,
@@ -1283,12 +1095,16 @@ svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const 
     p.c = c;
     p.ctx_len = ctx_len;
     p.cu = cu;
+    p.q = q;
+    p.q_stride = q_stride;
     p.n = n;
     p.m_cap = m_cap;
     p.w = w;
     p.hq = hq;
     p.G = hq / c.hkv;
     p.R = 128 / p.G;
+    // 8-bit pages and few rows: see chunk_short.cu
+    const bool few = kv == SVP_E4M3 && d <= 128 && (int64_t)p.G * w <= kShortRows;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = out;
     p.lse = lse;
@@ -1313,10 +1129,18 @@ svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const 
         const uint64_t str[3] = {(uint64_t)c.s_tok * esz, (uint64_t)c.s_head * esz, (uint64_t)c.s_page * esz};
         const uint32_t box[4] = {q8 ? (uint32_t)std::min(d, 128) : 64u, 1u << c.page_shift, 1, 1};   // a page of one head
         const CUtensorMapDataType type = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-        const CUtensorMapSwizzle sw = q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+        const CUtensorMapSwizzle sw = !q8 || (few && d == 128) ? CU_TENSOR_MAP_SWIZZLE_128B
+                                      : few ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
         if (!encode_tiled(&p.tm_k, type, sw, c.k, 4, dims, str, box) ||
             !encode_tiled(&p.tm_v, type, sw, c.v, 4, dims, str, box))
             return SVP_EUNSUPPORTED;
+    }
+    if (few) {
+        p.R = w;                          // a request is one token block
+        const svp_status st = chunk_short_run(p, d, stream);
+        if (st != SVP_OK)
+            return st;
+        return d == 64 ? chunk_join<64>(p, kShortRows, stream) : chunk_join<128>(p, kShortRows, stream);
     }
     if (kv == SVP_E4M3) {
         switch (d) {
