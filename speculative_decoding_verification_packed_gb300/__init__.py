@@ -622,7 +622,7 @@ def make_cache(k_cache, v_cache, block_table, *, k_exp=None, v_exp=None) -> svp_
         c.k_exp, c.v_exp = _dev(k_exp, "k_exp", torch.uint8), _dev(v_exp, "v_exp", torch.uint8)
     elif k_exp is not None or v_exp is not None:
         raise ValueError("exponent bytes belong to float8_e4m3fn pools")
-    c.device = k_cache.device
+    c.device, c.index, c.ws = k_cache.device, k_cache.device.index, None
     c.keep = (k_cache, v_cache, k_exp, v_exp, block_table)
     for x in c.keep:
         if x is not None and x.device != c.device:
@@ -631,28 +631,50 @@ def make_cache(k_cache, v_cache, block_table, *, k_exp=None, v_exp=None) -> svp_
     return c
 
 
+# These three run once a decode step and layer, so their checks cost little: plain attribute reads, and
+# the current stream's raw handle.
 def _rows(t, name: str, heads: int, cache: svp_cache) -> int:
     """Row stride of rows [m, heads, d] whose heads and elements are contiguous."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.d:
-        raise ValueError(f"{name} must be [rows, {heads}, {cache.d}]")
-    if t.device != cache.device:
-        raise ValueError(f"{name} must be on the cache's device")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != cache.d):
-        raise ValueError(f"{name} needs contiguous rows (any row stride)")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * cache.d)
+    d = cache.d
+    m, h, e = t.shape
+    if h != heads or e != d:
+        raise ValueError(f"{name} must be [rows, {heads}, {d}]")
+    s0, s1, s2 = t.stride()
+    if t.device != cache.device or s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError(f"{name} needs contiguous rows (any row stride) on the cache's device")
+    return s0 if m > 1 else max(s0, heads * d)
 
 
-def _requests(cu, ctx, cache: svp_cache, name: str) -> int:
-    """Number of requests of cu [n+1]; checks it, the per-request array and the block table."""
+def _i32(t, name: str, count: int, device) -> int:
+    """Address of a contiguous int32 vector of at least ``count`` entries (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.shape[0] < count:
+        raise ValueError(f"{name} must be {count} or more contiguous int32 values on the cache's device")
+    return t.data_ptr()
+
+
+def _requests(cu, cache: svp_cache, name: str) -> int:
+    """Number of requests of cu [n+1]."""
     n = cu.shape[0] - 1
-    _dev(cu, name, torch.int32)
     if n < 0 or n > cache.max_n:
         raise ValueError(f"{name} must have 1..{cache.max_n + 1} entries (rows of the block table)")
-    if ctx is not None and ctx.shape[0] < n:
-        raise ValueError("one cached length is needed for each request")
-    if cache.device.index != torch.cuda.current_device():
+    if cache.index != torch._C._cuda_getDevice():
         raise ValueError("the cache must be on the current CUDA device")
     return n
+
+
+def _raw_stream(stream, cache: svp_cache) -> int:
+    return torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else _stream(stream)
+
+
+def _cache_workspace(cache: svp_cache, stream) -> Workspace:
+    """Status word of cache_write / cache_read calls that bring no workspace: nothing else is
+    kept there, so every stream and graph may share it."""
+    ws = cache.ws
+    if ws is None:
+        ws = cache.ws = _workspace(("cache",), 256, cache.device, stream)
+    return ws
 
 
 def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
@@ -660,18 +682,19 @@ def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
     """Store packed rows k, v [m_cap, hkv, d] (bf16 or fp32; slices of a fused projection are
     fine) at positions ctx_len[i] + j of their requests (svp_cache_write).  take [n] int32:
     only the first take[i] rows of request i, e.g. the accept_len of margin_accept."""
-    n = _requests(cu_slots, ctx_len, cache, "cu_slots")
+    n = _requests(cu_slots, cache, "cu_slots")
+    dev = cache.device
     stride = _rows(k, "k", cache.hkv, cache)
-    if k.shape != v.shape or k.dtype != v.dtype or _rows(v, "v", cache.hkv, cache) != stride:
+    if k.dtype != v.dtype or k.shape != v.shape or _rows(v, "v", cache.hkv, cache) != stride:
         raise ValueError("k and v need one shape, type and row stride")
-    if take is not None and take.shape[0] < n:
-        raise ValueError("take needs one count for each request")
     if ws is None:
-        ws = _workspace(("cache",), 256, cache.device, stream)
-    _check(lib().svp_cache_write(
-        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref,
-        _dev(ctx_len, "ctx_len", torch.int32), cu_slots.data_ptr(), _dev(take, "take", torch.int32),
-        n, k.shape[0], cache.hkv, cache.d, ws.ptr, ws.nbytes, _stream(stream)), "svp_cache_write")
+        ws = _cache_workspace(cache, stream)
+    st = lib().svp_cache_write(
+        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref, _i32(ctx_len, "ctx_len", n, dev),
+        _i32(cu_slots, "cu_slots", n + 1, dev), _i32(take, "take", n, dev), n, k.shape[0], cache.hkv,
+        cache.d, ws.ptr, ws.nbytes, _raw_stream(stream, cache))
+    if st:
+        raise SvpError(st, "svp_cache_write")
 
 
 def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
@@ -680,23 +703,26 @@ def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
     """Positions start[i].. (0.. for None) of each request as contiguous rows
     cu_rows[i]..cu_rows[i+1]-1 of (k_out, v_out) [rows, hkv, d] (svp_cache_read).  Outputs that
     are not given are made with ``rows`` rows of ``dtype``, zeros where nothing is read."""
-    n = _requests(cu_rows, start, cache, "cu_rows")
+    n = _requests(cu_rows, cache, "cu_rows")
+    dev = cache.device
     if k_out is None or v_out is None:
         if rows is None or k_out is not None or v_out is not None:
             raise ValueError("give both k_out and v_out, or rows")
-        k_out = torch.zeros(rows, cache.hkv, cache.d, dtype=dtype, device=cache.device)
+        k_out = torch.zeros(rows, cache.hkv, cache.d, dtype=dtype, device=dev)
         v_out = torch.zeros_like(k_out)
-    for name, x in (("k_out", k_out), ("v_out", v_out)):
-        _rows(x, name, cache.hkv, cache)
-        _dev(x, name, k_out.dtype)
-    if k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out need one shape")
+    _rows(k_out, "k_out", cache.hkv, cache)
+    _rows(v_out, "v_out", cache.hkv, cache)
+    if (k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or not k_out.is_contiguous()
+            or not v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be contiguous, of one shape and type")
     if ws is None:
-        ws = _workspace(("cache",), 256, cache.device, stream)
-    _check(lib().svp_cache_read(
-        cache.ref, _dev(start, "start", torch.int32), cu_rows.data_ptr(), n, k_out.shape[0],
-        cache.hkv, cache.d, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.ptr,
-        ws.nbytes, _stream(stream)), "svp_cache_read")
+        ws = _cache_workspace(cache, stream)
+    st = lib().svp_cache_read(
+        cache.ref, _i32(start, "start", n, dev), _i32(cu_rows, "cu_rows", n + 1, dev), n, k_out.shape[0],
+        cache.hkv, cache.d, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.ptr, ws.nbytes,
+        _raw_stream(stream, cache))
+    if st:
+        raise SvpError(st, "svp_cache_read")
     return k_out, v_out
 
 
@@ -708,16 +734,19 @@ def chunk_attn_workspace_size(hq: int, hkv: int, d: int, dtype=torch.bfloat16) -
     return int(nb.value)
 
 
-def _chunk_workspace(hq: int, cache: svp_cache, dtype, stream) -> Workspace:
+_chunk_ws: dict = {}
+
+
+def _chunk_workspace(hq: int, cache: svp_cache, dtype, stream, raw: int) -> Workspace:
     """The scratch of chunk_attn calls that bring none: one for each stream, as calls on two
     streams may overlap; a call that is being captured gets its own, which lives in the graph's
     memory, as graphs may be replayed on any stream."""
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, stream)
-    key = (("chunk", cache.d, dtype, _stream(stream)), cache.device)
-    ws = _ws_cache.get(key)
+    key = (raw, cache.index, cache.d, dtype)
+    ws = _chunk_ws.get(key)
     if ws is None:
-        ws = _ws_cache[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
+        ws = _chunk_ws[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
                                         cache.device, stream)
     return ws
 
@@ -727,29 +756,33 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
                stream=None):
     """Attention of packed new rows q [m_cap, hq, d] over the cache; row j of request i sees
     positions 0..ctx_len[i]+j, its own (written by cache_write before) included.  w: largest
-    row count of a request (default m_cap).  Returns (out [m_cap, hq, d], lse [m_cap, hq] or
-    None); rows past cu_slots[n] are left as they were (zeros in outputs made here).  A call
-    captured on a stream that is not torch's current one needs its own ``ws``."""
-    n = _requests(cu_slots, ctx_len, cache, "cu_slots")
-    hq = q.shape[1]
-    if hq < 1 or hq % cache.hkv:
+    row count of a request (default m_cap; calls of few rows are planned by it).  Returns
+    (out [m_cap, hq, d], lse [m_cap, hq] or None); rows past cu_slots[n] are left as they were
+    (zeros in outputs made here).  A call captured on a stream that is not torch's current one
+    needs its own ``ws``."""
+    n = _requests(cu_slots, cache, "cu_slots")
+    dev = cache.device
+    hkv = cache.hkv
+    m_cap, hq, d = q.shape
+    if hq < 1 or hq % hkv:
         raise ValueError("the query heads must be a multiple of the cache's heads")
     stride = _rows(q, "q", hq, cache)
-    m_cap = q.shape[0]
     if out is None:
-        out = torch.zeros(m_cap, hq, cache.d, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is None and want_lse:
-        lse = torch.zeros(m_cap, hq, dtype=torch.float32, device=q.device)
-    elif lse is not None and tuple(lse.shape) != (m_cap, hq):
-        raise ValueError("lse must be [m_cap, hq]")
+        out = torch.zeros(m_cap, hq, d, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape, type and device")
+    if lse is None:
+        if want_lse:
+            lse = torch.zeros(m_cap, hq, dtype=torch.float32, device=dev)
+    elif lse.shape != (m_cap, hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [m_cap, hq] on q's device")
+    raw = _raw_stream(stream, cache)
     if ws is None:
-        ws = _chunk_workspace(hq, cache, q.dtype, stream)
-    h = _heads(hq, cache.hkv, cache.d, scale)
-    _check(lib().svp_chunk_attn(
-        q.data_ptr(), stride, cache.ref, _dev(ctx_len, "ctx_len", torch.int32), cu_slots.data_ptr(),
-        n, m_cap, max(m_cap, 1) if w is None else int(w), ctypes.byref(h), _dtype_code(q),
-        _dev(out, "out", q.dtype), _dev(lse, "lse", torch.float32), ws.ptr, ws.nbytes,
-        _stream(stream)), "svp_chunk_attn")
+        ws = _chunk_workspace(hq, cache, q.dtype, stream, raw)
+    st = lib().svp_chunk_attn(
+        q.data_ptr(), stride, cache.ref, _i32(ctx_len, "ctx_len", n, dev), _i32(cu_slots, "cu_slots", n + 1, dev),
+        n, m_cap, (m_cap or 1) if w is None else w, svp_heads(hq, hkv, d, scale), _dtype_code(q), out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, raw)
+    if st:
+        raise SvpError(st, "svp_chunk_attn")
     return out, lse

@@ -16,8 +16,8 @@
 
 namespace svp {
 
-constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 8;     // packed rows of a block, at most
+constexpr int kCacheThreads = 128;
+constexpr int kCacheRows = 4;     // packed rows of a block, at most (a read of 8-bit rows: 305 us; 16 rows 307)
 
 struct CacheMoveParams {
     CacheParams c;
@@ -90,193 +90,214 @@ __device__ __forceinline__ void cache_locate(const CacheMoveParams &p, int32_t r
     __syncthreads();
 }
 
-// Eight elements of a row as fp32, from bf16 / fp32 / e4m3 storage, and back.
-__device__ __forceinline__ void bf16x8_to_f32(const uint4 &w, float (&x)[8])
-{
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-    x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-}
-
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8])
-{
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-}
-
-// Raw storage of eight elements of a type.
-template <int T> struct Raw8;
-template <> struct Raw8<SVP_F32> { float4 a, b; };
-template <> struct Raw8<SVP_BF16> { uint4 a; };
-template <> struct Raw8<SVP_E4M3> { uint2 a; };
+// Sixteen elements of a row in storage, as words.
+template <int T> constexpr int kWords = T == SVP_F32 ? 16 : T == SVP_BF16 ? 8 : 4;
 
 template <int T>
-__device__ __forceinline__ Raw8<T> raw_load(const void *base, int64_t e)
+__device__ __forceinline__ void load16(const void *base, int64_t e, uint32_t (&w)[kWords<T>])
 {
-    Raw8<T> r;
-    if constexpr (T == SVP_F32) {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + e);
-        r.a = s[0];
-        r.b = s[1];
-    } else if constexpr (T == SVP_BF16) {
-        r.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + e);
-    } else {
-        r.a = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + e);
-    }
-    return r;
-}
-
-template <int T>
-__device__ __forceinline__ void raw_values(const Raw8<T> &r, float (&x)[8])
-{
-    if constexpr (T == SVP_F32) {
-        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-        x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-    } else if constexpr (T == SVP_BF16) {
-        bf16x8_to_f32(r.a, x);
-    } else {
-        float lo[4], hi[4];
-        e4m3x4_to_f32(r.a.x, lo);
-        e4m3x4_to_f32(r.a.y, hi);
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + e * (kWords<T> / 4));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = lo[e];
-            x[4 + e] = hi[e];
+    for (int i = 0; i < kWords<T> / 4; ++i) {
+        const uint4 v = s[i];
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store16(void *base, int64_t e, const uint32_t (&w)[kWords<T>])
+{
+    uint4 *s = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + e * (kWords<T> / 4));
+#pragma unroll
+    for (int i = 0; i < kWords<T> / 4; ++i)
+        s[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <int T>
+__device__ __forceinline__ void to_f32(const uint32_t (&w)[kWords<T>], float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i) {
+        if constexpr (T == SVP_F32) {
+            x[i] = __uint_as_float(w[i]);
+        } else if constexpr (T == SVP_BF16) {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        } else {
+            float f[4];
+            e4m3x4_to_f32(w[i], f);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                x[4 * i + y] = f[y];
         }
     }
 }
 
 template <int T>
-__device__ __forceinline__ void store_values(void *base, int64_t e, const float (&x)[8])
+__device__ __forceinline__ void from_f32(const float (&x)[16], uint32_t (&w)[kWords<T>])
 {
+    static_assert(T != SVP_E4M3, "8-bit rows are made with their exponent byte");
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i)
+        w[i] = T == SVP_F32 ? __float_as_uint(x[i]) : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+// Bits of the largest magnitude (as fp32) of sixteen elements.
+template <int T>
+__device__ __forceinline__ uint32_t amax16(const uint32_t (&w)[kWords<T>])
+{
+    uint32_t m = 0u;
     if constexpr (T == SVP_F32) {
-        float4 *s = reinterpret_cast<float4 *>(static_cast<float *>(base) + e);
-        s[0] = make_float4(x[0], x[1], x[2], x[3]);
-        s[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m = max(m, w[i] & 0x7fffffffu);
+        return m;
     } else {
-        static_assert(T == SVP_BF16, "8-bit rows are stored with their exponent byte");
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + e) = f32_to_bf16x8(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return max(m & 0xffff0000u, m << 16);
     }
 }
 
-// Items of a block: (packed row, head, K or V), one a group of gl = d / 8 lanes.
+// The items of a block, (packed row, K or V head), in the order in which its groups of gl = d / 16 lanes
+// take them; column c < hkv is K's head c, else V's c - hkv.
+struct CacheItem {
+    int32_t r, c;
+    __device__ __forceinline__ void skip(int32_t by, int32_t cols)
+    {
+        c += by;
+        while (c >= cols) {
+            c -= cols;
+            ++r;
+        }
+    }
+};
+
 template <int TIn, int TC>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid_constant__ CacheMoveParams p)
 {
-    constexpr int U = 2;   // items a group has in flight
     __shared__ CacheRowMap m;
     griddep_launch_dependents();
     griddep_wait();
     const int32_t r0 = (int32_t)blockIdx.x * p.rpb;
-    const int32_t nr = min(p.rpb, p.rows - r0);
-    const int gl = p.d >> 3;
+    const int32_t nr = min(p.rpb, p.rows - r0), hkv = p.c.hkv, cols = 2 * hkv;
+    const int gl = p.d >> 4;
     const int grp = threadIdx.x / gl, lane = threadIdx.x - grp * gl, ngrp = kCacheThreads / gl;
-    const int32_t items = nr * p.c.hkv * 2;
-    Raw8<TIn> raw[U];
-    auto fetch = [&](int32_t it, int u) {
-        const int32_t item = it + u * ngrp;
-        if (item < items) {
-            const int32_t half = item & 1, rh = item >> 1, r = rh / p.c.hkv, h = rh - r * p.c.hkv;
-            raw[u] = raw_load<TIn>(half ? p.v_in : p.k_in,
-                                   (int64_t)(r0 + r) * p.row_stride + (int64_t)h * p.d + lane * 8);
+    // one item a group in flight: more blocks fit (with two, 66 K rows took 37 us instead of 33)
+    uint32_t raw[kWords<TIn>];
+    CacheItem at{0, 0};
+    at.skip(grp, cols);
+    auto fetch = [&]() {
+        if (at.r < nr) {
+            const bool v = at.c >= hkv;
+            load16<TIn>(v ? p.v_in : p.k_in,
+                        (int64_t)(r0 + at.r) * p.row_stride + (int64_t)(v ? at.c - hkv : at.c) * p.d + lane * 16, raw);
         }
     };
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        fetch(grp, u);
+    fetch();
     cache_locate(p, r0, nr, m);
     // every thread of the block runs every turn: the reduction below is over whole warps
-    for (int32_t it = grp; it - grp < items; it += U * ngrp) {
-        if (it != grp) {
+    for (int32_t left = nr * cols; left > 0; left -= ngrp) {
+        const int64_t slot = at.r < nr ? m.slot[at.r] : -1;
+        const bool v = at.c >= hkv;
+        const int32_t h = v ? at.c - hkv : at.c;
+        const int64_t e = slot + h * p.c.s_head + lane * 16;
+        void *pool = v ? p.c.v : p.c.k;
+        if constexpr (TC == SVP_E4M3) {
+            uint32_t amax = slot >= 0 ? amax16<TIn>(raw) : 0u;
+            for (int o = gl >> 1; o > 0; o >>= 1)
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (slot >= 0) {
+                const bool fine = amax < 0x7f800000u;
+                const uint32_t b = fine ? exp_byte_of(amax) : 255u;
+                // 2^-(b - 127): exponent field 254 - b (b >= 15, and b <= 247 for finite rows)
+                const float inv = __uint_as_float((254u - b) << 23);
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (fine) {
+                    float x[16];
+                    to_f32<TIn>(raw, x);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                fetch(it, u);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int32_t item = it + u * ngrp;
-            const bool have = item < items;
-            const int32_t half = item & 1, rh = item >> 1, r = rh / p.c.hkv, h = rh - r * p.c.hkv;
-            const int64_t at = have ? m.slot[r] : -1;
-            const int64_t e = at + h * p.c.s_head + lane * 8;
-            void *pool = half ? p.c.v : p.c.k;
-            if constexpr (TC == SVP_E4M3) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (at >= 0)
-                    raw_values<TIn>(raw[u], x);
-                uint32_t amax = 0u;
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    amax = max(amax, __float_as_uint(x[v]) & 0x7fffffffu);
-                for (int o = gl >> 1; o > 0; o >>= 1)
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (at >= 0) {
-                    const bool fine = amax < 0x7f800000u;
-                    const uint32_t b = fine ? exp_byte_of(amax) : 255u;
-                    // 2^-(b - 127): exponent field 254 - b (b >= 15, and b <= 247 for finite rows)
-                    const float inv = fine ? __uint_as_float((254u - b) << 23) : 0.0f;
-                    uint2 w = make_uint2(0u, 0u);
-                    if (fine) {
-                        w.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | (pack_e4m3x2(x[2] * inv, x[3] * inv) << 16);
-                        w.y = pack_e4m3x2(x[4] * inv, x[5] * inv) | (pack_e4m3x2(x[6] * inv, x[7] * inv) << 16);
-                    }
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + e) = w;
-                    if (lane == 0)
-                        (half ? p.c.v_exp : p.c.k_exp)[m.eoff[r] + ((int64_t)h << p.c.page_shift)] = (uint8_t)b;
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = pack_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+                               (pack_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
                 }
-            } else if (at >= 0) {
-                if constexpr (TIn == TC && TIn == SVP_BF16) {
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(pool) + e) = raw[u].a;   // bits as they are
-                } else {
-                    float x[8];
-                    raw_values<TIn>(raw[u], x);
-                    store_values<TC>(pool, e, x);
-                }
+                store16<SVP_E4M3>(pool, e, w);
+                if (lane == 0)
+                    (v ? p.c.v_exp : p.c.k_exp)[m.eoff[at.r] + ((int64_t)h << p.c.page_shift)] = (uint8_t)b;
+            }
+        } else if (slot >= 0) {
+            if constexpr (TIn == TC) {
+                store16<TC>(pool, e, raw);                        // bits as they are
+            } else {
+                float x[16];
+                uint32_t w[kWords<TC>];
+                to_f32<TIn>(raw, x);
+                from_f32<TC>(x, w);
+                store16<TC>(pool, e, w);
             }
         }
+        at.skip(ngrp, cols);
+        fetch();
     }
 }
 
 template <int TC, int TOut>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_constant__ CacheMoveParams p)
 {
-    constexpr int U = 4;
+    constexpr int U = TC == SVP_E4M3 ? 1 : 2;   // items a group has in flight (8-bit rows: 2 took 340 us)
     __shared__ CacheRowMap m;
     griddep_launch_dependents();
     griddep_wait();
     const int32_t r0 = (int32_t)blockIdx.x * p.rpb;
-    const int32_t nr = min(p.rpb, p.rows - r0);
+    const int32_t nr = min(p.rpb, p.rows - r0), hkv = p.c.hkv, cols = 2 * hkv;
     cache_locate(p, r0, nr, m);
-    const int gl = p.d >> 3;
+    const int gl = p.d >> 4;
     const int grp = threadIdx.x / gl, lane = threadIdx.x - grp * gl, ngrp = kCacheThreads / gl;
-    const int32_t items = nr * p.c.hkv * 2;
-    for (int32_t it = grp; it < items; it += U * ngrp) {
-        Raw8<TC> raw[U];
-        uint32_t b[U];
+    CacheItem at{0, 0}, ahead;
+    at.skip(grp, cols);
+    ahead = at;
+    while (at.r < nr) {
+        uint32_t raw[U][kWords<TC>], b[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t item = it + u * ngrp;
-            const int32_t half = item & 1, rh = item >> 1, r = rh / p.c.hkv, h = rh - r * p.c.hkv;
-            if (item < items && m.slot[r] >= 0) {
-                raw[u] = raw_load<TC>(half ? p.c.v : p.c.k, m.slot[r] + h * p.c.s_head + lane * 8);
+            const int64_t slot = ahead.r < nr ? m.slot[ahead.r] : -1;
+            if (slot >= 0) {
+                const bool v = ahead.c >= hkv;
+                const int32_t h = v ? ahead.c - hkv : ahead.c;
+                load16<TC>(v ? p.c.v : p.c.k, slot + h * p.c.s_head + lane * 16, raw[u]);
                 if constexpr (TC == SVP_E4M3)
-                    b[u] = (half ? p.c.v_exp : p.c.k_exp)[m.eoff[r] + ((int64_t)h << p.c.page_shift)];
+                    b[u] = (v ? p.c.v_exp : p.c.k_exp)[m.eoff[ahead.r] + ((int64_t)h << p.c.page_shift)];
             }
+            ahead.skip(ngrp, cols);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t item = it + u * ngrp;
-            const int32_t half = item & 1, rh = item >> 1, r = rh / p.c.hkv, h = rh - r * p.c.hkv;
-            if (item < items && m.slot[r] >= 0) {
-                float x[8];
-                raw_values<TC>(raw[u], x);
-                if constexpr (TC == SVP_E4M3) {
-                    const float s = exp_byte_scale(b[u]);
+            if (at.r < nr && m.slot[at.r] >= 0) {
+                const bool v = at.c >= hkv;
+                const int32_t h = v ? at.c - hkv : at.c;
+                const int64_t e = ((int64_t)(r0 + at.r) * hkv + h) * p.d + lane * 16;
+                void *out = v ? p.v_out : p.k_out;
+                if constexpr (TC == TOut) {
+                    store16<TOut>(out, e, raw[u]);
+                } else {
+                    float x[16];
+                    uint32_t w[kWords<TOut>];
+                    to_f32<TC>(raw[u], x);
+                    if constexpr (TC == SVP_E4M3) {
+                        const float s = exp_byte_scale(b[u]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] *= s;
+                        for (int i = 0; i < 16; ++i)
+                            x[i] *= s;
+                    }
+                    from_f32<TOut>(x, w);
+                    store16<TOut>(out, e, w);
                 }
-                store_values<TOut>(half ? p.v_out : p.k_out, ((int64_t)(r0 + r) * p.c.hkv + h) * p.d + lane * 8, x);
             }
+            at.skip(ngrp, cols);
         }
     }
 }

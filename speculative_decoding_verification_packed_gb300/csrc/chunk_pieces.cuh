@@ -26,6 +26,7 @@ struct ChunkParams {
     int64_t q_stride;
     int32_t n, m_cap, w, hq, G, R;    // R: tokens of a query tile
     float scale_log2;
+    int32_t out32;                    // out is 32-byte aligned
     void *out;
     float *lse;
     int32_t *status;

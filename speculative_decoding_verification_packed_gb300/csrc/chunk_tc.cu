@@ -168,6 +168,14 @@ __device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// 32 bytes, a whole sector, in one store (16-byte ones of a row leave half sectors).
+__device__ __forceinline__ void ck_store8(void *at, const uint32_t *x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ the kernel
 template <int D, bool Q8>
 __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p)
@@ -818,16 +826,21 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 pk[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
-                            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) +
-                                                                   ((int64_t)row * p.hq + head) * D + cc * 32);
+                            uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + ((int64_t)row * p.hq + head) * D + cc * 32;
+                            if (p.out32) {
+                                ck_store8(dst, pk);
+                                ck_store8(dst + 16, pk + 8);
+                            } else {
+#pragma unroll
+                                for (int v = 0; v < 4; ++v)
+                                    reinterpret_cast<uint4 *>(dst)[v] =
+                                        make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                            }
+                        } else {
+                            float *dst = p.part_o + prow * D + cc * 32;
 #pragma unroll
                             for (int v = 0; v < 4; ++v)
-                                dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-                        } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + prow * D + cc * 32);
-#pragma unroll
-                            for (int v = 0; v < 8; ++v)
-                                dst[v] = make_uint4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+                                ck_store8(dst + 8 * v, ov + 8 * v);
                         }
                     }
                     if (live) {
@@ -943,7 +956,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
 // Block (c, y): rows of the pair whose first piece CTA c had, one row a warp: o = sum_q 2^(m_q - M)
 // O_q / L over the pieces in their order, L = sum_q 2^(m_q - M) l_q.  Launched behind the kernel above
 // as its dependent; most blocks find nothing to do.
-constexpr int kJoinWarps = 4, kJoinY = 8;
+constexpr int kJoinWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p, int32_t part_rows)
@@ -955,7 +968,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
     const ChunkDesc d = p.desc[c];
     if (d.np < 2)
         return;
-    for (int32_t rho = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); rho < d.ntok * p.G; rho += kJoinWarps * kJoinY) {
+    for (int32_t rho = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); rho < d.ntok * p.G; rho += kJoinWarps * (int32_t)gridDim.y) {
         const int32_t tok = rho / p.G, h = rho - tok * p.G;
         const bool second = tok >= p.R;                   // token of the second query tile
         const int32_t pr = (second ? 128 : 0) + (tok - (second ? p.R : 0)) * p.G + h;
@@ -1038,7 +1051,9 @@ svp_status chunk_short_run(ChunkParams &p, int32_t d, cudaStream_t stream);
 template <int D>
 static svp_status chunk_join(const ChunkParams &p, int32_t part_rows, cudaStream_t stream)
 {
-    return launch_pdl(chunk_join_kernel<D>, dim3(sm_count(), kJoinY), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
+    const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most; two a warp
+    const unsigned y = (unsigned)std::max(1, (rows + 2 * kJoinWarps - 1) / (2 * kJoinWarps));
+    return launch_pdl(chunk_join_kernel<D>, dim3(sm_count(), y), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
                    cudaSuccess
                ? SVP_OK
                : SVP_ECUDA;
@@ -1107,6 +1122,7 @@ svp_status chunk_tc_launch(const void *q, int64_t q_stride, svp_dtype kv, const 
     const bool few = kv == SVP_E4M3 && d <= 128 && (int64_t)p.G * w <= kShortRows;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = out;
+    p.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     p.lse = lse;
     const ChunkWs o = chunk_ws(d);
     uint8_t *wsb = static_cast<uint8_t *>(ws);
