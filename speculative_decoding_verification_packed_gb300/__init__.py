@@ -229,10 +229,11 @@ class Workspace:
     stream must be ordered after it (the same stream, a synchronize, or an event): torch's
     side streams do not wait for the default stream."""
 
-    def __init__(self, nbytes: int, device=None, stream=None):
+    def __init__(self, nbytes: int, device=None, stream=None, zeroed: Optional[int] = None):
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
-        _check(lib().svp_workspace_init(self.ptr, self.nbytes, _stream(stream)),
+        # (zeroed: the leading bytes that the entry point wants zeroed; None for all of them)
+        _check(lib().svp_workspace_init(self.ptr, self.nbytes if zeroed is None else zeroed, _stream(stream)),
                "svp_workspace_init")
 
     @property
@@ -742,12 +743,13 @@ def _chunk_workspace(hq: int, cache: svp_cache, dtype, stream, raw: int) -> Work
     streams may overlap; a call that is being captured gets its own, which lives in the graph's
     memory, as graphs may be replayed on any stream."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, stream)
+        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, stream,
+                         zeroed=256)
     key = (raw, cache.index, cache.d, dtype)
     ws = _chunk_ws.get(key)
     if ws is None:
         ws = _chunk_ws[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
-                                        cache.device, stream)
+                                        cache.device, stream, zeroed=256)
     return ws
 
 

@@ -9,7 +9,8 @@ namespace svp {
 constexpr int kCkKeys = 128;          // keys a KV tile
 constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
 constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
-constexpr int kShareKeys = 512;       // smallest share of a CTA, in keys
+constexpr int kShortCost = 3, kLongCost = 4;   // cost of a key with one query tile, and with two
+constexpr int kShareCost = 640;       // smallest share of a CTA (more than a tile's cost)
 constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
 
 constexpr int kShortRows = 16;        // query rows of a KV head up to which 8-bit pages take chunk_short.cu
@@ -44,24 +45,33 @@ struct ChunkPiece {
     int32_t off, k, L;                // the request's first packed row, rows, cached tokens
     int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
     int32_t nt, t0, t1;               // its KV tiles, and those of this piece
+    int32_t wt;                       // cost of a key
     int64_t base;                     // cost before the pair
 };
 
-__device__ __forceinline__ int64_t ck_before(int64_t a, int64_t B, int64_t b)   // cost of blocks 0..b-1
+__device__ __forceinline__ int64_t ck_before(int64_t a, int64_t B, int64_t b)   // keys of blocks 0..b-1
 {
     return b * a + B * (b * (b + 1) / 2);
 }
 
-// Cost of one KV head of a request: block b costs kStartKeys + L + (keys of its own tokens).
-__device__ __forceinline__ int64_t ck_head_cost(int32_t L, int32_t k, int32_t B)
+// A key of a request with blocks of two query tiles costs more (its tile is worked on twice).
+template <int NT>
+__device__ __forceinline__ int32_t ck_weight(int32_t k, int32_t R)
+{
+    return NT == 2 && k > R ? kLongCost : kShortCost;
+}
+
+// Keys of one KV head of a request: kStartKeys + L + (those of its own tokens) for each block.
+__device__ __forceinline__ int64_t ck_head_keys(int32_t L, int32_t k, int32_t B)
 {
     const int64_t nb = (k + B - 1) / B, a = (int64_t)kStartKeys + L;
     return nb == 0 ? 0 : ck_before(a, B, nb - 1) + a + k;
 }
 
-__device__ __forceinline__ int32_t ck_tile_at(int64_t x)   // first tile at or after cost x of a pair
+__device__ __forceinline__ int32_t ck_tile_at(int64_t x, int32_t wt)   // first tile at or after cost x of a pair
 {
-    return x <= kStartKeys ? 0 : (int32_t)((x - kStartKeys + kCkKeys - 1) / kCkKeys);
+    const int64_t s = (int64_t)kStartKeys * wt, tile = (int64_t)kCkKeys * wt;
+    return x <= s ? 0 : (int32_t)((x - s + tile - 1) / tile);
 }
 
 template <int NT>
@@ -74,23 +84,26 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int6
     s.nt = (s.len + kCkKeys - 1) / kCkKeys;
     s.t0 = t0;
     const int64_t y = v1 - s.base;
-    s.t1 = y >= (int64_t)kStartKeys + s.len ? s.nt : min(s.nt, ck_tile_at(y));
+    s.t1 = y >= (int64_t)s.wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, s.wt));
     return s.t0 < s.t1;
 }
 
-__device__ __forceinline__ void ck_request(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int32_t B)
+template <int NT>
+__device__ __forceinline__ void ck_request(const ChunkParams &p, ChunkPiece &s)
 {
+    const int32_t B = NT * p.R;
     s.off = __ldg(p.cu + s.i);
     s.k = __ldg(p.cu + s.i + 1) - s.off;
     s.L = __ldg(p.ctx_len + s.i);
     s.nb = (s.k + B - 1) / B;
+    s.wt = ck_weight<NT>(s.k, p.R);
 }
 
 // The next pair before cost v1, from its first tile.
 template <int NT>
 __device__ __forceinline__ bool ck_next(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int64_t v1)
 {
-    s.base += (int64_t)kStartKeys + s.len;
+    s.base += (int64_t)s.wt * (kStartKeys + (int64_t)s.len);
     if (s.base >= v1)
         return false;
     if (++s.b == s.nb) {
@@ -100,7 +113,7 @@ __device__ __forceinline__ bool ck_next(const ChunkParams &p, const int64_t *pre
             do
                 ++s.i;
             while (prefix[s.i + 1] == prefix[s.i]);   // (base < v1 <= the total: there is one)
-            ck_request(p, prefix, s, NT * p.R);
+            ck_request<NT>(p, s);
         }
     }
     return ck_set<NT>(p, s, v1, 0);
@@ -123,23 +136,23 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
             hi = mid;
     }
     s.i = lo;
-    ck_request(p, prefix, s, B);
-    const int64_t H = ck_head_cost(s.L, s.k, B);
+    ck_request<NT>(p, s);
+    const int64_t H = ck_head_keys(s.L, s.k, B) * s.wt;
     int64_t rem = v0 - prefix[lo];
     s.g = (int32_t)(rem / H);
     rem -= s.g * H;
-    // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem, put right
+    // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem / wt, put right
     const int64_t a = (int64_t)kStartKeys + s.L;
     const float h = (float)a + 0.5f * B;
-    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * (float)rem) - h) / B);
+    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / s.wt)) - h) / B);
     b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
-    while (b + 1 < s.nb && ck_before(a, B, b + 1) <= rem)
+    while (b + 1 < s.nb && ck_before(a, B, b + 1) * s.wt <= rem)
         ++b;
-    while (b > 0 && ck_before(a, B, b) > rem)
+    while (b > 0 && ck_before(a, B, b) * s.wt > rem)
         --b;
     s.b = (int32_t)b;
-    s.base = prefix[lo] + s.g * H + ck_before(a, B, b);
-    const int32_t t0 = ck_tile_at(v0 - s.base);
+    s.base = prefix[lo] + s.g * H + ck_before(a, B, b) * s.wt;
+    const int32_t t0 = ck_tile_at(v0 - s.base, s.wt);
     const bool have = ck_set<NT>(p, s, v1, t0);
     // a share that begins behind the pair's last tile begins with the next pair
     return have || (t0 >= s.nt && ck_next<NT>(p, prefix, s, v1));
@@ -159,8 +172,10 @@ __device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t
 
 // Cost before each request into prefix[0..n] (shared memory; every thread of the block, tot: one entry
 // a warp).  A request that breaks the contract costs nothing, and sets a status bit.  Ends in a barrier.
-__device__ __forceinline__ void ck_prologue(const ChunkParams &p, int32_t B, int64_t *prefix, int64_t *tot)
+template <int NT>
+__device__ __forceinline__ void ck_prologue(const ChunkParams &p, int64_t *prefix, int64_t *tot)
 {
+    const int32_t B = NT * p.R;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
     if (tid == 0)
         prefix[0] = 0;
@@ -178,7 +193,7 @@ __device__ __forceinline__ void ck_prologue(const ChunkParams &p, int32_t B, int
             if (bad && blockIdx.x == 0)
                 set_status(p.status, bad);
             if (!bad)
-                cost = ck_head_cost(L, end - off, B) * p.c.hkv;
+                cost = ck_head_keys(L, end - off, B) * ck_weight<NT>(end - off, p.R) * p.c.hkv;
         }
         int64_t incl = cost;
 #pragma unroll

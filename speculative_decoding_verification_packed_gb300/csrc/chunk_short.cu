@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
     griddep_wait();
     if (tid == 0)
         p.desc[blockIdx.x].np = 0;
-    ck_prologue(p, p.R, m->prefix, m->warp_tot);
+    ck_prologue<1>(p, m->prefix, m->warp_tot);
     const int64_t total = m->prefix[p.n];
-    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareKeys));
+    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
     const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
             }
             if (!whole && s.t0 == 0 && tid == 0) {
                 ChunkDesc d;
-                d.np = ck_owner(total, ncta, s.base + kStartKeys + (int64_t)kCkKeys * (s.nt - 1)) - cta + 1;
+                d.np = ck_owner(total, ncta, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                 d.row0 = s.off + s.tb0;
                 d.ntok = s.ntok;
                 d.g = s.g;

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     using Cfg = ChunkCfg<D, Q8>;
     constexpr int NT = Cfg::NT, NH = Cfg::NH, DH = Cfg::DH;
     constexpr bool kMono = NT == 1;
+    constexpr int kGiveAt = DH / 16 * 3 / 4;   // (products of S before the turn is given: 6 of 8 beat 4 and 2)
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -242,13 +243,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     griddep_wait();
     if (tid == 0)
         p.desc[blockIdx.x].np = 0;
-    ck_prologue(p, NT * p.R, m->prefix, m->warp_tot);
+    ck_prologue<NT>(p, m->prefix, m->warp_tot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
     const int64_t total = m->prefix[p.n];
-    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareKeys));
+    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
     const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
@@ -436,11 +437,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const uint32_t n = nturn++;
             return me == 0 ? n == 0 || wait_all(bar_turn(0), (n - 1) & 1u) : wait_all(bar_turn(1), n & 1u);
         };
-        auto yield = [&]() {
-            if (lane == 0)
-                mbar_arrive(bar_turn(me ^ 1));
-            __syncwarp();
-        };
         // NH slots of the other warp's: seen and released
         auto pass = [&]() -> bool {
             for (int h = 0; h < NH; ++h) {
@@ -468,7 +464,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             __syncwarp();
             ++q_loads;
         };
-        auto issue_s = [&](int buf) -> bool {                  // S of the tile at the ring position
+        // S of the tile at the ring position; give: the turn passes on before its last products, as the
+        // arrival queues behind the ones before it and the other issuer takes a while to wake
+        auto issue_s = [&](int buf, bool give) -> bool {
             for (int h = 0; h < NH; ++h) {
                 if (!wait_all(bar_full(slot), phase))
                     return false;
@@ -478,10 +476,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     const uint64_t kd = sw128_desc(sbase + p.off_ring + slot * Cfg::kSlot, 16, 1024);
                     const uint32_t qs16 = (uint32_t)p.qsub >> 4;
 #pragma unroll
-                    for (int ks = 0; ks < DH / 16; ++ks)
+                    for (int ks = 0; ks < DH / 16; ++ks) {
+                        if (ks == kGiveAt && give)
+                            mbar_arrive(bar_turn(me ^ 1));
                         tc_mma_ss(tmem + buf * 128, qd + (uint64_t)((ks >> 2) * qs16 + (ks & 3) * 2),
                                   kd + (uint64_t)((ks >> 2) * (kCkSub >> 4) + (ks & 3) * 2), idesc_s,
                                   (h | ks) ? 1u : 0u);
+                    }
                     if (h == NH - 1)
                         tc_commit(bar_s(buf));
                     tc_commit(bar_empty(slot));
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     if (me == 0) {
                         // the buffer's last P has been read
                         if (!(ok = nsp[buf] == 0 || wait_all(bar_pv(buf), (nsp[buf] - 1) & 1u)) ||
-                            !(ok = issue_s(buf)))
+                            !(ok = issue_s(buf, false)))
                             break;
                         ++nsp[buf];
                         if (t == nt - 1 && lane == 0)
@@ -579,15 +580,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     }
                 } else if (lng) {
                     // (the K wait is inside the turn: the other issuer needs the same tile)
-                    if ((t == 0 && !(ok = turn())) || !(ok = issue_s(me)))
+                    if ((t == 0 && !(ok = turn())) || !(ok = issue_s(me, true)) ||
+                        !(ok = issue_pv(me, me, kvalid, t == 0, t == nt - 1, true)))
                         break;
-                    yield();
-                    if (!(ok = issue_pv(me, me, kvalid, t == 0, t == nt - 1, true)))
-                        break;
-                    if (t == nt - 1)
-                        yield();
+                    if (t == nt - 1 && lane == 0)
+                        mbar_arrive(bar_turn(me ^ 1));
                 } else if ((t & 1) == me) {
-                    if (!(ok = issue_s(me)) || !(ok = issue_pv(me, me, kvalid, t < 2, t + 2 >= nt, false)))
+                    if (!(ok = issue_s(me, false)) || !(ok = issue_pv(me, me, kvalid, t < 2, t + 2 >= nt, false)))
                         break;
                 } else if (!(ok = pass()) || !(ok = pass())) {
                     break;
@@ -853,7 +852,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (!whole && s.t0 == 0 && a == 0 && r == 0) {
                     // this CTA has the pair's first piece: CTAs up to the owner of its last tile have the rest
                     ChunkDesc d;
-                    d.np = ck_owner(total, ncta, s.base + kStartKeys + (int64_t)kCkKeys * (s.nt - 1)) - cta + 1;
+                    d.np = ck_owner(total, ncta, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                     d.row0 = s.off + s.tb0;
                     d.ntok = s.ntok;
                     d.g = s.g;
