@@ -74,6 +74,14 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
+// True in one lane of a converged warp, always the same.
+__device__ __forceinline__ bool ck_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Four codes to fp16, times the row's power of two (both halves of mul).
 __device__ __forceinline__ void ck_codes(uint32_t w, uint32_t mul, uint32_t &lo, uint32_t &hi)
 {
@@ -471,7 +479,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (!wait_all(bar_full(slot), phase))
                     return false;
                 tc_fence_after();
-                if (lane == 0) {
+                if (ck_elect()) {
                     const uint64_t qd = sw128_desc(sbase + (me * (D / 64) + h * 2) * p.qsub, 16, 1024);
                     const uint64_t kd = sw128_desc(sbase + p.off_ring + slot * Cfg::kSlot, 16, 1024);
                     const uint32_t qs16 = (uint32_t)p.qsub >> 4;
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             if (lng && !turn())
                 return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (ck_elect()) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     const uint64_t vd = sw128_desc(sbase + p.off_ring + sl[h] * Cfg::kSlot, kCkSub, 1024);
@@ -1071,12 +1079,13 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     const int misc = (int)(sizeof(ChunkMisc) + (size_t)p.n * sizeof(int64_t) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
-    // rings that a K and a V loader share hold whole tiles (2 NH slots); the bf16 ring of 8-bit pages is
-    // filled by the converting warps in order and needs 3 slots (4 for d = 256: S of the next tile is
-    // issued before V of this one is released)
-    constexpr int kTile = 2 * Cfg::NH, kLeast = Cfg::NH == 2 ? 4 : 3;
+    // rings that a K and a V loader share hold whole tiles (2 NH slots); the 16-bit ring of 8-bit pages is
+    // filled by the converting warps in order and needs 3 slots
+    constexpr int kTile = 2 * Cfg::NH;
     if (Q8) {
-        p.nslot = 4;
+        // four 16-bit slots where two raw ones fit beside them, else three
+        const int raw2 = (Cfg::kTwoLoad ? kTile : 2) * Cfg::kRawSlot;
+        p.nslot = room >= 4 * Cfg::kSlot + raw2 ? 4 : 3;
         p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot);
         if (Cfg::kTwoLoad)
             p.nraw = p.nraw / kTile * kTile;
@@ -1086,7 +1095,7 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
         p.nraw = kTile;
         p.nslot = std::min(8, room / Cfg::kSlot) / kTile * kTile;
     }
-    if (p.nslot < kLeast || p.nraw < 2)
+    if (p.nslot < 3 || p.nraw < 2)
         return SVP_EUNSUPPORTED;
     p.off_raw = p.off_ring + p.nslot * Cfg::kSlot;
     p.off_misc = p.off_raw + (Q8 ? p.nraw * Cfg::kRawSlot : 0);

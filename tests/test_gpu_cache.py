@@ -369,6 +369,16 @@ def test_attend_many_requests(kind):
     check_attend(rows, [(37 * i) % 190 for i in range(300)], hq=2, hkv=1, d=64, kind=kind, seed=11)
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_the_most_requests(d, kind):
+    """1024 requests, most of them empty, among them rows of several query tiles."""
+    rows, ctx = [0] * 1024, [0] * 1024
+    for i, (r, c) in {3: (1, 40), 500: (150, 60), 900: (2, 129), 1023: (70, 1)}.items():
+        rows[i], ctx[i] = r, c
+    check_attend(rows, ctx, hq=4, hkv=1, d=d, kind=kind, seed=19, picks=(0, 1, 69, 149))
+
+
 def test_one_workspace_serves_any_size_twice():
     ws = svp.Workspace(svp.chunk_attn_workspace_size(8, 2, 128))
     for rows, ctx in (([1], [5000]), ([200, 1], [100, 3000]), ([1], [5000]), ([3] * 40, [257] * 40)):
