@@ -88,20 +88,34 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int6
     return s.t0 < s.t1;
 }
 
-template <int NT>
-__device__ __forceinline__ void ck_request(const ChunkParams &p, ChunkPiece &s)
+// Status bits of a request that breaks the contract.
+__device__ __forceinline__ int32_t ck_bad(const ChunkParams &p, int32_t off, int32_t end, int32_t L)
 {
-    const int32_t B = NT * p.R;
+    if (off < 0 || end < off || end - off > p.w || end > p.m_cap)
+        return SVP_DEV_BAD_SLOTS;
+    if (end > off && (L < 0 || (int64_t)L + (end - off) > ((int64_t)p.c.max_pages << p.c.page_shift)))
+        return SVP_DEV_BAD_CONTEXT;
+    return 0;
+}
+
+// Request s.i; false if it has no work.
+template <int NT>
+__device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
+{
+    const int32_t B = NT * p.R, end = __ldg(p.cu + s.i + 1);
     s.off = __ldg(p.cu + s.i);
-    s.k = __ldg(p.cu + s.i + 1) - s.off;
     s.L = __ldg(p.ctx_len + s.i);
+    s.k = end - s.off;
+    if (s.k <= 0 || ck_bad(p, s.off, end, s.L))
+        return false;
     s.nb = (s.k + B - 1) / B;
     s.wt = ck_weight<NT>(s.k, p.R);
+    return true;
 }
 
 // The next pair before cost v1, from its first tile.
 template <int NT>
-__device__ __forceinline__ bool ck_next(const ChunkParams &p, const int64_t *prefix, ChunkPiece &s, int64_t v1)
+__device__ __forceinline__ bool ck_next(const ChunkParams &p, ChunkPiece &s, int64_t v1)
 {
     s.base += (int64_t)s.wt * (kStartKeys + (int64_t)s.len);
     if (s.base >= v1)
@@ -110,10 +124,10 @@ __device__ __forceinline__ bool ck_next(const ChunkParams &p, const int64_t *pre
         s.b = 0;
         if (++s.g == p.c.hkv) {
             s.g = 0;
-            do
-                ++s.i;
-            while (prefix[s.i + 1] == prefix[s.i]);   // (base < v1 <= the total: there is one)
-            ck_request<NT>(p, s);
+            do {
+                if (++s.i >= p.n)
+                    return false;     // (never: base < v1 <= the total)
+            } while (!ck_request<NT>(p, s));
         }
     }
     return ck_set<NT>(p, s, v1, 0);
@@ -155,7 +169,7 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
     const int32_t t0 = ck_tile_at(v0 - s.base, s.wt);
     const bool have = ck_set<NT>(p, s, v1, t0);
     // a share that begins behind the pair's last tile begins with the next pair
-    return have || (t0 >= s.nt && ck_next<NT>(p, prefix, s, v1));
+    return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
 }
 
 __device__ __forceinline__ int64_t ck_bound(int64_t total, int32_t c, int32_t ncta)
@@ -170,8 +184,8 @@ __device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t
     return c < 0 ? 0 : c;
 }
 
-// Cost before each request into prefix[0..n] (shared memory; every thread of the block, tot: one entry
-// a warp).  A request that breaks the contract costs nothing, and sets a status bit.  Ends in a barrier.
+// Cost before each request into prefix[0..n] (shared memory that the pipeline uses later; every thread of
+// the block, tot: one entry a warp).  A request that breaks the contract costs nothing, and sets a status bit.  Ends in a barrier.
 template <int NT>
 __device__ __forceinline__ void ck_prologue(const ChunkParams &p, int64_t *prefix, int64_t *tot)
 {
@@ -185,11 +199,7 @@ __device__ __forceinline__ void ck_prologue(const ChunkParams &p, int64_t *prefi
         int64_t cost = 0;
         if (i < p.n) {
             const int32_t off = __ldg(p.cu + i), end = __ldg(p.cu + i + 1), L = __ldg(p.ctx_len + i);
-            int32_t bad = 0;
-            if (off < 0 || end < off || end - off > p.w || end > p.m_cap)
-                bad = SVP_DEV_BAD_SLOTS;
-            else if (end > off && (L < 0 || (int64_t)L + (end - off) > ((int64_t)p.c.max_pages << p.c.page_shift)))
-                bad = SVP_DEV_BAD_CONTEXT;
+            const int32_t bad = ck_bad(p, off, end, L);
             if (bad && blockIdx.x == 0)
                 set_status(p.status, bad);
             if (!bad)

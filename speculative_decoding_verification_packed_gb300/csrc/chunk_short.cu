@@ -39,7 +39,6 @@ struct ShortMisc {
     int32_t abort_flag, pad;
     int64_t warp_tot[12];
     float2 ml[kShWarps][16];          // [warp][row of its group]
-    int64_t prefix[1];                // [n + 1]
 };
 
 template <int D, int NB>
@@ -113,13 +112,17 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
     griddep_wait();
     if (tid == 0)
         p.desc[blockIdx.x].np = 0;
-    ck_prologue<1>(p, m->prefix, m->warp_tot);
-    const int64_t total = m->prefix[p.n];
+    int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
+    ck_prologue<1>(p, prefix, m->warp_tot);
+    const int64_t total = prefix[p.n];
     const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
     const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
     ChunkPiece s;
+    const bool have0 = ck_first<1>(p, prefix, s, v0, v1);
+    fence_proxy_async_smem();             // the loads overwrite the sums
+    __syncthreads();
 
     if (warp >= kShWarps) {
         // ============================================================ K loader, V loader
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         const bool loads = ((lane * 4) & in_page) == 0;
         uint32_t slot = kv, phase = 0, done = 0;
         bool ok = true;
-        for (bool have = ck_first<1>(p, m->prefix, s, v0, v1); have && ok; have = ck_next<1>(p, m->prefix, s, v1)) {
+        for (bool have = have0; have && ok; have = ck_next<1>(p, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
             constexpr int32_t kNone = INT32_MIN;
             auto page_of = [&](int32_t t) -> int32_t {
@@ -155,12 +158,13 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 const int64_t at = (((int64_t)id * p.c.hkv + s.g) << p.c.page_shift) + ((t * kCkKeys + lane * 4) & in_page);
                 return __ldg(reinterpret_cast<const uint32_t *>(exps + at));
             };
-            int32_t id = checked(page_of(s.t0)), id1 = page_of(s.t0 + 1);
-            uint32_t e = exps_of(s.t0, id);
+            // (page ids three tiles ahead, exponents two)
+            int32_t id = checked(page_of(s.t0)), id1 = checked(page_of(s.t0 + 1)), id2 = page_of(s.t0 + 2);
+            uint32_t e = exps_of(s.t0, id), e1 = exps_of(s.t0 + 1, id1);
             for (int32_t t = s.t0; t < s.t1; ++t, ++done) {
-                id1 = checked(id1);
-                const int32_t id2 = page_of(t + 2);
-                const uint32_t e1 = exps_of(t + 1, id1);
+                id2 = checked(id2);
+                const int32_t id3 = page_of(t + 3);
+                const uint32_t e2 = exps_of(t + 2, id2);
                 int got = 1;
                 if (lane == 0)
                     got = mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
@@ -186,8 +190,10 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     phase ^= 1u;
                 }
                 e = e1;
+                e1 = e2;
                 id = id1;
                 id1 = id2;
+                id2 = id3;
             }
         }
         if (lane == 0) {
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         float *red = reinterpret_cast<float *>(smem);       // [8 warps][8 NB rows][D + 8]
         uint32_t slot = 0, phase = 0;
         bool ok = true;
-        for (bool have = ck_first<1>(p, m->prefix, s, v0, v1); have; have = ck_next<1>(p, m->prefix, s, v1)) {
+        for (bool have = have0; have; have = ck_next<1>(p, s, v1)) {
             const int32_t nrows = s.ntok * p.G;
             // ---- Q: row r of each block in fp16, its largest magnitude at 2^14 or more, as operands; the
             // softmax factor (with the way back) and last visible key of rows 2 q and 2 q + 1
@@ -477,7 +483,7 @@ static svp_status short_launch(ChunkParams &p, cudaStream_t stream)
 {
     using Cfg = ShortCfg<D, NB>;
     constexpr int kBudget = 227 * 1024;
-    const int misc = (int)(sizeof(ShortMisc) + (size_t)p.n * sizeof(int64_t) + 127) / 128 * 128;
+    const int misc = (int)(sizeof(ShortMisc) + 127) / 128 * 128;
     p.off_ring = (Cfg::kRed + 1023) / 1024 * 1024;
     p.nslot = std::min(kShSlots, (kBudget - p.off_ring - misc) / (Cfg::kRaw + 512)) / 2 * 2;
     if (p.nslot < 4)

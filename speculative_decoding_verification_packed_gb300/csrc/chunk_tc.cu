@@ -58,7 +58,6 @@ struct ChunkMisc {
     float2 ml[128];                   // (m, l) of the second warpgroup's half of a short piece
     float o_scale;                    // and what its O is to be multiplied with
     float2 scales[16];                // 8-bit pages: (2^E of K, E of V) of a KV tile, by tile mod 16
-    int64_t prefix[1];                // [n + 1]: cost before request i
 };
 
 // ------------------------------------------------------------------ small device helpers
@@ -251,17 +250,21 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     griddep_wait();
     if (tid == 0)
         p.desc[blockIdx.x].np = 0;
-    ck_prologue<NT>(p, m->prefix, m->warp_tot);
+    int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
+    ck_prologue<NT>(p, prefix, m->warp_tot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    const int64_t total = m->prefix[p.n];
+    const int64_t total = prefix[p.n];
     const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
     const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
     ChunkPiece s;
+    const bool have0 = ck_first<NT>(p, prefix, s, v0, v1);
+    fence_proxy_async_smem();             // the loads overwrite the sums
+    __syncthreads();
     auto is_long = [&](const ChunkPiece &x) { return !kMono && x.ntok > p.R; };
 
     if (warp == 0 || (Cfg::kTwoLoad && warp == 3)) {
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         // looks after positions 4 u .. 4 u + 3 of a tile, which lie in one page, and the lane of a
         // page's first positions loads the page.  What lies past the block's last visible key, and
         // pages whose id is outside the pool, is loaded from a page past the pool: TMA fills zeros.
-        // Exponent bytes come by ordinary loads one tile ahead (page ids two), as copies of their own
+        // Exponent bytes come by ordinary loads two tiles ahead (page ids three), as copies of their own
         // would double the TMA's requests, and go to shared memory as the multipliers that the
         // converting warps need.
         const int kv0 = Cfg::kTwoLoad ? (warp == 0 ? 0 : 1) : 0, kv1 = Cfg::kTwoLoad ? kv0 + 1 : 2;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         const uint64_t pol_once = l2_policy_evict_first();
         const int32_t in_page = (1 << p.c.page_shift) - 1;
         const bool loads = ((lane * 4) & in_page) == 0;
-        for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have && ok; have = ck_next<NT>(p, m->prefix, s, v1)) {
+        for (bool have = have0; have && ok; have = ck_next<NT>(p, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
             constexpr int32_t kNone = INT32_MIN;             // nothing of the tile needs a page here
             auto page_of = [&](int32_t t) -> int32_t {
@@ -305,29 +308,33 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 return __ldg(reinterpret_cast<const uint32_t *>((kv ? p.c.v_exp : p.c.k_exp) + at));
             };
             const bool once = s.nb == 1;      // no other block of the request reads these keys
-            int32_t id = checked(page_of(s.t0)), id1 = page_of(s.t0 + 1);
-            uint32_t e[2] = {0, 0}, e1[2] = {0, 0};
-            for (int kv = kv0; kv < 2; ++kv)                 // (the K loader tells the softmax of V's too)
-                e[kv] = exps_of(kv, s.t0, id);
+            int32_t id = checked(page_of(s.t0)), id1 = checked(page_of(s.t0 + 1)), id2 = page_of(s.t0 + 2);
+            // (the K loader tells the softmax of V's exponents too)
+            uint32_t ek = kv0 == 0 ? exps_of(0, s.t0, id) : 0u, ek1 = kv0 == 0 ? exps_of(0, s.t0 + 1, id1) : 0u;
+            uint32_t ev = exps_of(1, s.t0, id), ev1 = exps_of(1, s.t0 + 1, id1);
             for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++done) {
-                id1 = checked(id1);
-                const int32_t id2 = page_of(t + 2);
-                for (int kv = kv0; kv < 2; ++kv)
-                    e1[kv] = exps_of(kv, t + 1, id1);
+                id2 = checked(id2);
+                const int32_t id3 = page_of(t + 3);
+                const uint32_t ek2 = kv0 == 0 ? exps_of(0, t + 2, id2) : 0u, ev2 = exps_of(1, t + 2, id2);
                 // the largest exponent of the tile's visible rows, at least 2^-60 (NaN rows apart)
-                uint32_t top[2] = {67, 67};
                 const int32_t left = s.len - t * kCkKeys - lane * 4;   // of this lane's rows, the visible
-                if constexpr (Q8) {
-                    for (int kv = kv0; kv < 2; ++kv) {
+                auto top_of = [&](uint32_t e) -> uint32_t {
+                    uint32_t top = 67;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t b = (e[kv] >> (8 * x)) & 0xffu;
-                            top[kv] = max(top[kv], x < left && b != 255u ? b : 0u);
-                        }
-                        top[kv] = __reduce_max_sync(0xffffffffu, top[kv]);
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t b = (e >> (8 * x)) & 0xffu;
+                        top = max(top, x < left && b != 255u ? b : 0u);
                     }
-                    if (kv0 == 0 && lane == 0)
-                        m->scales[done & 15] = make_float2(__uint_as_float(top[0] << 23), (float)((int32_t)top[1] - 127));
+                    return __reduce_max_sync(0xffffffffu, top);
+                };
+                uint32_t topk = 0, topv = 0;
+                if constexpr (Q8) {
+                    topv = top_of(ev);
+                    if (kv0 == 0) {
+                        topk = top_of(ek);
+                        if (lane == 0)
+                            m->scales[done & 15] = make_float2(__uint_as_float(topk << 23), (float)((int32_t)topv - 127));
+                    }
                 }
                 const int32_t page = id < 0 ? max(p.c.num_pages, 1) : id;
                 for (int kv = kv0; kv < kv1 && ok; ++kv) {
@@ -351,8 +358,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                             uint32_t mul[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                const uint32_t b = (e[kv] >> (8 * x)) & 0xffu;
-                                const int32_t down = (int32_t)top[kv] - (int32_t)b;
+                                const uint32_t b = ((kv ? ev : ek) >> (8 * x)) & 0xffu;
+                                const int32_t down = (int32_t)(kv ? topv : topk) - (int32_t)b;
                                 const uint32_t f = b == 255u ? 0x7e00u
                                                    : down <= 14 ? (uint32_t)(15 - down) << 10
                                                    : down <= 24 ? 1u << (24 - down) : 0u;
@@ -389,10 +396,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                         phase ^= 1u;
                     }
                 }
-                e[0] = e1[0];
-                e[1] = e1[1];
+                ek = ek1;
+                ek1 = ek2;
+                ev = ev1;
+                ev1 = ev2;
                 id = id1;
                 id1 = id2;
+                id2 = id3;
             }
         }
         // every load lands (and, of the bf16 ring, every release by the tensor core) before the
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             ++nsp[buf];
             if (!kMono && last) {
                 // this warp's last P of the piece: all its S are done and its query tile may be replaced
-                have_next = ck_next<NT>(p, m->prefix, s, v1);
+                have_next = ck_next<NT>(p, s, v1);
                 if (have_next)
                     load_q(s);
             }
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             __syncwarp();
             return true;
         };
-        bool have = ck_first<NT>(p, m->prefix, s, v0, v1);
+        bool have = have0;
         if (have)
             load_q(s);
         while (have && ok) {
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             if (mine > 0)
                 ++no;
             if (kMono || mine == 0) {
-                have_next = ck_next<NT>(p, m->prefix, s, v1);
+                have_next = ck_next<NT>(p, s, v1);
                 if (kMono && me == 0 && !(ok = wait_all(bar_sdone, npiece & 1u)))
                     break;
                 if (have_next)
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         };
-        for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have; have = ck_next<NT>(p, m->prefix, s, v1)) {
+        for (bool have = have0; have; have = ck_next<NT>(p, s, v1)) {
             const bool lng = is_long(s);
             const int32_t nt = s.t1 - s.t0;
             const int32_t tok = (lng ? a * p.R : 0) + r / p.G;      // token of the block
@@ -886,7 +896,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         // A thread takes 16 codes of one row at a time, its neighbours the rest of the row.
         if constexpr (Q8) {
             constexpr int CPR = DH / 16;                  // 16-code chunks a row
-            constexpr int RPI = 32 * Cfg::kConvWarps / CPR;   // rows a turn
+            constexpr int RPI = 32 * Cfg::kConvWarps / CPR, IT = 128 / RPI;   // rows a turn, turns
             const int ct = tid - Cfg::kConvWarp0 * 32;
             const int c = ct % CPR, row0 = ct / CPR;
             // which half of its 16 codes a thread takes first: the lanes of one access then cover all banks,
@@ -896,31 +906,52 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const uint32_t line = (c >> 2) * kCkSub + row0 * 128;
             const uint32_t out = line + (((2 * (c & 3) + odd) ^ (row0 & 7)) << 4);
             const uint32_t out2 = line + (((2 * (c & 3) + (odd ^ 1)) ^ (row0 & 7)) << 4);
-            uint32_t pos = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
+            // Half tiles of K and V apart (each has its own slots where the rings hold whole tiles), K one
+            // tile ahead: V's slot waits for a PV, which S of the next tile need not.
+            // (the ring positions of the kind at hand and of the other one change places)
+            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, slot2 = NH, phase2 = 0, rslot2 = NH, rphase2 = 0;
+            int kind = 0;
             bool ok = true;
-            uint32_t halves = 0;                          // of all pieces
-            for (bool have = ck_first<NT>(p, m->prefix, s, v0, v1); have; have = ck_next<NT>(p, m->prefix, s, v1))
-                halves += (uint32_t)(s.t1 - s.t0) * 2 * NH;
-            {
-                for (; pos < halves; ++pos) {
+            uint32_t tiles = 0;                           // of all pieces
+            for (bool have = have0; have; have = ck_next<NT>(p, s, v1))
+                tiles += (uint32_t)(s.t1 - s.t0);
+            const uint32_t turns = 2 * tiles;
+            uint32_t pos = 0;                             // half tiles done
+            for (uint32_t turn = 0; turn < turns && ok; ++turn) {
+                const int kv = Cfg::kTwoLoad ? (turn > 0 && ((turn & 1) == 0 || turn == turns - 1) ? 1 : 0) : (int)(turn & 1);
+                if (Cfg::kTwoLoad && kv != kind) {        // (one loader fills one ring in order)
+                    uint32_t x;
+                    x = slot, slot = slot2, slot2 = x;
+                    x = phase, phase = phase2, phase2 = x;
+                    x = rslot, rslot = rslot2, rslot2 = x;
+                    x = rphase, rphase = rphase2, rphase2 = x;
+                    kind = kv;
+                }
+                for (int h = 0; h < NH; ++h, ++pos) {
                     const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
                                      mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
                     if (!(ok = __all_sync(0xffffffffu, got)))
                         break;
                     const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
                     const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
-#pragma unroll 2
-                    for (int it = 0; it < 128 / RPI; ++it) {
-                        uint2 w = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
-                        uint2 w2 = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
-                        const uint32_t mul = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
-                        if (mul == 0u)                    // (the codes may be NaN, which 0 would not hide)
-                            w = w2 = make_uint2(0u, 0u);
+                    // all reads first: each takes long beside the tensor core's, and none may pass a write
+                    uint2 w[IT], w2[IT];
+                    uint32_t mul[IT];
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) {
+                        w[it] = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
+                        w2[it] = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
+                        mul[it] = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
+                    }
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) {
+                        if (mul[it] == 0u)                // (the codes may be NaN, which 0 would not hide)
+                            w[it] = w2[it] = make_uint2(0u, 0u);
                         uint32_t x[8];
-                        ck_codes(w.x, mul, x[0], x[1]);
-                        ck_codes(w.y, mul, x[2], x[3]);
-                        ck_codes(w2.x, mul, x[4], x[5]);
-                        ck_codes(w2.y, mul, x[6], x[7]);
+                        ck_codes(w[it].x, mul[it], x[0], x[1]);
+                        ck_codes(w[it].y, mul[it], x[2], x[3]);
+                        ck_codes(w2[it].x, mul[it], x[4], x[5]);
+                        ck_codes(w2[it].y, mul[it], x[6], x[7]);
                         st_shared_v4(dst + out + it * (RPI * 128), x[0], x[1], x[2], x[3]);
                         st_shared_v4(dst + out2 + it * (RPI * 128), x[4], x[5], x[6], x[7]);
                     }
@@ -930,12 +961,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                         mbar_arrive(bar_rempty(rslot));
                         mbar_arrive(bar_full(slot));
                     }
-                    if (++slot == (uint32_t)nslot) {
-                        slot = 0;
+                    // the next half; past a whole tile's two kinds of halves at its end
+                    const uint32_t by = Cfg::kTwoLoad && h == NH - 1 ? NH + 1 : 1;
+                    if ((slot += by) >= (uint32_t)nslot) {
+                        slot -= nslot;
                         phase ^= 1u;
                     }
-                    if (++rslot == (uint32_t)nraw) {
-                        rslot = 0;
+                    if ((rslot += by) >= (uint32_t)nraw) {
+                        rslot -= nraw;
                         rphase ^= 1u;
                     }
                 }
@@ -1076,7 +1109,7 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     p.Rb = std::min(p.R, p.w);
     p.qsub = (p.G * p.Rb + 7) / 8 * 1024;
     const int qbytes = Cfg::NT * (D / 64) * p.qsub;
-    const int misc = (int)(sizeof(ChunkMisc) + (size_t)p.n * sizeof(int64_t) + 127) / 128 * 128;
+    const int misc = (int)(sizeof(ChunkMisc) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
     // rings that a K and a V loader share hold whole tiles (2 NH slots); the 16-bit ring of 8-bit pages is
@@ -1091,11 +1124,13 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
             p.nraw = p.nraw / kTile * kTile;
         if (p.nraw >= 2)
             p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
+        if (Cfg::kTwoLoad)
+            p.nslot = p.nslot / kTile * kTile;
     } else {
         p.nraw = kTile;
         p.nslot = std::min(8, room / Cfg::kSlot) / kTile * kTile;
     }
-    if (p.nslot < 3 || p.nraw < 2)
+    if (p.nslot < 2 || p.nraw < 2)
         return SVP_EUNSUPPORTED;
     p.off_raw = p.off_ring + p.nslot * Cfg::kSlot;
     p.off_misc = p.off_raw + (Q8 ? p.nraw * Cfg::kRawSlot : 0);
