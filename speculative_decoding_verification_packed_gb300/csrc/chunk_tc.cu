@@ -40,12 +40,12 @@ struct ChunkCfg {
     static constexpr int DH = D / NH;
     static constexpr int kSlot = (DH / 64) * kCkSub;       // a half tile in bf16
     static constexpr int kRaw = kCkKeys * DH;              // and in codes
-    static constexpr int kRawSlot = kRaw + 4 * kCkKeys;    // + the rows' multipliers
-    // warps: 0 K loader, 1 and 2 MMA issuers, 3 V loader, then warpgroups of softmax and converting warps
+    static constexpr int kRawSlot = kRaw + 2 * kCkKeys;    // + the rows' multipliers
+    // warps: 0 and 3 loaders, 1 and 2 MMA issuers, then warpgroups of softmax and converting warps
     static constexpr int kSoftWarp0 = 4;
     static constexpr int kConvWarp0 = kSoftWarp0 + 4 * NT;
     static constexpr int kConvWarps = Q8 ? 4 : 0;
-    static constexpr bool kTwoLoad = !(Q8 && NH == 2);     // (there the raw ring has no room for two tiles)
+    static constexpr bool kByKind = NH == 1;               // the loaders share a ring by K and V, else by halves of d
     static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
     static constexpr int kPartRows = 128 * NT;
 };
@@ -71,6 +71,11 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+__device__ __forceinline__ void ck_st_v2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 // True in one lane of a converged warp, always the same.
@@ -267,24 +272,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     __syncthreads();
     auto is_long = [&](const ChunkPiece &x) { return !kMono && x.ntok > p.R; };
 
-    if (warp == 0 || (Cfg::kTwoLoad && warp == 3)) {
-        // ============================================================ K / V producers
-        // One warp loads K and one V (issuing the copies of 16-token pages is what bounds a single one);
-        // the ring holds whole tiles, so each has its own slots.  A warp runs its loop together: lane u
-        // looks after positions 4 u .. 4 u + 3 of a tile, which lie in one page, and the lane of a
-        // page's first positions loads the page.  What lies past the block's last visible key, and
-        // pages whose id is outside the pool, is loaded from a page past the pool: TMA fills zeros.
-        // Exponent bytes come by ordinary loads two tiles ahead (page ids three), as copies of their own
-        // would double the TMA's requests, and go to shared memory as the multipliers that the
-        // converting warps need.
-        const int kv0 = Cfg::kTwoLoad ? (warp == 0 ? 0 : 1) : 0, kv1 = Cfg::kTwoLoad ? kv0 + 1 : 2;
+    if (warp == 0 || warp == 3) {
+        // ============================================================ K / V loaders
+        // Two warps, as issuing the copies of 16-token pages is what bounds a single one: the ring's
+        // positions (K and V of a tile, in halves for d = 256) are theirs in turn, and it has an even
+        // number of slots.  A warp runs its loop together: lane u looks after positions 4 u .. 4 u + 3
+        // of a tile, which lie in one page, and the lane of a page's first positions loads the page.
+        // What lies past the block's last visible key, and pages whose id is outside the pool, is
+        // loaded from a page past the pool: TMA fills zeros.  Exponent bytes come by ordinary loads two
+        // tiles ahead (page ids three), as copies of their own would double the TMA's requests, and go
+        // to shared memory as the multipliers that the converting warps need.
+        const int me = warp == 0 ? 0 : 1;
         bool ok = true;
         const int32_t nring = Q8 ? nraw : nslot;
-        uint32_t done = 0;            // tiles loaded
-        uint32_t slot = kv0 * NH, phase = 0;
+        uint32_t done = 0, fills = 0; // tiles loaded, ring slots filled by this warp
+        uint32_t slot = me, phase = 0;
         const uint64_t pol_once = l2_policy_evict_first();
         const int32_t in_page = (1 << p.c.page_shift) - 1;
         const bool loads = ((lane * 4) & in_page) == 0;
+        const bool needs_k = me == 0 || !Cfg::kByKind;    // (the first loader tells the softmax of both)
         for (bool have = have0; have && ok; have = ck_next<NT>(p, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
             constexpr int32_t kNone = INT32_MIN;             // nothing of the tile needs a page here
@@ -309,13 +315,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             };
             const bool once = s.nb == 1;      // no other block of the request reads these keys
             int32_t id = checked(page_of(s.t0)), id1 = checked(page_of(s.t0 + 1)), id2 = page_of(s.t0 + 2);
-            // (the K loader tells the softmax of V's exponents too)
-            uint32_t ek = kv0 == 0 ? exps_of(0, s.t0, id) : 0u, ek1 = kv0 == 0 ? exps_of(0, s.t0 + 1, id1) : 0u;
+            uint32_t ek = needs_k ? exps_of(0, s.t0, id) : 0u, ek1 = needs_k ? exps_of(0, s.t0 + 1, id1) : 0u;
             uint32_t ev = exps_of(1, s.t0, id), ev1 = exps_of(1, s.t0 + 1, id1);
             for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++done) {
                 id2 = checked(id2);
                 const int32_t id3 = page_of(t + 3);
-                const uint32_t ek2 = kv0 == 0 ? exps_of(0, t + 2, id2) : 0u, ev2 = exps_of(1, t + 2, id2);
+                const uint32_t ek2 = needs_k ? exps_of(0, t + 2, id2) : 0u, ev2 = exps_of(1, t + 2, id2);
                 // the largest exponent of the tile's visible rows, at least 2^-60 (NaN rows apart)
                 const int32_t left = s.len - t * kCkKeys - lane * 4;   // of this lane's rows, the visible
                 auto top_of = [&](uint32_t e) -> uint32_t {
@@ -330,68 +335,64 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 uint32_t topk = 0, topv = 0;
                 if constexpr (Q8) {
                     topv = top_of(ev);
-                    if (kv0 == 0) {
+                    if (needs_k) {
                         topk = top_of(ek);
-                        if (lane == 0)
+                        if (me == 0 && lane == 0)
                             m->scales[done & 15] = make_float2(__uint_as_float(topk << 23), (float)((int32_t)topv - 127));
                     }
                 }
                 const int32_t page = id < 0 ? max(p.c.num_pages, 1) : id;
-                for (int kv = kv0; kv < kv1 && ok; ++kv) {
+                for (int j = 0; j < NH; ++j) {
+                    const int kv = Cfg::kByKind ? me : j, h = Cfg::kByKind ? 0 : me;
                     const CUtensorMap *tm = kv ? &p.tm_v : &p.tm_k;
-                    for (int h = 0; h < NH; ++h) {
-                        const uint32_t full = Q8 ? bar_rfull(slot) : bar_full(slot);
-                        int got = 1;
-                        if (lane == 0)
-                            got = mbar_wait(Q8 ? bar_rempty(slot) : bar_empty(slot), phase ^ 1u, abort_flag);
-                        if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0))
-                            break;
-                        if constexpr (Q8) {
-                            const uint32_t dst = sbase + p.off_raw + slot * Cfg::kRawSlot;
-                            if (loads) {
-                                if (once)
-                                    tma_load_4d_hint(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page, pol_once);
-                                else
-                                    tma_load_4d(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page);
-                            }
-                            // 2^(b - top) twice in fp16 (NaN for byte 255, 0 past the last visible key)
-                            uint32_t mul[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint32_t b = ((kv ? ev : ek) >> (8 * x)) & 0xffu;
-                                const int32_t down = (int32_t)(kv ? topv : topk) - (int32_t)b;
-                                const uint32_t f = b == 255u ? 0x7e00u
-                                                   : down <= 14 ? (uint32_t)(15 - down) << 10
-                                                   : down <= 24 ? 1u << (24 - down) : 0u;
-                                mul[x] = x < left ? f * 0x10001u : 0u;
-                            }
-                            st_shared_v4(dst + Cfg::kRaw + lane * 16, mul[0], mul[1], mul[2], mul[3]);
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(full, (uint32_t)Cfg::kRaw);
-                        } else {
-                            const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(full, (uint32_t)Cfg::kSlot);
-                            __syncwarp();
-                            if (loads) {
-#pragma unroll
-                                for (int c = 0; c < DH / 64; ++c) {
-                                    const uint32_t at = dst + c * kCkSub + lane * 512;
-                                    if (once)
-                                        tma_load_4d_hint(at, tm, full, h * DH + c * 64, 0, s.g, page, pol_once);
-                                    else
-                                        tma_load_4d(at, tm, full, h * DH + c * 64, 0, s.g, page);
-                                }
-                            }
+                    const uint32_t full = Q8 ? bar_rfull(slot) : bar_full(slot);
+                    int got = 1;
+                    if (lane == 0)
+                        got = mbar_wait(Q8 ? bar_rempty(slot) : bar_empty(slot), phase ^ 1u, abort_flag);
+                    if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0))
+                        break;
+                    if constexpr (Q8) {
+                        const uint32_t dst = sbase + p.off_raw + slot * Cfg::kRawSlot;
+                        if (loads) {
+                            if (once)
+                                tma_load_4d_hint(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page, pol_once);
+                            else
+                                tma_load_4d(dst + lane * 4 * DH, tm, full, h * DH, 0, s.g, page);
                         }
+                        // 2^(b - top) in fp16 (NaN for byte 255, 0 past the last visible key)
+                        uint32_t mul[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t b = ((kv ? ev : ek) >> (8 * x)) & 0xffu;
+                            const int32_t down = (int32_t)(kv ? topv : topk) - (int32_t)b;
+                            const uint32_t f = b == 255u ? 0x7e00u
+                                               : down <= 14 ? (uint32_t)(15 - down) << 10
+                                               : down <= 24 ? 1u << (24 - down) : 0u;
+                            mul[x] = x < left ? f : 0u;
+                        }
+                        ck_st_v2(dst + Cfg::kRaw + lane * 8, mul[0] | (mul[1] << 16), mul[2] | (mul[3] << 16));
                         __syncwarp();
-                        if (++slot == (uint32_t)nring) {
-                            slot = 0;
-                            phase ^= 1u;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full, (uint32_t)Cfg::kRaw);
+                    } else {
+                        const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full, (uint32_t)Cfg::kSlot);
+                        __syncwarp();
+                        if (loads) {
+#pragma unroll
+                            for (int c = 0; c < DH / 64; ++c) {
+                                const uint32_t at = dst + c * kCkSub + lane * 512;
+                                if (once)
+                                    tma_load_4d_hint(at, tm, full, h * DH + c * 64, 0, s.g, page, pol_once);
+                                else
+                                    tma_load_4d(at, tm, full, h * DH + c * 64, 0, s.g, page);
+                            }
                         }
                     }
-                    if (Cfg::kTwoLoad && (slot += NH) >= (uint32_t)nring) {   // past the other warp's
+                    __syncwarp();
+                    ++fills;
+                    if ((slot += 2) >= (uint32_t)nring) {
                         slot -= nring;
                         phase ^= 1u;
                     }
@@ -409,17 +410,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         // CTA's shared memory is given back; a fill that did not happen is not waited for
         if (lane == 0) {
             volatile int drain = 0;
-            const uint32_t back = nring / (2 * NH) + 1;
-            for (uint32_t x = done > back ? done - back : 0u; x < done; ++x)
-                for (int kv = kv0; kv < kv1; ++kv)
-                    for (int h = 0; h < NH; ++h) {
-                        const uint32_t k = x * 2 * NH + kv * NH + h;
-                        if (k + nring < done * 2 * NH)
-                            continue;         // filled again later
-                        mbar_wait(Q8 ? bar_rfull(k % nring) : bar_full(k % nring), (k / nring) & 1u, &drain);
-                        if (!Q8 && ok)
-                            mbar_wait(bar_empty(k % nring), (k / nring) & 1u, abort_flag);
-                    }
+            const uint32_t per = nring / 2;       // this warp's slots
+            for (uint32_t x = fills > per ? fills - per : 0u; x < fills; ++x) {
+                const uint32_t sl = (2 * x + me) % nring, ph = (x / per) & 1u;
+                mbar_wait(Q8 ? bar_rfull(sl) : bar_full(sl), ph, &drain);
+                if (!Q8 && ok)
+                    mbar_wait(bar_empty(sl), ph, abort_flag);
+            }
         }
         __syncwarp();
     } else if (warp == 1 || warp == 2) {
@@ -906,71 +903,52 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const uint32_t line = (c >> 2) * kCkSub + row0 * 128;
             const uint32_t out = line + (((2 * (c & 3) + odd) ^ (row0 & 7)) << 4);
             const uint32_t out2 = line + (((2 * (c & 3) + (odd ^ 1)) ^ (row0 & 7)) << 4);
-            // Half tiles of K and V apart (each has its own slots where the rings hold whole tiles), K one
-            // tile ahead: V's slot waits for a PV, which S of the next tile need not.
-            // (the ring positions of the kind at hand and of the other one change places)
-            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, slot2 = NH, phase2 = 0, rslot2 = NH, rphase2 = 0;
-            int kind = 0;
-            bool ok = true;
-            uint32_t tiles = 0;                           // of all pieces
+            uint32_t pos = 0, halves = 0;                 // ring positions done, of all pieces
             for (bool have = have0; have; have = ck_next<NT>(p, s, v1))
-                tiles += (uint32_t)(s.t1 - s.t0);
-            const uint32_t turns = 2 * tiles;
-            uint32_t pos = 0;                             // half tiles done
-            for (uint32_t turn = 0; turn < turns && ok; ++turn) {
-                const int kv = Cfg::kTwoLoad ? (turn > 0 && ((turn & 1) == 0 || turn == turns - 1) ? 1 : 0) : (int)(turn & 1);
-                if (Cfg::kTwoLoad && kv != kind) {        // (one loader fills one ring in order)
-                    uint32_t x;
-                    x = slot, slot = slot2, slot2 = x;
-                    x = phase, phase = phase2, phase2 = x;
-                    x = rslot, rslot = rslot2, rslot2 = x;
-                    x = rphase, rphase = rphase2, rphase2 = x;
-                    kind = kv;
+                halves += (uint32_t)(s.t1 - s.t0) * 2 * NH;
+            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
+            bool ok = true;
+            for (; pos < halves; ++pos) {
+                const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
+                                 mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, got)))
+                    break;
+                const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
+                const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
+                // all reads first: each takes long beside the tensor core's, and none may pass a write
+                uint2 w[IT], w2[IT];
+                uint32_t mul[IT];
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    w[it] = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
+                    w2[it] = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
+                    mul[it] = *reinterpret_cast<const uint16_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 2) * 0x10001u;
                 }
-                for (int h = 0; h < NH; ++h, ++pos) {
-                    const bool got = mbar_wait(bar_rfull(rslot), rphase, abort_flag) &&
-                                     mbar_wait(bar_empty(slot), phase ^ 1u, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, got)))
-                        break;
-                    const uint8_t *raw = smem + p.off_raw + rslot * Cfg::kRawSlot;
-                    const uint32_t dst = sbase + p.off_ring + slot * Cfg::kSlot;
-                    // all reads first: each takes long beside the tensor core's, and none may pass a write
-                    uint2 w[IT], w2[IT];
-                    uint32_t mul[IT];
 #pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        w[it] = *reinterpret_cast<const uint2 *>(raw + src + it * (RPI * DH));
-                        w2[it] = *reinterpret_cast<const uint2 *>(raw + src2 + it * (RPI * DH));
-                        mul[it] = *reinterpret_cast<const uint32_t *>(raw + Cfg::kRaw + (it * RPI + row0) * 4);
-                    }
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        if (mul[it] == 0u)                // (the codes may be NaN, which 0 would not hide)
-                            w[it] = w2[it] = make_uint2(0u, 0u);
-                        uint32_t x[8];
-                        ck_codes(w[it].x, mul[it], x[0], x[1]);
-                        ck_codes(w[it].y, mul[it], x[2], x[3]);
-                        ck_codes(w2[it].x, mul[it], x[4], x[5]);
-                        ck_codes(w2[it].y, mul[it], x[6], x[7]);
-                        st_shared_v4(dst + out + it * (RPI * 128), x[0], x[1], x[2], x[3]);
-                        st_shared_v4(dst + out2 + it * (RPI * 128), x[4], x[5], x[6], x[7]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar_rempty(rslot));
-                        mbar_arrive(bar_full(slot));
-                    }
-                    // the next half; past a whole tile's two kinds of halves at its end
-                    const uint32_t by = Cfg::kTwoLoad && h == NH - 1 ? NH + 1 : 1;
-                    if ((slot += by) >= (uint32_t)nslot) {
-                        slot -= nslot;
-                        phase ^= 1u;
-                    }
-                    if ((rslot += by) >= (uint32_t)nraw) {
-                        rslot -= nraw;
-                        rphase ^= 1u;
-                    }
+                for (int it = 0; it < IT; ++it) {
+                    if (mul[it] == 0u)                // (the codes may be NaN, which 0 would not hide)
+                        w[it] = w2[it] = make_uint2(0u, 0u);
+                    uint32_t x[8];
+                    ck_codes(w[it].x, mul[it], x[0], x[1]);
+                    ck_codes(w[it].y, mul[it], x[2], x[3]);
+                    ck_codes(w2[it].x, mul[it], x[4], x[5]);
+                    ck_codes(w2[it].y, mul[it], x[6], x[7]);
+                    st_shared_v4(dst + out + it * (RPI * 128), x[0], x[1], x[2], x[3]);
+                    st_shared_v4(dst + out2 + it * (RPI * 128), x[4], x[5], x[6], x[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_rempty(rslot));
+                    mbar_arrive(bar_full(slot));
+                }
+                if (++slot == (uint32_t)nslot) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+                if (++rslot == (uint32_t)nraw) {
+                    rslot = 0;
+                    rphase ^= 1u;
                 }
             }
             // the tensor core's releases land before the CTA's shared memory is given back
@@ -1112,25 +1090,17 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     const int misc = (int)(sizeof(ChunkMisc) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
-    // rings that a K and a V loader share hold whole tiles (2 NH slots); the 16-bit ring of 8-bit pages is
-    // filled by the converting warps in order and needs 3 slots
-    constexpr int kTile = 2 * Cfg::NH;
+    // the loaders' ring has an even number of slots; four 16-bit slots beside four raw ones where they fit, else three
     if (Q8) {
-        // four 16-bit slots where two raw ones fit beside them, else three
-        const int raw2 = (Cfg::kTwoLoad ? kTile : 2) * Cfg::kRawSlot;
-        p.nslot = room >= 4 * Cfg::kSlot + raw2 ? 4 : 3;
-        p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot);
-        if (Cfg::kTwoLoad)
-            p.nraw = p.nraw / kTile * kTile;
+        p.nslot = room >= 4 * Cfg::kSlot + 4 * Cfg::kRawSlot ? 4 : 3;
+        p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot) / 2 * 2;
         if (p.nraw >= 2)
             p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
-        if (Cfg::kTwoLoad)
-            p.nslot = p.nslot / kTile * kTile;
     } else {
-        p.nraw = kTile;
-        p.nslot = std::min(8, room / Cfg::kSlot) / kTile * kTile;
+        p.nraw = 2;
+        p.nslot = std::min(8, room / Cfg::kSlot) / 2 * 2;
     }
-    if (p.nslot < 2 || p.nraw < 2)
+    if (p.nslot < 3 || p.nraw < 2)
         return SVP_EUNSUPPORTED;
     p.off_raw = p.off_ring + p.nslot * Cfg::kSlot;
     p.off_misc = p.off_raw + (Q8 ? p.nraw * Cfg::kRawSlot : 0);
