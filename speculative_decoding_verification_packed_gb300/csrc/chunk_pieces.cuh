@@ -8,12 +8,21 @@ namespace svp {
 
 constexpr int kCkKeys = 128;          // keys a KV tile
 constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
-constexpr int kStartKeys = 256;       // cost of starting a pair, in keys
-constexpr int kShortCost = 3, kLongCost = 4;   // cost of a key with one query tile, and with two
-constexpr int kShareCost = 640;       // smallest share of a CTA (more than a tile's cost)
+// Cost of starting a pair, in keys.  A prompt of 4096 tokens and 24 blocks of 8 among two prompts of 2048
+// (8-bit) took 182 and 354 us with 64, 149 and 349 with 256, 151 and 344 with 512.
+constexpr int kStartKeys = 256;
+// Cost of a key with one query tile, and with two: 3 to 4 took 341 us on those blocks and prompts, 2 to 3
+// 356, 1 to 1 361 (calls of one kind are indifferent).
+constexpr int kShortCost = 3, kLongCost = 4;
+// Smallest share of a CTA, more than a tile's cost and a multiple of 128: a shorter one is not worth its
+// join.  One token over 500 keys 14.6 us, with 2048 16.5.
+constexpr int kShareCost = 640;
 constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
 
-constexpr int kShortRows = 16;        // query rows of a KV head up to which 8-bit pages take chunk_short.cu
+// Query rows of a KV head up to which 8-bit pages take chunk_short.cu.  64 requests x 18000 keys, 8 KV heads,
+// d 128, 4 and 16 rows: 362 and 470 us there, 640 and 643 in chunk_tc.cu (d 64, 2 and 16 rows: 333 and 360
+// against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 634 in chunk_tc.cu.
+constexpr int kShortRows = 16;
 
 struct ChunkDesc {                    // a pair that was split: read by the joining kernel
     int32_t np, row0, ntok, g;        // pieces (0: none), first packed row, tokens, KV head
@@ -45,7 +54,6 @@ struct ChunkPiece {
     int32_t off, k, L;                // the request's first packed row, rows, cached tokens
     int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
     int32_t nt, t0, t1;               // its KV tiles, and those of this piece
-    int32_t wt;                       // cost of a key
     int64_t base;                     // cost before the pair
 };
 
@@ -70,8 +78,11 @@ __device__ __forceinline__ int64_t ck_head_keys(int32_t L, int32_t k, int32_t B)
 
 __device__ __forceinline__ int32_t ck_tile_at(int64_t x, int32_t wt)   // first tile at or after cost x of a pair
 {
-    const int64_t s = (int64_t)kStartKeys * wt, tile = (int64_t)kCkKeys * wt;
-    return x <= s ? 0 : (int32_t)((x - s + tile - 1) / tile);
+    const int64_t s = (int64_t)kStartKeys * wt;
+    if (x <= s)
+        return 0;
+    const uint32_t y = (uint32_t)((x - s - 1) / kCkKeys);    // (x is at most a pair's cost: below 2^34)
+    return (int32_t)(wt == kShortCost ? y / kShortCost : y / kLongCost) + 1;
 }
 
 template <int NT>
@@ -83,8 +94,9 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int6
     s.len = s.L + s.tb0 + s.ntok;
     s.nt = (s.len + kCkKeys - 1) / kCkKeys;
     s.t0 = t0;
+    const int32_t wt = ck_weight<NT>(s.k, p.R);
     const int64_t y = v1 - s.base;
-    s.t1 = y >= (int64_t)s.wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, s.wt));
+    s.t1 = y >= (int64_t)wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, wt));
     return s.t0 < s.t1;
 }
 
@@ -109,7 +121,6 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
     if (s.k <= 0 || ck_bad(p, s.off, end, s.L))
         return false;
     s.nb = (s.k + B - 1) / B;
-    s.wt = ck_weight<NT>(s.k, p.R);
     return true;
 }
 
@@ -117,7 +128,7 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
 template <int NT>
 __device__ __forceinline__ bool ck_next(const ChunkParams &p, ChunkPiece &s, int64_t v1)
 {
-    s.base += (int64_t)s.wt * (kStartKeys + (int64_t)s.len);
+    s.base += (int64_t)ck_weight<NT>(s.k, p.R) * (kStartKeys + (int64_t)s.len);
     if (s.base >= v1)
         return false;
     if (++s.b == s.nb) {
@@ -151,37 +162,62 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
     }
     s.i = lo;
     ck_request<NT>(p, s);
-    const int64_t H = ck_head_keys(s.L, s.k, B) * s.wt;
+    const int32_t wt = ck_weight<NT>(s.k, p.R);
+    const int64_t H = ck_head_keys(s.L, s.k, B) * wt;
     int64_t rem = v0 - prefix[lo];
-    s.g = (int32_t)(rem / H);
+    s.g = min((int32_t)((float)rem / (float)H), p.c.hkv - 1);
     rem -= s.g * H;
+    if (rem < 0) {                    // (the quotient is off by one at most)
+        --s.g;
+        rem += H;
+    } else if (rem >= H) {
+        ++s.g;
+        rem -= H;
+    }
     // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem / wt, put right
     const int64_t a = (int64_t)kStartKeys + s.L;
     const float h = (float)a + 0.5f * B;
-    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / s.wt)) - h) / B);
+    int64_t b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / wt)) - h) / B);
     b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
-    while (b + 1 < s.nb && ck_before(a, B, b + 1) * s.wt <= rem)
+    while (b + 1 < s.nb && ck_before(a, B, b + 1) * wt <= rem)
         ++b;
-    while (b > 0 && ck_before(a, B, b) * s.wt > rem)
+    while (b > 0 && ck_before(a, B, b) * wt > rem)
         --b;
     s.b = (int32_t)b;
-    s.base = prefix[lo] + s.g * H + ck_before(a, B, b) * s.wt;
-    const int32_t t0 = ck_tile_at(v0 - s.base, s.wt);
+    s.base = prefix[lo] + s.g * H + ck_before(a, B, b) * wt;
+    const int32_t t0 = ck_tile_at(v0 - s.base, wt);
     const bool have = ck_set<NT>(p, s, v1, t0);
     // a share that begins behind the pair's last tile begins with the next pair
     return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
 }
 
-__device__ __forceinline__ int64_t ck_bound(int64_t total, int32_t c, int32_t ncta)
+// CTA c of ncta has the costs [c, c + 1) x share; ncta shares hold the total, and a share (but the last)
+// more than a tile.  Quotients are fp32 ones put right: a 64-bit division in each kind of warp is code
+// that the instruction cache misses (300 requests x 3 rows x 200 keys took 39.0 us with them, 37.3 without).
+struct ChunkShares {
+    int64_t total, share;
+    int32_t ncta;
+};
+
+__device__ __forceinline__ ChunkShares ck_shares(int64_t total)
 {
-    return total * c / ncta;
+    ChunkShares x;
+    x.total = total;
+    const uint32_t most = (uint32_t)min(total / 128, (int64_t)1 << 30) / (kShareCost / 128);
+    x.ncta = max(1, min((int32_t)gridDim.x, (int32_t)most));
+    x.share = (int64_t)((float)total / (float)x.ncta * (1.0f + 0x1p-20f)) + 1;
+    return x;
 }
 
-// The CTA that owns the tile that starts at cost u: the last c with ck_bound(c) <= u.
-__device__ __forceinline__ int32_t ck_owner(int64_t total, int32_t ncta, int64_t u)
+// The CTA that owns the tile that starts at cost u < total.
+__device__ __forceinline__ int32_t ck_owner(const ChunkShares &x, int64_t u)
 {
-    int32_t c = (int32_t)min((int64_t)ncta - 1, ((u + 1) * ncta + total - 1) / total - 1);
-    return c < 0 ? 0 : c;
+    int32_t c = (int32_t)((float)u / (float)x.share);
+    while (c > 0 && c * x.share > u)
+        --c;
+    while ((c + 1) * x.share <= u)
+        ++c;
+    return c;
 }
 
 // Cost before each request into prefix[0..n] (shared memory that the pipeline uses later; every thread of

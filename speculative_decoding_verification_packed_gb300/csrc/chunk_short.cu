@@ -114,11 +114,9 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         p.desc[blockIdx.x].np = 0;
     int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
     ck_prologue<1>(p, prefix, m->warp_tot);
-    const int64_t total = prefix[p.n];
-    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
+    const ChunkShares shares = ck_shares(prefix[p.n]);
     const int32_t cta = blockIdx.x;
-    const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
-    const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
+    const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     ChunkPiece s;
     const bool have0 = ck_first<1>(p, prefix, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
             }
             if (!whole && s.t0 == 0 && tid == 0) {
                 ChunkDesc d;
-                d.np = ck_owner(total, ncta, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
+                d.np = ck_owner(shares, s.base + (int64_t)ck_weight<1>(s.k, p.R) * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                 d.row0 = s.off + s.tb0;
                 d.ntok = s.ntok;
                 d.g = s.g;

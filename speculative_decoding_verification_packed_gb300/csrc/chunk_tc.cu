@@ -261,11 +261,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    const int64_t total = prefix[p.n];
-    const int32_t ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
+    const ChunkShares shares = ck_shares(prefix[p.n]);
     const int32_t cta = blockIdx.x;
-    const int64_t v0 = cta < ncta ? ck_bound(total, cta, ncta) : total;
-    const int64_t v1 = cta < ncta ? ck_bound(total, cta + 1, ncta) : total;
+    const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     ChunkPiece s;
     const bool have0 = ck_first<NT>(p, prefix, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
@@ -867,7 +865,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (!whole && s.t0 == 0 && a == 0 && r == 0) {
                     // this CTA has the pair's first piece: CTAs up to the owner of its last tile have the rest
                     ChunkDesc d;
-                    d.np = ck_owner(total, ncta, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
+                    d.np = ck_owner(shares, s.base + (int64_t)ck_weight<NT>(s.k, p.R) * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                     d.row0 = s.off + s.tb0;
                     d.ntok = s.ntok;
                     d.g = s.g;
