@@ -643,7 +643,7 @@ def _rows(t, name: str, heads: int, cache: svp_cache) -> int:
     s0, s1, s2 = t.stride()
     if t.device != cache.device or s2 != 1 or (heads > 1 and s1 != d):
         raise ValueError(f"{name} needs contiguous rows (any row stride) on the cache's device")
-    return s0 if m > 1 else max(s0, heads * d)
+    return s0 if m > 1 else heads * d
 
 
 def _i32(t, name: str, count: int, device) -> int:
@@ -667,6 +667,16 @@ def _requests(cu, cache: svp_cache, name: str) -> int:
 
 def _raw_stream(stream, cache: svp_cache) -> int:
     return torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else _stream(stream)
+
+
+def _other_stream(stream, cache: svp_cache):
+    """Context that makes ``stream`` torch's current one, None if it is: what a call allocates, clears
+    or captures belongs to the stream that it runs on."""
+    raw = _raw_stream(stream, cache)
+    if stream is None or raw == torch._C._cuda_getCurrentRawStream(cache.index):
+        return None
+    return torch.cuda.stream(torch.cuda.ExternalStream(raw, cache.device) if raw else
+                             torch.cuda.default_stream(cache.device))
 
 
 def _cache_workspace(cache: svp_cache, stream) -> Workspace:
@@ -706,6 +716,10 @@ def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
     are not given are made with ``rows`` rows of ``dtype``, zeros where nothing is read."""
     n = _requests(cu_rows, cache, "cu_rows")
     dev = cache.device
+    other = _other_stream(stream, cache)
+    if other is not None:
+        with other:
+            return cache_read(start, cu_rows, cache=cache, rows=rows, dtype=dtype, k_out=k_out, v_out=v_out, ws=ws)
     if k_out is None or v_out is None:
         if rows is None or k_out is not None or v_out is not None:
             raise ValueError("give both k_out and v_out, or rows")
@@ -738,18 +752,17 @@ def chunk_attn_workspace_size(hq: int, hkv: int, d: int, dtype=torch.bfloat16) -
 _chunk_ws: dict = {}
 
 
-def _chunk_workspace(hq: int, cache: svp_cache, dtype, stream, raw: int) -> Workspace:
+def _chunk_workspace(hq: int, cache: svp_cache, dtype, raw: int) -> Workspace:
     """The scratch of chunk_attn calls that bring none: one for each stream, as calls on two
     streams may overlap; a call that is being captured gets its own, which lives in the graph's
     memory, as graphs may be replayed on any stream."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, stream,
-                         zeroed=256)
+        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, zeroed=256)
     key = (raw, cache.index, cache.d, dtype)
     ws = _chunk_ws.get(key)
     if ws is None:
         ws = _chunk_ws[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
-                                        cache.device, stream, zeroed=256)
+                                        cache.device, zeroed=256)
     return ws
 
 
@@ -760,9 +773,13 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
     positions 0..ctx_len[i]+j, its own (written by cache_write before) included.  w: largest
     row count of a request (default m_cap; calls of few rows are planned by it).  Returns
     (out [m_cap, hq, d], lse [m_cap, hq] or None); rows past cu_slots[n] are left as they were
-    (zeros in outputs made here).  A call captured on a stream that is not torch's current one
-    needs its own ``ws``."""
+    (zeros in outputs made here)."""
     n = _requests(cu_slots, cache, "cu_slots")
+    other = _other_stream(stream, cache)
+    if other is not None:
+        with other:
+            return chunk_attn(q, ctx_len, cu_slots, cache=cache, w=w, out=out, lse=lse, want_lse=want_lse,
+                              scale=scale, ws=ws)
     dev = cache.device
     hkv = cache.hkv
     m_cap, hq, d = q.shape
@@ -778,9 +795,9 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
             lse = torch.zeros(m_cap, hq, dtype=torch.float32, device=dev)
     elif lse.shape != (m_cap, hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [m_cap, hq] on q's device")
-    raw = _raw_stream(stream, cache)
+    raw = _raw_stream(None, cache)
     if ws is None:
-        ws = _chunk_workspace(hq, cache, q.dtype, stream, raw)
+        ws = _chunk_workspace(hq, cache, q.dtype, raw)
     st = lib().svp_chunk_attn(
         q.data_ptr(), stride, cache.ref, _i32(ctx_len, "ctx_len", n, dev), _i32(cu_slots, "cu_slots", n + 1, dev),
         n, m_cap, (m_cap or 1) if w is None else w, svp_heads(hq, hkv, d, scale), _dtype_code(q), out.data_ptr(),

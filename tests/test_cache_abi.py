@@ -94,6 +94,8 @@ def test_attention_refusals(L):
     assert f(n=0) == OK and f(m=0) == OK
     f32 = cache(dtype=svp.SVP_F32, stride_page=2 * 16 * 128, stride_head=16 * 128)
     assert f(ca=ctypes.byref(f32)) == UNS                       # bf16 queries over an fp32 cache
+    for scale in (-0.5, float("nan"), float("inf"), -float("inf")):
+        assert f(h=heads(4, 2, 128, scale)) == INV
 
 
 def test_binding_refuses_cpu_tensors():

@@ -616,3 +616,144 @@ def test_empty_calls():
     out = torch.full_like(q, -7)
     svp.chunk_attn(q, i32([]), i32([0]), cache=cache, out=out)       # no request
     assert (out == -7).all()
+
+
+# ------------------------------------------------------------------ borders of the attention's kernels
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,rows", [(2, 2, 16), (2, 2, 17), (4, 2, 8), (4, 2, 9), (16, 1, 1), (17, 1, 1),
+                                         (8, 1, 1), (9, 1, 1), (3, 1, 3)])
+def test_attend_rows_around_the_short_kernel(hq, hkv, rows, d, kind):
+    """16 query rows of a KV head and one more, 8 and one more; requests of fewer rows among them."""
+    check_attend([rows, 1, rows, 0, max(1, rows - 1)], [700, 40, 0, 9, 255], hq=hq, hkv=hkv, d=d, kind=kind, seed=21)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("w", [1, 20])
+def test_every_code_and_exponent_through_one_key(d, w):
+    """A row that sees one key gets its value row, bit for bit: the probability is 1 (2^y with |y| below
+    2^-12, which fp16 rounds to 1 and which moves a code's 4 bits of mantissa by no bf16 step)."""
+    few = w == 1 and d < 256          # the kernel for few rows holds every byte that is written, the other 2^-60 up
+    parts = 256 // d
+    cases = [(b, x) for b in range(15 if few else 67, 247) for x in range(parts)]
+    n, page = len(cases), 16
+    codes = torch.zeros(n, 1, page, d, dtype=torch.uint8)
+    exps = torch.full((n, 1, page), 127, dtype=torch.uint8)
+    for i, (b, x) in enumerate(cases):
+        row = torch.arange(x * d, (x + 1) * d, dtype=torch.uint8)
+        codes[i, 0, 0] = torch.where((row & 127) == 127, torch.zeros_like(row), row)
+        exps[i, 0, 0] = b
+    kc = torch.randint(0, 120, codes.shape, generator=torch.Generator().manual_seed(22)).to(torch.uint8)
+    ke = torch.full_like(exps, 119)
+    cache = svp.make_cache(kc.cuda().view(E4M3), codes.cuda().view(E4M3),
+                           torch.arange(n, dtype=torch.int32)[:, None].cuda(), k_exp=ke.cuda(), v_exp=exps.cuda())
+    q = torch.randn(n, 1, d, generator=torch.Generator().manual_seed(23)).to(BF16).cuda()
+    out, _ = svp.chunk_attn(q, i32([0] * n), i32(list(range(n + 1))), cache=cache, w=w)
+    want = e4m3_values(codes[:, 0, 0].numpy()) * 2.0 ** (exps[:, 0, 0].numpy().astype(np.float64) - 127)[:, None]
+    assert (out[:, 0].double().cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_rows_of_very_different_sizes_in_one_tile(d, rows):
+    """Value rows 2^24 apart and key rows 2^6 apart, position by position.  An element is held to 2^-25 of
+    its tile's largest power of two 2^E, which the bound adds: 2^-24 2^E for V, and for a score 2^-24 2^E
+    of K times the sum of |q|."""
+    ctx, hq, hkv, page = 500, 4, 2, 16
+    T = ctx + rows
+    pool = Pool(1, [T], hkv, d, page, E4M3, seed=24)
+    g = torch.Generator().manual_seed(25)
+    for which, lo, hi in ((0, 116, 123), (1, 107, 132)):
+        e = torch.randint(lo, hi, pool.exps[which].shape, generator=g).to(torch.uint8)
+        live = pool.exps[which] != 255
+        pool.exps[which] = torch.where(live, e, pool.exps[which])
+        pool.vals[which] = e4m3_values(pool.raw[which].numpy()) * 2.0 ** (pool.exps[which].double().numpy() - 127)[..., None]
+    cache = pool.cuda()
+    q = torch.randn(rows, hq, d, generator=g).to(BF16).cuda() * 2.0 ** -6
+    out, lse = svp.chunk_attn(q, i32([ctx]), i32([0, rows]), cache=cache)
+    scale = 1 / math.sqrt(d)
+    o, l, tol, ltol = attend_exact(pool, q, [rows], [ctx], scale)
+    dsum = q.double().abs().sum(-1).cpu().numpy() * scale * 2.0 ** -24 * 2.0 ** -5     # score: K's E is 2^(122 - 127)
+    big = np.abs(pool.vals[1][np.isfinite(pool.vals[1])]).max()
+    extra = 2.0 ** -24 * 2.0 ** 4 + 2 * dsum[..., None] * big
+    assert (np.abs(out.double().cpu().numpy() - o) <= tol + extra).all()
+    assert (np.abs(lse.double().cpu().numpy() - l) <= ltol + dsum).all()
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 50])
+def test_output_on_a_16_byte_boundary(kind, rows):
+    pool = Pool(1, [300], 2, 128, 16, kind, seed=26)
+    cache = pool.cuda()
+    q = torch.randn(rows, 16, 128, device="cuda").to(BF16)
+    ctx, cu = i32([300 - rows]), i32([0, rows])
+    want, _ = svp.chunk_attn(q, ctx, cu, cache=cache)
+    buf = torch.full((rows * 16 * 128 + 16,), -7.0, device="cuda", dtype=BF16)
+    out = buf[8:-8].view(rows, 16, 128)
+    assert out.data_ptr() % 32 == 16
+    svp.chunk_attn(q, ctx, cu, cache=cache, out=out)
+    assert torch.equal(out, want) and (buf[:8] == -7).all() and (buf[-8:] == -7).all()
+
+
+def test_a_stream_that_is_not_the_current_one():
+    """Outputs made by the call are cleared on the stream that the call runs on."""
+    pool = Pool(1, [260], 2, 128, 16, BF16, seed=27)
+    cache = pool.cuda()
+    q = torch.randn(200, 8, 128, device="cuda").to(BF16)
+    ctx, cu = i32([60]), i32([0, 200])
+    want = svp.chunk_attn(q, ctx, cu, cache=cache)
+    kw, vw = svp.cache_read(None, i32([0, 260]), cache=cache, rows=260)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    load = torch.randn(4096, 4096, device="cuda")
+    for _ in range(3):
+        for _ in range(8):
+            load = load @ load * 1e-4          # the current stream is busy when the calls are made
+        got = svp.chunk_attn(q, ctx, cu, cache=cache, stream=side)
+        k, v = svp.cache_read(None, i32([0, 260]), cache=cache, rows=260, stream=side.cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(k, kw) and torch.equal(v, vw)
+
+
+def test_two_graphs_replayed_at_once():
+    pool = Pool(2, [3000, 2500], 2, 128, 16, E4M3, seed=28)
+    cache = pool.cuda()
+    cu, ctx = i32([0, 5, 10]), i32([2900, 2400])
+    qs = [torch.randn(10, 8, 128, device="cuda").to(BF16) for _ in range(2)]
+    want = [svp.chunk_attn(q, ctx, cu, cache=cache, w=5)[0] for q in qs]
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(svp.chunk_attn(q, ctx, cu, cache=cache, w=5)[0])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_one_workspace_for_every_head_layout_and_size():
+    nb = max(svp.chunk_attn_workspace_size(hq, hkv, d) for hq, hkv, d in ((8, 2, 64), (8, 2, 128), (8, 2, 256)))
+    ws = svp.Workspace(nb, zeroed=256)
+    ws.buf[256:] = 255                # (NaN bits: nothing may rest on what is there)
+    for d in (64, 256, 128, 64):
+        for kind in (BF16, E4M3):
+            for rows, ctx in (([1], [4000]), ([70, 3], [300, 2000])):
+                check_attend(rows, ctx, hq=8, hkv=2, d=d, kind=kind, ws=ws, picks=(0, 2, 63, 64), seed=29)
+
+
+def test_take_outside_its_range():
+    pool = Pool(3, [40, 40, 40], 2, 64, 16, BF16, seed=30, stale="keep")
+    cache = pool.cuda()
+    before = [x.clone() for x in pool.dev]
+    k = torch.randn(12, 2, 64, device="cuda").to(BF16)
+    svp.cache_write(k, k, i32([5, 6, 7]), i32([0, 4, 8, 12]), cache=cache, take=i32([-3, 1 << 30, -(1 << 31)]))
+    for x, y in zip(pool.dev, before):
+        pg = pool.table.long().cuda()
+        assert torch.equal(x[pg[0]], y[pg[0]]) and torch.equal(x[pg[2]], y[pg[2]])
+        assert torch.equal(x[int(pool.table[1, 0]), :, 6:10], k[4:8].transpose(0, 1))
