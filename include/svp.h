@@ -42,7 +42,8 @@
  *   - Kernels never trap.  Every wait inside a kernel is bounded; on expiry the kernel
  *     sets SVP_DEV_TIMEOUT in the status word and returns.
  *   - The DVL allocator, the row gathers, the verification attention, the margin /
- *     accept calls and the stochastic verifier's second pass are launched as
+ *     accept calls, the stochastic verifier's second pass, the cache's write and read
+ *     and the chunk attention (with the kernel that joins its parts) are launched as
  *     programmatic dependents of the previous kernel on their stream: they may be
  *     scheduled while it finishes, but read nothing before it has completed, so the
  *     results are those of plain stream order (also inside a captured CUDA graph).
@@ -483,12 +484,22 @@ svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const in
  * q      [m_cap, hq, d], row r at element r * q_row_stride (>= hq * d; 16-byte aligned, a
  *        multiple of 16 bytes); out [m_cap, hq, d] contiguous, lse [m_cap, hq] fp32
  * w      largest allowed k_i (host; 1 <= w); a request with k_i > w is skipped
- * dtype  of q and out: SVP_BF16 with an SVP_BF16 or SVP_E4M3 cache (tcgen05 kernel, fp32
- *        accumulation, probabilities rounded to bf16), SVP_F32 with an SVP_F32 cache (FFMA)
- * ws     at least svp_chunk_attn_workspace_size bytes (it depends on d and dtype only),
- *        zeroed once by svp_workspace_init; every call leaves it ready for the next one of
- *        any size.
+ * heads  scale 0 selects 1/sqrt(d); a negative, infinite or NaN one is SVP_EINVAL
+ * dtype  of q and out: SVP_BF16 with an SVP_BF16 or SVP_E4M3 cache, SVP_F32 with an SVP_F32
+ *        cache (anything else: SVP_EUNSUPPORTED)
+ * ws     at least svp_chunk_attn_workspace_size bytes (it depends on d and dtype only), its
+ *        first 256 zeroed once by svp_workspace_init; every call leaves it ready for the next
+ *        one of any size, head layout or type that it is large enough for.
  * 0 <= n <= 1024, hq / hkv <= 128, d = 64, 128 or 256 (SVP_EUNSUPPORTED otherwise).
+ *
+ * Precision.  Scores, the softmax's maximum and sum, and the output are accumulated in fp32; the
+ * probabilities that multiply V are rounded to bf16 over SVP_BF16 pages and to fp16 over SVP_E4M3
+ * ones (not at all in fp32).  8-bit rows with hq / hkv * w <= 16 and d <= 128 are used as they are;
+ * otherwise 128 positions (a tile) at a time in units of their largest power of two 2^E (of K and
+ * of V each, of visible rows, at least 2^-60): exact for rows within 2^15 of it, and an element below
+ * 2^(E - 25) counts as 0.  8-bit value rows of one request should have powers of two within 2^100 of
+ * one another: beyond, a key's weight can be lost.
+ *
  * Rows >= cu_slots[n] and rows of skipped requests are not written.  Device checks as for
  * svp_cache_write, for positions 0 .. ctx_len[i] + k_i - 1; a page id outside the pool reads
  * as a page of zeros (SVP_DEV_BAD_CONTEXT).  Cache positions past a request's last row (the

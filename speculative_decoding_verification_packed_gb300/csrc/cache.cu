@@ -10,8 +10,8 @@
 // cu_slots -> context length -> block table -> data below that.  So a block takes a few packed
 // rows of all heads: its threads look at all requests at once (one round trip) and the one
 // whose request owns a row resolves the row's page; the write has its rows' data already on
-// the way then, because their addresses need no lookup.  A group of d / 8 lanes moves one row
-// of one head, eight elements a lane (16-byte accesses for bf16).
+// the way then, because their addresses need no lookup.  A group of d / 16 lanes moves one row
+// of one head, sixteen elements a lane.
 #include "svp_cache.cuh"
 
 namespace svp {

@@ -4,23 +4,25 @@
 // (G heads times w tokens) and d <= 128, where the pages' bytes bound the time.  There tcgen05 does
 // not pay: its operands come from shared memory in 16 bits, so every code is read, widened, written
 // and read again by the tensor core, more shared-memory traffic than the bytes' time allows (64
-// requests x 18000 tokens took 810 us, against 661 us for bf16 pages twice the size).  Here codes go
-// from shared memory to registers, are widened there (cvt: two codes an instruction), and warp-level
-// m16n8k16 products take them as they are.
+// requests x 18000 tokens, 8 KV heads, d 128: 640 us).  Here codes go from shared memory to registers,
+// are widened there (cvt: two codes an instruction), and warp-level m16n8k16 products take them as
+// they are: 362 us, 6.6 TB/s with 16-token pages and 344 us with 128-token ones.
 //
 // Keys are the products' 16-row side and query rows the 8-column side,
 //   S^T (16 keys x 8 rows) = K Q^T,   O^T (16 of d x 8 rows) += V^T P^T,
 // as the rate of these products bounds the kernel next (with rows on the 16-row side, half of them
-// empty for G = 4 tokens, the same calls took 467 us; this way 381 us, 6.2 TB/s).  Eight warps share the
+// empty for G = 4 tokens, the same call took 467 us when this way took 381).  Eight warps share the
 // 128 positions of a KV tile, 16 each.  A warp keeps Q (fp16, the row's power of two taken out), its rows'
 // running maximum and sum and its O in registers; the warps join at the end of a piece through shared
-// memory.  NB = 1 or 2 blocks of 8 rows (510 us with 16 rows; with 32 rows in two groups of warps 854 us
-// against the tcgen05 kernel's 808 us, which takes over there).  d is taken in the order in which a thread finds it: for S,
+// memory.  NB = 1 or 2 blocks of 8 rows (470 us with 16 rows, bound by the products).  d = 64 takes 333 us
+// for half the bytes: the chain of a tile is as long, and copies of 1 KB come no faster than those
+// of 2 KB (263 us with 128-token pages).  d is taken in the order in which a thread finds it: for S,
 // thread q of a quad has d = D/4 q .. of its key in one read; for O, d = D/8 n + i belongs to row n of
 // the product's half i.  P^T turns from accumulator to operand by movmatrix.
 // An 8-bit row's power of two multiplies its row of S^T; V's goes into the exponent,
 //   P' = 2^(s c + e_key - m),  O += P' codes,  l += P' 2^-e_key,
-// with m the running maximum of s c + e_key, so that P' stays within fp16 whatever the exponents.
+// with m the running maximum of s c + e_key, so that P' stays within fp16 whatever the exponents (it is
+// rounded to fp16 because the products take 16 bits; scores, m, l and O are fp32).
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
 #include <algorithm>
 #include <cstring>

@@ -4,7 +4,7 @@
 //
 // Tiles.  The G query heads that share a KV head are packed with R = 128 / G tokens into a
 // 128-row query tile (row = token * G + head), so a key / value tile of 128 positions serves
-// all of them:  S = Q K^T (TMEM, 128 x 128 fp32), P = 2^(S c - m) in bf16 over the first
+// all of them:  S = Q K^T (TMEM, 128 x 128 fp32), P = 2^(S c - m) in 16 bits over the first
 // half of S's columns, O += P V with P taken straight from TMEM.  One thread owns one row.
 //   * long pieces (more than R tokens, d <= 128): two query tiles share one K / V stream; the
 //     softmax of one runs while the tensor pipe works on the other.
@@ -14,11 +14,26 @@
 //   * d = 256: O fills the TMEM that a second tile would need, so one warpgroup works through
 //     one query tile with two S buffers (its MMAs take twice as long a tile).
 // The exponent reference m is the row's maximum over the piece's first tile; it moves (and O is
-// rescaled) only when a later score lies more than 2^8 above it.
+// rescaled) only when a later score lies more than 2^8 above it.  Scores, m, l and O are fp32; P is
+// rounded to bf16 because the products take 16 bits (l sums it unrounded), the output to its type.
 //
-// 8-bit rows.  Four more warps turn the raw tile (e4m3 codes and exponent bytes, by TMA) into
-// the bf16 tile that the MMAs read.  Since the scale is a power of two the bf16 values are
-// exact: a code's fields are moved to those of a bf16 number and multiplied by 2^(120 + e).
+// Warps.  Two loaders take the ring's positions in turn (one, alone, is bound by issuing the copies of
+// 16-token pages: 64 requests x 8 rows over 8-bit pages took 808 us, two take 634), two warps issue
+// MMAs, the softmax has four warps a query tile, and 8-bit pages four more.
+//
+// 8-bit rows.  Those four warps turn the raw tile (e4m3 codes by TMA, the rows' exponents beside them
+// as fp16 multipliers) into the fp16 tile that the MMAs read, in units of the tile's largest power of
+// two 2^E.  A code has 4 bits of mantissa and fp16 11 and 2^-24 as its smallest step, so elements are
+// exact down to 2^-15 of the tile's largest row scale, and what lies under 2^-25 of it becomes zero.
+// K's E multiplies the softmax factor; V's goes into the exponent, P' = 2^(s c + E - m) with m the
+// running maximum of s c + E, so tiles of any E add up in one accumulator; l takes E back out.  The
+// query is made fp16 in shared memory, each row times the power of two that leaves it 15 bits of range.
+// fp16 rather than bf16: P' is rounded 8 times finer, and a code widens in one conversion.
+//
+// What bounds it.  Short pieces over bf16 pages: their bytes (64 requests x 18000 keys, 8 KV heads, d 128:
+// 661 us, 7.1 TB/s; with 8 rows each 686 us).  Over 8-bit pages: the conversion, and the shared memory
+// that it shares with the MMAs (634 us for half the bytes).  Prompts: the chain S -> softmax -> P V of a
+// tile (4096 rows on 8192 keys, 32 heads: 570 us, 1.2 PFLOP/s; the MMAs alone took 342 us).
 //
 // Split.  Work is the sequence of pairs (request, KV head, token block); a pair costs its
 // keys plus kStartKeys, and every CTA (one per SM) takes an equal share of the total, so long
@@ -38,7 +53,7 @@ struct ChunkCfg {
     static constexpr int NT = D == 256 ? 1 : 2;            // query tiles of a long piece
     static constexpr int NH = D == 256 ? 2 : 1;            // 128-column halves of d
     static constexpr int DH = D / NH;
-    static constexpr int kSlot = (DH / 64) * kCkSub;       // a half tile in bf16
+    static constexpr int kSlot = (DH / 64) * kCkSub;       // a half tile in 16 bits
     static constexpr int kRaw = kCkKeys * DH;              // and in codes
     static constexpr int kRawSlot = kRaw + 2 * kCkKeys;    // + the rows' multipliers
     // warps: 0 and 3 loaders, 1 and 2 MMA issuers, then warpgroups of softmax and converting warps
@@ -61,7 +76,7 @@ struct ChunkMisc {
 };
 
 // ------------------------------------------------------------------ small device helpers
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
+// D[tmem] (+)= A[tmem] * B[smem], bf16 or fp16 inputs, fp32 accumulate.
 __device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate)
 {
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     ChunkMisc *m = reinterpret_cast<ChunkMisc *>(smem + p.off_misc);
     const uint32_t bar0 = smem_u32(m->bars);
-    // bf16 tile slots (filled by TMA, or by the converting warps), raw slots
+    // 16-bit tile slots (filled by TMA, or by the converting warps), raw slots
     auto bar_full = [&](int s) { return bar0 + 8u * s; };
     auto bar_empty = [&](int s) { return bar0 + 8u * (8 + s); };
     auto bar_rfull = [&](int s) { return bar0 + 8u * (16 + s); };
@@ -887,7 +902,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 ++nml;
         }
     } else if (Q8 && warp >= Cfg::kConvWarp0) {
-        // ============================================================ codes -> bf16 tiles
+        // ============================================================ codes -> fp16 tiles
         // A thread takes 16 codes of one row at a time, its neighbours the rest of the row.
         if constexpr (Q8) {
             constexpr int CPR = DH / 16;                  // 16-code chunks a row
@@ -1088,7 +1103,8 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     const int misc = (int)(sizeof(ChunkMisc) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
-    // the loaders' ring has an even number of slots; four 16-bit slots beside four raw ones where they fit, else three
+    // The loaders' ring has an even number of slots.  8-bit pages: four 16-bit slots where four raw ones fit
+    // beside them, else three (d = 256, 32 blocks of 7: four and two 89 us, three and four 75).
     if (Q8) {
         p.nslot = room >= 4 * Cfg::kSlot + 4 * Cfg::kRawSlot ? 4 : 3;
         p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot) / 2 * 2;
