@@ -288,8 +288,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     if (warp == 0 || warp == 3) {
         // ============================================================ K / V loaders
         // Two warps, as issuing the copies of 16-token pages is what bounds a single one: the ring's
-        // positions (K and V of a tile, in halves for d = 256) are theirs in turn, and it has an even
-        // number of slots.  A warp runs its loop together: lane u looks after positions 4 u .. 4 u + 3
+        // positions (K and V of a tile, in halves for d = 256) are theirs in turn.  A warp runs its loop together: lane u looks after positions 4 u .. 4 u + 3
         // of a tile, which lie in one page, and the lane of a page's first positions loads the page.
         // What lies past the block's last visible key, and pages whose id is outside the pool, is
         // loaded from a page past the pool: TMA fills zeros.  Exponent bytes come by ordinary loads two
@@ -423,9 +422,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         // CTA's shared memory is given back; a fill that did not happen is not waited for
         if (lane == 0) {
             volatile int drain = 0;
-            const uint32_t per = nring / 2;       // this warp's slots
-            for (uint32_t x = fills > per ? fills - per : 0u; x < fills; ++x) {
-                const uint32_t sl = (2 * x + me) % nring, ph = (x / per) & 1u;
+            // Of this warp's positions 2 x + me, those that no later one has waited for: of its own, nring
+            // further on, or of the other warp's last.
+            const int32_t seen = 2 * ((int32_t)fills - 1) + (me == 0 && ok ? 1 : 0) - nring;
+            for (uint32_t x = seen < 0 ? 0u : (uint32_t)seen / 2 + 1; x < fills; ++x) {
+                const uint32_t sl = (2 * x + me) % nring, ph = ((2 * x + me) / nring) & 1u;
                 mbar_wait(Q8 ? bar_rfull(sl) : bar_full(sl), ph, &drain);
                 if (!Q8 && ok)
                     mbar_wait(bar_empty(sl), ph, abort_flag);
@@ -1103,16 +1104,15 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     const int misc = (int)(sizeof(ChunkMisc) + 127) / 128 * 128;
     p.off_ring = qbytes;
     const int room = kBudget - qbytes - misc;
-    // The loaders' ring has an even number of slots.  8-bit pages: four 16-bit slots where four raw ones fit
-    // beside them, else three (d = 256, 32 blocks of 7: four and two 89 us, three and four 75).
+    // 8-bit pages: four 16-bit slots where three raw ones fit beside them, else three
     if (Q8) {
-        p.nslot = room >= 4 * Cfg::kSlot + 4 * Cfg::kRawSlot ? 4 : 3;
-        p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot) / 2 * 2;
+        p.nslot = room >= 4 * Cfg::kSlot + 3 * Cfg::kRawSlot ? 4 : 3;
+        p.nraw = std::min(8, (room - p.nslot * Cfg::kSlot) / Cfg::kRawSlot);
         if (p.nraw >= 2)
             p.nslot = std::min(8, (room - p.nraw * Cfg::kRawSlot) / Cfg::kSlot);
     } else {
         p.nraw = 2;
-        p.nslot = std::min(8, room / Cfg::kSlot) / 2 * 2;
+        p.nslot = std::min(8, room / Cfg::kSlot);
     }
     if (p.nslot < 3 || p.nraw < 2)
         return SVP_EUNSUPPORTED;
