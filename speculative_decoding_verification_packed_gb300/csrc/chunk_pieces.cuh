@@ -54,6 +54,7 @@ struct ChunkPiece {
     int32_t off, k, L;                // the request's first packed row, rows, cached tokens
     int32_t tb0, ntok, len;           // first token and tokens of the block; keys it sees
     int32_t nt, t0, t1;               // its KV tiles, and those of this piece
+    int32_t wt;                       // cost of a key
     int64_t base;                     // cost before the pair
 };
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, ChunkPiece &s, int6
     s.len = s.L + s.tb0 + s.ntok;
     s.nt = (s.len + kCkKeys - 1) / kCkKeys;
     s.t0 = t0;
-    const int32_t wt = ck_weight<NT>(s.k, p.R);
+    const int32_t wt = s.wt;
     const int64_t y = v1 - s.base;
     s.t1 = y >= (int64_t)wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, wt));
     return s.t0 < s.t1;
@@ -121,6 +122,7 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
     if (s.k <= 0 || ck_bad(p, s.off, end, s.L))
         return false;
     s.nb = (s.k + B - 1) / B;
+    s.wt = ck_weight<NT>(s.k, p.R);
     return true;
 }
 
@@ -128,7 +130,7 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
 template <int NT>
 __device__ __forceinline__ bool ck_next(const ChunkParams &p, ChunkPiece &s, int64_t v1)
 {
-    s.base += (int64_t)ck_weight<NT>(s.k, p.R) * (kStartKeys + (int64_t)s.len);
+    s.base += (int64_t)s.wt * (kStartKeys + (int64_t)s.len);
     if (s.base >= v1)
         return false;
     if (++s.b == s.nb) {
@@ -162,7 +164,7 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
     }
     s.i = lo;
     ck_request<NT>(p, s);
-    const int32_t wt = ck_weight<NT>(s.k, p.R);
+    const int32_t wt = s.wt;
     const int64_t H = ck_head_keys(s.L, s.k, B) * wt;
     int64_t rem = v0 - prefix[lo];
     s.g = min((int32_t)((float)rem / (float)H), p.c.hkv - 1);

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
             }
             if (!whole && s.t0 == 0 && tid == 0) {
                 ChunkDesc d;
-                d.np = ck_owner(shares, s.base + (int64_t)ck_weight<1>(s.k, p.R) * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
+                d.np = ck_owner(shares, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                 d.row0 = s.off + s.tb0;
                 d.ntok = s.ntok;
                 d.g = s.g;

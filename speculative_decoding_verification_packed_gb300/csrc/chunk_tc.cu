@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (!whole && s.t0 == 0 && a == 0 && r == 0) {
                     // this CTA has the pair's first piece: CTAs up to the owner of its last tile have the rest
                     ChunkDesc d;
-                    d.np = ck_owner(shares, s.base + (int64_t)ck_weight<NT>(s.k, p.R) * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
+                    d.np = ck_owner(shares, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                     d.row0 = s.off + s.tb0;
                     d.ntok = s.ntok;
                     d.g = s.g;
