@@ -678,26 +678,32 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 if (live) {
                     const uint32_t line = sbase + a * (D / 64) * p.qsub + r * 128;
                     uint32_t top = 0;
+                    // (32 columns at a time: all reads, then what is done with them)
 #pragma unroll 1
                     for (int pass = 0; pass < 2; ++pass) {
                         const int32_t up = 141 - (int32_t)(top >> 7);    // 2^14 over the largest (bf16 bits in top)
                         const int32_t shift = top < 128u ? 0 : max(-100, min(up, 100));
                         const float f = ck_pow2(shift);
-#pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x) {
-                            const uint32_t at = line + (x >> 3) * p.qsub + (((x & 7) ^ (r & 7)) << 4);
-                            const int4 w = ld_shared_i4(at);
-                            const uint32_t v[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
-                            if (pass == 0) {
+#pragma unroll 1
+                        for (int x = 0; x < D / 8; x += 4) {
+                            int4 w[4];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    top = max(top, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
-                            } else {
-                                uint32_t u[4];
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = ld_shared_i4(line + (x >> 3) * p.qsub + ((((x & 7) + y) ^ (r & 7)) << 4));
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    u[y] = ck_pack_f16x2(bf16_lo(v[y]) * f, bf16_hi(v[y]) * f);
-                                st_shared_v4(at, u[0], u[1], u[2], u[3]);
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t v[4] = {(uint32_t)w[y].x, (uint32_t)w[y].y, (uint32_t)w[y].z, (uint32_t)w[y].w};
+                                if (pass == 0) {
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z)
+                                        top = max(top, max(v[z] & 0x7fffu, (v[z] >> 16) & 0x7fffu));
+                                } else {
+                                    uint32_t u[4];
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z)
+                                        u[z] = ck_pack_f16x2(bf16_lo(v[z]) * f, bf16_hi(v[z]) * f);
+                                    st_shared_v4(line + (x >> 3) * p.qsub + ((((x & 7) + y) ^ (r & 7)) << 4), u[0], u[1], u[2], u[3]);
+                                }
                             }
                         }
                         if (pass == 1)
@@ -993,7 +999,7 @@ constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p, int32_t part_rows)
 {
-    constexpr int E = D / 32;                             // columns a lane
+    constexpr int V = D == 64 ? 2 : 4, E = D / 32;        // columns a lane: E, V of them side by side in a group of 32 V
     griddep_launch_dependents();
     griddep_wait();
     const int32_t c = blockIdx.x, lane = threadIdx.x & 31;
@@ -1030,13 +1036,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
             for (int32_t q = 0; q < cnt; ++q) {
                 const float wq = __shfl_sync(0xffffffffu, w, q);
                 L += __shfl_sync(0xffffffffu, wl, q);
-                const float *o = p.part_o + at(q0 + q) * D + lane * E;
+                const float *o = p.part_o + at(q0 + q) * D + lane * V;
                 float x[E];
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(o + e));
-                    x[e] = v.x;
-                    x[e + 1] = v.y;
+                for (int e = 0; e < E; e += V) {
+                    if constexpr (V == 2) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(o + 32 * e));
+                        x[e] = v.x;
+                        x[e + 1] = v.y;
+                    } else {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 32 * e));
+                        x[e] = v.x;
+                        x[e + 1] = v.y;
+                        x[e + 2] = v.z;
+                        x[e + 3] = v.w;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e)
@@ -1045,10 +1059,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
         }
         const float inv = 1.0f / L;
         const int64_t orow = (int64_t)(d.row0 + tok) * p.hq + d.g * p.G + h;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * E);
+        uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * V;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        for (int e = 0; e < E; e += V) {
+            const uint32_t lo = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+            if constexpr (V == 2)
+                *reinterpret_cast<uint32_t *>(dst) = lo;
+            else
+                *reinterpret_cast<uint2 *>(dst + 32 * e) =
+                    make_uint2(lo, pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
+        }
         if (lane == 0 && p.lse)
             p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
     }
@@ -1083,8 +1103,8 @@ svp_status chunk_short_run(ChunkParams &p, int32_t d, cudaStream_t stream);
 template <int D>
 static svp_status chunk_join(const ChunkParams &p, int32_t part_rows, cudaStream_t stream)
 {
-    const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most; two a warp
-    const unsigned y = (unsigned)std::max(1, (rows + 2 * kJoinWarps - 1) / (2 * kJoinWarps));
+    const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most; one a warp
+    const unsigned y = (unsigned)std::max(1, (rows + kJoinWarps - 1) / kJoinWarps);
     return launch_pdl(chunk_join_kernel<D>, dim3(sm_count(), y), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
                    cudaSuccess
                ? SVP_OK
