@@ -11,11 +11,10 @@ constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
 // Cost of starting a pair, in keys.  A prompt of 4096 tokens and 24 blocks of 8 among two prompts of 2048
 // (8-bit) took 182 and 354 us with 64, 149 and 349 with 256, 151 and 344 with 512.
 constexpr int kStartKeys = 256;
-// Cost of a key with one query tile, and with two: 3 to 4 took 341 us on those blocks and prompts, 2 to 3
-// 356, 1 to 1 361 (calls of one kind are indifferent).
+// Cost of a key with one query tile, and with two: when 3 to 4 took 341 us on those blocks and prompts, 2 to
+// 3 took 356 and 1 to 1 361 (calls of one kind are indifferent).
 constexpr int kShortCost = 3, kLongCost = 4;
-// Smallest share of a CTA, more than a tile's cost and a multiple of 128: a shorter one is not worth its
-// join.  One token over 500 keys 14.6 us, with 2048 16.5.
+// Smallest share of a CTA, more than a tile's cost: a shorter one is not worth its join.  One token over 500 keys 14.6 us, with 2048 16.5.
 constexpr int kShareCost = 640;
 constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
 
@@ -167,15 +166,8 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
     const int32_t wt = s.wt;
     const int64_t H = ck_head_keys(s.L, s.k, B) * wt;
     int64_t rem = v0 - prefix[lo];
-    s.g = min((int32_t)((float)rem / (float)H), p.c.hkv - 1);
+    s.g = (int32_t)(rem / H);
     rem -= s.g * H;
-    if (rem < 0) {                    // (the quotient is off by one at most)
-        --s.g;
-        rem += H;
-    } else if (rem >= H) {
-        ++s.g;
-        rem -= H;
-    }
     // last block with cost before it <= rem: the root of B/2 b^2 + (a + B/2) b = rem / wt, put right
     const int64_t a = (int64_t)kStartKeys + s.L;
     const float h = (float)a + 0.5f * B;
@@ -194,8 +186,7 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
 }
 
 // CTA c of ncta has the costs [c, c + 1) x share; ncta shares hold the total, and a share (but the last)
-// more than a tile.  Quotients are fp32 ones put right: a 64-bit division in each kind of warp is code
-// that the instruction cache misses (300 requests x 3 rows x 200 keys took 39.0 us with them, 37.3 without).
+// more than a tile.
 struct ChunkShares {
     int64_t total, share;
     int32_t ncta;
@@ -205,20 +196,15 @@ __device__ __forceinline__ ChunkShares ck_shares(int64_t total)
 {
     ChunkShares x;
     x.total = total;
-    const uint32_t most = (uint32_t)min(total / 128, (int64_t)1 << 30) / (kShareCost / 128);
-    x.ncta = max(1, min((int32_t)gridDim.x, (int32_t)most));
-    x.share = (int64_t)((float)total / (float)x.ncta * (1.0f + 0x1p-20f)) + 1;
+    x.ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
+    x.share = max((int64_t)1, (total + x.ncta - 1) / x.ncta);
     return x;
 }
 
 // The CTA that owns the tile that starts at cost u < total.
 __device__ __forceinline__ int32_t ck_owner(const ChunkShares &x, int64_t u)
 {
-    int32_t c = (int32_t)((float)u / (float)x.share);
-    while (c > 0 && c * x.share > u)
-        --c;
-    while ((c + 1) * x.share <= u)
-        ++c;
+    const int32_t c = (int32_t)(u / x.share);
     return c;
 }
 
