@@ -47,6 +47,35 @@ struct ChunkParams {
     int32_t Rb, qsub;                 // tokens of a query box: min(R, w); bytes of its [rows][64] blocks
 };
 
+// One CTA an SM.  A dependent of the previous kernel starts 3 us earlier, but its CTAs go to SMs as these
+// fall free, and where neighbours land matters: a CTA with long pieces that shares a TPC with one with
+// short pieces takes 12% longer.  So chunk_tc.cu is launched as a dependent in clusters of two, which
+// keep neighbours on one TPC (blocks among prompts over 8-bit pages, back to back: 375 us without
+// clusters, 322 with; no dependent 327), and chunk_short.cu, which clusters do not help, as one only
+// when the call may be short (see there).
+inline cudaError_t launch_ctas(void (*kernel)(ChunkParams), int ctas, int threads, size_t smem, cudaStream_t stream,
+                               const ChunkParams &p, bool dependent, bool pairs)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if (dependent) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (pairs) {                          // (clusters of one are placed otherwise than no clusters)
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // ------------------------------------------------------------------ the sequence of pairs
 struct ChunkPiece {
     int32_t i, g, b, nb;              // request, KV head, token block, blocks of the request

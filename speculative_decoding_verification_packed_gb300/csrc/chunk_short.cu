@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         set_status(p.status, SVP_DEV_TIMEOUT);
 }
 
-int sm_count();
+int chunk_ctas();
 
 template <int D, int NB>
 static svp_status short_launch(ChunkParams &p, cudaStream_t stream)
@@ -493,8 +493,11 @@ static svp_status short_launch(ChunkParams &p, cudaStream_t stream)
     static std::atomic<uint64_t> configured{0};
     if (set_smem_limit_once(chunk_short_kernel<D, NB>, kBudget, configured) != cudaSuccess)
         return SVP_ECUDA;
-    return launch_pdl(chunk_short_kernel<D, NB>, dim3(sm_count()), dim3(kShThreads), (size_t)(p.off_misc + misc), stream,
-                      p) == cudaSuccess
+    // Back to back, 64 requests x 18000 keys (2.3 GB) take 365 us as dependents and 349 otherwise: 3 us earlier
+    // do not pay from 0.4 GB on.  The host knows the block table's room only.
+    const bool small = (int64_t)p.n * p.c.hkv * ((int64_t)p.c.max_pages << p.c.page_shift) * (2 * D) < ((int64_t)400 << 20);
+    return launch_ctas(chunk_short_kernel<D, NB>, chunk_ctas(), kShThreads, (size_t)(p.off_misc + misc), stream, p, small,
+                       false) == cudaSuccess
                ? SVP_OK
                : SVP_ECUDA;
 }

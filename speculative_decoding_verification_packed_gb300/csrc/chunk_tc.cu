@@ -1079,6 +1079,8 @@ int sm_count();
 bool encode_tiled(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *base, int rank,
                   const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box);
 
+int chunk_ctas() { return sm_count() & ~1; }              // (pairs)
+
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct ChunkWs {
@@ -1087,7 +1089,7 @@ struct ChunkWs {
 
 static ChunkWs chunk_ws(int32_t d)
 {
-    const size_t g = (size_t)sm_count(), rows = d == 256 ? 128 : 256;
+    const size_t g = (size_t)chunk_ctas(), rows = d == 256 ? 128 : 256;
     ChunkWs w;
     w.desc = kWsHeader;
     w.ml = up256(w.desc + g * sizeof(ChunkDesc));
@@ -1105,7 +1107,7 @@ static svp_status chunk_join(const ChunkParams &p, int32_t part_rows, cudaStream
 {
     const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most; one a warp
     const unsigned y = (unsigned)std::max(1, (rows + kJoinWarps - 1) / kJoinWarps);
-    return launch_pdl(chunk_join_kernel<D>, dim3(sm_count(), y), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
+    return launch_pdl(chunk_join_kernel<D>, dim3(chunk_ctas(), y), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
                    cudaSuccess
                ? SVP_OK
                : SVP_ECUDA;
@@ -1142,8 +1144,8 @@ static svp_status chunk_run(ChunkParams &p, cudaStream_t stream)
     static std::atomic<uint64_t> configured{0};
     if (set_smem_limit_once(chunk_tc_kernel<D, Q8>, kBudget, configured) != cudaSuccess)
         return SVP_ECUDA;
-    const int grid = sm_count();
-    if (launch_pdl(chunk_tc_kernel<D, Q8>, dim3(grid), dim3(Cfg::kThreads), (size_t)smem, stream, p) != cudaSuccess)
+    if (launch_ctas(chunk_tc_kernel<D, Q8>, chunk_ctas(), Cfg::kThreads, (size_t)smem, stream, p, true, true) !=
+        cudaSuccess)
         return SVP_ECUDA;
     return chunk_join<D>(p, Cfg::kPartRows, stream);
 }
