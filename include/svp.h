@@ -43,7 +43,7 @@
  *     sets SVP_DEV_TIMEOUT in the status word and returns.
  *   - The DVL allocator, the row gathers, the verification attention, the margin /
  *     accept calls, the stochastic verifier's second pass, the cache's write and read
- *     and the chunk attention (with the kernel that joins its parts) are launched as
+ *     and the chunk attention (unless the call may be a long one) are launched as
  *     programmatic dependents of the previous kernel on their stream: they may be
  *     scheduled while it finishes, but read nothing before it has completed, so the
  *     results are those of plain stream order (also inside a captured CUDA graph).

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
     const int32_t nr = min(p.rpb, p.rows - r0), hkv = p.c.hkv, cols = 2 * hkv;
     const int gl = p.d >> 4;
     const int grp = threadIdx.x / gl, lane = threadIdx.x - grp * gl, ngrp = kCacheThreads / gl;
-    // one item a group in flight: more blocks fit (with two, 66 K rows took 37 us instead of 33)
+    // one item a group in flight: more blocks fit (with two, 159 MB of prompts took 37 us instead of 33)
     uint32_t raw[kWords<TIn>];
     CacheItem at{0, 0};
     at.skip(grp, cols);
