@@ -494,7 +494,8 @@ svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const in
  *
  * Precision.  Scores, the softmax's maximum and sum, and the output are accumulated in fp32; the
  * probabilities that multiply V are rounded to bf16 over SVP_BF16 pages and to fp16 over SVP_E4M3
- * ones (not at all in fp32).  8-bit rows with hq / hkv * w <= 16 and d <= 128 are used as they are;
+ * ones (not at all in fp32), where one (times its value row's power of two) below 2^-21 of the
+ * row's largest has fewer digits and one below 2^-32 counts in the sum only.  8-bit rows with hq / hkv * w <= 16 and d <= 128 are used as they are;
  * otherwise 128 positions (a tile) at a time in units of their largest power of two 2^E (of K and
  * of V each, of visible rows, at least 2^-60): exact for rows within 2^15 of it, and an element below
  * 2^(E - 25) counts as 0.  8-bit value rows of one request should have powers of two within 2^100 of

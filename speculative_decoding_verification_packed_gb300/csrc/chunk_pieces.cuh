@@ -16,11 +16,14 @@ constexpr int kStartKeys = 256;
 constexpr int kShortCost = 3, kLongCost = 4;
 // Smallest share of a CTA, more than a tile's cost: a shorter one is not worth its join.  One token over 500 keys 14.6 us, with 2048 16.5.
 constexpr int kShareCost = 640;
-constexpr float kCkSlack = 8.0f;      // exponents of P stay below 2^8 above the reference
+constexpr float kCkSlack = 8.0f;      // P stays below 2^8 times its value at the reference
+// P in fp16 (8-bit pages) is 2^7 at the reference: with the slack it stays below 2^15, and what fp16 cannot
+// hold (digits under 2^-24) is 2^-31 of the row's largest probability, so that a million keys lose no weight.
+constexpr float kCkLift = 7.0f;
 
 // Query rows of a KV head up to which 8-bit pages take chunk_short.cu.  64 requests x 18000 keys, 8 KV heads,
 // d 128, 4 and 16 rows: 362 and 470 us there, 640 and 643 in chunk_tc.cu (d 64, 2 and 16 rows: 333 and 360
-// against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 634 in chunk_tc.cu.
+// against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 644 in chunk_tc.cu.
 constexpr int kShortRows = 16;
 
 struct ChunkDesc {                    // a pair that was split: read by the joining kernel

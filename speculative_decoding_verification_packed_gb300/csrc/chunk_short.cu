@@ -21,8 +21,8 @@
 // the product's half i.  P^T turns from accumulator to operand by movmatrix.
 // An 8-bit row's power of two multiplies its row of S^T; V's goes into the exponent,
 //   P' = 2^(s c + e_key - m),  O += P' codes,  l += P' 2^-e_key,
-// with m the running maximum of s c + e_key, so that P' stays within fp16 whatever the exponents (it is
-// rounded to fp16 because the products take 16 bits; scores, m, l and O are fp32).
+// with m the running maximum of s c + e_key (less kCkLift), so that P' stays within fp16 whatever the
+// exponents (it is rounded to fp16 because the products take 16 bits; scores, m, l and O are fp32).
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
 #include <algorithm>
 #include <cstring>
@@ -34,7 +34,6 @@ namespace svp {
 constexpr int kShWarps = 8;           // computing warps; then a K and a V loader
 constexpr int kShThreads = 32 * (kShWarps + 2);
 constexpr int kShSlots = 16;          // ring slots at most
-constexpr float kShSlack = 8.0f;
 
 struct ShortMisc {
     uint64_t bars[2 * kShSlots];
@@ -330,12 +329,13 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                         top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w2));
                         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w2));
                     }
-                    const bool up0 = top[0] > mx[nb][0] + kShSlack || (mx[nb][0] == -INFINITY && top[0] != -INFINITY);
-                    const bool up1 = top[1] > mx[nb][1] + kShSlack || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
+                    // (mx: the reference, the largest score less kCkLift when it last moved)
+                    const bool up0 = top[0] > mx[nb][0] + (kCkSlack + kCkLift) || (mx[nb][0] == -INFINITY && top[0] != -INFINITY);
+                    const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
                     if (__any_sync(0xffffffffu, up0 || up1)) {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const float mn = fmaxf(mx[nb][x], top[x]);
+                            const float mn = fmaxf(mx[nb][x], top[x] - kCkLift);
                             const float alpha = mx[nb][x] == -INFINITY ? 0.0f : fast_exp2(mx[nb][x] - mn);
                             mx[nb][x] = mn;
                             l[nb][x] *= alpha;

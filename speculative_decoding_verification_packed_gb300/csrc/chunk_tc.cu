@@ -18,7 +18,7 @@
 // rounded to bf16 because the products take 16 bits (l sums it unrounded), the output to its type.
 //
 // Warps.  Two loaders take the ring's positions in turn (one, alone, is bound by issuing the copies of
-// 16-token pages: 64 requests x 8 rows over 8-bit pages took 808 us, two take 634), two warps issue
+// 16-token pages: 64 requests x 8 rows over 8-bit pages took 808 us, two 634), two warps issue
 // MMAs, the softmax has four warps a query tile, and 8-bit pages four more.
 //
 // 8-bit rows.  Those four warps turn the raw tile (e4m3 codes by TMA, the rows' exponents beside them
@@ -28,12 +28,13 @@
 // K's E multiplies the softmax factor; V's goes into the exponent, P' = 2^(s c + E - m) with m the
 // running maximum of s c + E, so tiles of any E add up in one accumulator; l takes E back out.  The
 // query is made fp16 in shared memory, each row times the power of two that leaves it 15 bits of range.
-// fp16 rather than bf16: P' is rounded 8 times finer, and a code widens in one conversion.
+// fp16 rather than bf16: P' is rounded 8 times finer, and a code widens in one conversion.  What fp16 lacks
+// in range is made up by the units (above) and by P' = 2^7 at the reference.
 //
 // What bounds it.  Short pieces over bf16 pages: their bytes (64 requests x 18000 keys, 8 KV heads, d 128:
 // 661 us, 7.1 TB/s; with 8 rows each 686 us).  Over 8-bit pages: the conversion, and the shared memory
-// that it shares with the MMAs (634 us for half the bytes).  Prompts: the chain S -> softmax -> P V of a
-// tile (4096 rows on 8192 keys, 32 heads: 573 us, 1.2 PFLOP/s, 8-bit pages 635; the MMAs alone 342 us).
+// that it shares with the MMAs (8 rows each 644 us for half the bytes).  Prompts: the chain S -> softmax -> P V of a
+// tile (4096 rows on 8192 keys, 32 heads: 570 us, 1.2 PFLOP/s, 8-bit pages 642; the MMAs alone 342 us).
 //
 // Split.  Work is the sequence of pairs (request, KV head, token block); a pair costs its
 // keys plus kStartKeys, and every CTA (one per SM) takes an equal share of the total, so long
@@ -747,9 +748,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                             e_first = ev;
                     }
                     const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * ct + ev;
-                    // the reference moves when a score lies more than 2^8 above it (or there is none yet)
-                    if (__any_sync(0xffffffffu, live && (tmax > m_ref + kCkSlack || (m_ref == -INFINITY && tmax != m_ref)))) {
-                        const float m_new = fmaxf(m_ref, tmax);
+                    // the reference moves when a score lies more than 2^8 above it (or there is none yet); it is
+                    // the largest score less kLift
+                    constexpr float kLift = Q8 ? kCkLift : 0.0f;
+                    if (__any_sync(0xffffffffu,
+                                   live && (tmax > m_ref + (kCkSlack + kLift) || (m_ref == -INFINITY && tmax != m_ref)))) {
+                        const float m_new = fmaxf(m_ref, tmax - kLift);
                         if (done > 0) {
                             const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - m_new);
                             if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
@@ -787,8 +791,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             const bool both = !kMono && !lng && nt > 1;   // two accumulators of one query tile
             float o_scale = 1.0f;                         // O and m in units of 1 from here on
             if constexpr (Q8) {
-                o_scale = ck_pow2((int32_t)e_first);
-                m_ref -= e_first;
+                o_scale = ck_pow2((int32_t)(e_first - kCkLift));
+                l *= ck_pow2(-(int32_t)kCkLift);
+                m_ref += kCkLift - e_first;
                 ntile += (uint32_t)nt;
             }
             if (both && a == 1) {

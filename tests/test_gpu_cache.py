@@ -681,6 +681,40 @@ def test_rows_of_very_different_sizes_in_one_tile(d, rows):
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_tail_under_one_large_score(rows, kind):
+    """The first key is 2^26 times as probable as each of the others and its value is zero: what comes
+    out is the others'.  A probability over 8-bit pages is off by 2^-11 relative, or below 2^-21 of the
+    largest by 2^-32 of it, here 2^-6 of the others' own; over bf16 pages by 2^-8.  More heads than
+    CTAs, so that most of them see all their keys in one piece."""
+    T, d, page, hkv, hq = 3000, 64, 128, 304, 608
+    pages = -(-T // page)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    k = torch.zeros(pages, hkv, page, d, device="cuda", dtype=BF16)
+    v = torch.randint(1, 4, (pages, hkv, page, d), device="cuda", generator=g).to(BF16)
+    k[0, :, 0, 0] = 26.0                  # (an e4m3 value)
+    v[0, :, 0] = 0
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None].contiguous()
+    if kind == E4M3:
+        exps = torch.full((pages, hkv, page), 127, dtype=torch.uint8, device="cuda")
+        cache = svp.make_cache(k.to(E4M3), v.to(E4M3), table, k_exp=exps, v_exp=exps.clone())
+    else:
+        cache = svp.make_cache(k, v, table)
+    q = torch.zeros(rows, hq, d, device="cuda", dtype=BF16)
+    q[..., 0] = 1.0                       # with this scale, a score of 26 is a factor of 2^26
+    out, lse = svp.chunk_attn(q, i32([T - rows]), i32([0, rows]), cache=cache, scale=math.log(2.0))
+    values = v.double().transpose(0, 1).reshape(hkv, pages * page, d)
+    for j in sorted({0, rows - 1}):
+        n = T - rows + j + 1
+        l = 1.0 + (n - 1) * 2.0 ** -26
+        y = (values[:, 1:n].sum(1) * 2.0 ** -26 / l).repeat_interleave(hq // hkv, 0)
+        steps = 26 * 2.0 ** -22 + (n / 32 + 64) * 2.0 ** -23
+        rel = (2.0 ** -8 if kind == BF16 else 2.0 ** -6 + 2.0 ** -11) + steps + 2.0 ** -8
+        assert ((out[j].double() - y).abs() <= rel * y).all(), float(((out[j].double() - y).abs() / y).max())
+        assert (lse[j].double() - (26 * math.log(2.0) + math.log(l))).abs().max() <= steps + 18.1 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
 @pytest.mark.parametrize("rows", [1, 50])
 def test_output_on_a_16_byte_boundary(kind, rows):
     pool = Pool(1, [300], 2, 128, 16, kind, seed=26)
