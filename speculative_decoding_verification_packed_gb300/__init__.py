@@ -233,8 +233,9 @@ class Workspace:
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
         # (zeroed: the leading bytes that the entry point wants zeroed; None for all of them)
-        _check(lib().svp_workspace_init(self.ptr, self.nbytes if zeroed is None else zeroed, _stream(stream)),
-               "svp_workspace_init")
+        if zeroed != 0:
+            _check(lib().svp_workspace_init(self.ptr, self.nbytes if zeroed is None else zeroed, _stream(stream)),
+                   "svp_workspace_init")
 
     @property
     def ptr(self) -> int:
@@ -755,9 +756,10 @@ _chunk_ws: dict = {}
 def _chunk_workspace(hq: int, cache: svp_cache, dtype, raw: int) -> Workspace:
     """The scratch of chunk_attn calls that bring none: one for each stream, as calls on two
     streams may overlap; a call that is being captured gets its own, which lives in the graph's
-    memory, as graphs may be replayed on any stream."""
+    memory, as graphs may be replayed on any stream (and is not zeroed, as its status word, which
+    kernels only add bits to, is out of reach)."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, zeroed=256)
+        return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, zeroed=0)
     key = (raw, cache.index, cache.d, dtype)
     ws = _chunk_ws.get(key)
     if ws is None:
