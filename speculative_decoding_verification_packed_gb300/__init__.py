@@ -642,23 +642,23 @@ def _rows(t, name: str, heads: int, cache: svp_cache) -> int:
     if h != heads or e != d:
         raise ValueError(f"{name} must be [rows, {heads}, {d}]")
     s0, s1, s2 = t.stride()
-    if t.device != cache.device or s2 != 1 or (heads > 1 and s1 != d):
+    if t.get_device() != cache.index or s2 != 1 or (heads > 1 and s1 != d):
         raise ValueError(f"{name} needs contiguous rows (any row stride) on the cache's device")
     return s0 if m > 1 else heads * d
 
 
-def _i32(t, name: str, count: int, device) -> int:
+def _i32(t, name: str, count: int, cache: svp_cache) -> int:
     """Address of a contiguous int32 vector of at least ``count`` entries (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.shape[0] < count:
+    if t.dtype is not torch.int32 or t.get_device() != cache.index or not t.is_contiguous() or t.numel() < count:
         raise ValueError(f"{name} must be {count} or more contiguous int32 values on the cache's device")
     return t.data_ptr()
 
 
 def _requests(cu, cache: svp_cache, name: str) -> int:
     """Number of requests of cu [n+1]."""
-    n = cu.shape[0] - 1
+    n = cu.numel() - 1
     if n < 0 or n > cache.max_n:
         raise ValueError(f"{name} must have 1..{cache.max_n + 1} entries (rows of the block table)")
     if cache.index != torch._C._cuda_getDevice():
@@ -695,15 +695,14 @@ def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
     fine) at positions ctx_len[i] + j of their requests (svp_cache_write).  take [n] int32:
     only the first take[i] rows of request i, e.g. the accept_len of margin_accept."""
     n = _requests(cu_slots, cache, "cu_slots")
-    dev = cache.device
     stride = _rows(k, "k", cache.hkv, cache)
-    if k.dtype != v.dtype or k.shape != v.shape or _rows(v, "v", cache.hkv, cache) != stride:
+    if k.dtype is not v.dtype or _rows(v, "v", cache.hkv, cache) != stride or k.numel() != v.numel():
         raise ValueError("k and v need one shape, type and row stride")
     if ws is None:
         ws = _cache_workspace(cache, stream)
     st = lib().svp_cache_write(
-        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref, _i32(ctx_len, "ctx_len", n, dev),
-        _i32(cu_slots, "cu_slots", n + 1, dev), _i32(take, "take", n, dev), n, k.shape[0], cache.hkv,
+        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref, _i32(ctx_len, "ctx_len", n, cache),
+        _i32(cu_slots, "cu_slots", n + 1, cache), _i32(take, "take", n, cache), n, k.shape[0], cache.hkv,
         cache.d, ws.ptr, ws.nbytes, _raw_stream(stream, cache))
     if st:
         raise SvpError(st, "svp_cache_write")
@@ -734,7 +733,7 @@ def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
     if ws is None:
         ws = _cache_workspace(cache, stream)
     st = lib().svp_cache_read(
-        cache.ref, _i32(start, "start", n, dev), _i32(cu_rows, "cu_rows", n + 1, dev), n, k_out.shape[0],
+        cache.ref, _i32(start, "start", n, cache), _i32(cu_rows, "cu_rows", n + 1, cache), n, k_out.shape[0],
         cache.hkv, cache.d, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.ptr, ws.nbytes,
         _raw_stream(stream, cache))
     if st:
@@ -801,7 +800,7 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
     if ws is None:
         ws = _chunk_workspace(hq, cache, q.dtype, raw)
     st = lib().svp_chunk_attn(
-        q.data_ptr(), stride, cache.ref, _i32(ctx_len, "ctx_len", n, dev), _i32(cu_slots, "cu_slots", n + 1, dev),
+        q.data_ptr(), stride, cache.ref, _i32(ctx_len, "ctx_len", n, cache), _i32(cu_slots, "cu_slots", n + 1, cache),
         n, m_cap, (m_cap or 1) if w is None else w, svp_heads(hq, hkv, d, scale), _dtype_code(q), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, raw)
     if st:
