@@ -196,6 +196,45 @@ __device__ __forceinline__ float ck_row_exp(uint32_t ts, int32_t kmax, float cl2
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// The same of an unmasked tile in one reading, with a reference from before: if every live row's sum stays
+// within limit (it does not with no reference, -inf, nor with NaN), P is stored, else nothing is and the
+// scores are still there.
+template <bool F16>
+__device__ __forceinline__ bool ck_row_once(uint32_t ts, float cl2, float m, float limit, bool live, float &sum)
+{
+    const uint64_t c2 = f32x2_pack(cl2, cl2), nm2 = f32x2_pack(-m, -m);
+    uint64_t acc[2] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f)};
+    uint32_t p0[32], p1[32];
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t sv[2][32];
+        tmem_ld32(ts + half * 64, sv[0]);
+        tmem_ld32(ts + half * 64 + 32, sv[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const int k0 = 2 * e;
+            float y0, y1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[k0 >> 5][k0 & 31]),
+                                              __uint_as_float(sv[k0 >> 5][(k0 & 31) + 1])), c2, nm2), y0, y1);
+            y0 = fast_exp2(y0);
+            y1 = fast_exp2(y1);
+            p0[e] = p1[e];
+            p1[e] = F16 ? ck_pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
+            acc[e & 1] = f32x2_add(acc[e & 1], f32x2_pack(y0, y1));
+        }
+    }
+    float s[4];
+    f32x2_unpack(acc[0], s[0], s[1]);
+    f32x2_unpack(acc[1], s[2], s[3]);
+    sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if (!__all_sync(0xffffffffu, !live || sum <= limit))
+        return false;
+    tmem_st32(ts, p0);
+    tmem_st32(ts + 32, p1);
+    return true;
+}
+
 // 32 bytes, a whole sector, in one store (16-byte ones of a row leave half sectors).
 __device__ __forceinline__ void ck_store8(void *at, const uint32_t *x)
 {
@@ -747,35 +786,41 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                         if (done == 0)
                             e_first = ev;
                     }
-                    const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * ct + ev;
-                    // the reference moves when a score lies more than 2^8 above it (or there is none yet); it is
-                    // the largest score less kLift
-                    constexpr float kLift = Q8 ? kCkLift : 0.0f;
-                    if (__any_sync(0xffffffffu,
-                                   live && (tmax > m_ref + (kCkSlack + kLift) || (m_ref == -INFINITY && tmax != m_ref)))) {
-                        const float m_new = fmaxf(m_ref, tmax - kLift);
-                        if (done > 0) {
-                            const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - m_new);
-                            if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
-                                break;
-                            pv_seen = true;
-                            tc_fence_after();
+                    // Without a mask, and with a reference that still holds, the scores are read once: where the
+                    // registers hold a row's P (4096 rows on 8192 keys 570 -> 520 us)
+                    constexpr bool kOnce = !Q8;
+                    float sum = 0.0f;
+                    if (!kOnce || masked || done == 0 || !ck_row_once<Q8>(ts, ct, m_ref - ev, 32768.0f, live, sum)) {
+                        const float tmax = (masked ? ck_row_max<true>(ts, kmax) : ck_row_max<false>(ts, kmax)) * ct + ev;
+                        // the reference moves when a score lies more than 2^8 above it (or there is none yet); it is
+                        // the largest score less kLift
+                        constexpr float kLift = Q8 ? kCkLift : 0.0f;
+                        if (__any_sync(0xffffffffu,
+                                       live && (tmax > m_ref + (kCkSlack + kLift) || (m_ref == -INFINITY && tmax != m_ref)))) {
+                            const float m_new = fmaxf(m_ref, tmax - kLift);
+                            if (done > 0) {
+                                const float alpha = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - m_new);
+                                if (!pv_seen && !(ok = wait_all(bar_pv(buf ^ 1), (ns_[buf ^ 1] - 1) & 1u)))
+                                    break;
+                                pv_seen = true;
+                                tc_fence_after();
 #pragma unroll 1
-                            for (int cc = 0; cc < D / 32; ++cc) {
-                                uint32_t ov[32];
-                                tmem_ld32(to + cc * 32, ov);
-                                tmem_wait_ld();
+                                for (int cc = 0; cc < D / 32; ++cc) {
+                                    uint32_t ov[32];
+                                    tmem_ld32(to + cc * 32, ov);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                tmem_st32(to + cc * 32, ov);
+                                    for (int e = 0; e < 32; ++e)
+                                        ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                    tmem_st32(to + cc * 32, ov);
+                                }
+                                l *= alpha;
                             }
-                            l *= alpha;
+                            m_ref = m_new;
                         }
-                        m_ref = m_new;
+                        const float mm = (m_ref == -INFINITY ? 0.0f : m_ref) - ev;
+                        sum = masked ? ck_row_exp<true, Q8>(ts, kmax, ct, mm) : ck_row_exp<false, Q8>(ts, kmax, ct, mm);
                     }
-                    const float mm = (m_ref == -INFINITY ? 0.0f : m_ref) - ev;
-                    const float sum = masked ? ck_row_exp<true, Q8>(ts, kmax, ct, mm) : ck_row_exp<false, Q8>(ts, kmax, ct, mm);
                     l += Q8 ? sum * ck_pow2((int32_t)(e_first - ev)) : sum;
                     tmem_wait_st();
                 }
