@@ -14,7 +14,8 @@
 //   * d = 256: O fills the TMEM that a second tile would need, so one warpgroup works through
 //     one query tile with two S buffers (its MMAs take twice as long a tile).
 // The exponent reference m is the row's maximum over the piece's first tile; it moves (and O is
-// rescaled) only when a later score lies more than 2^8 above it.  Scores, m, l and O are fp32; P is
+// rescaled) only when a later score lies more than 2^8 above it; over bf16 pages a full tile is first tried
+// with the reference as it is, and only looked through where a row's sum exceeds 2^15.  Scores, m, l and O are fp32; P is
 // rounded to bf16 because the products take 16 bits (l sums it unrounded), the output to its type.
 //
 // Warps.  Two loaders take the ring's positions in turn (one, alone, is bound by issuing the copies of
@@ -34,7 +35,7 @@
 // What bounds it.  Short pieces over bf16 pages: their bytes (64 requests x 18000 keys, 8 KV heads, d 128:
 // 661 us, 7.1 TB/s; with 8 rows each 686 us).  Over 8-bit pages: the conversion, and the shared memory
 // that it shares with the MMAs (8 rows each 644 us for half the bytes).  Prompts: the chain S -> softmax -> P V of a
-// tile (4096 rows on 8192 keys, 32 heads: 570 us, 1.2 PFLOP/s, 8-bit pages 642; the MMAs alone 342 us).
+// tile (4096 rows on 8192 keys, 32 heads: 507 us, 1.35 PFLOP/s, 8-bit pages 645; the MMAs alone 342 us).
 //
 // Split.  Work is the sequence of pairs (request, KV head, token block); a pair costs its
 // keys plus kStartKeys, and every CTA (one per SM) takes an equal share of the total, so long
@@ -116,7 +117,7 @@ __device__ __forceinline__ void ck_codes(uint32_t w, uint32_t mul, uint32_t &lo,
 }
 
 // The softmax of one S tile in this thread's row, 64 columns a turn: its instructions are kept few, as
-// seven kinds of warps share the instruction cache (whole rows unrolled took twice as long).
+// seven kinds of warps share the instruction cache (both passes unrolled over whole rows took twice as long).
 
 // 32 columns of this thread's TMEM lane, and the largest of them.
 __device__ __forceinline__ float ck_ld32_max(uint32_t taddr, uint32_t (&r)[32])
@@ -205,7 +206,7 @@ __device__ __forceinline__ bool ck_row_once(uint32_t ts, float cl2, float m, flo
     const uint64_t c2 = f32x2_pack(cl2, cl2), nm2 = f32x2_pack(-m, -m);
     uint64_t acc[2] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f)};
     uint32_t p0[32], p1[32];
-#pragma unroll 1
+#pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t sv[2][32];
         tmem_ld32(ts + half * 64, sv[0]);
@@ -219,8 +220,7 @@ __device__ __forceinline__ bool ck_row_once(uint32_t ts, float cl2, float m, flo
                                               __uint_as_float(sv[k0 >> 5][(k0 & 31) + 1])), c2, nm2), y0, y1);
             y0 = fast_exp2(y0);
             y1 = fast_exp2(y1);
-            p0[e] = p1[e];
-            p1[e] = F16 ? ck_pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
+            (half ? p1 : p0)[e] = F16 ? ck_pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
             acc[e & 1] = f32x2_add(acc[e & 1], f32x2_pack(y0, y1));
         }
     }
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                             e_first = ev;
                     }
                     // Without a mask, and with a reference that still holds, the scores are read once: where the
-                    // registers hold a row's P (4096 rows on 8192 keys 570 -> 520 us)
+                    // registers hold a row's P (4096 rows on 8192 keys 507 us, read twice 570)
                     constexpr bool kOnce = !Q8;
                     float sum = 0.0f;
                     if (!kOnce || masked || done == 0 || !ck_row_once<Q8>(ts, ct, m_ref - ev, 32768.0f, live, sum)) {
