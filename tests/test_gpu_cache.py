@@ -681,6 +681,40 @@ def test_rows_of_very_different_sizes_in_one_tile(d, rows):
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 40, 140])
+def test_scores_that_jump_between_tiles(rows, kind):
+    """Keys 40, 120 and 416 above the others in score (2^600 in probability) in later tiles, in either
+    half of one, and a first tile at -416: more heads than CTAs, so that most see all tiles in one piece."""
+    d, hkv, ctx, page = 64, 200, 900, 64
+    pool = Pool(1, [ctx + rows], hkv, d, page, kind, seed=32)
+    at = {t: -416.0 for t in range(128)} | {300: 40.0, 470: 120.0, 660: 416.0}
+    for t, x in at.items():
+        row = np.zeros(d)
+        row[0] = x                        # (bf16 and e4m3 values)
+        pg = int(pool.table[0, t // page])
+        pool.vals[0][pg, :, t % page] = row
+        codes, b = pack_rows(row)
+        if kind == E4M3:
+            pool.raw[0][pg, :, t % page] = torch.from_numpy(codes)
+            pool.exps[0][pg, :, t % page] = int(b)
+        else:
+            pool.raw[0][pg, :, t % page] = torch.from_numpy(row).to(BF16)
+    for upto in (300, 470, 660, ctx):     # the last jump that is seen
+        q = torch.randn(rows, hkv, d, generator=torch.Generator().manual_seed(33)).to(BF16)
+        q[..., 0] = 8.0                   # the scale is 1 / 8
+        q = q.cuda()
+        ws = svp.Workspace(svp.chunk_attn_workspace_size(hkv, hkv, d))
+        cache = pool.cuda()
+        out, lse = svp.chunk_attn(q, i32([upto]), i32([0, rows]), cache=cache, ws=ws)
+        assert ws.read_status() == 0
+        picks = (0, 39, 100)
+        o, l, tol, ltol = attend_exact(pool, q, [rows], [upto], 1 / math.sqrt(d), picks)
+        r = picked_rows([rows], picks)
+        assert (np.abs(out.double().cpu().numpy()[r] - o) <= tol).all()
+        assert (np.abs(lse.double().cpu().numpy()[r] - l) <= ltol).all()
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
 @pytest.mark.parametrize("rows", [1, 40])
 def test_a_tail_under_one_large_score(rows, kind):
     """The first key is 2^26 times as probable as each of the others and its value is zero: what comes
