@@ -1041,86 +1041,96 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
 }
 
 // ------------------------------------------------------------------ joining split pairs
-// Block (c, y): rows of the pair whose first piece CTA c had, one row a warp: o = sum_q 2^(m_q - M)
+// Block (c, y): rows of the pair whose first piece CTA c had, one row a half warp: o = sum_q 2^(m_q - M)
 // O_q / L over the pieces in their order, L = sum_q 2^(m_q - M) l_q.  Launched behind the kernel above
-// as its dependent; most blocks find nothing to do.
-constexpr int kJoinWarps = 4;
+// as its dependent; most blocks find nothing to do.  Bound by its chain of reads, descriptor -> (m, l)
+// and O: the first pieces' O are asked for together with (m, l).
+constexpr int kJoinWarps = 4, kJoinRows = 2 * kJoinWarps;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __grid_constant__ ChunkParams p, int32_t part_rows)
 {
-    constexpr int V = D == 64 ? 2 : 4, E = D / 32;        // columns a lane: E, V of them side by side in a group of 32 V
+    constexpr int E = D / 16, A = D == 256 ? 2 : 4;       // columns a lane, four side by side; pieces read ahead
     griddep_launch_dependents();
     griddep_wait();
-    const int32_t c = blockIdx.x, lane = threadIdx.x & 31;
+    const int32_t c = blockIdx.x, lane = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
     const ChunkDesc d = p.desc[c];
-    if (d.np < 2)
+    const int32_t np = d.np, rows = d.ntok * p.G;
+    if (np < 2)
         return;
-    for (int32_t rho = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); rho < d.ntok * p.G; rho += kJoinWarps * (int32_t)gridDim.y) {
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    for (int32_t base = blockIdx.y * kJoinRows + (threadIdx.x >> 5) * 2; base < rows; base += kJoinRows * (int32_t)gridDim.y) {
+        const int32_t rho = min(base + half, rows - 1);   // (an odd last row is done twice, and stored once)
         const int32_t tok = rho / p.G, h = rho - tok * p.G;
         const bool second = tok >= p.R;                   // token of the second query tile
         const int32_t pr = (second ? 128 : 0) + (tok - (second ? p.R : 0)) * p.G + h;
         auto at = [&](int32_t q) { return (int64_t)(q == 0 ? 2 * c + 1 : 2 * (c + q)) * part_rows + pr; };
-        float M = -INFINITY;
-        for (int32_t q = lane; q < d.np; q += 32) {
+        auto load = [&](int32_t q, float (&x)[E]) {
+            const float *o = p.part_o + at(q) * D + lane * 4;
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 16 * e));
+                x[e] = v.x;
+                x[e + 1] = v.y;
+                x[e + 2] = v.z;
+                x[e + 3] = v.w;
+            }
+        };
+        const float2 ml0 = lane < np ? __ldcg(p.part_ml + at(lane)) : none;
+        float ahead[A][E];
+#pragma unroll
+        for (int q = 0; q < A; ++q)
+            load(min(q, np - 1), ahead[q]);
+        // (a piece without a visible key of this row, l = 0, is left out whatever its O holds)
+        float M = ml0.y != 0.0f ? ml0.x : -INFINITY;
+        for (int32_t q = 16 + lane; q < np; q += 16) {
             const float2 ml = __ldcg(p.part_ml + at(q));
             M = fmaxf(M, ml.y != 0.0f ? ml.x : -INFINITY);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = 8; o > 0; o >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float acc[E], L = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             acc[e] = 0.0f;
-        for (int32_t q0 = 0; q0 < d.np; q0 += 32) {
-            float w = 0.0f, wl = 0.0f;
-            if (q0 + lane < d.np) {
-                const float2 ml = __ldcg(p.part_ml + at(q0 + lane));
-                // a piece without a visible key of this row (l = 0) is left out whatever its O holds
-                w = ml.y != 0.0f ? fast_exp2(ml.x - M) : 0.0f;
-                wl = ml.y != 0.0f ? w * ml.y : 0.0f;
-            }
-            const int32_t cnt = min(32, d.np - q0);
-#pragma unroll 4
-            for (int32_t q = 0; q < cnt; ++q) {
-                const float wq = __shfl_sync(0xffffffffu, w, q);
-                L += __shfl_sync(0xffffffffu, wl, q);
-                const float *o = p.part_o + at(q0 + q) * D + lane * V;
-                float x[E];
-#pragma unroll
-                for (int e = 0; e < E; e += V) {
-                    if constexpr (V == 2) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(o + 32 * e));
-                        x[e] = v.x;
-                        x[e + 1] = v.y;
-                    } else {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 32 * e));
-                        x[e] = v.x;
-                        x[e + 1] = v.y;
-                        x[e + 2] = v.z;
-                        x[e + 3] = v.w;
-                    }
-                }
+        for (int32_t q0 = 0; q0 < np; q0 += 16) {
+            const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? __ldcg(p.part_ml + at(q0 + lane)) : none;
+            const float w = ml.y != 0.0f ? fast_exp2(ml.x - M) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
+            auto add = [&](int32_t q, const float (&x)[E]) {
+                const float wq = __shfl_sync(0xffffffffu, w, q, 16);
+                L += __shfl_sync(0xffffffffu, wl, q, 16);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     acc[e] = wq != 0.0f ? fmaf(wq, x[e], acc[e]) : acc[e];
+            };
+            int32_t q = 0;
+            if (q0 == 0) {
+#pragma unroll
+                for (int k = 0; k < A; ++k)
+                    add(k, ahead[k]);                     // (weight 0 from np on)
+                q = A;
+            }
+            const int32_t cnt = min(16, np - q0);
+#pragma unroll 2
+            for (; q < cnt; ++q) {
+                float x[E];
+                load(q0 + q, x);
+                add(q, x);
             }
         }
-        const float inv = 1.0f / L;
-        const int64_t orow = (int64_t)(d.row0 + tok) * p.hq + d.g * p.G + h;
-        uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * V;
+        if (base + half < rows) {
+            const float inv = 1.0f / L;
+            const int64_t orow = (int64_t)(d.row0 + tok) * p.hq + d.g * p.G + h;
+            uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * 4;
 #pragma unroll
-        for (int e = 0; e < E; e += V) {
-            const uint32_t lo = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-            if constexpr (V == 2)
-                *reinterpret_cast<uint32_t *>(dst) = lo;
-            else
-                *reinterpret_cast<uint2 *>(dst + 32 * e) =
-                    make_uint2(lo, pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
+            for (int e = 0; e < E; e += 4)
+                *reinterpret_cast<uint2 *>(dst + 16 * e) = make_uint2(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv),
+                                                                      pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
+            if (lane == 0 && p.lse)
+                p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
         }
-        if (lane == 0 && p.lse)
-            p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
+        __syncwarp();
     }
 }
 
@@ -1155,8 +1165,8 @@ svp_status chunk_short_run(ChunkParams &p, int32_t d, cudaStream_t stream);
 template <int D>
 static svp_status chunk_join(const ChunkParams &p, int32_t part_rows, cudaStream_t stream)
 {
-    const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most; one a warp
-    const unsigned y = (unsigned)std::max(1, (rows + kJoinWarps - 1) / kJoinWarps);
+    const int rows = (int)std::min<int64_t>(part_rows, (int64_t)p.G * p.w);   // of a pair, at most
+    const unsigned y = (unsigned)std::max(1, (rows + kJoinRows - 1) / kJoinRows);
     return launch_pdl(chunk_join_kernel<D>, dim3(chunk_ctas(), y), dim3(kJoinWarps * 32), 0, stream, p, part_rows) ==
                    cudaSuccess
                ? SVP_OK
