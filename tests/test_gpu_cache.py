@@ -482,6 +482,26 @@ def test_nan_rows_reach_the_rows_that_see_them():
         assert torch.isfinite(early).all()
 
 
+@pytest.mark.parametrize("kind", [BF16, E4M3, F32])
+@pytest.mark.parametrize("rows,ctx", [(3, 200), (50, 100), (130, 130)])
+def test_a_nan_key_that_only_the_last_row_sees(rows, ctx, kind):
+    hq, hkv, d = 4, 2, 128
+    pool = Pool(1, [ctx + rows], hkv, d, 16, kind, seed=34)
+    cache = pool.cuda()
+    qt = F32 if kind == F32 else BF16
+    x = torch.full((1, hkv, d), float("nan"), device="cuda", dtype=qt)
+    q = torch.randn(rows, hq, d, generator=torch.Generator().manual_seed(35)).to(qt).cuda()
+    last = ctx + rows - 1
+    v = torch.from_numpy(pool.rows(1, 0, last, last + 1)).to(qt).cuda()
+    svp.cache_write(x, v, i32([last]), i32([0, 1]), cache=cache)
+    out, lse = svp.chunk_attn(q, i32([ctx]), i32([0, rows]), cache=cache)
+    assert torch.isnan(out[-1]).all() and torch.isnan(lse[-1]).all()
+    o, l, tol, ltol = attend_exact(pool, q[:-1], [rows - 1], [ctx], 1 / math.sqrt(d), picks=(0, 1, 31, 32, 48, 100))
+    at = picked_rows([rows - 1], (0, 1, 31, 32, 48, 100))
+    assert (np.abs(out.double().cpu().numpy()[at] - o) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy()[at] - l) <= ltol).all()
+
+
 # ------------------------------------------------------------------ as they are used
 @pytest.mark.parametrize("kind", [BF16, E4M3])
 def test_a_generation_step_captured_and_replayed(kind):
