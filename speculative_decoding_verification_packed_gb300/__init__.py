@@ -629,7 +629,6 @@ def make_cache(k_cache, v_cache, block_table, *, k_exp=None, v_exp=None) -> svp_
     for x in c.keep:
         if x is not None and x.device != c.device:
             raise ValueError("the cache's tensors must be on one device")
-    c.ref = ctypes.byref(c)
     return c
 
 
@@ -701,7 +700,7 @@ def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
     if ws is None:
         ws = _cache_workspace(cache, stream)
     st = lib().svp_cache_write(
-        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache.ref, _i32(ctx_len, "ctx_len", n, cache),
+        k.data_ptr(), v.data_ptr(), stride, _dtype_code(k), cache, _i32(ctx_len, "ctx_len", n, cache),
         _i32(cu_slots, "cu_slots", n + 1, cache), _i32(take, "take", n, cache), n, k.shape[0], cache.hkv,
         cache.d, ws.ptr, ws.nbytes, _raw_stream(stream, cache))
     if st:
@@ -733,7 +732,7 @@ def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
     if ws is None:
         ws = _cache_workspace(cache, stream)
     st = lib().svp_cache_read(
-        cache.ref, _i32(start, "start", n, cache), _i32(cu_rows, "cu_rows", n + 1, cache), n, k_out.shape[0],
+        cache, _i32(start, "start", n, cache), _i32(cu_rows, "cu_rows", n + 1, cache), n, k_out.shape[0],
         cache.hkv, cache.d, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.ptr, ws.nbytes,
         _raw_stream(stream, cache))
     if st:
@@ -800,7 +799,7 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
     if ws is None:
         ws = _chunk_workspace(hq, cache, q.dtype, raw)
     st = lib().svp_chunk_attn(
-        q.data_ptr(), stride, cache.ref, _i32(ctx_len, "ctx_len", n, cache), _i32(cu_slots, "cu_slots", n + 1, cache),
+        q.data_ptr(), stride, cache, _i32(ctx_len, "ctx_len", n, cache), _i32(cu_slots, "cu_slots", n + 1, cache),
         n, m_cap, (m_cap or 1) if w is None else w, svp_heads(hq, hkv, d, scale), _dtype_code(q), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, raw)
     if st:
