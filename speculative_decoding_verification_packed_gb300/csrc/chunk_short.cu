@@ -20,9 +20,14 @@
 // thread q of a quad has d = D/4 q .. of its key in one read; for O, d = D/8 n + i belongs to row n of
 // the product's half i.  P^T turns from accumulator to operand by movmatrix.
 // An 8-bit row's power of two multiplies its row of S^T; V's goes into the exponent,
-//   P' = 2^(s c + e_key - m),  O += P' codes,  l += P' 2^-e_key,
+//   P' = 2^(s c + e_key - m),  O += P' codes,  l += P' 2^(e_ref - e_key),
 // with m the running maximum of s c + e_key (less kCkLift), so that P' stays within fp16 whatever the
 // exponents (it is rounded to fp16 because the products take 16 bits; scores, m, l and O are fp32).
+// e_ref, one a warp, keeps l in range: 0 until a visible row has e_key < -kShSpan (a row of zeros is written
+// with -112), then kShSpan above the smallest e_key so far.  With P' < 2^15 a term is below 2^79, and 2^20
+// keys add up to less than 2^100; P' = 2^7 of a key whose e_key is 2^100 above the smallest, or 2^100 above 1
+// where none is below it, counts 2^-93 or more, far from the end of fp32's range.  The test shares
+// the vote on m; with one of its own the call took 363 us, and with the factors made by the V loader 392.
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
 #include <algorithm>
 #include <cstring>
@@ -34,6 +39,7 @@ namespace svp {
 constexpr int kShWarps = 8;           // computing warps; then a K and a V loader
 constexpr int kShThreads = 32 * (kShWarps + 2);
 constexpr int kShSlots = 16;          // ring slots at most
+constexpr float kShSpan = 64.0f;      // e_ref - e_key, at most
 
 struct ShortMisc {
     uint64_t bars[2 * kShSlots];
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     last[nb][x] = rx < nrows ? s.L + s.tb0 + rx / p.G : -1;
                 }
             }
-            float o[NB][NI / 2][4], mx[NB][2], l[NB][2];
+            float o[NB][NI / 2][4], mx[NB][2], l[NB][2], e_ref = 0.0f;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 mx[nb][0] = mx[nb][1] = -INFINITY;
@@ -308,7 +314,8 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 // ---- exponents and the running maximum
                 const int key = kb + r;
                 const float kf[2] = {ke[key], ke[key + 8]}, e[2] = {ve[key], ve[key + 8]};
-                const float back[2] = {ck_pow2(-(int32_t)e[0]), ck_pow2(-(int32_t)e[1])};
+                const bool low = fmaxf(e_ref - e[0], e_ref - e[1]) > kShSpan;
+                float back[2] = {ck_pow2((int32_t)(e_ref - e[0])), ck_pow2((int32_t)(e_ref - e[1]))};
                 uint32_t pb[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
@@ -332,7 +339,21 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     // (mx: the reference, the largest score less kCkLift when it last moved)
                     const bool up0 = top[0] > mx[nb][0] + (kCkSlack + kCkLift) || (mx[nb][0] == -INFINITY && top[0] != -INFINITY);
                     const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
-                    if (__any_sync(0xffffffffu, up0 || up1)) {
+                    if (__any_sync(0xffffffffu, up0 || up1 || (nb == 0 && low))) {
+                        if (nb == 0 && __any_sync(0xffffffffu, low)) {
+                            // (a row past the last visible key may have any byte)
+                            const float e0 = k0 + key < s.len ? e[0] : 0.0f, e1 = k0 + key + 8 < s.len ? e[1] : 0.0f;
+                            const int32_t least = __reduce_min_sync(0xffffffffu, (int32_t)fminf(fminf(e0, e1), 0.0f));
+                            const float to = fminf(e_ref, (float)least + kShSpan), down = ck_pow2((int32_t)(to - e_ref));
+                            e_ref = to;
+                            back[0] = ck_pow2((int32_t)(e_ref - e[0]));
+                            back[1] = ck_pow2((int32_t)(e_ref - e[1]));
+#pragma unroll
+                            for (int y = 0; y < NB; ++y) {
+                                l[y][0] *= down;
+                                l[y][1] *= down;
+                            }
+                        }
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float mn = fmaxf(mx[nb][x], top[x] - kCkLift);
@@ -402,7 +423,9 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     phase ^= 1u;
                 }
             }
-            // ---- join the warps: every warp's (m, l) and O to shared memory, then four columns of a row a thread
+            // ---- join the warps: every warp's (m, l) and O, in units of 1, to shared memory, then four columns of a
+            // row a thread
+            const float o_scale = ck_pow2((int32_t)e_ref);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -413,13 +436,13 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                         z += __shfl_xor_sync(0xffffffffu, z, w2);
                     const int row = nb * 8 + 2 * q + x;
                     if (r == 0)
-                        m->ml[warp][row] = make_float2(mx[nb][x], z);
+                        m->ml[warp][row] = make_float2(mx[nb][x] - e_ref, z);
                     // d = NI r + 2 i and + 1 at columns (2 i) 8 + r and (2 i + 1) 8 + r
                     float *dst = red + (warp * 8 * NB + row) * (D + 8) + r;
 #pragma unroll
                     for (int i = 0; i < NI / 2; ++i) {
-                        dst[16 * i] = o[nb][i][x];
-                        dst[16 * i + 8] = o[nb][i][2 + x];
+                        dst[16 * i] = o[nb][i][x] * o_scale;
+                        dst[16 * i + 8] = o[nb][i][2 + x] * o_scale;
                     }
                 }
             if (named_bar_any(1, 32 * kShWarps, !ok))

@@ -1,0 +1,167 @@
+"""chunk_attn over 8-bit pages at the ends of the value range: value rows of zeros, exponent bytes
+0 and 255, in calls of few query rows a KV head and of many, against softmax attention in 64 bits.
+
+A rounding to nearest is off by eps / 2 relative: bf16 2^-8, fp16 2^-11, fp32 2^-24."""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_packed_gb300 as svp
+
+pytestmark = pytest.mark.gpu
+
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+# (query heads, KV heads, d, rows of a request): 1, 4 and 16 query rows of a KV head, which 8-bit pages of
+# d <= 128 take apart from more; then 20, 160 (two query tiles) and d 256; last, more heads than SMs, so that
+# no context is split
+CALLS = [(2, 2, 64, 1), (8, 2, 128, 1), (8, 2, 128, 4), (4, 2, 64, 8), (8, 2, 128, 5), (8, 2, 64, 40), (4, 2, 256, 1),
+         (304, 304, 64, 1), (304, 304, 128, 2), (304, 304, 64, 17)]
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Cache8:
+    """One request's 8-bit cache of T positions, keys and values [T, hkv, d] written by cache_write."""
+
+    def __init__(self, T, hkv, d, seed, page=16, k=None, v=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.T, self.hkv, self.d, self.page = T, hkv, d, page
+        pages = -(-T // page)
+        self.table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+        self.codes = [torch.full((pages, hkv, page, d), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.exps = [torch.full((pages, hkv, page), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.cache = svp.make_cache(self.codes[0].view(E4M3), self.codes[1].view(E4M3), self.table,
+                                    k_exp=self.exps[0], v_exp=self.exps[1])
+        k = torch.randn(T, hkv, d, generator=g, device="cuda").to(BF16) if k is None else k
+        v = torch.randn(T, hkv, d, generator=g, device="cuda").to(BF16) if v is None else v
+        svp.cache_write(k, v, i32([0]), i32([0, T]), cache=self.cache)
+
+    def at(self, pos):
+        """(pages, tokens) of positions."""
+        pos = torch.as_tensor(pos, device="cuda")
+        return self.table[0][pos // self.page].long(), pos % self.page
+
+    def set_bytes(self, which, pos, byte):
+        pg, tok = self.at(pos)
+        self.exps[which][pg, :, tok] = byte
+
+    def rows(self, which):
+        """(values [T, hkv, d], powers of two [T, hkv]) in 64 bits: byte 0 stands for 0, 255 for NaN."""
+        pg, tok = self.at(torch.arange(self.T))
+        b = self.exps[which][pg, :, tok].to(torch.int64)
+        e = ((b - 127 + 1023) << 52).view(torch.float64)
+        x = self.codes[which][pg, :, tok].view(E4M3).double() * e[..., None]
+        x = torch.where((b == 0)[..., None], torch.zeros_like(x), x)
+        return torch.where((b == 255)[..., None], torch.full_like(x, float("nan")), x), e
+
+
+def exact(c, q, rows, scale):
+    """(o, lse, bounds) of `rows` last rows q [rows, hq, d] in 64 bits.  A = sum p |v| / l.  A probability
+    is rounded to fp16: off by 2^-11, or, far below the largest, by 2^-25 where the largest product of
+    a probability and its row's power of two is held at 2^7 or more; and by the error of its score, an
+    fp32 sum of d products.  fp32 sums over the keys, exponentials and the logarithm add a few steps."""
+    hq = q.shape[1]
+    K, _ = c.rows(0)
+    V, e = c.rows(1)
+    G, T, d = hq // c.hkv, c.T, c.d
+    qh = q.double().view(rows, c.hkv, G, d).permute(1, 0, 2, 3).reshape(c.hkv, rows * G, d)
+    last = T - rows + torch.arange(rows, device="cuda").repeat_interleave(G)
+    hidden = torch.arange(T, device="cuda")[None] > last[:, None]
+    s = (qh @ K.permute(1, 2, 0) * scale).masked_fill(hidden, -math.inf)
+    ds = (d + 2) * 2.0 ** -23 * (qh.abs() @ K.abs().permute(1, 2, 0) * scale).masked_fill(hidden, 0).amax(-1)
+    top = s.amax(-1, keepdim=True)
+    p = torch.exp(s - top)
+    l = p.sum(-1, keepdim=True)
+    v, ex = V.permute(1, 0, 2), e.permute(1, 0)[:, None]
+    y = p @ v / l
+    A = p @ v.abs() / l
+    codes = (v.abs() / ex.transpose(1, 2))
+    floor = 2.0 ** -32 * (p * ex).amax(-1, keepdim=True) * codes.sum(1, keepdim=True) / l
+    steps = (T / 32 + 64) * 2.0 ** -23
+    tol = (2.0 ** -11 + 2 * ds[..., None] + steps) * A + floor + 2.0 ** -8 * y.abs() + 1e-30
+    lse = (top + torch.log(l)).squeeze(-1)
+    ltol = ds + steps + lse.abs() * 2.0 ** -22
+
+    def back(x):
+        return x.view(c.hkv, rows, G, -1).permute(1, 0, 2, 3).reshape(rows, hq, -1)
+    return back(y), back(lse).squeeze(-1), back(tol), back(ltol).squeeze(-1)
+
+
+def attend(c, q, rows, scale=0.0):
+    ws = svp.Workspace(svp.chunk_attn_workspace_size(q.shape[1], c.hkv, c.d))
+    out, lse = svp.chunk_attn(q, i32([c.T - rows]), i32([0, rows]), cache=c.cache, w=rows, scale=scale, ws=ws)
+    assert ws.read_status() == 0
+    return out.double(), lse.double()
+
+
+def check(c, q, rows, scale=0.0, out_too=True):
+    out, lse = attend(c, q, rows, scale)
+    o, l, tol, ltol = exact(c, q, rows, scale or 1 / math.sqrt(c.d))
+    assert torch.isfinite(lse).all()
+    assert ((lse - l).abs() <= ltol).all(), float(((lse - l).abs() / ltol).max())
+    if out_too:
+        assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
+    return out, lse
+
+
+def query(rows, hq, d, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(rows, hq, d, generator=g, device="cuda").to(BF16)
+
+
+# ------------------------------------------------------------------ value rows of zeros
+@pytest.mark.parametrize("T", [600, 16384])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_every_value_row_is_zero(hq, hkv, d, rows, T):
+    """As cache_write stores them (byte 15): the output is 0 and the normaliser that of the scores."""
+    if hkv > 2 and T > 600:
+        T = 2500                       # (the 64-bit form's memory)
+    c = Cache8(T, hkv, d, 1, v=torch.zeros(T, hkv, d, dtype=BF16, device="cuda"))
+    assert (c.rows(1)[1] == 2.0 ** -112).all()
+    out, _ = check(c, query(rows, hq, d, 2), rows)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("where", ["first", "last", "every other", "one row is not"])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_some_value_rows_are_zero(hq, hkv, d, rows, where):
+    T = 2500
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.randn(T, hkv, d, generator=g, device="cuda").to(BF16)
+    zero = {"first": slice(0, 2300), "last": slice(900, T), "every other": slice(0, T, 2)}.get(where)
+    if zero is None:
+        v[:1203] = 0
+        v[1204:] = 0
+    else:
+        v[zero] = 0
+    check(Cache8(T, hkv, d, 4, v=v), query(rows, hq, d, 5), rows)
+
+
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_a_value_row_of_zeros_takes_nearly_all_weight(hq, hkv, d, rows):
+    """The first key, as probable as 2^20 of the others, has a value of zeros."""
+    T = 2500
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v = torch.zeros(T, hkv, d, dtype=BF16, device="cuda"), torch.randn(T, hkv, d, generator=g, device="cuda").to(BF16)
+    k[0, :, 0] = 20.0
+    v[0] = 0
+    q = torch.zeros(rows, hq, d, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    check(Cache8(T, hkv, d, 7, k=k, v=v), q, rows, scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("low,high", [(1, 10), (1, 67), (20, 100), (100, 180), (150, 246)])
+@pytest.mark.parametrize("hq,hkv,d,rows", [x for x in CALLS if x[2] <= 128 and x[0] // x[1] * x[3] <= 16])
+def test_value_rows_of_any_power_of_two(hq, hkv, d, rows, low, high):
+    """Bytes low..high in one request, the rows past its last one among the smallest."""
+    T = 2500
+    c = Cache8(T, hkv, d, 8)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    used = c.exps[1] != 255
+    c.exps[1][:] = torch.where(used, torch.randint(low, high + 1, c.exps[1].shape, generator=g, device="cuda").to(torch.uint8),
+                               torch.ones_like(c.exps[1]))
+    check(c, query(rows, hq, d, 10), rows)
