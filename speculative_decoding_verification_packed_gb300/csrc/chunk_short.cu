@@ -40,11 +40,13 @@ constexpr int kShWarps = 8;           // computing warps; then a K and a V loade
 constexpr int kShThreads = 32 * (kShWarps + 2);
 constexpr int kShSlots = 16;          // ring slots at most
 constexpr float kShSpan = 64.0f;      // e_ref - e_key, at most
+constexpr float kShNan = -128.0f;     // e_key of a value row that stands for NaN
 
 struct ShortMisc {
     uint64_t bars[2 * kShSlots];
     int32_t abort_flag, pad;
     int64_t warp_tot[12];
+    int32_t nan_at[kShWarps];         // position of the first value row of a warp's that stands for NaN
     float2 ml[kShWarps][16];          // [warp][row of its group]
 };
 
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         // Even ring slots hold K, odd ones V.  Lane u looks after positions 4 u .. 4 u + 3 of a tile; the
         // lane of a page's first positions loads the page; pages that are not needed or not in the
         // pool are loaded from past the pool (zeros).  The rows' exponents go beside the codes as fp32:
-        // K's as factors, V's as exponents.
+        // K's as factors, V's as exponents (kShNan for byte 255).
         const int kv = warp - kShWarps;
         const CUtensorMap *tm = kv ? &p.tm_v : &p.tm_k;
         const uint8_t *exps = kv ? p.c.v_exp : p.c.k_exp;
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint32_t b = (e >> (8 * x)) & 0xffu;
-                    f[x] = kv && b != 255u ? (float)((int32_t)b - 127) : exp_byte_scale(b);   // (255: NaN)
+                    f[x] = kv ? (float)(int8_t)(uint8_t)(b + 129u) : exp_byte_scale(b);   // b - 127, of 255 -128
                 }
                 st_shared_v4(sbase + p.off_raw + slot * 512 + lane * 16, __float_as_uint(f[0]), __float_as_uint(f[1]),
                              __float_as_uint(f[2]), __float_as_uint(f[3]));
@@ -263,6 +265,9 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 for (int i = 0; i < NI / 2; ++i)
                     o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.0f;
             }
+            if (lane == 0)
+                m->nan_at[warp] = INT32_MAX;
+            __syncwarp();
             for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
                 const uint32_t vs = slot + 1;               // (slots come in pairs, nslot is even)
                 ok = __all_sync(0xffffffffu, mbar_wait(bar_full(slot), phase, abort_flag) &&
@@ -313,7 +318,8 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 }
                 // ---- exponents and the running maximum
                 const int key = kb + r;
-                const float kf[2] = {ke[key], ke[key + 8]}, e[2] = {ve[key], ve[key + 8]};
+                const float kf[2] = {ke[key], ke[key + 8]};
+                float e[2] = {ve[key], ve[key + 8]};
                 const bool low = fmaxf(e_ref - e[0], e_ref - e[1]) > kShSpan;
                 float back[2] = {ck_pow2((int32_t)(e_ref - e[0])), ck_pow2((int32_t)(e_ref - e[1]))};
                 uint32_t pb[NB][2];
@@ -341,9 +347,33 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
                     if (__any_sync(0xffffffffu, up0 || up1 || (nb == 0 && low))) {
                         if (nb == 0 && __any_sync(0xffffffffu, low)) {
-                            // (a row past the last visible key may have any byte)
-                            const float e0 = k0 + key < s.len ? e[0] : 0.0f, e1 = k0 + key + 8 < s.len ? e[1] : 0.0f;
-                            const int32_t least = __reduce_min_sync(0xffffffffu, (int32_t)fminf(fminf(e0, e1), 0.0f));
+                            // A row of NaN counts as one of zeros, with e = 0, and where it lies is noted.  (A row
+                            // past the last visible key may have any byte.)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int32_t at = k0 + key + 8 * y;
+                                const bool seen = at < s.len;
+                                if (seen && e[y] == kShNan) {
+                                    atomicMin(&m->nan_at[warp], at);
+#pragma unroll
+                                    for (int x = 0; x < D / 64; ++x)
+                                        st_shared_v4(smem_u32(vt) + sh_chunk<D>(key + 8 * y, q * (D / 64) + x), 0u, 0u, 0u, 0u);
+                                    fence_proxy_async_smem();
+                                }
+                                if (!seen || e[y] == kShNan) {
+                                    sc[0][2 * y] -= e[y];
+                                    sc[0][2 * y + 1] -= e[y];
+                                    e[y] = 0.0f;
+                                }
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                top[x] = fmaxf(sc[0][x], sc[0][2 + x]);
+#pragma unroll
+                                for (int w2 = 4; w2 < 32; w2 <<= 1)
+                                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], w2));
+                            }
+                            const int32_t least = __reduce_min_sync(0xffffffffu, (int32_t)fminf(fminf(e[0], e[1]), 0.0f));
                             const float to = fminf(e_ref, (float)least + kShSpan), down = ck_pow2((int32_t)(to - e_ref));
                             e_ref = to;
                             back[0] = ck_pow2((int32_t)(e_ref - e[0]));
@@ -353,6 +383,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                                 l[y][0] *= down;
                                 l[y][1] *= down;
                             }
+                            __syncwarp();
                         }
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -423,8 +454,10 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     phase ^= 1u;
                 }
             }
-            // ---- join the warps: every warp's (m, l) and O, in units of 1, to shared memory, then four columns of a
-            // row a thread
+            // ---- join the warps: every warp's (m, l) and O, in units of 1 (NaN where the row sees a value row of
+            // NaN), to shared memory, then four columns of a row a thread
+            __syncwarp();
+            const int32_t nan_at = m->nan_at[warp];
             const float o_scale = ck_pow2((int32_t)e_ref);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -437,12 +470,13 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     const int row = nb * 8 + 2 * q + x;
                     if (r == 0)
                         m->ml[warp][row] = make_float2(mx[nb][x] - e_ref, z);
+                    const float f = nan_at <= last[nb][x] ? NAN : o_scale;
                     // d = NI r + 2 i and + 1 at columns (2 i) 8 + r and (2 i + 1) 8 + r
                     float *dst = red + (warp * 8 * NB + row) * (D + 8) + r;
 #pragma unroll
                     for (int i = 0; i < NI / 2; ++i) {
-                        dst[16 * i] = o[nb][i][x] * o_scale;
-                        dst[16 * i + 8] = o[nb][i][2 + x] * o_scale;
+                        dst[16 * i] = o[nb][i][x] * f;
+                        dst[16 * i + 8] = o[nb][i][2 + x] * f;
                     }
                 }
             if (named_bar_any(1, 32 * kShWarps, !ok))

@@ -165,3 +165,38 @@ def test_value_rows_of_any_power_of_two(hq, hkv, d, rows, low, high):
     c.exps[1][:] = torch.where(used, torch.randint(low, high + 1, c.exps[1].shape, generator=g, device="cuda").to(torch.uint8),
                                torch.ones_like(c.exps[1]))
     check(c, query(rows, hq, d, 10), rows)
+
+
+# ------------------------------------------------------------------ byte 255: NaN
+@pytest.mark.parametrize("at", [0, 700, 1999])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_nan_in_a_value_row_alone(hq, hkv, d, rows, at):
+    """Every element of a row that sees it is NaN; the normaliser, which has no value row in it, and the
+    other heads are those of the finite rows."""
+    T, other = 2500, hkv - 1
+    q = query(rows, hq, d, 13)
+    c = Cache8(T, hkv, d, 12)
+    o, l, tol, ltol = exact(c, q, rows, 1 / math.sqrt(d))
+    pg, tok = c.at([at])
+    c.exps[1][pg, other, tok] = 255
+    out, lse = attend(c, q, rows)
+    G = hq // hkv
+    assert ((lse - l).abs() <= ltol).all()
+    assert torch.isnan(out[:, other * G:]).all()
+    assert ((out - o).abs() <= tol)[:, :other * G].all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,rows", [x for x in CALLS if x[3] > 1])
+def test_nan_in_the_value_row_of_the_last_key(hq, hkv, d, rows):
+    """It is not in the normaliser of any row, and in calls of few rows not in the output of rows that do
+    not see it."""
+    T = 2500
+    q = query(rows, hq, d, 15)
+    c = Cache8(T, hkv, d, 14)
+    o, l, tol, ltol = exact(c, q, rows, 1 / math.sqrt(d))
+    c.set_bytes(1, [T - 1], 255)
+    out, lse = attend(c, q, rows)
+    assert ((lse - l).abs() <= ltol).all()
+    assert torch.isnan(out[-1]).all()
+    if d <= 128 and hq // hkv * rows <= 16:
+        assert ((out - o).abs() <= tol)[:-1].all()
