@@ -40,7 +40,7 @@ constexpr int kShWarps = 8;           // computing warps; then a K and a V loade
 constexpr int kShThreads = 32 * (kShWarps + 2);
 constexpr int kShSlots = 16;          // ring slots at most
 constexpr float kShSpan = 64.0f;      // e_ref - e_key, at most
-constexpr float kShNan = -128.0f;     // e_key of a value row that stands for NaN
+constexpr float kShNan = -128.0f, kShZero = -127.0f;   // e_key of a value row that stands for NaN, for zeros
 
 struct ShortMisc {
     uint64_t bars[2 * kShSlots];
@@ -347,20 +347,22 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
                     if (__any_sync(0xffffffffu, up0 || up1 || (nb == 0 && low))) {
                         if (nb == 0 && __any_sync(0xffffffffu, low)) {
-                            // A row of NaN counts as one of zeros, with e = 0, and where it lies is noted.  (A row
-                            // past the last visible key may have any byte.)
+                            // A row whose byte stands for zeros has codes 0 and e = 0 from here on.  One of NaN counts
+                            // as such a row, and where it lies is noted.  (A row past the last visible key may have
+                            // any byte.)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const int32_t at = k0 + key + 8 * y;
                                 const bool seen = at < s.len;
-                                if (seen && e[y] == kShNan) {
-                                    atomicMin(&m->nan_at[warp], at);
+                                if (seen && e[y] <= kShZero) {
+                                    if (e[y] == kShNan)
+                                        atomicMin(&m->nan_at[warp], at);
 #pragma unroll
                                     for (int x = 0; x < D / 64; ++x)
                                         st_shared_v4(smem_u32(vt) + sh_chunk<D>(key + 8 * y, q * (D / 64) + x), 0u, 0u, 0u, 0u);
                                     fence_proxy_async_smem();
                                 }
-                                if (!seen || e[y] == kShNan) {
+                                if (!seen || e[y] <= kShZero) {
                                     sc[0][2 * y] -= e[y];
                                     sc[0][2 * y + 1] -= e[y];
                                     e[y] = 0.0f;

@@ -200,3 +200,20 @@ def test_nan_in_the_value_row_of_the_last_key(hq, hkv, d, rows):
     assert torch.isnan(out[-1]).all()
     if d <= 128 and hq // hkv * rows <= 16:
         assert ((out - o).abs() <= tol)[:-1].all()
+
+
+# ------------------------------------------------------------------ byte 0: zeros
+@pytest.mark.parametrize("where", ["all", "first", "every other", "keys too"])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_exponent_byte_0_stands_for_zeros(hq, hkv, d, rows, where):
+    """Whatever the row's codes, as in a cache whose bytes are zeros."""
+    T = 2500
+    c = Cache8(T, hkv, d, 16)
+    pos = torch.arange(T)
+    pos = {"all": pos, "first": pos[:2300], "every other": pos[::2], "keys too": pos[100:2300]}[where]
+    c.set_bytes(1, pos, 0)
+    if where == "keys too":
+        c.set_bytes(0, pos[:1000], 0)
+    out, _ = check(c, query(rows, hq, d, 17), rows)
+    if where == "all":
+        assert (out == 0).all()
