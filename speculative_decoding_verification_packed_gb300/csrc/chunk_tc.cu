@@ -43,6 +43,7 @@
 // from per-request prefix sums; the first and last piece of a CTA may be parts of a pair, whose
 // (O, m, l) go to the workspace and are joined by a second kernel in the pieces' order.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     float ct = cl2, ev = 0.0f;
                     if constexpr (Q8) {
                         const float2 sc = m->scales[(ntile + t) & 15];
-                        ct *= sc.x;
+                        ct = fmaxf(ct * sc.x, FLT_MIN);   // (0 times the -inf of a hidden key would be NaN)
                         ev = sc.y;
                         if (done == 0)
                             e_first = ev;

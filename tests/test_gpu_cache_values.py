@@ -217,3 +217,22 @@ def test_exponent_byte_0_stands_for_zeros(hq, hkv, d, rows, where):
     out, _ = check(c, query(rows, hq, d, 17), rows)
     if where == "all":
         assert (out == 0).all()
+
+
+# ------------------------------------------------------------------ queries and keys of any size
+def sized(rows, hq, hkv, d, qe, ke, seed):
+    """A cache and query of normal numbers times 2^ke and 2^qe, and the scale of unit scores."""
+    T = 2500
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = (torch.randn(T, hkv, d, generator=g, device="cuda") * 2.0 ** ke).to(BF16)
+    q = (query(rows, hq, d, seed + 1).float() * 2.0 ** (qe / 2) * 2.0 ** (qe / 2)).to(BF16)
+    return Cache8(T, hkv, d, seed + 2, k=k), q, 2.0 ** -(qe + ke) / math.sqrt(d)
+
+
+@pytest.mark.parametrize("qe", [0, -85])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_every_score_is_zero(hq, hkv, d, rows, qe):
+    """Keys of zeros (byte 15), which hide from no row what it may not see."""
+    T = 2500
+    c = Cache8(T, hkv, d, 18, k=torch.zeros(T, hkv, d, dtype=BF16, device="cuda"))
+    check(c, (query(rows, hq, d, 19).float() * 2.0 ** qe).to(BF16), rows)
