@@ -290,6 +290,15 @@ __device__ __forceinline__ float ck_pow2(int32_t e)      // 2^e, e clamped to th
     return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23);
 }
 
+// Power of two that takes a query row to fp16: its largest magnitude (bf16 bits in top) to 2^14 or more, 8 bits
+// of mantissa in range for elements down to 2^-31 of it.  Rows under 2^-106 are taken up by 2^120 only, so
+// that the inverse times the scale is a normal number: a row of 2^-126 lies at 2^-6 and loses digits of elements
+// below 2^-11 of its largest.
+__device__ __forceinline__ int32_t ck_q_shift(uint32_t top)
+{
+    return top == 0u ? 0 : min(141 - (int32_t)(top >> 7), 120);
+}
+
 __device__ __forceinline__ uint32_t ck_pack_f16x2(float lo, float hi)
 {
     uint32_t r;

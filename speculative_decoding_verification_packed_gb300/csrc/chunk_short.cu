@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int32_t shift = top < 128u ? 0 : max(-100, min(141 - (int32_t)(top >> 7), 100));
+                const int32_t shift = ck_q_shift(top);
                 const float f = ck_pow2(shift), back = p.scale_log2 * ck_pow2(-shift);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {

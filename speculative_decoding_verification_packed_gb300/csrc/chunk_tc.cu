@@ -711,8 +711,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
             float e_first = 0.0f;                                    // 8-bit pages: E of V in its first tile
             if (Q8 && (lng || kMono || a < nt)) {
                 // This row of the query in fp16, times the power of two that takes its largest magnitude
-                // to 2^14 or more: 8 bits of mantissa fit, and what falls under fp16's range is less than
-                // 2^-38 of the largest.
+                // to 2^14 or more
                 if (!(ok = wait_all(bar_q(a), nq & 1u)))
                     break;
                 ++nq;
@@ -722,8 +721,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     // (32 columns at a time: all reads, then what is done with them)
 #pragma unroll 1
                     for (int pass = 0; pass < 2; ++pass) {
-                        const int32_t up = 141 - (int32_t)(top >> 7);    // 2^14 over the largest (bf16 bits in top)
-                        const int32_t shift = top < 128u ? 0 : max(-100, min(up, 100));
+                        const int32_t shift = ck_q_shift(top);
                         const float f = ck_pow2(shift);
 #pragma unroll 1
                         for (int x = 0; x < D / 8; x += 4) {

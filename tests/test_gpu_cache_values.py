@@ -236,3 +236,10 @@ def test_every_score_is_zero(hq, hkv, d, rows, qe):
     T = 2500
     c = Cache8(T, hkv, d, 18, k=torch.zeros(T, hkv, d, dtype=BF16, device="cuda"))
     check(c, (query(rows, hq, d, 19).float() * 2.0 ** qe).to(BF16), rows)
+
+
+@pytest.mark.parametrize("qe,ke", [(118, -50), (124, 0), (-116, 60), (-108, 40), (-60, 0)])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_queries_of_any_size(hq, hkv, d, rows, qe, ke):
+    c, q, scale = sized(rows, hq, hkv, d, qe, ke, 18)
+    check(c, q, rows, scale=scale)
