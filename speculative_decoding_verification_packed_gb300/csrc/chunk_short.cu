@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            float z = fmaf(sc[nb][2 * y + x] * kf[y], c[nb][x], e[y]);
+                            float z = fmaf(sc[nb][2 * y + x], kf[y] * c[nb][x], e[y]);
                             if (masked)
                                 z = k0 + key + 8 * y <= last[nb][x] ? z : -INFINITY;
                             sc[nb][2 * y + x] = z;

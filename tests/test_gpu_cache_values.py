@@ -243,3 +243,10 @@ def test_every_score_is_zero(hq, hkv, d, rows, qe):
 def test_queries_of_any_size(hq, hkv, d, rows, qe, ke):
     c, q, scale = sized(rows, hq, hkv, d, qe, ke, 18)
     check(c, q, rows, scale=scale)
+
+
+@pytest.mark.parametrize("qe,ke", [(-104, 112), (-90, 100), (60, -50)])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_keys_of_any_size(hq, hkv, d, rows, qe, ke):
+    c, q, scale = sized(rows, hq, hkv, d, qe, ke, 20)
+    check(c, q, rows, scale=scale)
