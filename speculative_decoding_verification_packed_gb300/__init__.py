@@ -749,6 +749,7 @@ def chunk_attn_workspace_size(hq: int, hkv: int, d: int, dtype=torch.bfloat16) -
 
 
 _chunk_ws: dict = {}
+_CHUNK_WS_MOST = 16       # scratch buffers kept (20 MB each at d = 64, else 40)
 
 
 def _chunk_workspace(hq: int, cache: svp_cache, dtype, raw: int) -> Workspace:
@@ -761,6 +762,9 @@ def _chunk_workspace(hq: int, cache: svp_cache, dtype, raw: int) -> Workspace:
     key = (raw, cache.index, cache.d, dtype)
     ws = _chunk_ws.get(key)
     if ws is None:
+        while len(_chunk_ws) >= _CHUNK_WS_MOST:
+            # (the oldest; torch's allocator gives its memory to later work of its own stream only)
+            _chunk_ws.pop(next(iter(_chunk_ws)), None)
         ws = _chunk_ws[key] = Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype),
                                         cache.device, zeroed=256)
     return ws

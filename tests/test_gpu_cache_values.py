@@ -250,3 +250,22 @@ def test_queries_of_any_size(hq, hkv, d, rows, qe, ke):
 def test_keys_of_any_size(hq, hkv, d, rows, qe, ke):
     c, q, scale = sized(rows, hq, hkv, d, qe, ke, 20)
     check(c, q, rows, scale=scale)
+
+
+# ------------------------------------------------------------------ scratch of calls that bring none
+def test_scratch_of_many_streams_is_bounded():
+    """More streams than scratch buffers are kept for, all at once and in turn."""
+    c = Cache8(3000, 2, 64, 22)
+    q = query(1, 8, 64, 23)
+    ctx, cu = i32([2999]), i32([0, 1])
+    want = svp.chunk_attn(q, ctx, cu, cache=c.cache)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(24)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(svp.chunk_attn(q, ctx, cu, cache=c.cache))
+            assert len(svp._chunk_ws) <= 16
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want[0]) and torch.equal(b, want[1]) for a, b in got)
