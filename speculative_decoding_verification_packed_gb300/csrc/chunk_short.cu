@@ -23,8 +23,8 @@
 //   P' = 2^(s c + e_key - m),  O += P' codes,  l += P' 2^(e_ref - e_key),
 // with m the running maximum of s c + e_key (less kCkLift), so that P' stays within fp16 whatever the
 // exponents (it is rounded to fp16 because the products take 16 bits; scores, m, l and O are fp32).
-// e_ref, one a warp, keeps l in range: 0 until a visible row has e_key < -kShSpan (a row of zeros is written
-// with -112), then kShSpan above the smallest e_key so far.  With P' < 2^15 a term is below 2^79, and 2^20
+// e_ref, one a warp, keeps l in range: 0 until a visible row that is not all zeros has e_key < -kShSpan,
+// then kShSpan above the smallest e_key so far.  With P' < 2^15 a term is below 2^79, and 2^20
 // keys add up to less than 2^100; P' = 2^7 of a key whose e_key is 2^100 above the smallest, or 2^100 above 1
 // where none is below it, counts 2^-93 or more, far from the end of fp32's range.  The test shares
 // the vote on m; with one of its own the call took 363 us, and with the factors made by the V loader 392.
@@ -347,22 +347,33 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
                     if (__any_sync(0xffffffffu, up0 || up1 || (nb == 0 && low))) {
                         if (nb == 0 && __any_sync(0xffffffffu, low)) {
-                            // A row whose byte stands for zeros has codes 0 and e = 0 from here on.  One of NaN counts
-                            // as such a row, and where it lies is noted.  (A row past the last visible key may have
-                            // any byte.)
+                            // A row of zeros has e = 0 from here on: at the e = -112 with which it is written, P' would
+                            // lose its weight beside rows of 2^10 or more.  A row whose byte stands for zeros becomes
+                            // one; one of NaN counts as one, and where it lies is noted.  (A row past the last
+                            // visible key may have any byte.)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const int32_t at = k0 + key + 8 * y;
                                 const bool seen = at < s.len;
+                                uint32_t some = 0;
+#pragma unroll
+                                for (int x = 0; x < D / 64; ++x) {
+                                    const uint32_t chunk = sh_chunk<D>(key + 8 * y, q * (D / 64) + x);
+                                    if (seen && e[y] <= kShZero) {
+                                        st_shared_v4(smem_u32(vt) + chunk, 0u, 0u, 0u, 0u);
+                                    } else {
+                                        const uint4 w4 = *reinterpret_cast<const uint4 *>(vt + chunk);
+                                        some |= (w4.x | w4.y | w4.z | w4.w) & 0x7f7f7f7fu;
+                                    }
+                                }
+                                some |= __shfl_xor_sync(0xffffffffu, some, 1);
+                                some |= __shfl_xor_sync(0xffffffffu, some, 2);
                                 if (seen && e[y] <= kShZero) {
                                     if (e[y] == kShNan)
                                         atomicMin(&m->nan_at[warp], at);
-#pragma unroll
-                                    for (int x = 0; x < D / 64; ++x)
-                                        st_shared_v4(smem_u32(vt) + sh_chunk<D>(key + 8 * y, q * (D / 64) + x), 0u, 0u, 0u, 0u);
                                     fence_proxy_async_smem();
                                 }
-                                if (!seen || e[y] <= kShZero) {
+                                if (!seen || some == 0u) {
                                     sc[0][2 * y] -= e[y];
                                     sc[0][2 * y + 1] -= e[y];
                                     e[y] = 0.0f;

@@ -269,3 +269,23 @@ def test_scratch_of_many_streams_is_bounded():
             assert len(svp._chunk_ws) <= 16
     torch.cuda.synchronize()
     assert all(torch.equal(a, want[0]) and torch.equal(b, want[1]) for a, b in got)
+
+
+# ------------------------------------------------------------------ rows of zeros among large values
+@pytest.mark.parametrize("ve", [0, 30, 45])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_value_rows_of_zeros_among_large_ones_keep_their_weight(hq, hkv, d, rows, ve):
+    """A few keys have values of normal numbers times 2^ve and score 12 powers of two above the others,
+    whose values are zeros and which have a good part of the weight together."""
+    T = 2500 if hkv > 2 else 40000
+    g = torch.Generator(device="cuda").manual_seed(24)
+    k = torch.zeros(T, hkv, d, dtype=BF16, device="cuda")
+    v = (torch.randn(T, hkv, d, generator=g, device="cuda") * 2.0 ** ve).to(BF16)
+    loud = torch.arange(0, T, 5000 if hkv <= 2 else 2501, device="cuda")
+    k[loud, :, 0] = 12.0
+    quiet = torch.ones(T, dtype=torch.bool, device="cuda")
+    quiet[loud] = False
+    v[quiet] = 0
+    q = torch.zeros(rows, hq, d, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    check(Cache8(T, hkv, d, 25, k=k, v=v), q, rows, scale=math.log(2.0))
