@@ -420,12 +420,12 @@ svp_status svp_act_truncate(const float *margins, int64_t stride, int32_t n, int
 /*                                                                                      */
 /* 8-bit rows (SVP_E4M3): the d elements of one token and head are e4m3 codes with one   */
 /* exponent byte b; an element is code * 2^(b - 127).  svp_cache_write picks the smallest */
-/* power of two that takes the row's largest magnitude to 448 or less (b >= 15; an        */
-/* element below 2^-9 of that power rounds to a multiple of it), so scaling is exact and  */
-/* each element is rounded once, to nearest even: at most 2^-4 relative for elements down */
-/* to 2^-15 of the row's largest.  A row with an infinite or NaN element gets b = 255 and */
-/* codes 0: every element of it reads as NaN, as do codes 0x7f and 0xff.  Readers take    */
-/* any byte (b = 0 as 0).                                                                 */
+/* power of two that takes the row's largest magnitude to 448 or less (b >= 15), so        */
+/* scaling is exact and each element is rounded once, to nearest even: at most 2^-4       */
+/* relative for elements down to 2^-13 of the row's largest (2^-6 of that power or more;  */
+/* smaller ones round to a multiple of 2^-9 of it).  A row with an infinite or NaN        */
+/* element gets b = 255 and codes 0: every element of it reads as NaN, as do codes 0x7f   */
+/* and 0xff.  Readers take any byte (b = 0 as 0).                                         */
 typedef struct {
     void *k, *v;                /* page pools, [num_pages] pages of page_size tokens; 16-byte
                                    aligned                                                 */
@@ -495,11 +495,13 @@ svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const in
  * Precision.  Scores, the softmax's maximum and sum, and the output are accumulated in fp32; the
  * probabilities that multiply V are rounded to bf16 over SVP_BF16 pages and to fp16 over SVP_E4M3
  * ones (not at all in fp32), where one (times its value row's power of two) below 2^-21 of the
- * row's largest has fewer digits and one below 2^-32 counts in the sum only.  8-bit rows with hq / hkv * w <= 16 and d <= 128 are used as they are;
- * otherwise 128 positions (a tile) at a time in units of their largest power of two 2^E (of K and
- * of V each, of visible rows, at least 2^-60): exact for rows within 2^15 of it, and an element below
- * 2^(E - 25) counts as 0.  8-bit value rows of one request should have powers of two within 2^100 of
- * one another: beyond, a key's weight can be lost.
+ * row's largest has fewer digits and one below 2^-32 counts in the sum only.  8-bit rows with
+ * hq / hkv * w <= 16 and d <= 128 are used as they are; otherwise 128 positions (a tile) at a time
+ * in units of their largest power of two 2^E (of K and of V each, of visible rows, at least 2^-60):
+ * exact for rows within 2^15 of it, and an element of 2^(E - 25) or less counts as 0.  8-bit value
+ * rows of one request should have powers of two within 2^100 of one another (rows of zeros count as
+ * 2^-60 whatever their byte): beyond, a key's weight can be lost.  lse takes nothing from the
+ * values: it is finite where they are NaN.
  *
  * Rows >= cu_slots[n] and rows of skipped requests are not written.  Device checks as for
  * svp_cache_write, for positions 0 .. ctx_len[i] + k_i - 1; a page id outside the pool reads

@@ -692,7 +692,8 @@ def cache_write(k, v, ctx_len, cu_slots, *, cache: svp_cache, take=None,
                 ws: Optional[Workspace] = None, stream=None) -> None:
     """Store packed rows k, v [m_cap, hkv, d] (bf16 or fp32; slices of a fused projection are
     fine) at positions ctx_len[i] + j of their requests (svp_cache_write).  take [n] int32:
-    only the first take[i] rows of request i, e.g. the accept_len of margin_accept."""
+    only the first take[i] rows of request i, e.g. the accept_len of margin_accept.  ws: 256
+    bytes for the device status, which a call without one does not report."""
     n = _requests(cu_slots, cache, "cu_slots")
     stride = _rows(k, "k", cache.hkv, cache)
     if k.dtype is not v.dtype or _rows(v, "v", cache.hkv, cache) != stride or k.numel() != v.numel():
@@ -712,7 +713,8 @@ def cache_read(start, cu_rows, *, cache: svp_cache, rows: Optional[int] = None,
                ws: Optional[Workspace] = None, stream=None):
     """Positions start[i].. (0.. for None) of each request as contiguous rows
     cu_rows[i]..cu_rows[i+1]-1 of (k_out, v_out) [rows, hkv, d] (svp_cache_read).  Outputs that
-    are not given are made with ``rows`` rows of ``dtype``, zeros where nothing is read."""
+    are not given are made with ``rows`` rows of ``dtype``, zeros where nothing is read.  ws as for
+    cache_write."""
     n = _requests(cu_rows, cache, "cu_rows")
     dev = cache.device
     other = _other_stream(stream, cache)
@@ -754,8 +756,8 @@ _CHUNK_WS_MOST = 16       # scratch buffers kept (20 MB each at d = 64, else 40)
 
 def _chunk_workspace(hq: int, cache: svp_cache, dtype, raw: int) -> Workspace:
     """The scratch of chunk_attn calls that bring none: one for each stream, as calls on two
-    streams may overlap; a call that is being captured gets its own, which lives in the graph's
-    memory, as graphs may be replayed on any stream (and is not zeroed, as its status word, which
+    streams may overlap; a call that is being captured gets its own, which lives in the memory
+    pool that torch.cuda.graph gives the graph, as graphs may be replayed on any stream (and is not zeroed, as its status word, which
     kernels only add bits to, is out of reach)."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return Workspace(chunk_attn_workspace_size(hq, cache.hkv, cache.d, dtype), cache.device, zeroed=0)
@@ -777,7 +779,13 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
     positions 0..ctx_len[i]+j, its own (written by cache_write before) included.  w: largest
     row count of a request (default m_cap; calls of few rows are planned by it).  Returns
     (out [m_cap, hq, d], lse [m_cap, hq] or None); rows past cu_slots[n] are left as they were
-    (zeros in outputs made here)."""
+    (zeros in outputs made here).
+
+    ws: a Workspace of chunk_attn_workspace_size bytes.  Without one the call takes scratch kept for
+    its stream, whose device status nobody can read: what has to see skipped requests, bad pages or
+    time-outs brings ws and asks ws.read_status.  So does a capture begun otherwise than by
+    torch.cuda.graph (or CUDAGraph.capture_begin), as only there the scratch belongs to the graph, and
+    work on a stream that is destroyed before it has run, as a later stream may get the same handle."""
     n = _requests(cu_slots, cache, "cu_slots")
     other = _other_stream(stream, cache)
     if other is not None:
