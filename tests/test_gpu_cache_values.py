@@ -289,3 +289,17 @@ def test_value_rows_of_zeros_among_large_ones_keep_their_weight(hq, hkv, d, rows
     q = torch.zeros(rows, hq, d, dtype=BF16, device="cuda")
     q[..., 0] = 1.0
     check(Cache8(T, hkv, d, 25, k=k, v=v), q, rows, scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("low,high", [(67, 167), (120, 220), (140, 240)])
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_tiles_of_any_power_of_two_within_2_to_the_100(hq, hkv, d, rows, low, high, down):
+    """Value rows of one power of two per 128 positions, over a range of 2^100 up or down the context."""
+    T = 2500
+    c = Cache8(T, hkv, d, 26)
+    tiles = -(-T // 128)
+    for t in range(tiles):
+        at = tiles - 1 - t if down else t
+        c.set_bytes(1, list(range(128 * t, min(T, 128 * t + 128))), low + (high - low) * at // (tiles - 1))
+    check(c, query(rows, hq, d, 27), rows)
