@@ -9,21 +9,25 @@ namespace svp {
 constexpr int kCkKeys = 128;          // keys a KV tile
 constexpr int kCkSub = 16384;         // [128 rows][64] bf16, 128-byte swizzled
 // Cost of starting a pair, in keys.  A prompt of 4096 tokens and 24 blocks of 8 among two prompts of 2048
-// (8-bit) took 182 and 354 us with 64, 149 and 349 with 256, 151 and 344 with 512.
+// (8-bit) take 178 and 332 us with 64, 146 and 325 with 256, 140 and 319 with 512.  (512 was not looked at
+// over other calls.)
 constexpr int kStartKeys = 256;
-// Cost of a key with one query tile, and with two: when 3 to 4 took 341 us on those blocks and prompts, 2 to
-// 3 took 356 and 1 to 1 361 (calls of one kind are indifferent).
+// Cost of a key with one query tile, and with two: where 3 to 4 takes 325 us on those blocks and prompts, 2 to
+// 3 takes 329 and 1 to 1 345 (the one prompt takes 146 to 147 with each).
 constexpr int kShortCost = 3, kLongCost = 4;
-// Smallest share of a CTA, more than a tile's cost: a shorter one is not worth its join.  One token over 500 keys 14.6 us, with 2048 16.5.
+// Smallest share of a CTA, more than a tile's cost: a shorter one is not worth its join.  One token over 500
+// keys takes 14.6 us, with 2048 16.6 (700 keys 14.6 and 19.0).
 constexpr int kShareCost = 640;
-constexpr float kCkSlack = 8.0f;      // P stays below 2^8 times its value at the reference
+// P stays below 2^8 times its value at the reference, but over bf16 pages in a tile that is read once: there it
+// may go on as long as a row's sum over the tile is at most 2^15 (chunk_tc.cu).
+constexpr float kCkSlack = 8.0f;
 // P in fp16 (8-bit pages) is 2^7 at the reference: with the slack it stays below 2^15, and what fp16 cannot
 // hold (digits under 2^-24) is 2^-31 of the row's largest probability, so that a million keys lose no weight.
 constexpr float kCkLift = 7.0f;
 
 // Query rows of a KV head up to which 8-bit pages take chunk_short.cu.  64 requests x 18000 keys, 8 KV heads,
-// d 128, 4 and 16 rows: 362 and 470 us there, 640 and 643 in chunk_tc.cu (d 64, 2 and 16 rows: 333 and 360
-// against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 644 in chunk_tc.cu.
+// d 128, 4 and 16 rows: 361 and 489 us there, 640 and 643 in chunk_tc.cu (d 64, 4 and 16 rows: 328 and 352
+// against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 646 in chunk_tc.cu.
 constexpr int kShortRows = 16;
 
 struct ChunkDesc {                    // a pair that was split: read by the joining kernel
