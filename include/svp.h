@@ -494,14 +494,14 @@ svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const in
  *
  * Precision.  Scores, the softmax's maximum and sum, and the output are accumulated in fp32; the
  * probabilities that multiply V are rounded to bf16 over SVP_BF16 pages and to fp16 over SVP_E4M3
- * ones (not at all in fp32), where one (times its value row's power of two) below 2^-21 of the
- * row's largest has fewer digits and one below 2^-32 counts in the sum only.  8-bit rows with
- * hq / hkv * w <= 16 and d <= 128 are used as they are; otherwise 128 positions (a tile) at a time
- * in units of their largest power of two 2^E (of K and of V each, of visible rows, at least 2^-60):
- * exact for rows within 2^15 of it, and an element of 2^(E - 25) or less counts as 0.  8-bit value
- * rows of one request should have powers of two within 2^100 of one another (rows of zeros count as
- * 2^-60 whatever their byte): beyond, a key's weight can be lost.  lse takes nothing from the
- * values: it is finite where they are NaN.
+ * ones (not at all in fp32), where one (times the power of two of its value row, or of its tile,
+ * see below) under 2^-21 of the row's largest has fewer digits and one under 2^-32 counts in the
+ * sum only.  8-bit rows with hq / hkv * w <= 16 and d <= 128 are used as they are; otherwise 128
+ * positions (a tile) at a time in units of their largest power of two 2^E (of K and of V each, of
+ * visible rows, at least 2^-60): exact for rows within 2^15 of it, and an element of 2^(E - 25) or
+ * less counts as 0.  8-bit value rows of one request should have powers of two within 2^100 of one
+ * another (rows of zeros count as 2^-60 whatever their byte): beyond, a key's weight can be lost.
+ * lse takes nothing from the values: it is finite where they are NaN.
  *
  * Rows >= cu_slots[n] and rows of skipped requests are not written.  Device checks as for
  * svp_cache_write, for positions 0 .. ctx_len[i] + k_i - 1; a page id outside the pool reads

@@ -42,6 +42,9 @@ constexpr int kShThreads = 32 * (kShWarps + 2);
 constexpr int kShSlots = 16;          // ring slots at most
 constexpr float kShSpan = 64.0f;      // e_ref - e_key, at most
 constexpr float kShNan = -128.0f, kShZero = -127.0f;   // e_key of a value row that stands for NaN, for zeros
+// e_key that rows of zeros get: above -kShSpan, so that they do not move e_ref, and low, so that one that takes
+// most of the weight leaves fp16's range to the others (at 0, one of 2^24 times their weight took their digits)
+constexpr float kShZeros = -60.0f;
 
 struct ShortMisc {
     uint64_t bars[2 * kShSlots];
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
             };
             auto exps_of = [&](int32_t t, int32_t id) -> uint32_t {
                 if (id < 0)
-                    return 0x7f7f7f7fu;
+                    return 0x43434343u;          // (2^kShZeros)
                 const int64_t at = (((int64_t)id * p.c.hkv + s.g) << p.c.page_shift) + ((t * kCkKeys + lane * 4) & in_page);
                 return __ldg(reinterpret_cast<const uint32_t *>(exps + at));
             };
@@ -348,8 +351,8 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     const bool up1 = top[1] > mx[nb][1] + (kCkSlack + kCkLift) || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
                     if (__any_sync(0xffffffffu, up0 || up1 || (nb == 0 && low))) {
                         if (nb == 0 && __any_sync(0xffffffffu, low)) {
-                            // A row of zeros has e = 0 from here on: at the e = -112 with which it is written, P' would
-                            // lose its weight beside rows of 2^10 or more.  A row whose byte stands for zeros becomes
+                            // A row of zeros has e = kShZeros from here on: at the e = -112 with which it is written, P'
+                            // would lose its weight beside rows of 2^10 or more.  A row whose byte stands for zeros becomes
                             // one; one of NaN counts as one, and where it lies is noted.  (A row past the last
                             // visible key may have any byte.)
 #pragma unroll
@@ -375,9 +378,9 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                                     fence_proxy_async_smem();
                                 }
                                 if (!seen || some == 0u) {
-                                    sc[0][2 * y] -= e[y];
-                                    sc[0][2 * y + 1] -= e[y];
-                                    e[y] = 0.0f;
+                                    sc[0][2 * y] += kShZeros - e[y];
+                                    sc[0][2 * y + 1] += kShZeros - e[y];
+                                    e[y] = kShZeros;
                                 }
                             }
 #pragma unroll

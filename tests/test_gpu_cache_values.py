@@ -303,3 +303,21 @@ def test_tiles_of_any_power_of_two_within_2_to_the_100(hq, hkv, d, rows, low, hi
         at = tiles - 1 - t if down else t
         c.set_bytes(1, list(range(128 * t, min(T, 128 * t + 128))), low + (high - low) * at // (tiles - 1))
     check(c, query(rows, hq, d, 27), rows)
+
+
+@pytest.mark.parametrize("up", [8, 24, 60])
+@pytest.mark.parametrize("hq,hkv,d,rows", [x for x in CALLS if x[2] <= 128 and x[0] // x[1] * x[3] <= 16])
+def test_digits_beside_a_value_row_of_zeros(hq, hkv, d, rows, up):
+    """The first key's value is zeros and it is 2^up times as probable as the few others, whose
+    probabilities keep their digits: what comes out is theirs."""
+    T = rows + 2
+    g = torch.Generator(device="cuda").manual_seed(28)
+    k = torch.randn(T, hkv, d, generator=g, device="cuda") * 0.5
+    v = torch.randn(T, hkv, d, generator=g, device="cuda").to(BF16)
+    k[:, :, 0] = 0
+    k[0] = 0
+    k[0, :, 0] = up
+    v[0] = 0
+    q = query(rows, hq, d, 29)
+    q[..., 0] = 1.0
+    check(Cache8(T, hkv, d, 30, k=k.to(BF16), v=v), q, rows, scale=math.log(2.0))
