@@ -28,7 +28,8 @@
 // keys add up to less than 2^100; P' = 2^7 of a key whose e_key is 2^100 above the smallest, or 2^100 above 1
 // where none is below it, counts 2^-93 or more, far from the end of fp32's range.  The test shares
 // the vote on m; with one of its own the call took 363 us, and with the factors made by the V loader 392.
-// (Without e_ref, when rows of zeros made l infinite, it took 358, and 16 rows 469.)
+// (Without e_ref, when rows of zeros made l infinite, it took 358, and 16 rows 469.)  Where most tiles have
+// rows of zeros, which are looked at again in each, it takes 480, and 16 rows 682.
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
 #include <algorithm>
 #include <cstring>
