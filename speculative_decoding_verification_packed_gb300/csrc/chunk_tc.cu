@@ -867,14 +867,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar_mlfree);
-                    // a half without a visible key has l = 0 and is left out whatever its O holds
+                    // a half without a visible key has l = 0 and is left out whatever its O holds (not so one whose
+                    // weight underflows: its O may be NaN)
                     if (o.y != 0.0f) {
                         const float mx = fmaxf(m_ref, o.x);
                         f0 = m_ref == -INFINITY ? 0.0f : fast_exp2(m_ref - mx);
                         f1 = fast_exp2(o.x - mx);
                         l = l * f0 + o.y * f1;
                         m_ref = mx;
-                        f1 *= o1_scale;
+                        f1 = fmaxf(f1 * o1_scale, FLT_MIN);
                     }
                 }
                 f0 *= o_scale;
@@ -1097,7 +1098,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const __gri
             acc[e] = 0.0f;
         for (int32_t q0 = 0; q0 < np; q0 += 16) {
             const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? __ldcg(p.part_ml + at(q0 + lane)) : none;
-            const float w = ml.y != 0.0f ? fast_exp2(ml.x - M) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
+            // (more than 0 where there is a visible key: its O may be NaN)
+            const float w = ml.y != 0.0f ? fmaxf(fast_exp2(ml.x - M), FLT_MIN) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
             auto add = [&](int32_t q, const float (&x)[E]) {
                 const float wq = __shfl_sync(0xffffffffu, w, q, 16);
                 L += __shfl_sync(0xffffffffu, wl, q, 16);

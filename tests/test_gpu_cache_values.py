@@ -321,3 +321,33 @@ def test_digits_beside_a_value_row_of_zeros(hq, hkv, d, rows, up):
     q = query(rows, hq, d, 29)
     q[..., 0] = 1.0
     check(Cache8(T, hkv, d, 30, k=k.to(BF16), v=v), q, rows, scale=math.log(2.0))
+
+
+# ------------------------------------------------------------------ NaN under no weight
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("at", [100, 200, 8000])
+@pytest.mark.parametrize("hq,hkv,d,rows", CALLS)
+def test_nan_value_under_a_vanishing_probability(hq, hkv, d, rows, at, kind):
+    """A value row of NaN whose key scores 2^300 below the first: 0 times NaN, as in the plain form, in
+    whichever part of the keys it lies."""
+    T = 9000 if hkv <= 2 else 300
+    at = min(at, T - rows - 1)
+    k = torch.zeros(T, hkv, d, dtype=BF16, device="cuda")
+    v = torch.ones(T, hkv, d, dtype=BF16, device="cuda")
+    k[0, :, 0] = 304.0
+    v[at, hkv - 1] = float("nan")
+    q = torch.zeros(rows, hq, d, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    if kind == E4M3:
+        cache = Cache8(T, hkv, d, 31, k=k, v=v).cache
+    else:
+        pages = -(-T // 16)
+        pools = [torch.zeros(pages, hkv, 16, d, dtype=BF16, device="cuda") for _ in range(2)]
+        cache = svp.make_cache(*pools, torch.arange(pages, device="cuda", dtype=torch.int32)[None].contiguous())
+        svp.cache_write(k, v, i32([0]), i32([0, T]), cache=cache)
+    out, lse = svp.chunk_attn(q, i32([T - rows]), i32([0, rows]), cache=cache, w=rows, scale=math.log(2.0))
+    G = hq // hkv
+    assert torch.isnan(out[:, -G:]).all()
+    assert (out[:, :-G] == 1).all()
+    top = 304.0 if kind == BF16 else 320.0          # (304 = 9.5 * 32 goes to 10 * 32 in e4m3)
+    assert (lse - top * math.log(2.0)).abs().max() < 1e-3
