@@ -152,15 +152,16 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         bool ok = true;
         for (bool have = have0; have && ok; have = ck_next<1>(p, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
-            constexpr int32_t kNone = INT32_MIN;
+            constexpr int32_t kNone = INT32_MIN;   // (a table may hold it too: see checked)
             auto page_of = [&](int32_t t) -> int32_t {
                 const int32_t at = t * kCkKeys + lane * 4;
                 return t >= s.t1 || (at & ~in_page) >= s.len ? kNone : __ldg(bt + (at >> p.c.page_shift));
             };
-            auto checked = [&](int32_t id) -> int32_t {
+            auto needed = [&](int32_t t) { return t < s.t1 && ((t * kCkKeys + lane * 4) & ~in_page) < s.len; };
+            auto checked = [&](int32_t id, int32_t t) -> int32_t {
                 if (id >= 0 && id < p.c.num_pages)
                     return id;
-                if (id != kNone)
+                if (id != kNone || needed(t))
                     set_status(p.status, SVP_DEV_BAD_CONTEXT);
                 return -1;
             };
@@ -171,10 +172,10 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 return __ldg(reinterpret_cast<const uint32_t *>(exps + at));
             };
             // (page ids three tiles ahead, exponents two)
-            int32_t id = checked(page_of(s.t0)), id1 = checked(page_of(s.t0 + 1)), id2 = page_of(s.t0 + 2);
+            int32_t id = checked(page_of(s.t0), s.t0), id1 = checked(page_of(s.t0 + 1), s.t0 + 1), id2 = page_of(s.t0 + 2);
             uint32_t e = exps_of(s.t0, id), e1 = exps_of(s.t0 + 1, id1);
             for (int32_t t = s.t0; t < s.t1; ++t, ++done) {
-                id2 = checked(id2);
+                id2 = checked(id2, t + 2);
                 const int32_t id3 = page_of(t + 3);
                 const uint32_t e2 = exps_of(t + 2, id2);
                 int got = 1;

@@ -348,17 +348,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
         const bool needs_k = me == 0 || !Cfg::kByKind;    // (the first loader tells the softmax of both)
         for (bool have = have0; have && ok; have = ck_next<NT>(p, s, v1)) {
             const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
-            constexpr int32_t kNone = INT32_MIN;             // nothing of the tile needs a page here
+            auto needed = [&](int32_t t) { return t < s.t1 && ((t * kCkKeys + lane * 4) & ~in_page) < s.len; };
             auto page_of = [&](int32_t t) -> int32_t {
-                const int32_t at = t * kCkKeys + lane * 4;
-                if (t >= s.t1 || (at & ~in_page) >= s.len)
-                    return kNone;
-                return __ldg(bt + (at >> p.c.page_shift));
+                return needed(t) ? __ldg(bt + ((t * kCkKeys + lane * 4) >> p.c.page_shift)) : -1;
             };
-            auto checked = [&](int32_t id) -> int32_t {      // -1: none, or none in the pool
+            auto checked = [&](int32_t id, int32_t t) -> int32_t {   // -1: none, or none in the pool
                 if (id >= 0 && id < p.c.num_pages)
                     return id;
-                if (id != kNone)
+                if (needed(t))
                     set_status(p.status, SVP_DEV_BAD_CONTEXT);
                 return -1;
             };
@@ -369,11 +366,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 return __ldg(reinterpret_cast<const uint32_t *>((kv ? p.c.v_exp : p.c.k_exp) + at));
             };
             const bool once = s.nb == 1;      // no other block of the request reads these keys
-            int32_t id = checked(page_of(s.t0)), id1 = checked(page_of(s.t0 + 1)), id2 = page_of(s.t0 + 2);
+            int32_t id = checked(page_of(s.t0), s.t0), id1 = checked(page_of(s.t0 + 1), s.t0 + 1), id2 = page_of(s.t0 + 2);
             uint32_t ek = needs_k ? exps_of(0, s.t0, id) : 0u, ek1 = needs_k ? exps_of(0, s.t0 + 1, id1) : 0u;
             uint32_t ev = exps_of(1, s.t0, id), ev1 = exps_of(1, s.t0 + 1, id1);
             for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++done) {
-                id2 = checked(id2);
+                id2 = checked(id2, t + 2);
                 const int32_t id3 = page_of(t + 3);
                 const uint32_t ek2 = needs_k ? exps_of(0, t + 2, id2) : 0u, ev2 = exps_of(1, t + 2, id2);
                 // the largest exponent of the tile's visible rows, at least 2^-60 (NaN rows apart)

@@ -351,3 +351,32 @@ def test_nan_value_under_a_vanishing_probability(hq, hkv, d, rows, at, kind):
     assert (out[:, :-G] == 1).all()
     top = 304.0 if kind == BF16 else 320.0          # (304 = 9.5 * 32 goes to 10 * 32 in e4m3)
     assert (lse - top * math.log(2.0)).abs().max() < 1e-3
+
+
+# ------------------------------------------------------------------ page ids
+@pytest.mark.parametrize("bad", [-(1 << 31), -(1 << 31) + 1, -1, (1 << 31) - 1])
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("rows,d", [(1, 64), (40, 128), (1, 256)])
+def test_every_page_id_outside_the_pool_sets_the_status(rows, d, kind, bad):
+    T, hkv, hq = 1000, 2, 8
+    pages = -(-T // 16)
+    g = torch.Generator(device="cuda").manual_seed(32)
+    x = [torch.randn(pages, hkv, 16, d, generator=g, device="cuda").to(BF16).to(kind) for _ in range(2)]
+    e = [torch.full((pages, hkv, 16), 127, dtype=torch.uint8, device="cuda") for _ in range(2)] if kind == E4M3 else [None, None]
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None].contiguous()
+    cache = svp.make_cache(*x, table, k_exp=e[0], v_exp=e[1])
+    q = query(rows, hq, d, 33)
+    got = []
+    for page in (bad, None):
+        if page is None:                  # the same page as zeros
+            table[0, 7] = 7
+            for z in x:
+                z.view(torch.uint8)[7] = 0
+        else:
+            table[0, 7] = page
+        ws = svp.Workspace(svp.chunk_attn_workspace_size(hq, hkv, d))
+        got.append(svp.chunk_attn(q, i32([T - rows]), i32([0, rows]), cache=cache, w=rows, ws=ws))
+        assert ws.read_status() == (svp.DEV_BAD_CONTEXT if page is not None else 0)
+    # (a page of zeros may have another power of two than the rows of zeros written here: two more roundings)
+    assert (got[0][0].float() - got[1][0].float()).abs().max() <= 2 * 2.0 ** -8 * got[1][0].float().abs().max()
+    assert (got[0][1] - got[1][1]).abs().max() <= 1e-4
