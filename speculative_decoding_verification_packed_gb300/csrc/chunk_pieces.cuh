@@ -26,7 +26,7 @@ constexpr float kCkSlack = 8.0f;
 constexpr float kCkLift = 7.0f;
 
 // Query rows of a KV head up to which 8-bit pages take chunk_short.cu.  64 requests x 18000 keys, 8 KV heads,
-// d 128, 4 and 16 rows: 361 and 489 us there, 640 and 643 in chunk_tc.cu (d 64, 4 and 16 rows: 328 and 352
+// d 128, 4 and 16 rows: 363 and 488 us there, 640 and 643 in chunk_tc.cu (d 64, 4 and 16 rows: 330 and 352
 // against 571 and 574).  32 rows, in two groups of warps, took 854 us there and take 649 in chunk_tc.cu.
 constexpr int kShortRows = 16;
 

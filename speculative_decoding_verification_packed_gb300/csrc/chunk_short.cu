@@ -6,7 +6,7 @@
 // and read again by the tensor core, more shared-memory traffic than the bytes' time allows (64
 // requests x 18000 tokens, 8 KV heads, d 128: 640 us).  Here codes go from shared memory to registers,
 // are widened there (cvt: two codes an instruction), and warp-level m16n8k16 products take them as
-// they are: 361 us, 6.6 TB/s with 16-token pages and 344 us with 128-token ones.
+// they are: 363 us, 6.6 TB/s with 16-token pages and 344 us with 128-token ones.
 //
 // Keys are the products' 16-row side and query rows the 8-column side,
 //   S^T (16 keys x 8 rows) = K Q^T,   O^T (16 of d x 8 rows) += V^T P^T,
@@ -14,7 +14,7 @@
 // empty for G = 4 tokens, the same call took 467 us when this way took 381).  Eight warps share the
 // 128 positions of a KV tile, 16 each.  A warp keeps Q (fp16, the row's power of two taken out), its rows'
 // running maximum and sum and its O in registers; the warps join at the end of a piece through shared
-// memory.  NB = 1 or 2 blocks of 8 rows (489 us with 16 rows, bound by the products).  d = 64 takes 328 us
+// memory.  NB = 1 or 2 blocks of 8 rows (488 us with 16 rows, bound by the products).  d = 64 takes 330 us
 // for half the bytes: the chain of a tile is as long, and copies of 1 KB come no faster than those
 // of 2 KB (262 us with 128-token pages).  d is taken in the order in which a thread finds it: for S,
 // thread q of a quad has d = D/4 q .. of its key in one read; for O, d = D/8 n + i belongs to row n of
@@ -27,7 +27,7 @@
 // then kShSpan above the smallest e_key so far.  With P' < 2^15 a term is below 2^79, and 2^20
 // keys add up to less than 2^100; P' = 2^7 of a key whose e_key is 2^100 above the smallest, or 2^100 above 1
 // where none is below it, counts 2^-93 or more, far from the end of fp32's range.  The test shares
-// the vote on m; with one of its own the call took 363 us, and with the factors made by the V loader 392.
+// the vote on m; one of its own cost 3 us more, and the factors made by the V loader 32.
 // (Without e_ref, when rows of zeros made l infinite, it took 358, and 16 rows 469.)  Where most tiles have
 // rows of zeros, which are looked at again in each, it takes 480, and 16 rows 682.
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
