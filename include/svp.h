@@ -516,6 +516,70 @@ svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *
                           int32_t m_cap, int32_t w, const svp_heads *heads, svp_dtype dtype,
                           void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------- */
+/* Rotary positions for the rows of a step, and the same together with the cache's write.  */
+/*   pos = ctx_len[i] + j of row j of request i (or pos[row]);  pair t < rot / 2 of a head   */
+/*   turns by the angle 2 pi pos freq[t] / 2^64:                                            */
+/*     (x, y) -> scale (x cos - y sin, x sin + y cos)                                       */
+/*   with (x, y) = elements (t, t + rot / 2), or (2 t, 2 t + 1) when interleaved.  Elements   */
+/*   from rot on stay as they are.  pos * freq is taken modulo 2^64, i.e. whole turns drop   */
+/*   out exactly, so far positions lose nothing; sine, cosine and the products are fp32.     */
+/*   Negative positions turn back: rows rotated at pos and then at -pos are the rows again   */
+/*   (but for their roundings), which is also the gradient's way back.                       */
+typedef enum {
+    SVP_ROPE_NONE = 0,       /* base^(-2t / rot) radians a position                         */
+    SVP_ROPE_LINEAR = 1,     /* divided by factor (positions interpolated)                  */
+    SVP_ROPE_NTK = 2,        /* base * factor^(rot / (rot - 2)) in base's place             */
+    SVP_ROPE_YARN = 3        /* pairs that turn more than `fast` times in `original` tokens
+                                as NONE, those that turn less than `slow` times as LINEAR, a
+                                straight line (in t) between.  That method's factor on the
+                                scores, 0.1 ln(factor) + 1 on q and k each, is `scale`.      */
+} svp_rope_scaling;
+
+/* Fills freq[0 .. rot / 2 - 1] (HOST memory): turns a position in units of 2^-64, from 64-bit
+ * radians.  rot even and >= 2, base > 1, factor > 0; YARN: original >= 1, 0 < slow < fast
+ * (SVP_EINVAL otherwise).  For SVP_ROPE_NTK rot = 2 has nothing to change. */
+svp_status svp_rope_frequencies(int32_t rot, double base, svp_rope_scaling scaling, double factor,
+                                int32_t original, double slow, double fast, uint64_t *freq);
+
+typedef struct {
+    const uint64_t *freq;    /* device [rot / 2]                                            */
+    int32_t rot;             /* elements of a head that turn: even, 2 <= rot <= d           */
+    int32_t interleaved;     /* 0: pairs (t, t + rot / 2), 1: (2 t, 2 t + 1)                 */
+    float scale;             /* on the elements that turn; finite                           */
+} svp_rotary;
+
+/*
+ * q [m_cap, hq, d], k [m_cap, hkv, d] (dtype SVP_F32 or SVP_BF16), row r at element r * row
+ * stride (slices of a fused projection); q_out, k_out of the same type and shape with strides of
+ * their own.  An output may be its input itself (the same address and stride); otherwise no output
+ * overlaps an input or another output.  q and q_out, or k and k_out, may be NULL (hq or hkv is then
+ * not looked at).  All 16-byte aligned, strides >= heads * d and multiples of 16 bytes.
+ * pos [m_cap] int32 or NULL; ctx_len [n] int32 (NULL only with pos); cu_slots [n+1] int32
+ * ws at least 256 bytes, zeroed once by svp_workspace_init (status word only)
+ * d = 64, 128 or 256.  Rows of no request are not written.  A request whose rows leave [0, m_cap) or
+ * run backwards is skipped (SVP_DEV_BAD_SLOTS), without pos one with ctx_len < 0 or positions past
+ * 2^31 - 1 too (SVP_DEV_BAD_CONTEXT).
+ */
+svp_status svp_rope(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                    svp_dtype dtype, const svp_rotary *rotary, const int32_t *pos,
+                    const int32_t *ctx_len, const int32_t *cu_slots, int32_t n, int32_t m_cap,
+                    int32_t hq, int32_t hkv, int32_t d, void *q_out, int64_t q_out_stride,
+                    void *k_out, int64_t k_out_stride, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * svp_rope for q (NULL: none) and k, with the rotated k and v written to the cache as
+ * svp_cache_write does (positions ctx_len[i] + j, take, types, errors and status bits are its own;
+ * pos, where given, is for the angles only).  k goes from fp32 to the cache's type in one rounding.
+ * A request that svp_cache_write skips is skipped for q too; rows behind take[i] are rotated in q.
+ */
+svp_status svp_rope_cache_write(const void *q, int64_t q_row_stride, const void *k, const void *v,
+                                int64_t kv_row_stride, svp_dtype dtype, const svp_rotary *rotary,
+                                const svp_cache *cache, const int32_t *pos, const int32_t *ctx_len,
+                                const int32_t *cu_slots, const int32_t *take, int32_t n,
+                                int32_t m_cap, int32_t hq, int32_t hkv, int32_t d, void *q_out,
+                                int64_t q_out_stride, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,8 @@ Entry points (same names as the C ABI, without the ``svp_`` prefix):
   cache_read           cached positions back to contiguous rows
   chunk_attn           attention of decode tokens, candidate blocks and prompt chunks whose
                        keys and values are in the cache already
+  rope                 rotary positions of query / key rows (rope_frequencies makes the table)
+  rope_cache_write     the same with the rotated keys and the values written into the cache
 """
 from __future__ import annotations
 
@@ -35,6 +37,7 @@ SVP_OK, SVP_EINVAL, SVP_EUNSUPPORTED, SVP_EWORKSPACE, SVP_ECUDA = 0, 1, 2, 3, 4
 SVP_F32, SVP_BF16, SVP_E4M3 = 0, 1, 2
 TILE_AUTO, TILE_SHORT, TILE_FIXED128, TILE_WIDE, TILE_SHORT_UNPACKED = 0, 1, 2, 3, 4
 DEV_BAD_SLOTS, DEV_BAD_CONTEXT, DEV_TIMEOUT, DEV_WORKSPACE = 0x1, 0x2, 0x4, 0x8
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class SvpError(RuntimeError):
@@ -72,6 +75,11 @@ class svp_cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int64), ("stride_page", ctypes.c_int64),
                 ("stride_head", ctypes.c_int64), ("stride_tok", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
+
+
+class svp_rotary(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 GATHER_MAX_FIELDS = 8
@@ -157,6 +165,19 @@ _SIGS = {
         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(svp_heads),
         ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
         ctypes.c_void_p]),
+    "svp_rope_frequencies": (ctypes.c_int, [
+        ctypes.c_int32, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_int32, ctypes.c_double,
+        ctypes.c_double, ctypes.c_void_p]),
+    "svp_rope": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(svp_rotary),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_rope_cache_write": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+        ctypes.POINTER(svp_rotary), ctypes.POINTER(svp_cache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "svp_margin_accept": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
@@ -817,3 +838,148 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
     if st:
         raise SvpError(st, "svp_chunk_attn")
     return out, lse
+
+
+# ----------------------------------------------------------------- rotary positions
+def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original: int = 0, slow: float = 1.0, fast: float = 32.0, device="cuda") -> torch.Tensor:
+    """Table [rot / 2] of rope's pairs: turns a position in units of 2^-64 (svp_rope_frequencies), as int64
+    that holds the unsigned bits.  scaling: "none", "linear" (frequencies / factor), "ntk" (base * factor^(rot /
+    (rot - 2))) or "yarn" (by how often a pair turns in ``original`` positions)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    _check(lib().svp_rope_frequencies(int(rot), base, ROPE_SCALINGS[scaling], factor, int(original), slow, fast,
+                                      out.data_ptr()), "svp_rope_frequencies")
+    return out.to(device)
+
+
+def _rope_index(*tensors) -> int:
+    """Index of the one CUDA device that the tensors are on, which has to be the current one."""
+    index = -1
+    for t in tensors:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("the rows must be CUDA tensors (no CPU path exists)")
+            if index not in (-1, t.get_device()):
+                raise ValueError("the rows must be on one device")
+            index = t.get_device()
+    if index < 0:
+        raise ValueError("give q or k")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError("the rows must be on the current CUDA device")
+    return index
+
+
+def _rope_rows(t, name: str) -> int:
+    """Row stride of rows [m, heads, d] whose heads and elements are contiguous."""
+    m, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
+        raise ValueError(f"{name} needs contiguous rows (any row stride)")
+    return s0 if m > 1 else h * d
+
+
+def _rope_out(x, out, name: str):
+    """The output rows of x: given, or zeros."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"{name} without its input")
+        return None, 0, 0
+    if out is None:
+        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != x.get_device():
+        raise ValueError(f"{name} must have its input's shape, type and device")
+    return out, out.data_ptr(), _rope_rows(out, name)
+
+
+def _rope_i32(t, name: str, count: int, index: int) -> int:
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name} must be {count} or more contiguous int32 values on the rows' device")
+    return t.data_ptr()
+
+
+def _rotary(freq, interleaved: bool, scale: float, index: int) -> svp_rotary:
+    if freq.dtype is not torch.int64 or freq.get_device() != index or not freq.is_contiguous() or freq.dim() != 1:
+        raise ValueError("freq must be rope_frequencies' table on the rows' device")
+    return svp_rotary(freq.data_ptr(), 2 * freq.numel(), 1 if interleaved else 0, scale)
+
+
+def _stream_context(stream, device, index: int):
+    """As _other_stream, for calls without a cache."""
+    raw = _stream(stream)
+    if raw == torch._C._cuda_getCurrentRawStream(index):
+        return None
+    return torch.cuda.stream(torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device))
+
+
+def rope(q, k, ctx_len, cu_slots, *, freq, interleaved: bool = False, scale: float = 1.0, pos=None, q_out=None,
+         k_out=None, ws: Optional[Workspace] = None, stream=None):
+    """Rotary positions (svp_rope) of packed rows q [m_cap, hq, d] and k [m_cap, hkv, d] (bf16 or fp32, slices
+    of a fused projection are fine; either may be None): row j of request i at position ctx_len[i] + j, or at
+    pos[row] (int32 [m_cap]; ctx_len may be None then).  freq: rope_frequencies' table, whose length is half the
+    number of elements of a head that turn.  Returns (q_out, k_out), which may be given and may be q and k
+    themselves; rows past cu_slots[n] are left as they were (zeros in outputs made here).  ws as for
+    cache_write."""
+    if stream is not None:
+        t = q if q is not None else k
+        other = _stream_context(stream, t.device, _rope_index(t))
+        if other is not None:
+            with other:
+                return rope(q, k, ctx_len, cu_slots, freq=freq, interleaved=interleaved, scale=scale, pos=pos,
+                            q_out=q_out, k_out=k_out, ws=ws)
+    index = _rope_index(q, k)
+    if q is not None and k is not None and (q.dtype is not k.dtype or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]):
+        raise ValueError("q and k need one type, number of rows and head size")
+    m, _, d = (q if q is not None else k).shape
+    qs, hq = (0, 0) if q is None else (_rope_rows(q, "q"), q.shape[1])
+    ks, hkv = (0, 0) if k is None else (_rope_rows(k, "k"), k.shape[1])
+    q_out, qo, qos = _rope_out(q, q_out, "q_out")
+    k_out, ko, kos = _rope_out(k, k_out, "k_out")
+    n = cu_slots.numel() - 1
+    if ws is None:
+        ws = _workspace(("cache",), 256, (q if q is not None else k).device, None)
+    st = lib().svp_rope(
+        0 if q is None else q.data_ptr(), qs, 0 if k is None else k.data_ptr(), ks, _dtype_code(q if q is not None else k),
+        _rotary(freq, interleaved, scale, index), _rope_i32(pos, "pos", m, index), _rope_i32(ctx_len, "ctx_len", n, index),
+        _rope_i32(cu_slots, "cu_slots", n + 1, index), n, m, hq, hkv, d, qo, qos, ko, kos, ws.ptr, ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        raise SvpError(st, "svp_rope")
+    return q_out, k_out
+
+
+def rope_cache_write(q, k, v, ctx_len, cu_slots, *, cache: svp_cache, freq, interleaved: bool = False,
+                     scale: float = 1.0, pos=None, q_out=None, take=None, ws: Optional[Workspace] = None, stream=None):
+    """rope of q (None: none) and k with k and v then stored in the cache as cache_write stores them, in one
+    launch (svp_rope_cache_write); pos is for the angles only, the cache positions are ctx_len[i] + j.  Returns
+    q_out (q itself may be given)."""
+    n = _requests(cu_slots, cache, "cu_slots")
+    other = _other_stream(stream, cache)
+    if other is not None:
+        with other:
+            return rope_cache_write(q, k, v, ctx_len, cu_slots, cache=cache, freq=freq, interleaved=interleaved,
+                                    scale=scale, pos=pos, q_out=q_out, take=take, ws=ws)
+    m = k.shape[0]
+    stride = _rows(k, "k", cache.hkv, cache)
+    if k.dtype is not v.dtype or _rows(v, "v", cache.hkv, cache) != stride or v.shape[0] != m:
+        raise ValueError("k and v need one shape, type and row stride")
+    qs, hq = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        qs = _rows(q, "q", hq, cache)
+        if q.dtype is not k.dtype or q.shape[0] != m:
+            raise ValueError("q and k need one type and number of rows")
+    q_out, qo, qos = _rope_out(q, q_out, "q_out")
+    if ws is None:
+        ws = _cache_workspace(cache, stream)
+    st = lib().svp_rope_cache_write(
+        0 if q is None else q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), stride, _dtype_code(k),
+        _rotary(freq, interleaved, scale, cache.index), cache, _i32(pos, "pos", m, cache),
+        _i32(ctx_len, "ctx_len", n, cache), _i32(cu_slots, "cu_slots", n + 1, cache), _i32(take, "take", n, cache), n, m,
+        hq, cache.hkv, cache.d, qo, qos, ws.ptr, ws.nbytes, _raw_stream(None, cache))
+    if st:
+        raise SvpError(st, "svp_rope_cache_write")
+    return q_out

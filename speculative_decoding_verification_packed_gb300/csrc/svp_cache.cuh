@@ -55,4 +55,77 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
     return r;
 }
 
+// Sixteen elements of a row in storage, as words.
+template <int T> constexpr int kWords = T == SVP_F32 ? 16 : T == SVP_BF16 ? 8 : 4;
+
+template <int T>
+__device__ __forceinline__ void load16(const void *base, int64_t e, uint32_t (&w)[kWords<T>])
+{
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + e * (kWords<T> / 4));
+#pragma unroll
+    for (int i = 0; i < kWords<T> / 4; ++i) {
+        const uint4 v = s[i];
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store16(void *base, int64_t e, const uint32_t (&w)[kWords<T>])
+{
+    uint4 *s = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + e * (kWords<T> / 4));
+#pragma unroll
+    for (int i = 0; i < kWords<T> / 4; ++i)
+        s[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <int T>
+__device__ __forceinline__ void to_f32(const uint32_t (&w)[kWords<T>], float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i) {
+        if constexpr (T == SVP_F32) {
+            x[i] = __uint_as_float(w[i]);
+        } else if constexpr (T == SVP_BF16) {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        } else {
+            float f[4];
+            e4m3x4_to_f32(w[i], f);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                x[4 * i + y] = f[y];
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void from_f32(const float (&x)[16], uint32_t (&w)[kWords<T>])
+{
+    static_assert(T != SVP_E4M3, "8-bit rows are made with their exponent byte");
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i)
+        w[i] = T == SVP_F32 ? __float_as_uint(x[i]) : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+// Bits of the largest magnitude (as fp32) of sixteen elements.
+template <int T>
+__device__ __forceinline__ uint32_t amax16(const uint32_t (&w)[kWords<T>])
+{
+    uint32_t m = 0u;
+    if constexpr (T == SVP_F32) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m = max(m, w[i] & 0x7fffffffu);
+        return m;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return max(m & 0xffff0000u, m << 16);
+    }
+}
+
 }  // namespace svp
