@@ -74,6 +74,7 @@ typedef enum {
 #define SVP_DEV_TIMEOUT     0x4   /* a bounded in-kernel wait expired                    */
 #define SVP_DEV_WORKSPACE   0x8   /* workspace last used with another head_dim or tile mode:
                                      nothing was computed; run svp_workspace_init first     */
+#define SVP_DEV_NO_PAGES    0x10  /* svp_pages_*: not enough free pages for all requests       */
 
 typedef enum {
     SVP_F32 = 0,
@@ -579,6 +580,73 @@ svp_status svp_rope_cache_write(const void *q, int64_t q_row_stride, const void 
                                 const int32_t *cu_slots, const int32_t *take, int32_t n,
                                 int32_t m_cap, int32_t hq, int32_t hkv, int32_t d, void *q_out,
                                 int64_t q_out_stride, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* The pages of a cache: who holds them, and their sharing, freeing and moving, all on the */
+/* device (no host round trip, so a captured step may allocate).                           */
+/*   block_table [n, max_pages]: entries 0 .. used[i] - 1 of row i are request i's pages.   */
+/*   refs [num_pages]: how many entries hold a page; 0 means free.                         */
+/* To start: refs and used 0 (then every page is free), and resize the requests.  A page   */
+/* shared by several requests is read by all and written by none: every request's last,    */
+/* partly filled page stays its own, see svp_pages_fork and svp_pages_resize.              */
+typedef struct {
+    int32_t *block_table;    /* device [n, max_pages], the block_table of svp_cache         */
+    int32_t *used;           /* device [n]                                                  */
+    int32_t *refs;           /* device [num_pages]                                          */
+    int32_t n, max_pages;    /* 0 <= n <= 1024                                              */
+    int32_t page_size;       /* tokens per page: 16, 32, 64 or 128                          */
+    int64_t num_pages;       /* < 2^31                                                      */
+} svp_pages;
+
+#define SVP_PAGES_MAX_CACHES 64
+
+/* Workspace bytes for the three calls below (host; grows with num_pages). */
+svp_status svp_pages_workspace_size(const svp_pages *pages, size_t *bytes);
+
+/*
+ * Request i ends with ceil(length[i] / page_size) pages (length [n] int32, device; a negative one
+ * leaves the request as it is): before a step that writes up to ctx_len + k_i, after an acceptance that
+ * kept fewer, with 0 when it is done.  First every shrinking request gives back its pages from the end
+ * (refs - 1, entries -1); then the growing ones get the free pages with the lowest ids, in the order
+ * of requests and positions (refs 1).  Without enough free pages a request i is left as it was when what
+ * requests 0 .. i ask for together is more than there are (SVP_DEV_NO_PAGES).
+ * Left as they were too (SVP_DEV_BAD_CONTEXT): a request with used[i] outside 0 .. max_pages, a length
+ * past max_pages * page_size, and one that would keep part of a page that another holds as well (refs > 1
+ * before the call), as its next write would go there: give it a whole page less, or fork it instead.
+ * An entry that names no page of the pool, or one whose refs is 0 already, is given back as -1 without
+ * counting (SVP_DEV_BAD_CONTEXT).
+ * ws     at least svp_pages_workspace_size bytes, its first 256 zeroed once by svp_workspace_init
+ */
+svp_status svp_pages_resize(const svp_pages *pages, const int32_t *length, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Request dst[f], which holds no page, gets the first length[f] tokens of src[f] (0 <= f < forks;
+ * int32 [forks], device): the whole pages among them are shared (refs + 1), and a part of a page at the
+ * end is copied, its tokens only, to a page of its own (refs 1): the lowest free ids in the order of f.
+ * caches: HOST array of the n_caches <= SVP_PAGES_MAX_CACHES caches (a model's layers) that this block
+ * table serves, of one type, strides, page size and num_pages, hkv heads of d; read during the call and
+ * not retained.  n_caches may be 0 (the caller copies).  The rest of block_table's row dst[f] is -1.
+ * Not done: a src or dst outside 0 .. n - 1, a dst that holds pages or is that of an earlier fork of the
+ * call (SVP_DEV_BAD_SLOTS); a length outside 0 .. used[src] * page_size (SVP_DEV_BAD_CONTEXT); a fork when
+ * forks 0 .. f together need more pages than are free (SVP_DEV_NO_PAGES).  An entry of src that names no
+ * page of the pool is passed on as -1 (SVP_DEV_BAD_CONTEXT).  0 <= forks <= 1024, hkv <= 4096.
+ */
+svp_status svp_pages_fork(const svp_pages *pages, const svp_cache *caches, int32_t n_caches,
+                          int32_t hkv, int32_t d, const int32_t *src, const int32_t *dst,
+                          const int32_t *length, int32_t forks, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/*
+ * Moves pages so that the L pages in use (refs other than 0) are pages 0 .. L - 1: of those with
+ * ids >= L, in their order, the k-th goes to the k-th free id below L, with its contents in every cache, its
+ * refs and every entry that holds it.  live: device int32 that gets L, or NULL.  Pages >= L are free
+ * then (and hold what they held).  An entry that holds a page with refs 0 is left as it is
+ * (SVP_DEV_BAD_CONTEXT when its id is >= L).  caches as above.
+ */
+svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, int32_t n_caches,
+                             int32_t hkv, int32_t d, int32_t *live, void *ws, size_t ws_bytes,
+                             void *stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,9 @@ Entry points (same names as the C ABI, without the ``svp_`` prefix):
                        keys and values are in the cache already
   rope                 rotary positions of query / key rows (rope_frequencies makes the table)
   rope_cache_write     the same with the rotated keys and the values written into the cache
+  pages_resize         pages for requests that grow, and back from those that shrink or end (make_pages)
+  pages_fork           requests that share another's first tokens, page by page
+  pages_compact        the pages in use moved to the lowest ids
 """
 from __future__ import annotations
 
@@ -36,7 +39,7 @@ LIB_PATH = os.path.join(_HERE, "libsvp.so")
 SVP_OK, SVP_EINVAL, SVP_EUNSUPPORTED, SVP_EWORKSPACE, SVP_ECUDA = 0, 1, 2, 3, 4
 SVP_F32, SVP_BF16, SVP_E4M3 = 0, 1, 2
 TILE_AUTO, TILE_SHORT, TILE_FIXED128, TILE_WIDE, TILE_SHORT_UNPACKED = 0, 1, 2, 3, 4
-DEV_BAD_SLOTS, DEV_BAD_CONTEXT, DEV_TIMEOUT, DEV_WORKSPACE = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_SLOTS, DEV_BAD_CONTEXT, DEV_TIMEOUT, DEV_WORKSPACE, DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8, 0x10
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -82,7 +85,15 @@ class svp_rotary(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class svp_pages(ctypes.Structure):
+    """Who holds a cache's pages, for the pages_* calls; see make_pages."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("used", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64)]
+
+
 GATHER_MAX_FIELDS = 8
+PAGES_MAX_CACHES = 64
 
 _lib = None
 
@@ -178,6 +189,16 @@ _SIGS = {
         ctypes.POINTER(svp_rotary), ctypes.POINTER(svp_cache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_pages_workspace_size": (ctypes.c_int, [ctypes.POINTER(svp_pages), ctypes.POINTER(ctypes.c_size_t)]),
+    "svp_pages_resize": (ctypes.c_int, [
+        ctypes.POINTER(svp_pages), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_pages_fork": (ctypes.c_int, [
+        ctypes.POINTER(svp_pages), ctypes.POINTER(svp_cache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_void_p]),
+    "svp_pages_compact": (ctypes.c_int, [
+        ctypes.POINTER(svp_pages), ctypes.POINTER(svp_cache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "svp_margin_accept": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
@@ -983,3 +1004,90 @@ def rope_cache_write(q, k, v, ctx_len, cu_slots, *, cache: svp_cache, freq, inte
     if st:
         raise SvpError(st, "svp_rope_cache_write")
     return q_out
+
+
+# ----------------------------------------------------------------- pages
+def make_pages(block_table, used, refs, *, page_size: int) -> svp_pages:
+    """svp_pages over block_table [n, max_pages] (the caches' own), used [n] and refs [num_pages], all int32 on
+    the current device; used and refs zero means that every page is free.  The struct keeps the tensors alive
+    and brings a Workspace, ``.ws``, which the pages_* calls use (in the order of one stream, as they change
+    the same tables) and whose read_status() tells what they reported."""
+    p = svp_pages()
+    p.block_table, p.used, p.refs = (_dev(t, name, torch.int32) for t, name in (
+        (block_table, "block_table"), (used, "used"), (refs, "refs")))
+    if block_table.dim() != 2 or used.shape != block_table.shape[:1] or refs.dim() != 1:
+        raise ValueError("block_table must be [n, max_pages], used [n] and refs [num_pages]")
+    if not block_table.device == used.device == refs.device:
+        raise ValueError("the pages' tensors must be on one device")
+    p.n, p.max_pages = block_table.shape
+    p.page_size, p.num_pages = int(page_size), refs.numel()
+    p.index = block_table.get_device()
+    if p.index != torch._C._cuda_getDevice():
+        raise ValueError("the pages must be on the current CUDA device")
+    p.keep = (block_table, used, refs)
+    nb = ctypes.c_size_t(0)
+    _check(lib().svp_pages_workspace_size(ctypes.byref(p), ctypes.byref(nb)), "svp_pages_workspace_size")
+    p.ws = Workspace(int(nb.value), block_table.device, zeroed=256)
+    return p
+
+
+def _pages_i32(t, name: str, count: Optional[int], pages: svp_pages) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != pages.index or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be {count} contiguous int32 values on the pages' device")
+    return t.data_ptr()
+
+
+def _pages_stream(pages: svp_pages, stream) -> int:
+    if pages.index != torch._C._cuda_getDevice():
+        raise ValueError("the pages must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(pages.index) if stream is None else _stream(stream)
+
+
+def _pages_caches(caches, pages: svp_pages):
+    """(host array, number, hkv, d) of the caches of one block table."""
+    count = len(caches)
+    if count == 0:
+        return None, 0, 1, 128
+    if count > PAGES_MAX_CACHES:
+        raise ValueError(f"at most {PAGES_MAX_CACHES} caches")
+    first = caches[0]
+    for c in caches:
+        if c.block_table != pages.block_table or c.hkv != first.hkv or c.d != first.d:
+            raise ValueError("the caches must have the pages' block table and one head layout")
+    return (svp_cache * count)(*caches), count, first.hkv, first.d
+
+
+def pages_resize(pages: svp_pages, length, *, ws: Optional[Workspace] = None, stream=None) -> None:
+    """Request i ends with the pages of length[i] tokens (int32 [n]; a negative length leaves it as it is): pages
+    from its end go back, or the free pages with the lowest ids come to it (svp_pages_resize)."""
+    raw = _pages_stream(pages, stream)
+    ws = pages.ws if ws is None else ws
+    st = lib().svp_pages_resize(pages, _pages_i32(length, "length", pages.n, pages), ws.ptr, ws.nbytes, raw)
+    if st:
+        raise SvpError(st, "svp_pages_resize")
+
+
+def pages_fork(pages: svp_pages, src, dst, length, *, caches=(), ws: Optional[Workspace] = None, stream=None) -> None:
+    """Requests dst[f], which hold nothing, start with the first length[f] tokens of src[f] (int32 tensors of one
+    length): whole pages are shared, the part of a page at the end is copied in every one of ``caches`` (a model's
+    layers; svp_pages_fork)."""
+    raw = _pages_stream(pages, stream)
+    ws = pages.ws if ws is None else ws
+    forks = length.numel()
+    arr, count, hkv, d = _pages_caches(caches, pages)
+    st = lib().svp_pages_fork(pages, arr, count, hkv, d, _pages_i32(src, "src", forks, pages), _pages_i32(dst, "dst", forks, pages),
+                              _pages_i32(length, "length", forks, pages), forks, ws.ptr, ws.nbytes, raw)
+    if st:
+        raise SvpError(st, "svp_pages_fork")
+
+
+def pages_compact(pages: svp_pages, *, caches=(), live=None, ws: Optional[Workspace] = None, stream=None) -> None:
+    """Moves pages in every one of ``caches`` so that the L pages in use have ids below L, and their entries and refs
+    with them (svp_pages_compact).  live: int32 tensor of one element that gets L."""
+    raw = _pages_stream(pages, stream)
+    ws = pages.ws if ws is None else ws
+    arr, count, hkv, d = _pages_caches(caches, pages)
+    st = lib().svp_pages_compact(pages, arr, count, hkv, d, 0 if live is None else _pages_i32(live, "live", 1, pages), ws.ptr,
+                                 ws.nbytes, raw)
+    if st:
+        raise SvpError(st, "svp_pages_compact")
