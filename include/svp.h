@@ -648,6 +648,38 @@ svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, in
                              int32_t hkv, int32_t d, int32_t *live, void *ws, size_t ws_bytes,
                              void *stream);
 
+/* ---------------------------------------------------------------------------------- */
+/* Attention of requests that share a beginning (samples of one prompt, a common system    */
+/* prompt; svp_pages_fork makes such requests).                                            */
+/*
+ * The result is svp_chunk_attn's, argument by argument; in addition, requests cu_groups[g] ..
+ * cu_groups[g+1] - 1 form group g (requests outside all groups are alone), and the first prefix_len[g]
+ * tokens of each of them lie in the same pages: the block table's rows of a group's requests (of
+ * those with k_i > 0) have the same ids there, and only the first one's are read.  The whole pages of a
+ * prefix are read once for 256 / (hq / hkv) rows of the group (128 / (hq / hkv) at d = 256) instead of once
+ * for every request, where that is fewer times.
+ * cu_groups [n_groups+1], prefix_len [n_groups] int32 (device); 0 <= n_groups <= 1024
+ * With an SVP_F32 cache, or without groups, the call is svp_chunk_attn (groups are not looked at).
+ * ws     at least svp_prefix_attn_workspace_size bytes (it grows with m_cap), its first 256 zeroed once by
+ *        svp_workspace_init; every call leaves it ready for the next one that it is large enough for; 16-byte
+ *        aligned
+ * Device checks are svp_chunk_attn's, but cu_slots that run backwards or leave [0, m_cap] anywhere reject the
+ * whole call (SVP_DEV_BAD_SLOTS; nothing is written).  Groups that run backwards or leave [0, n] anywhere are
+ * none (SVP_DEV_BAD_SLOTS), and a group with prefix_len < 0 or > a member's ctx_len (SVP_DEV_BAD_CONTEXT), or
+ * with a member that is skipped, is not shared; its other requests then use their own entries.
+ * Precision: as svp_chunk_attn's tile kernel (8-bit pages: units of a tile's largest power of two), a row's
+ * two parts in fp32 until they are joined.
+ */
+svp_status svp_prefix_attn_workspace_size(const svp_heads *heads, svp_dtype dtype, int32_t m_cap,
+                                          size_t *bytes);
+
+svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache *cache,
+                           const int32_t *ctx_len, const int32_t *cu_slots, int32_t n,
+                           int32_t m_cap, int32_t w, const int32_t *cu_groups,
+                           const int32_t *prefix_len, int32_t n_groups, const svp_heads *heads,
+                           svp_dtype dtype, void *out, float *lse, void *ws, size_t ws_bytes,
+                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif

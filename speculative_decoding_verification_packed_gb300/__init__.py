@@ -19,6 +19,8 @@ Entry points (same names as the C ABI, without the ``svp_`` prefix):
   cache_read           cached positions back to contiguous rows
   chunk_attn           attention of decode tokens, candidate blocks and prompt chunks whose
                        keys and values are in the cache already
+  prefix_attn          chunk_attn for groups of requests that share their first pages, which are
+                       read once a group
   rope                 rotary positions of query / key rows (rope_frequencies makes the table)
   rope_cache_write     the same with the rotated keys and the values written into the cache
   pages_resize         pages for requests that grow, and back from those that shrink or end (make_pages)
@@ -199,6 +201,13 @@ _SIGS = {
     "svp_pages_compact": (ctypes.c_int, [
         ctypes.POINTER(svp_pages), ctypes.POINTER(svp_cache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svp_prefix_attn_workspace_size": (ctypes.c_int, [
+        ctypes.POINTER(svp_heads), ctypes.c_int, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "svp_prefix_attn": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(svp_cache), ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int32, ctypes.POINTER(svp_heads), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_size_t, ctypes.c_void_p]),
     "svp_margin_accept": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
@@ -858,6 +867,72 @@ def chunk_attn(q, ctx_len, cu_slots, *, cache: svp_cache, w: Optional[int] = Non
         0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, raw)
     if st:
         raise SvpError(st, "svp_chunk_attn")
+    return out, lse
+
+
+def prefix_attn_workspace_size(hq: int, hkv: int, d: int, m_cap: int, dtype=torch.bfloat16) -> int:
+    nb = ctypes.c_size_t(0)
+    h = _heads(hq, hkv, d, 0.0)
+    _check(lib().svp_prefix_attn_workspace_size(ctypes.byref(h), SVP_BF16 if dtype == torch.bfloat16 else SVP_F32, m_cap,
+                                                ctypes.byref(nb)), "svp_prefix_attn_workspace_size")
+    return int(nb.value)
+
+
+def _prefix_workspace(hq: int, m_cap: int, cache: svp_cache, dtype, raw: int) -> Workspace:
+    """As _chunk_workspace; a stream's scratch grows with the calls' rows."""
+    nb = prefix_attn_workspace_size(hq, cache.hkv, cache.d, m_cap, dtype)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return Workspace(nb, cache.device, zeroed=0)
+    key = (raw, cache.index, "prefix")
+    ws = _chunk_ws.get(key)
+    if ws is None or ws.nbytes < nb:
+        _chunk_ws.pop(key, None)
+        while len(_chunk_ws) >= _CHUNK_WS_MOST:
+            _chunk_ws.pop(next(iter(_chunk_ws)), None)
+        ws = _chunk_ws[key] = Workspace(nb, cache.device, zeroed=256)
+    return ws
+
+
+def prefix_attn(q, ctx_len, cu_slots, cu_groups, prefix_len, *, cache: svp_cache, w: Optional[int] = None, out=None,
+                lse=None, want_lse: bool = True, scale: float = 0.0, ws: Optional[Workspace] = None, stream=None):
+    """chunk_attn (the same arguments and results) for groups of requests that share a beginning
+    (svp_prefix_attn): requests cu_groups[g]..cu_groups[g+1]-1 (int32) have their first prefix_len[g] tokens (int32)
+    in the same pages, as pages_fork leaves them, and those are read once for the group.  ws: a Workspace of
+    prefix_attn_workspace_size bytes; without one as for chunk_attn."""
+    n = _requests(cu_slots, cache, "cu_slots")
+    other = _other_stream(stream, cache)
+    if other is not None:
+        with other:
+            return prefix_attn(q, ctx_len, cu_slots, cu_groups, prefix_len, cache=cache, w=w, out=out, lse=lse,
+                               want_lse=want_lse, scale=scale, ws=ws)
+    dev = cache.device
+    hkv = cache.hkv
+    m_cap, hq, d = q.shape
+    if hq < 1 or hq % hkv:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    stride = _rows(q, "q", hq, cache)
+    if out is None:
+        out = torch.zeros(m_cap, hq, d, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape, type and device")
+    if lse is None:
+        if want_lse:
+            lse = torch.zeros(m_cap, hq, dtype=torch.float32, device=dev)
+    elif lse.shape != (m_cap, hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [m_cap, hq] on q's device")
+    ng = cu_groups.numel() - 1
+    if ng < 0:
+        raise ValueError("cu_groups must have one entry at least")
+    raw = _raw_stream(None, cache)
+    if ws is None:
+        ws = _prefix_workspace(hq, m_cap, cache, q.dtype, raw)
+    st = lib().svp_prefix_attn(
+        q.data_ptr(), stride, cache, _i32(ctx_len, "ctx_len", n, cache), _i32(cu_slots, "cu_slots", n + 1, cache),
+        n, m_cap, (m_cap or 1) if w is None else w, _i32(cu_groups, "cu_groups", ng + 1, cache),
+        _i32(prefix_len, "prefix_len", ng, cache), ng, svp_heads(hq, hkv, d, scale), _dtype_code(q), out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, raw)
+    if st:
+        raise SvpError(st, "svp_prefix_attn")
     return out, lse
 
 

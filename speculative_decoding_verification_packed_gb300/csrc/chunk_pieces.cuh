@@ -52,6 +52,12 @@ struct ChunkParams {
     int32_t nslot, nraw;              // bf16 tile slots, raw slots (8-bit pages)
     int32_t off_ring, off_raw, off_misc;
     int32_t Rb, qsub;                 // tokens of a query box: min(R, w); bytes of its [rows][64] blocks
+    // groups of requests with common first pages (prefix_pieces.cuh)
+    const int32_t *cu_groups, *prefix_len;
+    int32_t ng;
+    int4 *plan;                       // [grid][2 * kPxMost]
+    struct PrefixRec *rec;            // [n]
+    int64_t *total;
 };
 
 // One CTA an SM.  A dependent of the previous kernel starts 3 us earlier, but its CTAs go to SMs as these
@@ -161,6 +167,12 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, ChunkPiece &s)
     return true;
 }
 
+// What of a piece is otherwise behind a common beginning (prefix_pieces.cuh): where its pages stand in the
+// block table, the last key that token tok of its block sees, and whether its result waits for another's.
+__device__ __forceinline__ int64_t ck_table(const ChunkParams &p, const ChunkPiece &s) { return (int64_t)s.i * p.c.max_pages; }
+__device__ __forceinline__ int32_t ck_last(const ChunkPiece &s, int32_t tok) { return s.L + s.tb0 + tok; }
+__device__ __forceinline__ bool ck_kept(const ChunkPiece &) { return false; }
+
 // The next pair before cost v1, from its first tile.
 template <int NT>
 __device__ __forceinline__ bool ck_next(const ChunkParams &p, ChunkPiece &s, int64_t v1)
@@ -228,14 +240,16 @@ struct ChunkShares {
     int32_t ncta;
 };
 
-__device__ __forceinline__ ChunkShares ck_shares(int64_t total)
+__device__ __forceinline__ ChunkShares ck_shares(int64_t total, int32_t ctas)
 {
     ChunkShares x;
     x.total = total;
-    x.ncta = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, total / kShareCost));
+    x.ncta = (int32_t)max((int64_t)1, min((int64_t)ctas, total / kShareCost));
     x.share = max((int64_t)1, (total + x.ncta - 1) / x.ncta);
     return x;
 }
+
+__device__ __forceinline__ ChunkShares ck_shares(int64_t total) { return ck_shares(total, (int32_t)gridDim.x); }
 
 // The CTA that owns the tile that starts at cost u < total.
 __device__ __forceinline__ int32_t ck_owner(const ChunkShares &x, int64_t u)

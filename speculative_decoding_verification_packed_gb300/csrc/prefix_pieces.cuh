@@ -1,0 +1,337 @@
+// prefix_pieces.cuh -- how the work of svp_prefix_attn is cut: the sequence of pairs of chunk_pieces.cuh with
+// the groups that share a beginning in front of the requests.
+//
+// A shared group is one more "request": its rows are those of all its requests, which lie side by side, its
+// keys the P positions that they have in common, seen by every row.  Its requests come after all groups and
+// have the keys from P on.  So both kinds are split over the CTAs together, and a group's pages are read
+// once for as many rows as a block takes (256 / G tokens) instead of once a request.
+//
+// A group is shared where that saves a pass: where its rows fill fewer blocks together than apart (two
+// requests at least, and not prompts that fill their own blocks), P taken down to whole pages.  Else, or where
+// the group's numbers are not in order, its requests have all their keys themselves.
+#pragma once
+
+#include "chunk_pieces.cuh"
+
+namespace svp {
+
+constexpr int kPxMost = 1024;         // requests, and groups, of a call
+
+// What the joining kernel needs of a request, written by the first CTA.
+struct PrefixRec {
+    int32_t off, k, L, P;             // first row, rows, cached tokens behind the P common ones (k 0: skipped)
+    int32_t goff, gk;                 // first row and rows of its group
+    int64_t base, gbase;              // cost before the request's pairs, and before the group's
+};
+
+struct PrefixPiece : ChunkPiece {     // i: place in the sequence of groups and requests
+    int32_t ne, ng;                   // length of the sequence, and groups in it
+    const int4 *plan;                 // this CTA's copy: (first row, rows, P, row of the block table), then (first
+                                      // row, rows, tokens behind P, P)
+    int32_t row, first;               // row of the block table, and the first key's position
+    bool group;
+};
+
+__device__ __forceinline__ int64_t ck_table(const ChunkParams &p, const PrefixPiece &s)
+{
+    return (int64_t)s.row * p.c.max_pages + (s.first >> p.c.page_shift);
+}
+__device__ __forceinline__ int32_t ck_last(const PrefixPiece &s, int32_t tok)
+{
+    return s.group ? s.L - 1 : s.L + s.tb0 + tok;
+}
+__device__ __forceinline__ bool ck_kept(const PrefixPiece &s) { return s.group || s.first > 0; }
+
+// Keys of one KV head of a group of k rows, B a block: each block sees all L.
+__device__ __forceinline__ int64_t px_head_keys(int32_t L, int32_t k, int32_t B)
+{
+    return (int64_t)((k + B - 1) / B) * ((int64_t)kStartKeys + L);
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_set(const ChunkParams &p, PrefixPiece &s, int64_t v1, int32_t t0)
+{
+    const int32_t B = NT * p.R;
+    s.tb0 = s.b * B;
+    s.ntok = min(B, s.k - s.tb0);
+    s.len = s.group ? s.L : s.L + s.tb0 + s.ntok;
+    s.nt = (s.len + kCkKeys - 1) / kCkKeys;
+    s.t0 = t0;
+    const int32_t wt = s.wt;
+    const int64_t y = v1 - s.base;
+    s.t1 = y >= (int64_t)wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, wt));
+    return s.t0 < s.t1;
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_request(const ChunkParams &p, PrefixPiece &s)
+{
+    const int32_t B = NT * p.R;
+    const int4 x = __ldcg(s.plan + (s.i < s.ng ? s.i : kPxMost + s.i - s.ng));
+    s.group = s.i < s.ng;
+    s.off = x.x;
+    s.k = x.y;
+    s.L = x.z;
+    s.row = s.group ? x.w : s.i - s.ng;
+    s.first = s.group ? 0 : x.w;
+    if (s.k <= 0)
+        return false;
+    s.nb = (s.k + B - 1) / B;
+    s.wt = ck_weight<NT>(s.k, p.R);
+    return true;
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_next(const ChunkParams &p, PrefixPiece &s, int64_t v1)
+{
+    s.base += (int64_t)s.wt * (kStartKeys + (int64_t)s.len);
+    if (s.base >= v1)
+        return false;
+    if (++s.b == s.nb) {
+        s.b = 0;
+        if (++s.g == p.c.hkv) {
+            s.g = 0;
+            do {
+                if (++s.i >= s.ne)
+                    return false;     // (never: base < v1 <= the total)
+            } while (!ck_request<NT>(p, s));
+        }
+    }
+    return ck_set<NT>(p, s, v1, 0);
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *prefix, PrefixPiece &s, int64_t v0, int64_t v1)
+{
+    if (v0 >= v1)
+        return false;
+    const int32_t B = NT * p.R;
+    int32_t lo = 0, hi = s.ne;
+    while (hi - lo > 1) {             // last pairs with prefix <= v0 (they have a cost: v0 < total)
+        const int32_t mid = (lo + hi) >> 1;
+        if (prefix[mid] <= v0)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    s.i = lo;
+    ck_request<NT>(p, s);
+    const int32_t wt = s.wt, slope = s.group ? 0 : B;
+    const int64_t H = (s.group ? px_head_keys(s.L, s.k, B) : ck_head_keys(s.L, s.k, B)) * wt;
+    int64_t rem = v0 - prefix[lo];
+    s.g = (int32_t)(rem / H);
+    rem -= s.g * H;
+    // last block with cost before it <= rem (chunk_pieces.cuh; a group's blocks cost the same each)
+    const int64_t a = (int64_t)kStartKeys + s.L;
+    int64_t b;
+    if (s.group) {
+        b = rem / (a * wt);
+    } else {
+        const float h = (float)a + 0.5f * B;
+        b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / wt)) - h) / B);
+    }
+    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
+    while (b + 1 < s.nb && ck_before(a, slope, b + 1) * wt <= rem)
+        ++b;
+    while (b > 0 && ck_before(a, slope, b) * wt > rem)
+        --b;
+    s.b = (int32_t)b;
+    s.base = prefix[lo] + s.g * H + ck_before(a, slope, b) * wt;
+    const int32_t t0 = ck_tile_at(v0 - s.base, wt);
+    const bool have = ck_set<NT>(p, s, v1, t0);
+    return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
+}
+
+// Shared memory of the prologue, where the ring (48 KB at least) is later.
+struct PrefixSums {
+    int64_t prefix[2 * kPxMost + 1];
+    int32_t cu[kPxMost + 1], gcu[kPxMost + 1], len[kPxMost];
+    int32_t blocks[kPxMost];          // blocks that the group's requests fill apart
+    int32_t bad[kPxMost];
+    int32_t lead[kPxMost];            // its first request with rows
+    int32_t slot[kPxMost];            // place of the group in the sequence, or -1
+    int32_t broken, groups_broken;
+    int32_t cnt[32];
+    int64_t tot[32];
+};
+
+// Exclusive sums of cost (and of 0 / 1 counts) over the block's threads, chunk by chunk.
+struct PrefixScan {
+    int64_t running;
+    int32_t count;
+};
+
+__device__ __forceinline__ void px_scan(PrefixSums &x, PrefixScan &run, int64_t cost, bool one, int64_t &before, int32_t &place)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+    int64_t incl = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    const uint32_t ones = __ballot_sync(0xffffffffu, one);
+    __syncthreads();                  // (the sums of the chunk before have been read)
+    if (lane == 31)
+        x.tot[warp] = incl;
+    if (lane == 0)
+        x.cnt[warp] = __popc(ones);
+    __syncthreads();
+    before = run.running + incl - cost;
+    place = run.count + __popc(ones & ((1u << lane) - 1u));
+    for (int w = 0; w < nwarp; ++w) {
+        if (w < warp) {
+            before += x.tot[w];
+            place += x.cnt[w];
+        }
+        run.running += x.tot[w];
+        run.count += x.cnt[w];
+    }
+}
+
+// Cost before each of the sequence's groups and requests into x->prefix, their places and sizes into this CTA's
+// plan, and (first CTA) what the joining kernel needs.  Returns the sequence's length.
+template <int NT>
+__device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
+{
+    PrefixSums &x = *static_cast<PrefixSums *>(smem);
+    const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, n = p.n, ng = p.ng;
+    const bool tells = blockIdx.x == 0;
+    int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
+    if (tid == 0)
+        x.broken = x.groups_broken = 0;
+    for (int32_t i = tid; i <= n; i += nt)
+        x.cu[i] = __ldg(p.cu + i);
+    for (int32_t g = tid; g <= ng; g += nt)
+        x.gcu[g] = ng > 0 ? __ldg(p.cu_groups + g) : 0;
+    for (int32_t g = tid; g < ng; g += nt) {
+        x.len[g] = __ldg(p.prefix_len + g);
+        x.blocks[g] = x.bad[g] = 0;
+        x.lead[g] = n;
+    }
+    __syncthreads();
+    for (int32_t i = tid; i < n; i += nt)
+        if (x.cu[i] < 0 || x.cu[i + 1] < x.cu[i] || x.cu[i + 1] > p.m_cap)
+            x.broken = 1;
+    for (int32_t g = tid; g < ng; g += nt)
+        if (x.gcu[g] < 0 || x.gcu[g + 1] < x.gcu[g] || x.gcu[g + 1] > n)
+            x.groups_broken = 1;
+    __syncthreads();
+    const bool broken = x.broken != 0, grouped = ng > 0 && x.groups_broken == 0 && !broken;
+    if (tells && tid == 0 && (broken || x.groups_broken))
+        set_status(p.status, SVP_DEV_BAD_SLOTS);
+    // request i's group, or -1
+    auto group_of = [&](int32_t i) -> int32_t {
+        if (!grouped || i < x.gcu[0] || i >= x.gcu[ng])
+            return -1;
+        int32_t lo = 0, hi = ng;
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (x.gcu[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    for (int32_t i = tid; i < n; i += nt) {
+        const int32_t k = x.cu[i + 1] - x.cu[i], g = group_of(i);
+        if (broken || k == 0)
+            continue;
+        const int32_t L = __ldg(p.ctx_len + i), bad = ck_bad(p, x.cu[i], x.cu[i + 1], L);
+        if (bad && tells)
+            set_status(p.status, bad);
+        if (g >= 0) {
+            if (!bad && x.len[g] > L && tells)
+                set_status(p.status, SVP_DEV_BAD_CONTEXT);
+            if (bad || x.len[g] > L)
+                x.bad[g] = 1;
+            atomicAdd(&x.blocks[g], bad ? 0 : (k + B - 1) / B);
+            atomicMin(&x.lead[g], i);
+        }
+    }
+    __syncthreads();
+    PrefixScan run{0, 0};
+    for (int32_t g0 = 0; g0 < ng; g0 += nt) {
+        const int32_t g = g0 + tid;
+        int64_t cost = 0;
+        int32_t off = 0, k = 0, P = 0, lead = 0;
+        bool shared = false;
+        if (g < ng && grouped) {
+            lead = x.lead[g];
+            off = x.cu[x.gcu[g]];
+            k = x.cu[x.gcu[g + 1]] - off;
+            if (x.len[g] < 0 && tells)
+                set_status(p.status, SVP_DEV_BAD_CONTEXT);
+            P = x.len[g] >> p.c.page_shift << p.c.page_shift;
+            shared = !x.bad[g] && P > 0 && k > 0 && (k + B - 1) / B < x.blocks[g];
+            if (shared)
+                cost = px_head_keys(P, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
+        }
+        int64_t before;
+        int32_t at;
+        px_scan(x, run, cost, shared, before, at);
+        if (g < ng) {
+            x.slot[g] = shared ? at : -1;
+            if (shared) {
+                x.prefix[at] = before;
+                plan[at] = make_int4(off, k, P, lead);
+            }
+        }
+    }
+    const int32_t first = run.count;
+    __syncthreads();
+    for (int32_t i0 = 0; i0 < n; i0 += nt) {
+        const int32_t i = i0 + tid;
+        int64_t cost = 0;
+        PrefixRec r{};
+        if (i < n && !broken) {
+            const int32_t off = x.cu[i], k = x.cu[i + 1] - off, L = __ldg(p.ctx_len + i), g = group_of(i);
+            const int32_t slot = g >= 0 ? x.slot[g] : -1;
+            if (k > 0 && !ck_bad(p, off, x.cu[i + 1], L)) {
+                const int32_t P = slot >= 0 ? x.len[g] >> p.c.page_shift << p.c.page_shift : 0;
+                r.off = off;
+                r.k = k;
+                r.L = L - P;
+                r.P = P;
+                cost = ck_head_keys(r.L, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
+                if (slot >= 0) {
+                    r.goff = x.cu[x.gcu[g]];
+                    r.gk = x.cu[x.gcu[g + 1]] - r.goff;
+                    r.gbase = x.prefix[slot];
+                }
+            }
+        }
+        int32_t none;
+        px_scan(x, run, cost, false, r.base, none);
+        if (i < n) {
+            x.prefix[first + i] = r.base;
+            plan[kPxMost + i] = make_int4(r.off, r.k, r.L, r.P);
+            if (tells)
+                p.rec[i] = r;
+        }
+    }
+    if (tid == 0) {
+        x.prefix[first + n] = run.running;
+        if (tells)
+            *p.total = run.running;
+    }
+    __syncthreads();
+    return first + n;
+}
+
+__device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, int32_t length)
+{
+    s.plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
+    s.ne = length;
+    s.ng = length - p.n;
+}
+
+// Row of the partial results that a whole pair has for (row, head): behind the CTAs' own, the groups' first.
+__device__ __forceinline__ int64_t px_place(const ChunkParams &p, bool group, int32_t row, int32_t head, int64_t behind)
+{
+    return behind + ((group ? 0 : (int64_t)p.m_cap) + row) * p.hq + head;
+}
+
+}  // namespace svp

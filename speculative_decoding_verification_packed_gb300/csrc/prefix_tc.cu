@@ -1,0 +1,297 @@
+// prefix_tc.cu -- svp_prefix_attn: chunk attention of requests in groups whose first tokens lie in the same pages.
+//
+// softmax over all keys of a row is the join of its softmax over the common ones and over its own:
+//   M = max(m_1, m_2),  L = sum l_x 2^(m_x - M),  o = sum O_x 2^(m_x - M) / L.
+// So the common keys are worked on once for all rows of a group (chunk_kernel.cuh over the sequence of
+// prefix_pieces.cuh): G heads times all tokens of the group fill the 128-row tiles that a decode token alone
+// leaves empty, and the pages are read once.  Every piece, of a group or of a request behind one, leaves (O, m, l)
+// in fp32, the joining kernel below adds a row's pieces up in their order.  Requests alone are svp_chunk_attn's.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+
+#include "chunk_kernel.cuh"
+
+namespace svp {
+
+// ------------------------------------------------------------------ joining
+// Where the pieces of one row's pair are: of the CTAs first .. first + np - 1, or, whole, in the row's own place.
+struct PxPieces {
+    int32_t first, np, pr;            // pr: the row in a CTA's partial results
+};
+
+// tok: the row among its group's, or its request's.
+template <int NT>
+__device__ __forceinline__ PxPieces px_pieces(const ChunkParams &p, const ChunkShares &x, bool group, int64_t base, int32_t k,
+                                              int32_t L, int32_t tok, int32_t g, int32_t h)
+{
+    const int32_t B = NT * p.R, b = tok / B, t = tok - b * B, wt = ck_weight<NT>(k, p.R);
+    const int64_t H = group ? px_head_keys(L, k, B) : ck_head_keys(L, k, B);
+    base += wt * (g * H + ck_before((int64_t)kStartKeys + L, group ? 0 : B, b));
+    const int32_t len = group ? L : L + b * B + min(B, k - b * B), nt = (len + kCkKeys - 1) / kCkKeys;
+    PxPieces y;
+    y.first = ck_owner(x, base + (int64_t)wt * kStartKeys);
+    y.np = ck_owner(x, base + (int64_t)wt * (kStartKeys + (int64_t)kCkKeys * (nt - 1))) - y.first + 1;
+    const bool second = t >= p.R;
+    y.pr = (second ? 128 : 0) + (t - (second ? p.R : 0)) * p.G + h;
+    return y;
+}
+
+// Block (row, y): heads 8 y .. 8 y + 7 of a packed row, one a half warp.  Bound by its chain of reads, offsets ->
+// request -> (m, l) and O.
+constexpr int kPxThreads = 128, kPxHeads = kPxThreads / 16;
+
+template <int D>
+__global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_constant__ ChunkParams p, int32_t ctas)
+{
+    constexpr int NT = D == 256 ? 1 : 2, kPartRows = 128 * NT;
+    constexpr int E = D / 16, A = D == 256 ? 2 : 4;       // columns a lane, four side by side; pieces read ahead
+    __shared__ int32_t owner;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 15;
+    if (tid == 0)
+        owner = -1;
+    __syncthreads();
+    const ChunkShares shares = ck_shares(__ldcg(p.total), ctas);
+    for (int32_t i = tid; i < p.n; i += kPxThreads)
+        if (__ldg(p.cu + i) <= row && row < __ldg(p.cu + i + 1))
+            owner = i;                                    // (one, but where nothing is computed)
+    __syncthreads();
+    if (owner < 0)
+        return;
+    const PrefixRec r = p.rec[owner];
+    const int32_t head = blockIdx.y * kPxHeads + (tid >> 4);
+    if (r.k <= 0 || head >= p.hq)
+        return;
+    const int32_t g = head / p.G, h = head - g * p.G;
+    const PxPieces own = px_pieces<NT>(p, shares, false, r.base, r.k, r.L, row - r.off, g, h);
+    if (r.P == 0 && own.np == 1)
+        return;                                           // (the output has it already)
+    PxPieces grp{0, 0, 0};
+    if (r.P > 0)
+        grp = px_pieces<NT>(p, shares, true, r.gbase, r.gk, r.P, row - r.goff, g, h);
+    const int32_t np = grp.np + own.np;
+    const int64_t behind = 2 * (int64_t)ctas * kPartRows;
+    auto at = [&](int32_t q) -> int64_t {
+        const bool mine = q >= grp.np;
+        const PxPieces &y = mine ? own : grp;
+        q -= mine ? grp.np : 0;
+        if (y.np == 1)
+            return px_place(p, !mine, row, head, behind);
+        return (int64_t)(q == 0 ? 2 * y.first + 1 : 2 * (y.first + q)) * kPartRows + y.pr;
+    };
+    auto load = [&](int32_t q, float (&x)[E]) {
+        const float *o = p.part_o + at(q) * D + lane * 4;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 16 * e));
+            x[e] = v.x;
+            x[e + 1] = v.y;
+            x[e + 2] = v.z;
+            x[e + 3] = v.w;
+        }
+    };
+    // (a warp's two heads may have different numbers of pieces, or one head fewer: shuffles are within the half)
+    const uint32_t mask = 0xffffu << (tid & 16);
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 ml0 = lane < np ? __ldcg(p.part_ml + at(lane)) : none;
+    float ahead[A][E];
+#pragma unroll
+    for (int q = 0; q < A; ++q)
+        load(min(q, np - 1), ahead[q]);
+    // (a piece without a visible key of this row, l = 0, is left out whatever its O holds)
+    float M = ml0.y != 0.0f ? ml0.x : -INFINITY;
+    for (int32_t q = 16 + lane; q < np; q += 16) {
+        const float2 ml = __ldcg(p.part_ml + at(q));
+        M = fmaxf(M, ml.y != 0.0f ? ml.x : -INFINITY);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(mask, M, o, 16));
+    float acc[E], L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.0f;
+    for (int32_t q0 = 0; q0 < np; q0 += 16) {
+        const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? __ldcg(p.part_ml + at(q0 + lane)) : none;
+        // (more than 0 where there is a visible key: its O may be NaN)
+        const float w = ml.y != 0.0f ? fmaxf(fast_exp2(ml.x - M), FLT_MIN) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
+        auto add = [&](int32_t q, const float (&x)[E]) {
+            const float wq = __shfl_sync(mask, w, q, 16);
+            L += __shfl_sync(mask, wl, q, 16);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = wq != 0.0f ? fmaf(wq, x[e], acc[e]) : acc[e];
+        };
+        int32_t q = 0;
+        if (q0 == 0) {
+#pragma unroll
+            for (int k = 0; k < A; ++k)
+                add(k, ahead[k]);                         // (weight 0 from np on)
+            q = A;
+        }
+        const int32_t cnt = min(16, np - q0);
+#pragma unroll 2
+        for (; q < cnt; ++q) {
+            float x[E];
+            load(q0 + q, x);
+            add(q, x);
+        }
+    }
+    const float inv = 1.0f / L;
+    const int64_t orow = (int64_t)row * p.hq + head;
+    uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + orow * D + lane * 4;
+#pragma unroll
+    for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<uint2 *>(dst + 16 * e) =
+            make_uint2(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
+    if (lane == 0 && p.lse)
+        p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host side
+int chunk_ctas();
+bool chunk_maps(ChunkParams &p, const void *q, int64_t q_stride, svp_dtype kv, int32_t m_cap, int32_t d, int32_t box_rows,
+                bool few);
+template <int D, bool Q8>
+bool chunk_layout(ChunkParams &p, int32_t rows, int &smem);
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct PrefixWs {
+    size_t total, rec, plan, ml, o, bytes;
+};
+
+static PrefixWs prefix_ws(int32_t hq, int32_t d, int32_t m_cap)
+{
+    // partial results: two pieces a CTA, and those of whole pairs of groups and of requests behind them
+    const size_t g = (size_t)chunk_ctas(), rows = 2 * g * (d == 256 ? 128 : 256) + 2 * (size_t)m_cap * hq;
+    PrefixWs w;
+    w.total = kWsHeader;
+    w.rec = w.total + 256;
+    w.plan = w.rec + up256(kPxMost * sizeof(PrefixRec));
+    w.ml = w.plan + g * 2 * kPxMost * sizeof(int4);
+    w.o = up256(w.ml + rows * sizeof(float2));
+    w.bytes = up256(w.o + rows * (size_t)d * sizeof(float));
+    return w;
+}
+
+template <int D, bool Q8>
+static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
+{
+    using Cfg = ChunkCfg<D, Q8>;
+    int smem = 0;
+    if (!chunk_layout<D, Q8>(p, p.m_cap, smem) || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
+        return SVP_EUNSUPPORTED;
+    static std::atomic<uint64_t> configured{0};
+    if (set_smem_limit_once(chunk_tc_kernel<D, Q8, true>, 227 * 1024, configured) != cudaSuccess)
+        return SVP_ECUDA;
+    const int ctas = chunk_ctas();
+    if (launch_ctas(chunk_tc_kernel<D, Q8, true>, ctas, Cfg::kThreads, (size_t)smem, stream, p, true, true) != cudaSuccess)
+        return SVP_ECUDA;
+    const unsigned y = (unsigned)((p.hq + kPxHeads - 1) / kPxHeads);
+    return launch_pdl(prefix_join_kernel<D>, dim3((unsigned)p.m_cap, y), dim3(kPxThreads), 0, stream, p, (int32_t)ctas) ==
+                   cudaSuccess
+               ? SVP_OK
+               : SVP_ECUDA;
+}
+
+static bool al16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
+
+}  // namespace svp
+
+using namespace svp;
+
+extern "C" {
+
+svp_status svp_prefix_attn_workspace_size(const svp_heads *heads, svp_dtype dtype, int32_t m_cap, size_t *bytes)
+{
+    const svp_status st = svp_chunk_attn_workspace_size(heads, dtype, bytes);
+    if (st != SVP_OK)
+        return st;
+    if (m_cap < 0)
+        return SVP_EINVAL;
+    if (dtype == SVP_BF16)
+        *bytes = std::max(*bytes, prefix_ws(heads->hq, heads->d, m_cap).bytes);
+    return SVP_OK;
+}
+
+svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache *cache, const int32_t *ctx_len,
+                           const int32_t *cu_slots, int32_t n, int32_t m_cap, int32_t w, const int32_t *cu_groups,
+                           const int32_t *prefix_len, int32_t n_groups, const svp_heads *heads, svp_dtype dtype, void *out,
+                           float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    size_t need = 0;
+    svp_status st = svp_prefix_attn_workspace_size(heads, dtype, m_cap, &need);
+    if (st != SVP_OK)
+        return st;
+    if (n_groups < 0)
+        return SVP_EINVAL;
+    if (n_groups > kPxMost)
+        return SVP_EUNSUPPORTED;
+    // no groups, fp32 pages (whose kernel reads every key for every row anyway), and every refusal
+    if (n_groups == 0 || n <= 0 || n > 1024 || m_cap <= 0 || w < 1 || dtype != SVP_BF16)
+        return svp_chunk_attn(q, q_row_stride, cache, ctx_len, cu_slots, n, m_cap, w, heads, dtype, out, lse, ws, ws_bytes,
+                              stream);
+    const float scale = heads->scale != 0.0f ? heads->scale : 1.0f / sqrtf((float)heads->d);
+    if (!(scale > 0.0f) || !std::isfinite(scale))
+        return SVP_EINVAL;
+    ChunkParams p;
+    std::memset(&p, 0, sizeof p);
+    st = cache_params(cache, heads->hkv, heads->d, p.c);
+    if (st != SVP_OK)
+        return st;
+    if (cache->dtype == SVP_F32)
+        return SVP_EUNSUPPORTED;
+    if (q_row_stride < (int64_t)heads->hq * heads->d || (q_row_stride * 2) % 16 != 0)
+        return SVP_EINVAL;
+    if (!ws || ws_bytes < need)
+        return SVP_EWORKSPACE;
+    if (!q || !ctx_len || !cu_slots || !cu_groups || !prefix_len || !out || !al16(q) || !al16(out) || !al16(ws))
+        return SVP_EINVAL;
+    const int32_t d = heads->d;
+    p.ctx_len = ctx_len;
+    p.cu = cu_slots;
+    p.q = q;
+    p.q_stride = q_row_stride;
+    p.n = n;
+    p.m_cap = m_cap;
+    p.w = w;
+    p.hq = heads->hq;
+    p.G = heads->hq / heads->hkv;
+    p.R = 128 / p.G;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out;
+    p.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+    p.lse = lse;
+    p.cu_groups = cu_groups;
+    p.prefix_len = prefix_len;
+    p.ng = n_groups;
+    const PrefixWs o = prefix_ws(p.hq, d, m_cap);
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    p.status = reinterpret_cast<int32_t *>(b);
+    p.total = reinterpret_cast<int64_t *>(b + o.total);
+    p.rec = reinterpret_cast<PrefixRec *>(b + o.rec);
+    p.plan = reinterpret_cast<int4 *>(b + o.plan);
+    p.part_ml = reinterpret_cast<float2 *>(b + o.ml);
+    p.part_o = reinterpret_cast<float *>(b + o.o);
+    if (!chunk_maps(p, q, q_row_stride, cache->dtype, m_cap, d, std::min(p.R, m_cap), false))
+        return SVP_EUNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cache->dtype == SVP_E4M3) {
+        switch (d) {
+        case 64: return prefix_run<64, true>(p, s);
+        case 128: return prefix_run<128, true>(p, s);
+        default: return prefix_run<256, true>(p, s);
+        }
+    }
+    switch (d) {
+    case 64: return prefix_run<64, false>(p, s);
+    case 128: return prefix_run<128, false>(p, s);
+    default: return prefix_run<256, false>(p, s);
+    }
+}
+
+}  // extern "C"
