@@ -108,6 +108,10 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int32_t r0, int32
     __syncthreads();
 }
 
+// One element of a pair: x w.x -+ y w.y, the same operations wherever it is made.
+__device__ __forceinline__ float rope_first(float x, float y, float2 w) { return fmaf(x, w.x, -__fmul_rn(y, w.y)); }
+__device__ __forceinline__ float rope_second(float x, float y, float2 w) { return fmaf(x, w.y, __fmul_rn(y, w.x)); }
+
 template <int T>
 __device__ __forceinline__ float rope_one(const void *base, int64_t e)
 {
@@ -161,8 +165,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                     if (t < half) {
                         const float2 w = m.cs[r][t];
                         const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = a * w.x - b * w.y;
-                        x[2 * i + 1] = a * w.y + b * w.x;
+                        x[2 * i] = rope_first(a, b, w);
+                        x[2 * i + 1] = rope_second(a, b, w);
                     }
                 }
             }
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 w = m.cs[r][t0 + i];
-                    x[i] = second ? y[i] * w.y + x[i] * w.x : x[i] * w.x - y[i] * w.y;
+                    x[i] = second ? rope_second(y[i], x[i], w) : rope_first(x[i], y[i], w);
                 }
             }
         } else {
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                         const bool second = e >= half;
                         const float y = rope_one<TIn>(base, at + (second ? e - half : e + half));
                         const float2 w = m.cs[r][second ? e - half : e];
-                        x[i] = second ? y * w.y + x[i] * w.x : x[i] * w.x - y * w.y;
+                        x[i] = second ? rope_second(y, x[i], w) : rope_first(x[i], y, w);
                     }
                 }
             }

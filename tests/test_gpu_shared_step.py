@@ -102,7 +102,7 @@ def test_samples_of_one_prompt(kind, prompt, captured):
     def plain():
         """The same rows through the cache without sharing; the kept ones are those that were accepted."""
         live = int(cu[-1])
-        lens = (ctx if not kind else ctx).tolist()
+        lens = ctx.tolist()
         for layer in range(LAYERS):
             qr, kr = svp.rope(bufs[0], bufs[1], before, cu, freq=freq)
             assert torch.equal(qr[:live], qo[layer][:live])
