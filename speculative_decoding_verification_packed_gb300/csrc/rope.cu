@@ -7,10 +7,12 @@
 //
 // A block takes a few packed rows with all their heads: the rows' sines and cosines are made once, in
 // shared memory, beside the lookup of their requests and pages; the first heads' data is on the way
-// then.  A group of d / 16 lanes has one head of one row, sixteen elements a lane; the other half of a
-// pair (t, t + rot / 2) comes by a shuffle from rot / 32 lanes away, or, for a rot / 2 that is no
-// multiple of 16, element by element from memory.  All reads of a row come before its writes (one
-// warp holds it), so an output may be its input.
+// then.  A group of d / 8 lanes has every few heads of one row, eight elements a lane, so that a lane's
+// sines and cosines stay in its registers from head to head (read from shared memory for each head they
+// took as long as the rows: 26000 prompt rows of 48 heads x 128 then 180 us).  The other half of a pair
+// (t, t + rot / 2) comes by a shuffle from rot / 16 lanes away, or, for a rot / 2 that is no multiple of 8,
+// element by element from memory.  All reads of a row come before its writes (one warp holds it), so
+// an output may be its input.
 //
 // What bounds it: the chain cu -> context -> angle -> row for few rows, memory for prompts.
 #include <cmath>
@@ -20,7 +22,8 @@
 namespace svp {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;          // packed rows of a block, at most
+constexpr int kRopeRows = 8;          // packed rows of a block, at most
+template <int T> constexpr int kRopeAhead = T == SVP_F32 ? 2 : 4;   // heads of a group in flight: 64 bytes a lane
 
 struct RopeParams {
     CacheParams c;
@@ -121,147 +124,209 @@ __device__ __forceinline__ float rope_one(const void *base, int64_t e)
         return __uint_as_float((uint32_t)static_cast<const uint16_t *>(base)[e] << 16);
 }
 
+// Eight elements of a row in storage, as words.
+template <int T> constexpr int kRopeWords = kWords<T> / 2;
+
+template <int T>
+__device__ __forceinline__ void rope_load(const void *base, int64_t e, uint32_t (&w)[kRopeWords<T>])
+{
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + e * (kWords<T> / 4));
+#pragma unroll
+    for (int i = 0; i < kRopeWords<T> / 4; ++i) {
+        const uint4 v = s[i];
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void rope_store(void *base, int64_t e, const uint32_t (&w)[kRopeWords<T>])
+{
+    uint8_t *at = static_cast<uint8_t *>(base) + e * (kWords<T> / 4);
+    if constexpr (T == SVP_E4M3) {
+        *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRopeWords<T> / 4; ++i)
+            reinterpret_cast<uint4 *>(at)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void rope_widen(const uint32_t (&w)[kRopeWords<T>], float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < kRopeWords<T>; ++i) {
+        if constexpr (T == SVP_F32) {
+            x[i] = __uint_as_float(w[i]);
+        } else {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void rope_narrow(const float (&x)[8], uint32_t (&w)[kRopeWords<T>])
+{
+#pragma unroll
+    for (int i = 0; i < kRopeWords<T>; ++i)
+        w[i] = T == SVP_F32 ? __float_as_uint(x[i]) : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
 // TIn: type of the rows; TC: of the cache, or kNoCache (k goes to k_out).
 template <int TIn, int TC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p)
 {
+    constexpr int A = kRopeAhead<TIn>;
     __shared__ RopeRows m;
     griddep_launch_dependents();
     griddep_wait();
     const int32_t r0 = (int32_t)blockIdx.x * p.rpb;
     const int32_t nr = min(p.rpb, p.rows - r0), hq = p.hq, hkv = p.hkv;
     const int32_t cols = hq + (TC == kNoCache ? 1 : 2) * hkv;
-    const int gl = p.d >> 4, half = p.rot >> 1;
-    const int grp = threadIdx.x / gl, lane = threadIdx.x - grp * gl, ngrp = kRopeThreads / gl;
-    const int e0 = lane * 16;
-    uint32_t raw[kWords<TIn>];
-    int32_t r = grp / cols, c = grp - r * cols;
-    auto source = [&](const void *&base) -> int64_t {     // of the row that (r, c) is
+    const int gl = p.d >> 3, half = p.rot >> 1;
+    const int grp = threadIdx.x / gl, lane = threadIdx.x - grp * gl;
+    // groups g, g + rpb, .. have row g (rpb divides their number), `step` of them
+    const int32_t step = kRopeThreads / gl / p.rpb, r = grp % p.rpb, first = grp / p.rpb;
+    const int32_t turns = (cols + step - 1) / step;       // heads of a group
+    const int e0 = lane * 8;
+    uint32_t raw[A][kRopeWords<TIn>];
+    auto source = [&](int32_t c, const void *&base) -> int64_t {
         base = c < hq ? p.q : c < hq + hkv ? p.k : p.v;
         return (int64_t)(r0 + r) * (c < hq ? p.q_stride : p.k_stride) +
                (int64_t)(c < hq ? c : c < hq + hkv ? c - hq : c - hq - hkv) * p.d;
     };
-    auto fetch = [&]() {
-        if (r < nr) {
+    auto fetch = [&](int32_t turn, uint32_t (&w)[kRopeWords<TIn>]) {
+        const int32_t c = first + turn * step;
+        if (r < nr && c < cols) {
             const void *base;
-            const int64_t at = source(base);
-            load16<TIn>(base, at + e0, raw);
+            const int64_t at = source(c, base);
+            rope_load<TIn>(base, at + e0, w);
         }
     };
-    fetch();
+#pragma unroll
+    for (int u = 0; u < A; ++u)
+        fetch(u, raw[u]);
     rope_rows<TC>(p, r0, nr, m);
+    const bool live = r < nr && m.req[r < nr ? r : 0] >= 0;
+    const int64_t slot0 = TC != kNoCache && live ? m.slot[r] : -1;
+    // this lane's sines and cosines.  Pairs (t, t + half) by eights: its elements are all first ones of their pairs,
+    // all second ones, or beyond rot
+    const bool eights = !p.inter && (half & 7) == 0, second = e0 >= half;
+    const bool mine = p.inter ? lane * 4 < half : e0 < p.rot;
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        cs[i] = make_float2(1.0f, 0.0f);
+    if (live && mine && (p.inter || eights)) {
+        const float2 *at = m.cs[r] + (p.inter ? lane * 4 : e0 - (second ? half : 0));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p.inter ? i < 4 && lane * 4 + i < half : true)
+                cs[i] = at[i];
+    }
+    const int there = (threadIdx.x & 31) + (!mine ? 0 : second ? -(half >> 3) : half >> 3);
     // every thread of the block runs every turn: the shuffles are over whole warps
-    for (int32_t left = nr * cols; left > 0; left -= ngrp) {
-        const bool have = r < nr && m.req[r] >= 0;
-        const bool turns = c < hq + hkv;
-        float x[16];
-        if (have)
-            to_f32<TIn>(raw, x);
-        if (p.inter) {
-            if (have && turns) {
+    for (int32_t t0 = 0; t0 < turns; t0 += A) {
+#pragma unroll
+        for (int u = 0; u < A; ++u) {
+            const int32_t c = first + (t0 + u) * step;
+            const bool have = live && c < cols, turn = have && c < hq + hkv;
+            float x[8];
+            if (have)
+                rope_widen<TIn>(raw[u], x);
+            if (p.inter) {
+                if (turn && mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (lane * 4 + i < half) {
+                            const float a = x[2 * i], b = x[2 * i + 1];
+                            x[2 * i] = rope_first(a, b, cs[i]);
+                            x[2 * i + 1] = rope_second(a, b, cs[i]);
+                        }
+                    }
+                }
+            } else if (eights) {
+                float y[8];
+                uint32_t other[kRopeWords<TIn>];
+#pragma unroll
+                for (int i = 0; i < kRopeWords<TIn>; ++i)
+                    other[i] = __shfl_sync(0xffffffffu, raw[u][i], there);
+                rope_widen<TIn>(other, y);
+                if (turn && mine) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = second ? rope_second(y[i], x[i], cs[i]) : rope_first(x[i], y[i], cs[i]);
+                }
+            } else if (turn && mine) {
+                const void *base;
+                const int64_t at = source(c, base);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int t = lane * 8 + i;
-                    if (t < half) {
-                        const float2 w = m.cs[r][t];
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = rope_first(a, b, w);
-                        x[2 * i + 1] = rope_second(a, b, w);
-                    }
-                }
-            }
-        } else if ((half & 15) == 0) {
-            // this lane's elements are all first ones of their pairs, all second ones, or beyond rot
-            const bool second = e0 >= half;
-            const int there = (threadIdx.x & 31) + (e0 >= p.rot ? 0 : second ? -(half >> 4) : half >> 4);
-            float y[16];
-            uint32_t other[kWords<TIn>];
-#pragma unroll
-            for (int i = 0; i < kWords<TIn>; ++i)
-                other[i] = __shfl_sync(0xffffffffu, raw[i], there);
-            to_f32<TIn>(other, y);
-            if (have && turns && e0 < p.rot) {
-                const int t0 = e0 - (second ? half : 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 w = m.cs[r][t0 + i];
-                    x[i] = second ? rope_second(y[i], x[i], w) : rope_first(x[i], y[i], w);
-                }
-            }
-        } else {
-            if (have && turns) {
-                const void *base;
-                const int64_t at = source(base);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
                     const int e = e0 + i;
                     if (e < p.rot) {
-                        const bool second = e >= half;
-                        const float y = rope_one<TIn>(base, at + (second ? e - half : e + half));
-                        const float2 w = m.cs[r][second ? e - half : e];
-                        x[i] = second ? rope_second(y, x[i], w) : rope_first(x[i], y, w);
+                        const bool late = e >= half;
+                        const float y = rope_one<TIn>(base, at + (late ? e - half : e + half));
+                        const float2 w = m.cs[r][late ? e - half : e];
+                        x[i] = late ? rope_second(y, x[i], w) : rope_first(x[i], y, w);
                     }
                 }
             }
-        }
-        __syncwarp();                                     // (the row has been read: its output may lie over it)
-        if (c < hq || TC == kNoCache) {
-            if (have) {
-                uint32_t w[kWords<TIn>];
-                from_f32<TIn>(x, w);
+            __syncwarp();                                 // (the row has been read: its output may lie over it)
+            if (have && (c < hq || TC == kNoCache)) {
+                uint32_t w[kRopeWords<TIn>];
+                rope_narrow<TIn>(x, w);
                 if (c < hq)
-                    store16<TIn>(p.q_out, (int64_t)(r0 + r) * p.qo_stride + (int64_t)c * p.d + e0, w);
+                    rope_store<TIn>(p.q_out, (int64_t)(r0 + r) * p.qo_stride + (int64_t)c * p.d + e0, w);
                 else
-                    store16<TIn>(p.k_out, (int64_t)(r0 + r) * p.ko_stride + (int64_t)(c - hq) * p.d + e0, w);
+                    rope_store<TIn>(p.k_out, (int64_t)(r0 + r) * p.ko_stride + (int64_t)(c - hq) * p.d + e0, w);
             }
-        }
-        if constexpr (TC != kNoCache) {
-            const bool v = c >= hq + hkv;
-            const int64_t slot = have && c >= hq ? m.slot[r] : -1;
-            const int32_t h = c - hq - (v ? hkv : 0);
-            const int64_t e = slot + h * p.c.s_head + e0;
-            void *pool = v ? p.c.v : p.c.k;
-            if constexpr (TC == SVP_E4M3) {
-                uint32_t amax = 0u;
-                if (slot >= 0) {
+            if constexpr (TC != kNoCache) {
+                const bool v = c >= hq + hkv;
+                const bool store = have && c >= hq && slot0 >= 0;
+                const int32_t h = c - hq - (v ? hkv : 0);
+                const int64_t e = slot0 + h * p.c.s_head + e0;
+                void *pool = v ? p.c.v : p.c.k;
+                if constexpr (TC == SVP_E4M3) {
+                    uint32_t amax = 0u;
+                    if (store) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-                }
-                for (int o = gl >> 1; o > 0; o >>= 1)
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (slot >= 0) {
-                    const bool fine = amax < 0x7f800000u;
-                    const uint32_t b = fine ? exp_byte_of(amax) : 255u;
-                    const float inv = __uint_as_float((254u - b) << 23);   // 2^-(b - 127)
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-                    if (fine) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = pack_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-                                   (pack_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+                        for (int i = 0; i < 8; ++i)
+                            amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
                     }
-                    store16<SVP_E4M3>(pool, e, w);
-                    if (lane == 0)
-                        (v ? p.c.v_exp : p.c.k_exp)[m.eoff[r] + ((int64_t)h << p.c.page_shift)] = (uint8_t)b;
-                }
-            } else if (slot >= 0) {
-                if (TIn == TC && v) {
-                    if constexpr (TIn == TC)
-                        store16<TC>(pool, e, raw);                        // bits as they are
-                } else {
-                    uint32_t w[kWords<TC>];
-                    from_f32<TC>(x, w);
-                    store16<TC>(pool, e, w);
+                    for (int o = gl >> 1; o > 0; o >>= 1)
+                        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (store) {
+                        const bool fine = amax < 0x7f800000u;
+                        const uint32_t b = fine ? exp_byte_of(amax) : 255u;
+                        const float inv = __uint_as_float((254u - b) << 23);   // 2^-(b - 127)
+                        uint32_t w[2] = {0u, 0u};
+                        if (fine) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                w[i] = pack_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+                                       (pack_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+                        }
+                        rope_store<SVP_E4M3>(pool, e, w);
+                        if (lane == 0)
+                            (v ? p.c.v_exp : p.c.k_exp)[m.eoff[r] + ((int64_t)h << p.c.page_shift)] = (uint8_t)b;
+                    }
+                } else if (store) {
+                    if (TIn == TC && v) {
+                        if constexpr (TIn == TC)
+                            rope_store<TC>(pool, e, raw[u]);              // bits as they are
+                    } else {
+                        uint32_t w[kRopeWords<TC>];
+                        rope_narrow<TC>(x, w);
+                        rope_store<TC>(pool, e, w);
+                    }
                 }
             }
+            fetch(t0 + u + A, raw[u]);
         }
-        c += ngrp;
-        while (c >= cols) {
-            c -= cols;
-            ++r;
-        }
-        fetch();
     }
 }
 
@@ -270,9 +335,12 @@ int sm_count();
 template <int TIn, int TC>
 static svp_status rope_launch(RopeParams &p, cudaStream_t stream)
 {
-    // one row a block while that leaves fewer than four blocks an SM
+    // one row a block while that leaves fewer than four blocks an SM, then a power of two (each row has as many groups
+    // of lanes; 8 at d = 256, where a block has eight)
     const int32_t want = p.rows / (4 * sm_count());
-    p.rpb = want < 1 ? 1 : want > kRopeRows ? kRopeRows : want;
+    p.rpb = 1;
+    while (p.rpb * 2 <= want && p.rpb < kRopeRows)
+        p.rpb *= 2;
     const unsigned grid = (unsigned)((p.rows + p.rpb - 1) / p.rpb);
     return launch_pdl(rope_kernel<TIn, TC>, dim3(grid), dim3(kRopeThreads), 0, stream, p) == cudaSuccess ? SVP_OK
                                                                                                          : SVP_ECUDA;
