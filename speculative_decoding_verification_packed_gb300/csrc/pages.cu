@@ -39,7 +39,7 @@ struct PagesCaches {
     void *k[SVP_PAGES_MAX_CACHES], *v[SVP_PAGES_MAX_CACHES];
     uint8_t *k_exp[SVP_PAGES_MAX_CACHES], *v_exp[SVP_PAGES_MAX_CACHES];
     int64_t s_page, s_head, s_tok;    // bytes
-    int32_t count, hkv, row;          // row: 16-byte pieces of a (token, head) row
+    int32_t count, hkv, row_shift;    // 2^row_shift 16-byte pieces in a (token, head) row
 };
 
 // ------------------------------------------------------------------ cluster
@@ -71,37 +71,41 @@ __device__ __forceinline__ int32_t cluster_load(const int32_t *x, uint32_t rank)
 }
 
 struct PagesShared {
-    int32_t warp[kPgWarps], before[kPgWarps];
+    uint64_t both[kPgWarps];
+    int32_t warp[kPgWarps];
     int32_t tot[2];                   // this block's count, of even and odd windows
     int32_t need[kPgRequests + 1], drop[kPgRequests + 1];   // before each request
     int32_t a[kPgRequests], b[kPgRequests];
 };
 
-// Exclusive prefix sums of x over the block's threads into out[0 .. kPgThreads]; ends in a barrier.
-__device__ __forceinline__ void pages_scan(PagesShared &s, int32_t x, int32_t *out)
+// Exclusive prefix sums of need and drop (both below 2^31 in all) over the block's threads into s.need and s.drop
+// [0 .. kPgThreads]; ends in a barrier.
+__device__ __forceinline__ void pages_scan(PagesShared &s, int32_t need, int32_t drop)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t incl = x;
+    uint64_t incl = (uint64_t)(uint32_t)need | (uint64_t)(uint32_t)drop << 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o)
             incl += v;
     }
     if (lane == 31)
-        s.warp[warp] = incl;
+        s.both[warp] = incl;
     __syncthreads();
-    int32_t w = s.warp[lane];
+    uint64_t w = s.both[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xffffffffu, w, o);
+        const uint64_t v = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o)
             w += v;
     }
-    const int32_t before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    out[threadIdx.x + 1] = before + incl;
+    const uint64_t ahead = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    incl += warp == 0 ? 0 : ahead;
+    s.need[threadIdx.x + 1] = (int32_t)incl;
+    s.drop[threadIdx.x + 1] = (int32_t)(incl >> 32);
     if (threadIdx.x == 0)
-        out[0] = 0;
+        s.need[0] = s.drop[0] = 0;
     __syncthreads();
 }
 
@@ -222,8 +226,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         s.a[i] = held;
         s.b[i] = want;
         // (sums of up to 1024 x max_pages < 2^31: checked on the host)
-        pages_scan(s, max(want - held, 0), s.need);
-        pages_scan(s, max(held - want, 0), s.drop);
+        pages_scan(s, max(want - held, 0), max(held - want, 0));
     }
     cluster_sync();
     if (rank != 0) {
@@ -237,19 +240,37 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     }
     const int32_t need = s.need[kPgThreads], drop = s.drop[kPgThreads];
     if (drop > 0) {
-        for (int32_t x = (int32_t)rank * kPgThreads + i; x < drop; x += kPgCluster * kPgThreads) {
-            const int32_t q = pages_owner(s.drop, kPgRequests, x);
-            int32_t *at = p.table + (int64_t)q * p.max_pages + s.b[q] + (x - s.drop[q]);
-            const int32_t page = __ldcg(at);
-            *at = -1;
-            if (page >= 0 && page < p.num_pages) {
-                if (atomicSub(p.refs + page, 1) <= 0) {
-                    atomicAdd(p.refs + page, 1);
+        // (four entries a thread in flight: one, with its chain entry -> count, took 28 us for 75000 entries)
+        constexpr int U = 4, kAll = kPgCluster * kPgThreads;
+        for (int32_t x0 = (int32_t)rank * kPgThreads + i; x0 < drop; x0 += U * kAll) {
+            int32_t page[U], old[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t x = x0 + (int64_t)u * kAll;
+                page[u] = -1;
+                if (x < drop) {
+                    const int32_t q = pages_owner(s.drop, kPgRequests, (int32_t)x);
+                    int32_t *at = p.table + (int64_t)q * p.max_pages + s.b[q] + ((int32_t)x - s.drop[q]);
+                    page[u] = __ldcg(at);
+                    *at = -1;
+                    if (page[u] < 0 || page[u] >= p.num_pages) {
+                        page[u] = -1;
+                        bits |= SVP_DEV_BAD_CONTEXT;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                old[u] = page[u] >= 0 ? atomicSub(p.refs + page[u], 1) : 1;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (old[u] <= 0) {                        // (a count that was none already)
+                    atomicAdd(p.refs + page[u], 1);
                     bits |= SVP_DEV_BAD_CONTEXT;
                 }
-            } else {
-                bits |= SVP_DEV_BAD_CONTEXT;
             }
+            if (drop - x0 <= U * kAll)
+                break;                                    // (x0 may not pass 2^31)
         }
         cluster_sync();
     }
@@ -319,7 +340,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         fine = false;
         bits = SVP_DEV_BAD_SLOTS;
     }
-    pages_scan(s, fine && part ? 1 : 0, s.need);
+    pages_scan(s, fine && part ? 1 : 0, 0);
     cluster_sync();
     const int32_t need = cluster_load(&s.need[kPgThreads], 0);
     uint32_t w = 0;
@@ -343,33 +364,34 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     }
 }
 
-// Copies 16-byte pieces [lo, hi) of a page's rows (head, token, piece), tokens below `tokens` of each head.
-__device__ __forceinline__ void pages_copy(const PagesCaches &c, void *pool, int32_t from, int32_t to, int32_t tokens)
+constexpr int kPgCopyThreads = 256;
+
+// Copies a page's rows (head, token) in 16-byte pieces, tokens below `tokens` of each head.  A row has a power of two
+// of pieces, a page one of tokens.
+__device__ __forceinline__ void pages_copy(const PagesCaches &c, void *pool, int32_t from, int32_t to, int32_t tokens,
+                                           int32_t page_shift)
 {
     constexpr int U = 8;
     const uint8_t *src = static_cast<const uint8_t *>(pool) + from * c.s_page;
     uint8_t *dst = static_cast<uint8_t *>(pool) + to * c.s_page;
-    const int32_t per = tokens * c.row, count = c.hkv * per;
-    for (int32_t x0 = threadIdx.x; x0 < count; x0 += U * (int32_t)blockDim.x) {
+    const int32_t count = c.hkv << (page_shift + c.row_shift);
+    for (int32_t x0 = threadIdx.x; x0 < count; x0 += U * kPgCopyThreads) {
         uint4 v[U];
         int64_t at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t x = x0 + u * (int32_t)blockDim.x;
-            if (x < count) {
-                const int32_t h = x / per, y = x - h * per, t = y / c.row;
-                at[u] = h * c.s_head + t * c.s_tok + (y - t * c.row) * 16;
+            const int32_t x = x0 + u * kPgCopyThreads, y = x >> c.row_shift;
+            const int32_t h = y >> page_shift, t = y - (h << page_shift);
+            at[u] = x < count && t < tokens ? h * c.s_head + t * c.s_tok + (x - (y << c.row_shift)) * 16 : -1;
+            if (at[u] >= 0)
                 v[u] = *reinterpret_cast<const uint4 *>(src + at[u]);
-            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (x0 + u * (int32_t)blockDim.x < count)
+            if (at[u] >= 0)
                 *reinterpret_cast<uint4 *>(dst + at[u]) = v[u];
     }
 }
-
-constexpr int kPgCopyThreads = 256;
 
 // Block (f, y): y = 0 the table's row of fork f, else K (odd y) or V of cache (y - 1) / 2.
 __global__ void __launch_bounds__(kPgCopyThreads) pages_fork_copy_kernel(const __grid_constant__ PagesParams p,
@@ -412,7 +434,7 @@ __global__ void __launch_bounds__(kPgCopyThreads) pages_fork_copy_kernel(const _
     }
     const int32_t x = (blockIdx.y - 1) >> 1;
     const bool v = (blockIdx.y - 1) & 1;
-    pages_copy(c, v ? c.v[x] : c.k[x], from, page, part);
+    pages_copy(c, v ? c.v[x] : c.k[x], from, page, part, p.page_shift);
     uint8_t *exps = v ? c.v_exp[x] : c.k_exp[x];
     if (exps)
         for (int32_t y = tid; y < c.hkv * part; y += kPgCopyThreads) {
@@ -536,7 +558,7 @@ __global__ void __launch_bounds__(kPgCopyThreads) pages_move_kernel(const __grid
         if (!inside(from, to))
             continue;
         const bool v = y & 1;
-        pages_copy(c, v ? c.v[y >> 1] : c.k[y >> 1], from, to, 1 << p.page_shift);
+        pages_copy(c, v ? c.v[y >> 1] : c.k[y >> 1], from, to, 1 << p.page_shift, p.page_shift);
         uint8_t *exps = v ? c.v_exp[y >> 1] : c.k_exp[y >> 1];
         if (exps) {
             const int32_t bytes = c.hkv << p.page_shift;  // (a multiple of 16)
@@ -643,7 +665,8 @@ static svp_status pages_caches(const svp_pages *pages, const svp_cache *caches, 
         c.s_head = caches[0].stride_head * esz;
         c.s_tok = caches[0].stride_tok * esz;
         c.hkv = hkv;
-        c.row = (int32_t)(d * esz / 16);
+        while ((16 << c.row_shift) < d * esz)
+            ++c.row_shift;
     }
     return SVP_OK;
 }

@@ -14,7 +14,10 @@
 // element by element from memory.  All reads of a row come before its writes (one warp holds it), so
 // an output may be its input.
 //
-// What bounds it: the chain cu -> context -> angle -> row for few rows, memory for prompts.
+// What bounds it: the chain cu -> context -> angle -> row for few rows (64 blocks of up to 16 rows, 11 MB: 5.0 us from
+// a graph); memory for prompts (those 519 MB: 94 us, 5.5 TB/s), with the issue slots 60% busy beside it, so that
+// occupancy counts: with 3 blocks an SM instead of 4, and four heads in flight instead of three, the
+// blocks take 6.6 us.
 #include <cmath>
 
 #include "svp_cache.cuh"
@@ -23,7 +26,7 @@ namespace svp {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 8;          // packed rows of a block, at most
-template <int T> constexpr int kRopeAhead = T == SVP_F32 ? 2 : 4;   // heads of a group in flight: 64 bytes a lane
+template <int T> constexpr int kRopeAhead = T == SVP_F32 ? 2 : 3;   // heads of a group in flight
 
 struct RopeParams {
     CacheParams c;
@@ -111,9 +114,15 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int32_t r0, int32
     __syncthreads();
 }
 
-// One element of a pair: x w.x -+ y w.y, the same operations wherever it is made.
-__device__ __forceinline__ float rope_first(float x, float y, float2 w) { return fmaf(x, w.x, -__fmul_rn(y, w.y)); }
-__device__ __forceinline__ float rope_second(float x, float y, float2 w) { return fmaf(x, w.y, __fmul_rn(y, w.x)); }
+// One element of a pair, x cos + y (-sin, or sin for the second one): the same operations wherever it is made.
+__device__ __forceinline__ float rope_turn(float x, float y, float c, float s) { return fmaf(x, c, __fmul_rn(y, s)); }
+
+__device__ __forceinline__ uint64_t rope_mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 template <int T>
 __device__ __forceinline__ float rope_one(const void *base, int64_t e)
@@ -178,7 +187,7 @@ __device__ __forceinline__ void rope_narrow(const float (&x)[8], uint32_t (&w)[k
 
 // TIn: type of the rows; TC: of the cache, or kNoCache (k goes to k_out).
 template <int TIn, int TC>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int A = kRopeAhead<TIn>;
     __shared__ RopeRows m;
@@ -194,18 +203,23 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
     const int32_t turns = (cols + step - 1) / step;       // heads of a group
     const int e0 = lane * 8;
     uint32_t raw[A][kRopeWords<TIn>];
-    auto source = [&](int32_t c, const void *&base) -> int64_t {
-        base = c < hq ? p.q : c < hq + hkv ? p.k : p.v;
-        return (int64_t)(r0 + r) * (c < hq ? p.q_stride : p.k_stride) +
-               (int64_t)(c < hq ? c : c < hq + hkv ? c - hq : c - hq - hkv) * p.d;
+    // column c (a head of q, then of k, then of v) of this row is at source(c) + c * d
+    constexpr int kSize = TIn == SVP_F32 ? 4 : 2;
+    const int32_t hd = p.d * kSize;
+    const uint8_t *const in_q = static_cast<const uint8_t *>(p.q) + (r0 + r) * p.q_stride * kSize;
+    const uint8_t *const in_k = static_cast<const uint8_t *>(p.k) + ((r0 + r) * p.k_stride - (int64_t)hq * p.d) * kSize;
+    const uint8_t *const in_v =
+        TC == kNoCache ? nullptr : static_cast<const uint8_t *>(p.v) + ((r0 + r) * p.k_stride - (int64_t)(hq + hkv) * p.d) * kSize;
+    uint8_t *const out_q = static_cast<uint8_t *>(p.q_out) + (r0 + r) * p.qo_stride * kSize + e0 * kSize;
+    uint8_t *const out_k =
+        TC != kNoCache ? nullptr : static_cast<uint8_t *>(p.k_out) + ((r0 + r) * p.ko_stride - (int64_t)hq * p.d) * kSize + e0 * kSize;
+    auto source = [&](int32_t c) -> const uint8_t * {
+        return (c < hq ? in_q : TC == kNoCache || c < hq + hkv ? in_k : in_v) + (int64_t)c * hd;
     };
     auto fetch = [&](int32_t turn, uint32_t (&w)[kRopeWords<TIn>]) {
         const int32_t c = first + turn * step;
-        if (r < nr && c < cols) {
-            const void *base;
-            const int64_t at = source(c, base);
-            rope_load<TIn>(base, at + e0, w);
-        }
+        if (r < nr && c < cols)
+            rope_load<TIn>(source(c), e0, w);
     };
 #pragma unroll
     for (int u = 0; u < A; ++u)
@@ -227,6 +241,11 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
         for (int i = 0; i < 8; ++i)
             if (p.inter ? i < 4 && lane * 4 + i < half : true)
                 cs[i] = at[i];
+        if (eights && !second) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                cs[i].y = -cs[i].y;
+        }
     }
     const int there = (threadIdx.x & 31) + (!mine ? 0 : second ? -(half >> 3) : half >> 3);
     // every thread of the block runs every turn: the shuffles are over whole warps
@@ -244,8 +263,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
                     for (int i = 0; i < 4; ++i) {
                         if (lane * 4 + i < half) {
                             const float a = x[2 * i], b = x[2 * i + 1];
-                            x[2 * i] = rope_first(a, b, cs[i]);
-                            x[2 * i + 1] = rope_second(a, b, cs[i]);
+                            x[2 * i] = rope_turn(a, b, cs[i].x, -cs[i].y);
+                            x[2 * i + 1] = rope_turn(b, a, cs[i].x, cs[i].y);
                         }
                     }
                 }
@@ -258,20 +277,21 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
                 rope_widen<TIn>(other, y);
                 if (turn && mine) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = second ? rope_second(y[i], x[i], cs[i]) : rope_first(x[i], y[i], cs[i]);
+                    for (int i = 0; i < 8; i += 2)
+                        f32x2_unpack(f32x2_fma(f32x2_pack(x[i], x[i + 1]), f32x2_pack(cs[i].x, cs[i + 1].x),
+                                               rope_mul2(f32x2_pack(y[i], y[i + 1]), f32x2_pack(cs[i].y, cs[i + 1].y))),
+                                     x[i], x[i + 1]);
                 }
             } else if (turn && mine) {
-                const void *base;
-                const int64_t at = source(c, base);
+                const uint8_t *base = source(c);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int e = e0 + i;
                     if (e < p.rot) {
                         const bool late = e >= half;
-                        const float y = rope_one<TIn>(base, at + (late ? e - half : e + half));
+                        const float y = rope_one<TIn>(base, late ? e - half : e + half);
                         const float2 w = m.cs[r][late ? e - half : e];
-                        x[i] = late ? rope_second(y, x[i], w) : rope_first(x[i], y, w);
+                        x[i] = rope_turn(x[i], y, w.x, late ? w.y : -w.y);
                     }
                 }
             }
@@ -279,10 +299,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
             if (have && (c < hq || TC == kNoCache)) {
                 uint32_t w[kRopeWords<TIn>];
                 rope_narrow<TIn>(x, w);
-                if (c < hq)
-                    rope_store<TIn>(p.q_out, (int64_t)(r0 + r) * p.qo_stride + (int64_t)c * p.d + e0, w);
-                else
-                    rope_store<TIn>(p.k_out, (int64_t)(r0 + r) * p.ko_stride + (int64_t)(c - hq) * p.d + e0, w);
+                rope_store<TIn>((TC != kNoCache || c < hq ? out_q : out_k) + (int64_t)c * hd, 0, w);
             }
             if constexpr (TC != kNoCache) {
                 const bool v = c >= hq + hkv;
