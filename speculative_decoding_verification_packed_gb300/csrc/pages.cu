@@ -19,7 +19,7 @@
 namespace svp {
 
 constexpr int kPgCluster = 8, kPgThreads = 1024, kPgWarps = kPgThreads / 32;
-constexpr int kPgMost = 8;            // pages of a lane in one window: a window is 8 x 1024 x 8 pages at most
+constexpr int kPgMost = 8;            // units of 32 pages that a warp has in one window, at most
 constexpr int kPgRequests = 1024;     // requests, or forks, of a call: one a thread
 
 struct PagesParams {
@@ -50,15 +50,29 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// Barrier of every thread of the cluster; what was written before it is seen after it.
-__device__ __forceinline__ void cluster_sync()
+// Barrier of every thread of the cluster.  What a thread that says `wrote` has written before it is seen by all after
+// it; warps without such a thread pay no fence (a window's 0.3 us otherwise).
+__device__ __forceinline__ void cluster_sync(bool wrote)
 {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (__any_sync(0xffffffffu, wrote))
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ int32_t cluster_load(const int32_t *x, uint32_t rank)   // block rank's copy of x
+__device__ __forceinline__ uint64_t cluster_load64(const uint64_t *x, uint32_t rank)   // block rank's copy of x
+{
+    uint64_t v;
+    asm volatile("{\n\t.reg .b32 a;\n\t"
+                 "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.b64 %0, [a];\n\t}"
+                 : "=l"(v)
+                 : "r"(smem_u32(x)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ int32_t cluster_load(const int32_t *x, uint32_t rank)
 {
     int32_t v;
     asm volatile("{\n\t.reg .b32 a;\n\t"
@@ -72,8 +86,10 @@ __device__ __forceinline__ int32_t cluster_load(const int32_t *x, uint32_t rank)
 
 struct PagesShared {
     uint64_t both[kPgWarps];
+    uint64_t units[2][kPgWarps], sum[2][2];   // counts of a window's units, 16 bits each: of the warps; of this block,
+                                              // of even and odd windows
     int32_t warp[kPgWarps];
-    int32_t tot[2];                   // this block's count, of even and odd windows
+    int32_t tot[2];
     int32_t need[kPgRequests + 1], drop[kPgRequests + 1];   // before each request
     int32_t a[kPgRequests], b[kPgRequests];
 };
@@ -128,7 +144,7 @@ __device__ __forceinline__ int32_t pages_total(PagesShared &s, uint32_t rank, ui
 {
     if (threadIdx.x == 0)
         s.tot[w & 1] = mine;
-    cluster_sync();
+    cluster_sync(threadIdx.x == 0);
     const int lane = threadIdx.x & 31;
     int32_t v = lane < kPgCluster ? cluster_load(&s.tot[w & 1], lane) : 0;
 #pragma unroll
@@ -142,47 +158,70 @@ __device__ __forceinline__ int32_t pages_total(PagesShared &s, uint32_t rank, ui
 }
 
 // Calls take(r, page) for the free pages with ranks r < need, by id; returns how many were looked up, which is
-// less than need only if there are no more.  w: windows so far (for pages_total).
+// less than need only if there are no more.  A window is `each` units of 32 pages a warp, dealt out in turn, so that the
+// first free pages, which are the ones that are taken, are spread over all blocks.
 template <class F>
-__device__ __forceinline__ int32_t pages_find(const PagesParams &p, PagesShared &s, uint32_t rank, uint32_t &w, int32_t need,
-                                              F take)
+__device__ __forceinline__ int32_t pages_find(const PagesParams &p, PagesShared &s, uint32_t rank, int32_t need, F take)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spread = ((int64_t)p.num_pages + kPgCluster * kPgThreads - 1) / (kPgCluster * kPgThreads);
-    const int each = (int)(spread < kPgMost ? spread : kPgMost);         // pages of a lane
+    const int each = (int)(spread < kPgMost ? spread : kPgMost);
     int32_t found = 0;
-    for (int64_t base = 0; base < p.num_pages && found < need; base += (int64_t)each * kPgCluster * kPgThreads) {
-        const int64_t first = base + ((int64_t)rank * kPgWarps + warp) * each * 32;
+    uint32_t w = 0;
+    for (int64_t base = 0; base < p.num_pages && found < need; base += (int64_t)each * kPgCluster * kPgThreads, ++w) {
+        const int64_t first = base + ((int64_t)rank * kPgWarps + warp) * 32 + lane;
         uint32_t mask[kPgMost];
-        int32_t cnt = 0;
+        uint64_t cnt[2] = {0, 0};                         // (a unit's counts are at most 8192 over the cluster)
 #pragma unroll
         for (int u = 0; u < kPgMost; ++u) {
-            const int64_t page = first + u * 32 + lane;
+            const int64_t page = first + u * (kPgCluster * kPgThreads);
             mask[u] = __ballot_sync(0xffffffffu, u < each && page < p.num_pages && __ldcg(p.refs + page) == 0);
-            cnt += __popc(mask[u]);
+            cnt[u >> 2] |= (uint64_t)__popc(mask[u]) << (16 * (u & 3));
         }
-        if (lane == 0)
-            s.warp[warp] = cnt;
+        if (lane < 2)
+            s.units[lane][warp] = cnt[lane];
         __syncthreads();
-        int32_t v = s.warp[lane];
+        uint64_t at[2], all[2];                           // free pages of each unit before this warp's, and in all
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o)
-                v += u;
+        for (int x = 0; x < 2; ++x) {
+            at[x] = all[x] = 0;
+            if (x * 4 >= each)
+                continue;
+            uint64_t v = s.units[x][lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o)
+                    v += y;
+            }
+            const uint64_t ahead = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
+            at[x] = warp == 0 ? 0 : ahead;
+            if (threadIdx.x == kPgThreads - 1)
+                s.sum[w & 1][x] = v;                      // (the other pair is still read, in the window before)
         }
-        const int32_t mine = __shfl_sync(0xffffffffu, v, 31), ahead = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
-        int32_t before;
-        const int32_t all = pages_total(s, rank, w++, mine, before);
-        int32_t r = found + before + (warp == 0 ? 0 : ahead);
+        cluster_sync(threadIdx.x == kPgThreads - 1);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (x * 4 >= each)
+                continue;
+            uint64_t v = lane < kPgCluster ? cluster_load64(&s.sum[w & 1][x], lane) : 0;
+#pragma unroll
+            for (int o = 1; o < kPgCluster; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o && lane < kPgCluster)
+                    v += y;
+            }
+            const uint64_t ahead = __shfl_sync(0xffffffffu, v, (int)(rank + 31) & 31);
+            at[x] += rank == 0 ? 0 : ahead;
+            all[x] = __shfl_sync(0xffffffffu, v, kPgCluster - 1);
+        }
 #pragma unroll
         for (int u = 0; u < kPgMost; ++u) {
-            const int32_t at = r + __popc(mask[u] & ((1u << lane) - 1u));
-            if ((mask[u] >> lane & 1u) && at < need)
-                take(at, (int32_t)(first + u * 32 + lane));
-            r += __popc(mask[u]);
+            const int32_t r = found + (int32_t)(at[u >> 2] >> (16 * (u & 3)) & 0xffffu) + __popc(mask[u] & ((1u << lane) - 1u));
+            if ((mask[u] >> lane & 1u) && r < need)
+                take(r, (int32_t)(first + u * (kPgCluster * kPgThreads)));
+            found += (int32_t)(all[u >> 2] >> (16 * (u & 3)) & 0xffffu);
         }
-        found += all;
     }
     return found;
 }
@@ -228,19 +267,22 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         // (sums of up to 1024 x max_pages < 2^31: checked on the host)
         pages_scan(s, max(want - held, 0), max(held - want, 0));
     }
-    cluster_sync();
+    cluster_sync(rank == 0);
     if (rank != 0) {
-        s.a[i] = cluster_load(&s.a[i], 0);
-        s.b[i] = cluster_load(&s.b[i], 0);
-        s.need[i + 1] = cluster_load(&s.need[i + 1], 0);
-        s.drop[i + 1] = cluster_load(&s.drop[i + 1], 0);
+        // (of the requests that there are: block 0 answers for seven)
+        if (i < p.n) {
+            s.a[i] = cluster_load(&s.a[i], 0);
+            s.b[i] = cluster_load(&s.b[i], 0);
+            s.need[i + 1] = cluster_load(&s.need[i + 1], 0);
+            s.drop[i + 1] = cluster_load(&s.drop[i + 1], 0);
+        }
         if (i == 0)
             s.need[0] = s.drop[0] = 0;
         __syncthreads();
     }
-    const int32_t need = s.need[kPgThreads], drop = s.drop[kPgThreads];
+    const int32_t need = s.need[p.n], drop = s.drop[p.n];
     if (drop > 0) {
-        // (four entries a thread in flight: one, with its chain entry -> count, took 28 us for 75000 entries)
+        // (four entries a thread in flight; 54700 entries take 12 us of a call's 21, bound by their blocks' atomics)
         constexpr int U = 4, kAll = kPgCluster * kPgThreads;
         for (int32_t x0 = (int32_t)rank * kPgThreads + i; x0 < drop; x0 += U * kAll) {
             int32_t page[U], old[U];
@@ -249,7 +291,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
                 const int64_t x = x0 + (int64_t)u * kAll;
                 page[u] = -1;
                 if (x < drop) {
-                    const int32_t q = pages_owner(s.drop, kPgRequests, (int32_t)x);
+                    const int32_t q = pages_owner(s.drop, p.n, (int32_t)x);
                     int32_t *at = p.table + (int64_t)q * p.max_pages + s.b[q] + ((int32_t)x - s.drop[q]);
                     page[u] = __ldcg(at);
                     *at = -1;
@@ -272,20 +314,19 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
             if (drop - x0 <= U * kAll)
                 break;                                    // (x0 may not pass 2^31)
         }
-        cluster_sync();
+        cluster_sync((int32_t)rank * kPgThreads + i < drop);
     }
     int32_t found = 0;
     if (need > 0) {
-        uint32_t w = 0;
-        found = pages_find(p, s, rank, w, need, [&](int32_t r, int32_t page) {
-            const int32_t q = pages_owner(s.need, kPgRequests, r);
+        found = pages_find(p, s, rank, need, [&](int32_t r, int32_t page) {
+            const int32_t q = pages_owner(s.need, p.n, r);
             p.table[(int64_t)q * p.max_pages + s.a[q] + (r - s.need[q])] = page;
             p.refs[page] = 1;
         });
         if (found < need) {
             // the request that the last pages did not suffice for gives its own back
-            cluster_sync();
-            const int32_t q = pages_owner(s.need, kPgRequests, found);
+            cluster_sync(true);
+            const int32_t q = pages_owner(s.need, p.n, found);
             for (int32_t x = s.need[q] + i; rank == 0 && x < found; x += kPgThreads) {
                 int32_t *at = p.table + (int64_t)q * p.max_pages + s.a[q] + (x - s.need[q]);
                 p.refs[__ldcg(at)] = 0;
@@ -299,7 +340,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         p.used[i] = want;
     if (bits)
         set_status(p.status, bits);
-    cluster_sync();                                       // (no block leaves while another reads its counts)
+    cluster_sync(false);                                       // (no block leaves while another reads its counts)
 }
 
 // ------------------------------------------------------------------ fork
@@ -341,16 +382,15 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         bits = SVP_DEV_BAD_SLOTS;
     }
     pages_scan(s, fine && part ? 1 : 0, 0);
-    cluster_sync();
+    cluster_sync(rank == 0);
     const int32_t need = cluster_load(&s.need[kPgThreads], 0);
-    uint32_t w = 0;
     int32_t found = 0;
     if (need > 0)
-        found = pages_find(p, s, rank, w, need, [&](int32_t r, int32_t page) {
+        found = pages_find(p, s, rank, need, [&](int32_t r, int32_t page) {
             p.tail[r] = page;
             p.refs[page] = 1;
         });
-    cluster_sync();                                       // the tails are written, `used` has been read
+    cluster_sync(need > 0);                                       // the tails are written, `used` has been read
     if (rank == 0 && f < p.forks) {
         const bool got = fine && s.need[f + 1] <= found;  // (forks behind the last page that there is need it too, or a later one)
         if (fine && !got)
@@ -515,7 +555,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         if (p.live)
             *p.live = live;
     }
-    cluster_sync();                                       // (no block leaves while another reads its counts)
+    cluster_sync(false);                                       // (no block leaves while another reads its counts)
 }
 
 __global__ void __launch_bounds__(kPgCopyThreads) pages_move_kernel(const __grid_constant__ PagesParams p,
