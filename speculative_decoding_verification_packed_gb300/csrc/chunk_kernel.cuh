@@ -888,9 +888,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                 const int32_t row = s.off + s.tb0 + tok, head = s.g * p.G + r % p.G;
                 const int32_t slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
                 int64_t prow = (int64_t)slot * Cfg::kPartRows + (lng ? a * 128 : 0) + r;
+                float *part_o = p.part_o;
+                float2 *part_ml = p.part_ml;
                 if constexpr (kShared) {
-                    if (s.t0 == 0 && s.t1 == s.nt)
-                        prow = px_place(p, s.group, row, head, 2 * (int64_t)gridDim.x * Cfg::kPartRows);
+                    if (s.t0 == 0 && s.t1 == s.nt) {
+                        prow = px_place(p, s.group, row, head);
+                        part_o = p.place_o;
+                        part_ml = p.place_ml;
+                    }
                 }
                 const float inv = 1.0f / l;
                 if (warp_live) {
@@ -932,7 +937,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                                         make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
                             }
                         } else {
-                            float *dst = p.part_o + prow * D + cc * 32;
+                            float *dst = part_o + prow * D + cc * 32;
 #pragma unroll
                             for (int v = 0; v < 4; ++v)
                                 ck_store8(dst + 8 * v, ov + 8 * v);
@@ -940,7 +945,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
                     }
                     if (live) {
                         if (!whole)
-                            p.part_ml[prow] = make_float2(m_ref, l);
+                            part_ml[prow] = make_float2(m_ref, l);
                         else if (p.lse)
                             p.lse[(int64_t)row * p.hq + head] = (m_ref + __log2f(l)) * 0.69314718055994531f;
                     }

@@ -55,9 +55,13 @@ struct ChunkParams {
     // groups of requests with common first pages (prefix_pieces.cuh)
     const int32_t *cu_groups, *prefix_len;
     int32_t ng;
+    int32_t part, share_rows;         // pairs of this kernel: kPxAll, ..; tokens of a block of the group kernel
     int4 *plan;                       // [grid][2 * kPxMost]
     struct PrefixRec *rec;            // [n]
-    int64_t *total;
+    struct PrefixGroup *grp;          // [n]
+    int64_t *total;                   // costs of the groups' kernel and of the requests'
+    float2 *place_ml;                 // [2][m_cap][hq]: parts of rows that one piece has all of
+    float *place_o;                   // [2][m_cap][hq][d]
 };
 
 // One CTA an SM.  A dependent of the previous kernel starts 3 us earlier, but its CTAs go to SMs as these

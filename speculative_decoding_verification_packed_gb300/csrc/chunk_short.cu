@@ -33,8 +33,9 @@
 // Pieces, their split over the CTAs and the joining of split pairs are those of chunk_tc.cu.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
-#include "chunk_pieces.cuh"
+#include "prefix_pieces.cuh"
 
 namespace svp {
 
@@ -98,9 +99,11 @@ __device__ __forceinline__ uint32_t sh_chunk(int row, int c)
     return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D, int NB>
+// kShared: the requests of svp_prefix_attn, behind what their groups share.
+template <int D, int NB, bool kShared>
 __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid_constant__ ChunkParams p)
 {
+    using Piece = std::conditional_t<kShared, PrefixPiece, ChunkPiece>;
     using Cfg = ShortCfg<D, NB>;
     constexpr int NI = Cfg::NI, KS = Cfg::KS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -124,14 +127,20 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
     }
     griddep_launch_dependents();
     griddep_wait();
-    if (tid == 0)
+    if (!kShared && tid == 0)
         p.desc[blockIdx.x].np = 0;
     int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
-    ck_prologue<1>(p, prefix, m->warp_tot);
-    const ChunkShares shares = ck_shares(prefix[p.n]);
+    int32_t pairs = p.n;
+    if constexpr (kShared)
+        pairs = px_prologue<1>(p, smem + p.off_ring);
+    else
+        ck_prologue<1>(p, prefix, m->warp_tot);
+    const ChunkShares shares = ck_shares(prefix[pairs]);
     const int32_t cta = blockIdx.x;
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
-    ChunkPiece s;
+    Piece s;
+    if constexpr (kShared)
+        px_bind(p, s, pairs);
     const bool have0 = ck_first<1>(p, prefix, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
         uint32_t slot = kv, phase = 0, done = 0;
         bool ok = true;
         for (bool have = have0; have && ok; have = ck_next<1>(p, s, v1)) {
-            const int32_t *bt = p.c.block_table + (int64_t)s.i * p.c.max_pages;
+            const int32_t *bt = p.c.block_table + ck_table(p, s);
             constexpr int32_t kNone = INT32_MIN;   // (a table may hold it too: see checked)
             auto page_of = [&](int32_t t) -> int32_t {
                 const int32_t at = t * kCkKeys + lane * 4;
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                 }
             if (named_bar_any(1, 32 * kShWarps, !ok))
                 break;                                      // (all eight warps leave together)
-            const bool whole = s.t0 == 0 && s.t1 == s.nt;
+            const bool all = s.t0 == 0 && s.t1 == s.nt, whole = all && !ck_kept(s);   // (whole: the output's)
             for (int32_t idx = tid; idx < nrows * (D / 4); idx += 32 * kShWarps) {
                 const int32_t rho = idx / (D / 4), c4 = idx - rho * (D / 4);   // columns 4 c4 .. 4 c4 + 3
                 const int32_t n = c4 / (NI / 4), i = (c4 - n * (NI / 4)) * 4;
@@ -530,13 +539,22 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
                     if (c4 == 0 && p.lse)
                         p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
                 } else {
-                    const int64_t prow = (int64_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kShortRows + rho;
-                    *reinterpret_cast<float4 *>(p.part_o + prow * D + 4 * c4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    int64_t prow = (int64_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kShortRows + rho;
+                    float *part_o = p.part_o;
+                    float2 *part_ml = p.part_ml;
+                    if constexpr (kShared) {
+                        if (all) {
+                            prow = px_place(p, false, s.off + s.tb0 + tok, s.g * p.G + h);
+                            part_o = p.place_o;
+                            part_ml = p.place_ml;
+                        }
+                    }
+                    *reinterpret_cast<float4 *>(part_o + prow * D + 4 * c4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (c4 == 0)
-                        p.part_ml[prow] = make_float2(M, L);
+                        part_ml[prow] = make_float2(M, L);
                 }
             }
-            if (!whole && s.t0 == 0 && tid == 0) {
+            if (!kShared && !whole && s.t0 == 0 && tid == 0) {
                 ChunkDesc d;
                 d.np = ck_owner(shares, s.base + (int64_t)s.wt * (kStartKeys + (int64_t)kCkKeys * (s.nt - 1))) - cta + 1;
                 d.row0 = s.off + s.tb0;
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
 
 int chunk_ctas();
 
-template <int D, int NB>
+template <int D, int NB, bool kShared>
 static svp_status short_launch(ChunkParams &p, cudaStream_t stream)
 {
     using Cfg = ShortCfg<D, NB>;
@@ -562,17 +580,17 @@ static svp_status short_launch(ChunkParams &p, cudaStream_t stream)
     const int misc = (int)(sizeof(ShortMisc) + 127) / 128 * 128;
     p.off_ring = (Cfg::kRed + 1023) / 1024 * 1024;
     p.nslot = std::min(kShSlots, (kBudget - p.off_ring - misc) / (Cfg::kRaw + 512)) / 2 * 2;
-    if (p.nslot < 4)
+    if (p.nslot < 4 || (kShared && p.nslot * Cfg::kRaw < (int)sizeof(PrefixSums)))
         return SVP_EUNSUPPORTED;
     p.off_raw = p.off_ring + p.nslot * Cfg::kRaw;
     p.off_misc = p.off_raw + p.nslot * 512;
     static std::atomic<uint64_t> configured{0};
-    if (set_smem_limit_once(chunk_short_kernel<D, NB>, kBudget, configured) != cudaSuccess)
+    if (set_smem_limit_once(chunk_short_kernel<D, NB, kShared>, kBudget, configured) != cudaSuccess)
         return SVP_ECUDA;
     // Back to back, 64 requests x 18000 keys (2.3 GB) take 365 us as dependents and 349 otherwise: 3 us earlier
     // do not pay from 0.4 GB on.  The host knows the block table's room only.
     const bool small = (int64_t)p.n * p.c.hkv * ((int64_t)p.c.max_pages << p.c.page_shift) * (2 * D) < ((int64_t)400 << 20);
-    return launch_ctas(chunk_short_kernel<D, NB>, chunk_ctas(), kShThreads, (size_t)(p.off_misc + misc), stream, p, small,
+    return launch_ctas(chunk_short_kernel<D, NB, kShared>, chunk_ctas(), kShThreads, (size_t)(p.off_misc + misc), stream, p, small,
                        false) == cudaSuccess
                ? SVP_OK
                : SVP_ECUDA;
@@ -582,8 +600,17 @@ svp_status chunk_short_run(ChunkParams &p, int32_t d, cudaStream_t stream)
 {
     const bool one = p.G * p.R <= 8;      // rows of one block
     if (d == 64)
-        return one ? short_launch<64, 1>(p, stream) : short_launch<64, 2>(p, stream);
-    return one ? short_launch<128, 1>(p, stream) : short_launch<128, 2>(p, stream);
+        return one ? short_launch<64, 1, false>(p, stream) : short_launch<64, 2, false>(p, stream);
+    return one ? short_launch<128, 1, false>(p, stream) : short_launch<128, 2, false>(p, stream);
+}
+
+// The requests of svp_prefix_attn (p.part is kPxRequests).
+svp_status chunk_short_prefix_run(ChunkParams &p, int32_t d, cudaStream_t stream)
+{
+    const bool one = p.G * p.R <= 8;
+    if (d == 64)
+        return one ? short_launch<64, 1, true>(p, stream) : short_launch<64, 2, true>(p, stream);
+    return one ? short_launch<128, 1, true>(p, stream) : short_launch<128, 2, true>(p, stream);
 }
 
 }  // namespace svp

@@ -17,11 +17,17 @@ namespace svp {
 
 constexpr int kPxMost = 1024;         // requests, and groups, of a call
 
-// What the joining kernel needs of a request, written by the first CTA.
+// One kernel for all pairs, or one for the groups and another for the requests (prefix_tc.cu says when).
+enum { kPxAll = 0, kPxGroups = 1, kPxRequests = 2 };
+
+// What the joining kernel needs of a request, and of its group, written by the first CTA of the kernel that has the pairs.
 struct PrefixRec {
     int32_t off, k, L, P;             // first row, rows, cached tokens behind the P common ones (k 0: skipped)
-    int32_t goff, gk;                 // first row and rows of its group
-    int64_t base, gbase;              // cost before the request's pairs, and before the group's
+    int64_t base;                     // cost before its pairs
+};
+struct PrefixGroup {
+    int32_t off, k;                   // first row and rows
+    int64_t base;
 };
 
 struct PrefixPiece : ChunkPiece {     // i: place in the sequence of groups and requests
@@ -197,7 +203,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
 {
     PrefixSums &x = *static_cast<PrefixSums *>(smem);
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, n = p.n, ng = p.ng;
-    const bool tells = blockIdx.x == 0;
+    const bool tells = blockIdx.x == 0, has_groups = p.part != kPxRequests, has_requests = p.part != kPxGroups;
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     if (tid == 0)
         x.broken = x.groups_broken = 0;
@@ -247,7 +253,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 set_status(p.status, SVP_DEV_BAD_CONTEXT);
             if (bad || x.len[g] > L)
                 x.bad[g] = 1;
-            atomicAdd(&x.blocks[g], bad ? 0 : (k + B - 1) / B);
+            atomicAdd(&x.blocks[g], bad ? 0 : (k + p.share_rows - 1) / p.share_rows);
             atomicMin(&x.lead[g], i);
         }
     }
@@ -265,8 +271,8 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
             if (x.len[g] < 0 && tells)
                 set_status(p.status, SVP_DEV_BAD_CONTEXT);
             P = x.len[g] >> p.c.page_shift << p.c.page_shift;
-            shared = !x.bad[g] && P > 0 && k > 0 && (k + B - 1) / B < x.blocks[g];
-            if (shared)
+            shared = !x.bad[g] && P > 0 && k > 0 && (k + p.share_rows - 1) / p.share_rows < x.blocks[g];
+            if (shared && has_groups)
                 cost = px_head_keys(P, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
         }
         int64_t before;
@@ -274,18 +280,19 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
         px_scan(x, run, cost, shared, before, at);
         if (g < ng) {
             x.slot[g] = shared ? at : -1;
-            if (shared) {
+            if (shared && has_groups) {
                 x.prefix[at] = before;
                 plan[at] = make_int4(off, k, P, lead);
             }
         }
     }
-    const int32_t first = run.count;
+    const int32_t first = has_groups ? run.count : 0;
     __syncthreads();
     for (int32_t i0 = 0; i0 < n; i0 += nt) {
         const int32_t i = i0 + tid;
         int64_t cost = 0;
         PrefixRec r{};
+        PrefixGroup gr{};
         if (i < n && !broken) {
             const int32_t off = x.cu[i], k = x.cu[i + 1] - off, L = __ldg(p.ctx_len + i), g = group_of(i);
             const int32_t slot = g >= 0 ? x.slot[g] : -1;
@@ -295,43 +302,51 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 r.k = k;
                 r.L = L - P;
                 r.P = P;
-                cost = ck_head_keys(r.L, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
-                if (slot >= 0) {
-                    r.goff = x.cu[x.gcu[g]];
-                    r.gk = x.cu[x.gcu[g + 1]] - r.goff;
-                    r.gbase = x.prefix[slot];
+                if (has_requests)
+                    cost = ck_head_keys(r.L, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
+                if (slot >= 0 && has_groups) {
+                    gr.off = x.cu[x.gcu[g]];
+                    gr.k = x.cu[x.gcu[g + 1]] - gr.off;
+                    gr.base = x.prefix[slot];
                 }
             }
         }
         int32_t none;
         px_scan(x, run, cost, false, r.base, none);
         if (i < n) {
-            x.prefix[first + i] = r.base;
-            plan[kPxMost + i] = make_int4(r.off, r.k, r.L, r.P);
-            if (tells)
+            if (has_requests) {
+                x.prefix[first + i] = r.base;
+                plan[kPxMost + i] = make_int4(r.off, r.k, r.L, r.P);
+            }
+            if (tells && has_requests)
                 p.rec[i] = r;
+            if (tells && has_groups)
+                p.grp[i] = gr;
         }
     }
+    const int32_t length = first + (has_requests ? n : 0);
     if (tid == 0) {
-        x.prefix[first + n] = run.running;
-        if (tells)
-            *p.total = run.running;
+        x.prefix[length] = run.running;
+        if (tells && has_groups)
+            p.total[0] = run.running;
+        if (tells && has_requests)
+            p.total[1] = run.running;
     }
     __syncthreads();
-    return first + n;
+    return length;
 }
 
 __device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, int32_t length)
 {
     s.plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     s.ne = length;
-    s.ng = length - p.n;
+    s.ng = p.part == kPxGroups ? length : p.part == kPxRequests ? 0 : length - p.n;
 }
 
-// Row of the partial results that a whole pair has for (row, head): behind the CTAs' own, the groups' first.
-__device__ __forceinline__ int64_t px_place(const ChunkParams &p, bool group, int32_t row, int32_t head, int64_t behind)
+// Place of (row, head) of a part that one piece has all of, a group's or a request's behind one.
+__device__ __forceinline__ int64_t px_place(const ChunkParams &p, bool group, int32_t row, int32_t head)
 {
-    return behind + ((group ? 0 : (int64_t)p.m_cap) + row) * p.hq + head;
+    return ((group ? 0 : (int64_t)p.m_cap) + row) * p.hq + head;
 }
 
 }  // namespace svp

@@ -21,29 +21,36 @@ struct PxPieces {
     int32_t first, np, pr;            // pr: the row in a CTA's partial results
 };
 
-// tok: the row among its group's, or its request's.
+// tok: the row among its group's, or its request's; R tokens a query tile, NT of them a block.
 template <int NT>
 __device__ __forceinline__ PxPieces px_pieces(const ChunkParams &p, const ChunkShares &x, bool group, int64_t base, int32_t k,
-                                              int32_t L, int32_t tok, int32_t g, int32_t h)
+                                              int32_t L, int32_t tok, int32_t g, int32_t h, int32_t R)
 {
-    const int32_t B = NT * p.R, b = tok / B, t = tok - b * B, wt = ck_weight<NT>(k, p.R);
+    const int32_t B = NT * R, b = tok / B, t = tok - b * B, wt = ck_weight<NT>(k, R);
     const int64_t H = group ? px_head_keys(L, k, B) : ck_head_keys(L, k, B);
     base += wt * (g * H + ck_before((int64_t)kStartKeys + L, group ? 0 : B, b));
     const int32_t len = group ? L : L + b * B + min(B, k - b * B), nt = (len + kCkKeys - 1) / kCkKeys;
     PxPieces y;
     y.first = ck_owner(x, base + (int64_t)wt * kStartKeys);
     y.np = ck_owner(x, base + (int64_t)wt * (kStartKeys + (int64_t)kCkKeys * (nt - 1))) - y.first + 1;
-    const bool second = t >= p.R;
-    y.pr = (second ? 128 : 0) + (t - (second ? p.R : 0)) * p.G + h;
+    const bool second = t >= R;
+    y.pr = (second ? 128 : 0) + (t - (second ? R : 0)) * p.G + h;
     return y;
 }
+
+// Where the requests' pieces are: the tile kernel's, beside the groups', or those of a kernel of their own.
+struct PxOwn {
+    int32_t few, R;                   // tokens of its query tile
+    const float2 *ml;
+    const float *o;
+};
 
 // Block (row, y): heads 8 y .. 8 y + 7 of a packed row, one a half warp.  Bound by its chain of reads, offsets ->
 // request -> (m, l) and O.
 constexpr int kPxThreads = 128, kPxHeads = kPxThreads / 16;
 
 template <int D>
-__global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_constant__ ChunkParams p, int32_t ctas)
+__global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_constant__ ChunkParams p, const PxOwn w, int32_t ctas)
 {
     constexpr int NT = D == 256 ? 1 : 2, kPartRows = 128 * NT;
     constexpr int E = D / 16, A = D == 256 ? 2 : 4;       // columns a lane, four side by side; pieces read ahead
@@ -54,7 +61,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (tid == 0)
         owner = -1;
     __syncthreads();
-    const ChunkShares shares = ck_shares(__ldcg(p.total), ctas);
+    const int64_t total[2] = {__ldcg(p.total), __ldcg(p.total + 1)};
     for (int32_t i = tid; i < p.n; i += kPxThreads)
         if (__ldg(p.cu + i) <= row && row < __ldg(p.cu + i + 1))
             owner = i;                                    // (one, but where nothing is computed)
@@ -62,28 +69,38 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (owner < 0)
         return;
     const PrefixRec r = p.rec[owner];
+    const PrefixGroup gr = p.grp[owner];
     const int32_t head = blockIdx.y * kPxHeads + (tid >> 4);
     if (r.k <= 0 || head >= p.hq)
         return;
     const int32_t g = head / p.G, h = head - g * p.G;
-    const PxPieces own = px_pieces<NT>(p, shares, false, r.base, r.k, r.L, row - r.off, g, h);
+    const PxPieces own = w.few ? px_pieces<1>(p, ck_shares(total[1], ctas), false, r.base, r.k, r.L, row - r.off, g, h, w.R)
+                               : px_pieces<NT>(p, ck_shares(total[1], ctas), false, r.base, r.k, r.L, row - r.off, g, h, w.R);
     if (r.P == 0 && own.np == 1)
         return;                                           // (the output has it already)
     PxPieces grp{0, 0, 0};
     if (r.P > 0)
-        grp = px_pieces<NT>(p, shares, true, r.gbase, r.gk, r.P, row - r.goff, g, h);
+        grp = px_pieces<NT>(p, ck_shares(total[0], ctas), true, gr.base, gr.k, r.P, row - gr.off, g, h, p.R);
     const int32_t np = grp.np + own.np;
-    const int64_t behind = 2 * (int64_t)ctas * kPartRows;
-    auto at = [&](int32_t q) -> int64_t {
+    auto at = [&](int32_t q, const float2 *&ml, const float *&o) {
         const bool mine = q >= grp.np;
         const PxPieces &y = mine ? own : grp;
         q -= mine ? grp.np : 0;
-        if (y.np == 1)
-            return px_place(p, !mine, row, head, behind);
-        return (int64_t)(q == 0 ? 2 * y.first + 1 : 2 * (y.first + q)) * kPartRows + y.pr;
+        int64_t x = y.np == 1 ? px_place(p, !mine, row, head)
+                              : (int64_t)(q == 0 ? 2 * y.first + 1 : 2 * (y.first + q)) * (mine && w.few ? kShortRows : kPartRows) + y.pr;
+        ml = (y.np == 1 ? p.place_ml : mine ? w.ml : p.part_ml) + x;
+        o = (y.np == 1 ? p.place_o : mine ? w.o : p.part_o) + x * D + lane * 4;
+    };
+    auto load_ml = [&](int32_t q) {
+        const float2 *ml;
+        const float *o;
+        at(q, ml, o);
+        return __ldcg(ml);
     };
     auto load = [&](int32_t q, float (&x)[E]) {
-        const float *o = p.part_o + at(q) * D + lane * 4;
+        const float2 *ml;
+        const float *o;
+        at(q, ml, o);
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + 16 * e));
@@ -96,7 +113,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     // (a warp's two heads may have different numbers of pieces, or one head fewer: shuffles are within the half)
     const uint32_t mask = 0xffffu << (tid & 16);
     const float2 none = make_float2(-INFINITY, 0.0f);
-    const float2 ml0 = lane < np ? __ldcg(p.part_ml + at(lane)) : none;
+    const float2 ml0 = lane < np ? load_ml(lane) : none;
     float ahead[A][E];
 #pragma unroll
     for (int q = 0; q < A; ++q)
@@ -104,7 +121,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     // (a piece without a visible key of this row, l = 0, is left out whatever its O holds)
     float M = ml0.y != 0.0f ? ml0.x : -INFINITY;
     for (int32_t q = 16 + lane; q < np; q += 16) {
-        const float2 ml = __ldcg(p.part_ml + at(q));
+        const float2 ml = load_ml(q);
         M = fmaxf(M, ml.y != 0.0f ? ml.x : -INFINITY);
     }
 #pragma unroll
@@ -115,7 +132,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     for (int e = 0; e < E; ++e)
         acc[e] = 0.0f;
     for (int32_t q0 = 0; q0 < np; q0 += 16) {
-        const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? __ldcg(p.part_ml + at(q0 + lane)) : none;
+        const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? load_ml(q0 + lane) : none;
         // (more than 0 where there is a visible key: its O may be NaN)
         const float w = ml.y != 0.0f ? fmaxf(fast_exp2(ml.x - M), FLT_MIN) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
         auto add = [&](int32_t q, const float (&x)[E]) {
@@ -157,32 +174,52 @@ bool chunk_maps(ChunkParams &p, const void *q, int64_t q_stride, svp_dtype kv, i
                 bool few);
 template <int D, bool Q8>
 bool chunk_layout(ChunkParams &p, int32_t rows, int &smem);
+svp_status chunk_short_prefix_run(ChunkParams &p, int32_t d, cudaStream_t stream);
+svp_status prefix_few_run(ChunkParams &p, int32_t d, cudaStream_t stream);
+
+constexpr int kPxFewPairs = 300;      // requests times KV heads
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct PrefixWs {
-    size_t total, rec, plan, ml, o, bytes;
+    size_t total, rec, grp, plan, ml, ml2, ml3, o, o2, o3, bytes;   // 2: of the kernel for few rows; 3: the rows' places
 };
 
 static PrefixWs prefix_ws(int32_t hq, int32_t d, int32_t m_cap)
 {
     // partial results: two pieces a CTA, and those of whole pairs of groups and of requests behind them
-    const size_t g = (size_t)chunk_ctas(), rows = 2 * g * (d == 256 ? 128 : 256) + 2 * (size_t)m_cap * hq;
+    const size_t g = (size_t)chunk_ctas(), one = 2 * g * (d == 256 ? 128 : 256), two = 2 * g * kShortRows,
+                 three = 2 * (size_t)m_cap * hq, row = (size_t)d * sizeof(float);
     PrefixWs w;
     w.total = kWsHeader;
     w.rec = w.total + 256;
-    w.plan = w.rec + up256(kPxMost * sizeof(PrefixRec));
+    w.grp = w.rec + up256(kPxMost * sizeof(PrefixRec));
+    w.plan = w.grp + up256(kPxMost * sizeof(PrefixGroup));
     w.ml = w.plan + g * 2 * kPxMost * sizeof(int4);
-    w.o = up256(w.ml + rows * sizeof(float2));
-    w.bytes = up256(w.o + rows * (size_t)d * sizeof(float));
+    w.ml2 = w.ml + up256(one * sizeof(float2));
+    w.ml3 = w.ml2 + up256(two * sizeof(float2));
+    w.o = w.ml3 + up256(three * sizeof(float2));
+    w.o2 = w.o + one * row;
+    w.o3 = w.o2 + two * row;
+    w.bytes = up256(w.o3 + three * row);
     return w;
 }
 
+// Requests of few rows have a kernel of their own where their pairs are many: then the tile kernel's 5 us for a
+// pair's start and end cost more than a third launch.
+static bool few_requests(const ChunkParams &p, int32_t d)
+{
+    return d <= 128 && (int64_t)p.G * p.w <= kShortRows && (int64_t)p.n * p.c.hkv >= kPxFewPairs;
+}
+
 template <int D, bool Q8>
-static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
+static svp_status prefix_run(ChunkParams &p, ChunkParams &few, cudaStream_t stream)
 {
     using Cfg = ChunkCfg<D, Q8>;
     int smem = 0;
+    p.share_rows = Cfg::NT * p.R;
+    const bool split = few_requests(p, D);
+    p.part = split ? kPxGroups : kPxAll;
     if (!chunk_layout<D, Q8>(p, p.m_cap, smem) || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
         return SVP_EUNSUPPORTED;
     static std::atomic<uint64_t> configured{0};
@@ -191,8 +228,19 @@ static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
     const int ctas = chunk_ctas();
     if (launch_ctas(chunk_tc_kernel<D, Q8, true>, ctas, Cfg::kThreads, (size_t)smem, stream, p, true, true) != cudaSuccess)
         return SVP_ECUDA;
+    PxOwn own{0, p.R, p.part_ml, p.part_o};
+    if (split) {
+        // (a pair of the kernel for few rows is a request's KV head: w tokens are one block)
+        few.share_rows = p.share_rows;
+        few.part = kPxRequests;
+        few.R = p.w;
+        const svp_status st = Q8 ? chunk_short_prefix_run(few, D, stream) : prefix_few_run(few, D, stream);
+        if (st != SVP_OK)
+            return st;
+        own = PxOwn{1, few.R, few.part_ml, few.part_o};
+    }
     const unsigned y = (unsigned)((p.hq + kPxHeads - 1) / kPxHeads);
-    return launch_pdl(prefix_join_kernel<D>, dim3((unsigned)p.m_cap, y), dim3(kPxThreads), 0, stream, p, (int32_t)ctas) ==
+    return launch_pdl(prefix_join_kernel<D>, dim3((unsigned)p.m_cap, y), dim3(kPxThreads), 0, stream, p, own, (int32_t)ctas) ==
                    cudaSuccess
                ? SVP_OK
                : SVP_ECUDA;
@@ -274,23 +322,31 @@ svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache 
     p.status = reinterpret_cast<int32_t *>(b);
     p.total = reinterpret_cast<int64_t *>(b + o.total);
     p.rec = reinterpret_cast<PrefixRec *>(b + o.rec);
+    p.grp = reinterpret_cast<PrefixGroup *>(b + o.grp);
     p.plan = reinterpret_cast<int4 *>(b + o.plan);
     p.part_ml = reinterpret_cast<float2 *>(b + o.ml);
     p.part_o = reinterpret_cast<float *>(b + o.o);
+    p.place_ml = reinterpret_cast<float2 *>(b + o.ml3);
+    p.place_o = reinterpret_cast<float *>(b + o.o3);
     if (!chunk_maps(p, q, q_row_stride, cache->dtype, m_cap, d, std::min(p.R, m_cap), false))
+        return SVP_EUNSUPPORTED;
+    ChunkParams few = p;
+    few.part_ml = reinterpret_cast<float2 *>(b + o.ml2);
+    few.part_o = reinterpret_cast<float *>(b + o.o2);
+    if (few_requests(p, d) && !chunk_maps(few, q, q_row_stride, cache->dtype, m_cap, d, 1, true))
         return SVP_EUNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->dtype == SVP_E4M3) {
         switch (d) {
-        case 64: return prefix_run<64, true>(p, s);
-        case 128: return prefix_run<128, true>(p, s);
-        default: return prefix_run<256, true>(p, s);
+        case 64: return prefix_run<64, true>(p, few, s);
+        case 128: return prefix_run<128, true>(p, few, s);
+        default: return prefix_run<256, true>(p, few, s);
         }
     }
     switch (d) {
-    case 64: return prefix_run<64, false>(p, s);
-    case 128: return prefix_run<128, false>(p, s);
-    default: return prefix_run<256, false>(p, s);
+    case 64: return prefix_run<64, false>(p, few, s);
+    case 128: return prefix_run<128, false>(p, few, s);
+    default: return prefix_run<256, false>(p, few, s);
     }
 }
 

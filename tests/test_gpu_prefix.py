@@ -127,6 +127,79 @@ def test_many_groups(kind):
     check_prefix(rows, ctx, groups, hq=2, hkv=1, d=64, kind=kind, seed=11)
 
 
+def crowd(n, rows, shared, rest, seed):
+    """n requests of up to `rows` rows (some none) in groups of different sizes, some alone."""
+    r = np.random.default_rng(seed)
+    k = r.integers(0, rows + 1, n).tolist()
+    ctx, groups, at = [0] * n, [], 0
+    while at < n:
+        size = int(r.integers(1, 30))
+        hi = min(n, at + size)
+        tokens = int(r.integers(0, shared)) if r.random() < 0.8 else 0
+        for i in range(at, hi):
+            ctx[i] = tokens + int(r.integers(0, rest))
+        groups.append((at, hi, tokens))
+        at = hi
+    return k, ctx, groups
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("hq,hkv,rows", [(4, 4, 1), (8, 8, 8), (16, 4, 2), (12, 4, 5), (32, 8, 4), (16, 16, 16), (20, 4, 3),
+                                         (64, 4, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_crowds_of_few_rows(hq, hkv, rows, d, kind):
+    """Requests of up to 16 rows a KV head, more than 300 of them times their heads: a kernel of their own."""
+    n = 320 // hkv + 9
+    k, ctx, groups = crowd(n, rows, 600, 300, hq + rows + d)
+    check_prefix(k, ctx, groups, hq=hq, hkv=hkv, d=d, kind=kind, seed=hq, page=32 if rows > 4 else 16, fused=True)
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("layout", ["head", "token"])
+def test_crowds_over_any_pages(page, layout, kind):
+    k, ctx, groups = crowd(80, 2, 700, 500, page)
+    check_prefix(k, ctx, groups, hq=8, hkv=4, kind=kind, page=page, layout=layout, seed=3)
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+def test_crowds_with_long_rests_and_wide_scores(kind):
+    """Own keys that are split over blocks, and scores far apart."""
+    n = 80
+    ctx = [64 + (9000 if i % 40 == 7 else 17 * i % 90) for i in range(n)]
+    check_prefix([1 + i % 2 for i in range(n)], ctx, [(0, 30, 64), (30, 80, 48)], hq=8, hkv=4, kind=kind, seed=5, picks=(0, 1))
+    check_prefix([1] * n, [700 + i for i in range(n)], [(0, n, 640)], hq=4, hkv=4, kind=kind, scale=2.0, std=4.0, seed=6)
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+def test_crowds_keep_their_neighbours_nan_out(kind):
+    """A key of NaN that one row of a crowd sees, another that is behind every row of its request."""
+    n, hkv, d = 80, 4, 128
+    rows, ctx, groups = [2] * n, [130 + i for i in range(n)], [(0, n, 128)]
+    pool = Shared(rows, ctx, groups, hkv, d, 16, kind, seed=7)
+    cache = pool.cuda()
+    q = torch.randn(2 * n, 8, d, device="cuda").to(BF16)
+    args = (i32(ctx), i32(packed(rows)), i32([0, n]), i32([128]))
+    before = svp.prefix_attn(q, *args, cache=cache, w=2)
+    x = torch.full((1, hkv, d), float("nan"), device="cuda", dtype=BF16)
+    at = [0] * n
+    at[5] = ctx[5] + 1                     # the last row's own
+    cu = [0] * 6 + [1] * (n - 5)
+    svp.cache_write(x, torch.ones_like(x), i32(at), i32(cu), cache=cache)
+    out, lse = svp.prefix_attn(q, *args, cache=cache, w=2)
+    assert torch.isnan(out[11]).all() and torch.isnan(lse[11]).all()
+    keep = [r for r in range(2 * n) if r not in (10, 11)]
+    assert torch.equal(out[keep], before[0][keep]) and torch.equal(lse[keep], before[1][keep])
+    assert torch.isfinite(out[10]).all() and torch.isfinite(lse[10]).all()
+    ws = svp.Workspace(svp.prefix_attn_workspace_size(8, hkv, d, 2 * n), zeroed=256)
+    ws.buf[256:] = 255
+    for c, bit in (([130 + i if i != 9 else -1 for i in range(n)], svp.DEV_BAD_CONTEXT), (ctx, 0)):
+        out, lse = torch.full((2 * n, 8, d), -7.0, dtype=BF16, device="cuda"), torch.full((2 * n, 8), -7.0, device="cuda")
+        svp.prefix_attn(q, i32(c), *args[1:], cache=cache, w=2, out=out, lse=lse, ws=ws)
+        assert ws.read_status() == bit
+        assert bool((out[18:20] == -7).all()) == bool(bit) and not (out[:18] == -7).all(-1).any()
+
+
 @pytest.mark.parametrize("kind", [BF16, E4M3])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_the_most_requests_and_groups(d, kind):
