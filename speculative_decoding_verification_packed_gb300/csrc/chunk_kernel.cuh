@@ -315,23 +315,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     griddep_wait();
     if (!kShared && tid == 0)
         p.desc[blockIdx.x].np = 0;
-    int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
-    int32_t pairs = p.n;                  // requests, or groups and requests
+    // costs before each request, or group and request (until the loaders start)
+    using Sums = std::conditional_t<kShared, PrefixSums, int64_t[1]>;
+    Sums &sums = *reinterpret_cast<Sums *>(smem + p.off_ring);
+    int32_t pairs = p.n;
     if constexpr (kShared)
         pairs = px_prologue<NT>(p, smem + p.off_ring);
     else
-        ck_prologue<NT>(p, prefix, m->warp_tot);
+        ck_prologue<NT>(p, sums, m->warp_tot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    const ChunkShares shares = ck_shares(prefix[pairs]);
+    const ChunkShares shares = ck_shares(px_total(sums, pairs));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     Piece s;
     if constexpr (kShared)
         px_bind(p, s, pairs);
-    const bool have0 = ck_first<NT>(p, prefix, s, v0, v1);
+    const bool have0 = ck_first<NT>(p, sums, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();
     auto is_long = [&](const Piece &x) { return !kMono && x.ntok > p.R; };

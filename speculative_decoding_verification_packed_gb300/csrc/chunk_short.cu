@@ -129,19 +129,20 @@ __global__ void __launch_bounds__(kShThreads, 1) chunk_short_kernel(const __grid
     griddep_wait();
     if (!kShared && tid == 0)
         p.desc[blockIdx.x].np = 0;
-    int64_t *prefix = reinterpret_cast<int64_t *>(smem + p.off_ring);   // (until the loaders start)
+    using Sums = std::conditional_t<kShared, PrefixSums, int64_t[1]>;
+    Sums &sums = *reinterpret_cast<Sums *>(smem + p.off_ring);          // (until the loaders start)
     int32_t pairs = p.n;
     if constexpr (kShared)
         pairs = px_prologue<1>(p, smem + p.off_ring);
     else
-        ck_prologue<1>(p, prefix, m->warp_tot);
-    const ChunkShares shares = ck_shares(prefix[pairs]);
+        ck_prologue<1>(p, sums, m->warp_tot);
+    const ChunkShares shares = ck_shares(px_total(sums, pairs));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     Piece s;
     if constexpr (kShared)
         px_bind(p, s, pairs);
-    const bool have0 = ck_first<1>(p, prefix, s, v0, v1);
+    const bool have0 = ck_first<1>(p, sums, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();
 

@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
     griddep_launch_dependents();
     griddep_wait();
     const int32_t pairs = px_prologue<1>(p, smem + p.off_ring);
-    const int64_t *prefix = reinterpret_cast<const int64_t *>(smem + p.off_ring);   // (until the loaders start)
-    const ChunkShares shares = ck_shares(prefix[pairs]);
+    const PrefixSums &sums = *reinterpret_cast<const PrefixSums *>(smem + p.off_ring);   // (until the loaders start)
+    const ChunkShares shares = ck_shares(px_total(sums, pairs));
     const int32_t cta = blockIdx.x;
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     PrefixPiece s;
     px_bind(p, s, pairs);
-    const bool have0 = ck_first<1>(p, prefix, s, v0, v1);
+    const bool have0 = ck_first<1>(p, sums, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();
 

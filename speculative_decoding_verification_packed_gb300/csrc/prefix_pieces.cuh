@@ -70,10 +70,9 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, PrefixPiece &s, int
 }
 
 template <int NT>
-__device__ __forceinline__ bool ck_request(const ChunkParams &p, PrefixPiece &s)
+__device__ __forceinline__ bool px_entry(const ChunkParams &p, PrefixPiece &s, const int4 x)
 {
     const int32_t B = NT * p.R;
-    const int4 x = __ldcg(s.plan + (s.i < s.ng ? s.i : kPxMost + s.i - s.ng));
     s.group = s.i < s.ng;
     s.off = x.x;
     s.k = x.y;
@@ -85,6 +84,14 @@ __device__ __forceinline__ bool ck_request(const ChunkParams &p, PrefixPiece &s)
     s.nb = (s.k + B - 1) / B;
     s.wt = ck_weight<NT>(s.k, p.R);
     return true;
+}
+
+__device__ __forceinline__ int32_t px_slot(const PrefixPiece &s) { return s.i < s.ng ? s.i : kPxMost + s.i - s.ng; }
+
+template <int NT>
+__device__ __forceinline__ bool ck_request(const ChunkParams &p, PrefixPiece &s)
+{
+    return px_entry<NT>(p, s, __ldcg(s.plan + px_slot(s)));
 }
 
 template <int NT>
@@ -106,56 +113,16 @@ __device__ __forceinline__ bool ck_next(const ChunkParams &p, PrefixPiece &s, in
     return ck_set<NT>(p, s, v1, 0);
 }
 
-template <int NT>
-__device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *prefix, PrefixPiece &s, int64_t v0, int64_t v1)
-{
-    if (v0 >= v1)
-        return false;
-    const int32_t B = NT * p.R;
-    int32_t lo = 0, hi = s.ne;
-    while (hi - lo > 1) {             // last pairs with prefix <= v0 (they have a cost: v0 < total)
-        const int32_t mid = (lo + hi) >> 1;
-        if (prefix[mid] <= v0)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    s.i = lo;
-    ck_request<NT>(p, s);
-    const int32_t wt = s.wt, slope = s.group ? 0 : B;
-    const int64_t H = (s.group ? px_head_keys(s.L, s.k, B) : ck_head_keys(s.L, s.k, B)) * wt;
-    int64_t rem = v0 - prefix[lo];
-    s.g = (int32_t)(rem / H);
-    rem -= s.g * H;
-    // last block with cost before it <= rem (chunk_pieces.cuh; a group's blocks cost the same each)
-    const int64_t a = (int64_t)kStartKeys + s.L;
-    int64_t b;
-    if (s.group) {
-        b = rem / (a * wt);
-    } else {
-        const float h = (float)a + 0.5f * B;
-        b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / wt)) - h) / B);
-    }
-    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
-    while (b + 1 < s.nb && ck_before(a, slope, b + 1) * wt <= rem)
-        ++b;
-    while (b > 0 && ck_before(a, slope, b) * wt > rem)
-        --b;
-    s.b = (int32_t)b;
-    s.base = prefix[lo] + s.g * H + ck_before(a, slope, b) * wt;
-    const int32_t t0 = ck_tile_at(v0 - s.base, wt);
-    const bool have = ck_set<NT>(p, s, v1, t0);
-    return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
-}
-
-// Shared memory of the prologue, where the ring (48 KB at least) is later.
+// Shared memory of the prologue, where the ring (96 KB at least) is later.
 struct PrefixSums {
     int64_t prefix[2 * kPxMost + 1];
-    int32_t cu[kPxMost + 1], gcu[kPxMost + 1], len[kPxMost];
+    int4 plan[2 * kPxMost];           // as the CTA's copy in the workspace
+    int32_t cu[kPxMost + 1], gcu[kPxMost + 1], len[kPxMost], ctx[kPxMost];
     int32_t blocks[kPxMost];          // blocks that the group's requests fill apart
     int32_t bad[kPxMost];
     int32_t lead[kPxMost];            // its first request with rows
-    int32_t slot[kPxMost];            // place of the group in the sequence, or -1
+    int32_t shared[kPxMost];          // tokens that it shares, 0: none
+    int32_t gbase[kPxMost];           // its place in the sequence
     int32_t broken, groups_broken;
     int32_t cnt[32];
     int64_t tot[32];
@@ -184,20 +151,27 @@ __device__ __forceinline__ void px_scan(PrefixSums &x, PrefixScan &run, int64_t 
     if (lane == 0)
         x.cnt[warp] = __popc(ones);
     __syncthreads();
-    before = run.running + incl - cost;
-    place = run.count + __popc(ones & ((1u << lane) - 1u));
-    for (int w = 0; w < nwarp; ++w) {
-        if (w < warp) {
-            before += x.tot[w];
-            place += x.cnt[w];
+    int64_t t = lane < nwarp ? x.tot[lane] : 0;
+    int32_t c = lane < nwarp ? x.cnt[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, t, o);
+        const int32_t u = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) {
+            t += v;
+            c += u;
         }
-        run.running += x.tot[w];
-        run.count += x.cnt[w];
     }
+    const int64_t ahead = __shfl_sync(0xffffffffu, t, (warp + 31) & 31);
+    const int32_t ahead_c = __shfl_sync(0xffffffffu, c, (warp + 31) & 31);
+    before = run.running + incl - cost + (warp == 0 ? 0 : ahead);
+    place = run.count + __popc(ones & ((1u << lane) - 1u)) + (warp == 0 ? 0 : ahead_c);
+    run.running += __shfl_sync(0xffffffffu, t, 31);
+    run.count += __shfl_sync(0xffffffffu, c, 31);
 }
 
-// Cost before each of the sequence's groups and requests into x->prefix, their places and sizes into this CTA's
-// plan, and (first CTA) what the joining kernel needs.  Returns the sequence's length.
+// Cost before each of the sequence's groups and requests into x->prefix, their places and sizes into x->plan and this
+// CTA's copy, and (first CTA) what the joining kernel needs.  Returns the sequence's length.
 template <int NT>
 __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
 {
@@ -207,29 +181,24 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     if (tid == 0)
         x.broken = x.groups_broken = 0;
-    for (int32_t i = tid; i <= n; i += nt)
+    // everything that is read, in one round trip
+    for (int32_t i = tid; i <= n; i += nt) {
         x.cu[i] = __ldg(p.cu + i);
-    for (int32_t g = tid; g <= ng; g += nt)
-        x.gcu[g] = ng > 0 ? __ldg(p.cu_groups + g) : 0;
-    for (int32_t g = tid; g < ng; g += nt) {
-        x.len[g] = __ldg(p.prefix_len + g);
-        x.blocks[g] = x.bad[g] = 0;
-        x.lead[g] = n;
+        if (i < n)
+            x.ctx[i] = __ldg(p.ctx_len + i);
+    }
+    for (int32_t g = tid; g <= ng; g += nt) {
+        x.gcu[g] = __ldg(p.cu_groups + g);
+        if (g < ng) {
+            x.len[g] = __ldg(p.prefix_len + g);
+            x.blocks[g] = x.bad[g] = 0;
+            x.lead[g] = n;
+        }
     }
     __syncthreads();
-    for (int32_t i = tid; i < n; i += nt)
-        if (x.cu[i] < 0 || x.cu[i + 1] < x.cu[i] || x.cu[i + 1] > p.m_cap)
-            x.broken = 1;
-    for (int32_t g = tid; g < ng; g += nt)
-        if (x.gcu[g] < 0 || x.gcu[g + 1] < x.gcu[g] || x.gcu[g + 1] > n)
-            x.groups_broken = 1;
-    __syncthreads();
-    const bool broken = x.broken != 0, grouped = ng > 0 && x.groups_broken == 0 && !broken;
-    if (tells && tid == 0 && (broken || x.groups_broken))
-        set_status(p.status, SVP_DEV_BAD_SLOTS);
-    // request i's group, or -1
+    // request i's group, or -1 (the group's bounds are looked at beside)
     auto group_of = [&](int32_t i) -> int32_t {
-        if (!grouped || i < x.gcu[0] || i >= x.gcu[ng])
+        if (i < x.gcu[0] || i >= x.gcu[ng])
             return -1;
         int32_t lo = 0, hi = ng;
         while (hi - lo > 1) {
@@ -241,11 +210,16 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
         }
         return lo;
     };
+    for (int32_t g = tid; g < ng; g += nt)
+        if (x.gcu[g] < 0 || x.gcu[g + 1] < x.gcu[g] || x.gcu[g + 1] > n)
+            x.groups_broken = 1;
     for (int32_t i = tid; i < n; i += nt) {
-        const int32_t k = x.cu[i + 1] - x.cu[i], g = group_of(i);
-        if (broken || k == 0)
+        const int32_t off = x.cu[i], end = x.cu[i + 1], L = x.ctx[i], k = end - off;
+        if (off < 0 || end < off || end > p.m_cap)
+            x.broken = 1;
+        if (off < 0 || end <= off)
             continue;
-        const int32_t L = __ldg(p.ctx_len + i), bad = ck_bad(p, x.cu[i], x.cu[i + 1], L);
+        const int32_t bad = ck_bad(p, off, end, L), g = group_of(i);
         if (bad && tells)
             set_status(p.status, bad);
         if (g >= 0) {
@@ -258,82 +232,137 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
         }
     }
     __syncthreads();
-    PrefixScan run{0, 0};
-    for (int32_t g0 = 0; g0 < ng; g0 += nt) {
-        const int32_t g = g0 + tid;
-        int64_t cost = 0;
-        int32_t off = 0, k = 0, P = 0, lead = 0;
-        bool shared = false;
-        if (g < ng && grouped) {
-            lead = x.lead[g];
-            off = x.cu[x.gcu[g]];
-            k = x.cu[x.gcu[g + 1]] - off;
+    const bool broken = x.broken != 0, grouped = x.groups_broken == 0 && !broken;
+    if (tells && tid == 0 && (broken || x.groups_broken))
+        set_status(p.status, SVP_DEV_BAD_SLOTS);
+    for (int32_t g = tid; g < ng; g += nt) {
+        int32_t P = 0;
+        if (grouped) {
+            const int32_t k = x.cu[x.gcu[g + 1]] - x.cu[x.gcu[g]];
             if (x.len[g] < 0 && tells)
                 set_status(p.status, SVP_DEV_BAD_CONTEXT);
-            P = x.len[g] >> p.c.page_shift << p.c.page_shift;
-            shared = !x.bad[g] && P > 0 && k > 0 && (k + p.share_rows - 1) / p.share_rows < x.blocks[g];
-            if (shared && has_groups)
-                cost = px_head_keys(P, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
+            if (!x.bad[g] && x.len[g] > 0 && k > 0 && (k + p.share_rows - 1) / p.share_rows < x.blocks[g])
+                P = x.len[g] >> p.c.page_shift << p.c.page_shift;
         }
-        int64_t before;
-        int32_t at;
-        px_scan(x, run, cost, shared, before, at);
-        if (g < ng) {
-            x.slot[g] = shared ? at : -1;
-            if (shared && has_groups) {
-                x.prefix[at] = before;
-                plan[at] = make_int4(off, k, P, lead);
-            }
-        }
+        x.shared[g] = P;
     }
-    const int32_t first = has_groups ? run.count : 0;
     __syncthreads();
-    for (int32_t i0 = 0; i0 < n; i0 += nt) {
-        const int32_t i = i0 + tid;
+    // the groups and the requests in one sequence of sums; the requests' places follow when the number of groups is known
+    const int32_t from = has_groups ? 0 : ng, to = ng + (has_requests ? n : 0);
+    PrefixScan run{0, 0};
+    for (int32_t e0 = from; e0 < to; e0 += nt) {
+        const int32_t e = e0 + tid;
         int64_t cost = 0;
-        PrefixRec r{};
-        PrefixGroup gr{};
-        if (i < n && !broken) {
-            const int32_t off = x.cu[i], k = x.cu[i + 1] - off, L = __ldg(p.ctx_len + i), g = group_of(i);
-            const int32_t slot = g >= 0 ? x.slot[g] : -1;
-            if (k > 0 && !ck_bad(p, off, x.cu[i + 1], L)) {
-                const int32_t P = slot >= 0 ? x.len[g] >> p.c.page_shift << p.c.page_shift : 0;
-                r.off = off;
-                r.k = k;
-                r.L = L - P;
-                r.P = P;
-                if (has_requests)
-                    cost = ck_head_keys(r.L, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
-                if (slot >= 0 && has_groups) {
-                    gr.off = x.cu[x.gcu[g]];
-                    gr.k = x.cu[x.gcu[g + 1]] - gr.off;
-                    gr.base = x.prefix[slot];
+        int4 what = make_int4(0, 0, 0, 0);
+        bool one = false;
+        if (e < to && !broken) {
+            if (e < ng) {
+                one = x.shared[e] > 0;                    // (else its bounds may be anything)
+                if (one) {
+                    what = make_int4(x.cu[x.gcu[e]], x.cu[x.gcu[e + 1]] - x.cu[x.gcu[e]], x.shared[e], x.lead[e]);
+                    cost = px_head_keys(what.z, what.y, B) * ck_weight<NT>(what.y, p.R) * p.c.hkv;
+                }
+            } else {
+                const int32_t i = e - ng, off = x.cu[i], k = x.cu[i + 1] - off, L = x.ctx[i];
+                if (k > 0 && !ck_bad(p, off, x.cu[i + 1], L)) {
+                    const int32_t g = grouped ? group_of(i) : -1, P = g >= 0 ? x.shared[g] : 0;
+                    what = make_int4(off, k, L - P, P);
+                    cost = ck_head_keys(what.z, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
                 }
             }
         }
-        int32_t none;
-        px_scan(x, run, cost, false, r.base, none);
-        if (i < n) {
-            if (has_requests) {
-                x.prefix[first + i] = r.base;
-                plan[kPxMost + i] = make_int4(r.off, r.k, r.L, r.P);
+        int64_t before;
+        int32_t at;
+        px_scan(x, run, cost, one, before, at);
+        if (e < ng) {
+            if (one) {
+                x.prefix[at] = before;
+                x.plan[at] = what;
+                plan[at] = what;
+                x.gbase[e] = at;
             }
-            if (tells && has_requests)
-                p.rec[i] = r;
-            if (tells && has_groups)
-                p.grp[i] = gr;
+        } else if (e < to) {
+            // (kept where groups cannot reach until all are counted: shifted below)
+            const int32_t i = e - ng;
+            x.plan[kPxMost + i] = what;
+            plan[kPxMost + i] = what;
+            x.prefix[kPxMost + i] = before;
+            if (tells)
+                p.rec[i] = PrefixRec{what.x, what.y, what.z, what.w, before};
         }
     }
-    const int32_t length = first + (has_requests ? n : 0);
+    const int32_t first = run.count, length = first + (has_requests ? n : 0);
     if (tid == 0) {
-        x.prefix[length] = run.running;
+        x.prefix[2 * kPxMost] = run.running;
         if (tells && has_groups)
             p.total[0] = run.running;
         if (tells && has_requests)
             p.total[1] = run.running;
     }
     __syncthreads();
+    if (tells && has_groups)
+        for (int32_t i = tid; i < n; i += nt) {
+            const int32_t g = grouped ? group_of(i) : -1;
+            PrefixGroup gr{0, 0, 0};
+            if (g >= 0 && x.shared[g] > 0) {
+                const int32_t at = x.gbase[g];
+                gr = PrefixGroup{x.plan[at].x, x.plan[at].y, x.prefix[at]};
+            }
+            p.grp[i] = gr;
+        }
     return length;
+}
+
+__device__ __forceinline__ int64_t px_total(const PrefixSums &x, int32_t) { return x.prefix[2 * kPxMost]; }
+__device__ __forceinline__ int64_t px_total(const int64_t *prefix, int32_t n) { return prefix[n]; }
+
+// Cost before entry i of a sequence of ne with ng groups.
+__device__ __forceinline__ int64_t px_before(const PrefixSums &x, int32_t ng, int32_t ne, int32_t i)
+{
+    return x.prefix[i == ne ? 2 * kPxMost : i < ng ? i : kPxMost + i - ng];
+}
+
+template <int NT>
+__device__ __forceinline__ bool ck_first(const ChunkParams &p, const PrefixSums &x, PrefixPiece &s, int64_t v0, int64_t v1)
+{
+    if (v0 >= v1)
+        return false;
+    const int32_t B = NT * p.R;
+    int32_t lo = 0, hi = s.ne;
+    while (hi - lo > 1) {             // last pairs with prefix <= v0 (they have a cost: v0 < total)
+        const int32_t mid = (lo + hi) >> 1;
+        if (px_before(x, s.ng, s.ne, mid) <= v0)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    s.i = lo;
+    px_entry<NT>(p, s, x.plan[px_slot(s)]);
+    const int64_t start = px_before(x, s.ng, s.ne, lo);
+    const int32_t wt = s.wt, slope = s.group ? 0 : B;
+    const int64_t H = (s.group ? px_head_keys(s.L, s.k, B) : ck_head_keys(s.L, s.k, B)) * wt;
+    int64_t rem = v0 - start;
+    s.g = (int32_t)(rem / H);
+    rem -= s.g * H;
+    // last block with cost before it <= rem (chunk_pieces.cuh; a group's blocks cost the same each)
+    const int64_t a = (int64_t)kStartKeys + s.L;
+    int64_t b;
+    if (s.group) {
+        b = rem / (a * wt);
+    } else {
+        const float h = (float)a + 0.5f * B;
+        b = (int64_t)((sqrtf(h * h + 2.0f * B * ((float)rem / wt)) - h) / B);
+    }
+    b = b < 0 ? 0 : b > s.nb - 1 ? s.nb - 1 : b;
+    while (b + 1 < s.nb && ck_before(a, slope, b + 1) * wt <= rem)
+        ++b;
+    while (b > 0 && ck_before(a, slope, b) * wt > rem)
+        --b;
+    s.b = (int32_t)b;
+    s.base = start + s.g * H + ck_before(a, slope, b) * wt;
+    const int32_t t0 = ck_tile_at(v0 - s.base, wt);
+    const bool have = ck_set<NT>(p, s, v1, t0);
+    return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
 }
 
 __device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, int32_t length)
