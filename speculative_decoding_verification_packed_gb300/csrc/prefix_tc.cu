@@ -45,19 +45,23 @@ struct PxOwn {
     const float *o;
 };
 
-// Block (row, y): heads 8 y .. 8 y + 7 of a packed row, one a half warp.  Bound by its chain of reads, offsets ->
-// request -> (m, l) and O.
-constexpr int kPxThreads = 128, kPxHeads = kPxThreads / 16;
+// Block (row, y): some heads of a packed row, 8 of them with a half warp each (kWays 1), or one with all eight half
+// warps, which take its pieces in turn and add up through shared memory (kWays 8): calls of few rows have
+// their keys cut into many pieces (8 tokens behind 4096: 20 each), which one half warp reads one after the other.
+// Bound by its chain of reads, offsets -> request -> (m, l) and O.
+constexpr int kPxThreads = 128, kPxHalves = kPxThreads / 16;
 
-template <int D>
+template <int D, int kWays>
 __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_constant__ ChunkParams p, const PxOwn w, int32_t ctas)
 {
     constexpr int NT = D == 256 ? 1 : 2, kPartRows = 128 * NT;
     constexpr int E = D / 16, A = D == 256 ? 2 : 4;       // columns a lane, four side by side; pieces read ahead
+    constexpr int kHeads = kPxHalves / kWays;
     __shared__ int32_t owner;
+    __shared__ __align__(16) float sums[kWays > 1 ? kPxHalves : 1][D + 4];
     griddep_launch_dependents();
     griddep_wait();
-    const int32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 15;
+    const int32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 15, way = kWays > 1 ? tid >> 4 : 0;
     if (tid == 0)
         owner = -1;
     __syncthreads();
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
         return;
     const PrefixRec r = p.rec[owner];
     const PrefixGroup gr = p.grp[owner];
-    const int32_t head = blockIdx.y * kPxHeads + (tid >> 4);
+    const int32_t head = blockIdx.y * kHeads + (kWays > 1 ? 0 : tid >> 4);
     if (r.k <= 0 || head >= p.hq)
         return;
     const int32_t g = head / p.G, h = head - g * p.G;
@@ -114,10 +118,10 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     const uint32_t mask = 0xffffu << (tid & 16);
     const float2 none = make_float2(-INFINITY, 0.0f);
     const float2 ml0 = lane < np ? load_ml(lane) : none;
-    float ahead[A][E];
+    float ahead[A][E];                                    // this half warp's first pieces: way, way + kWays, ..
 #pragma unroll
     for (int q = 0; q < A; ++q)
-        load(min(q, np - 1), ahead[q]);
+        load(min(way + q * kWays, np - 1), ahead[q]);
     // (a piece without a visible key of this row, l = 0, is left out whatever its O holds)
     float M = ml0.y != 0.0f ? ml0.x : -INFINITY;
     for (int32_t q = 16 + lane; q < np; q += 16) {
@@ -135,26 +139,52 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
         const float2 ml = q0 == 0 ? ml0 : q0 + lane < np ? load_ml(q0 + lane) : none;
         // (more than 0 where there is a visible key: its O may be NaN)
         const float w = ml.y != 0.0f ? fmaxf(fast_exp2(ml.x - M), FLT_MIN) : 0.0f, wl = ml.y != 0.0f ? w * ml.y : 0.0f;
-        auto add = [&](int32_t q, const float (&x)[E]) {
+        auto add = [&](int32_t q, const float (&x)[E]) {  // piece q0 + q
             const float wq = __shfl_sync(mask, w, q, 16);
             L += __shfl_sync(mask, wl, q, 16);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 acc[e] = wq != 0.0f ? fmaf(wq, x[e], acc[e]) : acc[e];
         };
-        int32_t q = 0;
+        const int32_t cnt = min(16, np - q0);
+        int32_t q = way;
         if (q0 == 0) {
 #pragma unroll
-            for (int k = 0; k < A; ++k)
-                add(k, ahead[k]);                         // (weight 0 from np on)
-            q = A;
+            for (int k = 0; k < A; ++k, q += kWays)
+                if (q < 16)
+                    add(q, ahead[k]);                     // (weight 0 from np on)
+        } else if (q0 == 16 && kWays * A > 16) {
+#pragma unroll
+            for (int k = 16 / kWays; k < A; ++k, q += kWays)
+                if (q < cnt)
+                    add(q, ahead[k]);
         }
-        const int32_t cnt = min(16, np - q0);
 #pragma unroll 2
-        for (; q < cnt; ++q) {
+        for (; q < cnt; q += kWays) {
             float x[E];
             load(q0 + q, x);
             add(q, x);
+        }
+    }
+    if constexpr (kWays > 1) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4 *>(&sums[way][16 * e + lane * 4]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        if (lane == 0)
+            sums[way][D] = L;
+        __syncthreads();
+        if (way > 0)
+            return;
+        for (int y = 1; y < kWays; ++y) {
+            L += sums[y][D];
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&sums[y][16 * e + lane * 4]);
+                acc[e] += v.x;
+                acc[e + 1] += v.y;
+                acc[e + 2] += v.z;
+                acc[e + 3] += v.w;
+            }
         }
     }
     const float inv = 1.0f / L;
@@ -239,11 +269,12 @@ static svp_status prefix_run(ChunkParams &p, ChunkParams &few, cudaStream_t stre
             return st;
         own = PxOwn{1, few.R, few.part_ml, few.part_o};
     }
-    const unsigned y = (unsigned)((p.hq + kPxHeads - 1) / kPxHeads);
-    return launch_pdl(prefix_join_kernel<D>, dim3((unsigned)p.m_cap, y), dim3(kPxThreads), 0, stream, p, own, (int32_t)ctas) ==
-                   cudaSuccess
-               ? SVP_OK
-               : SVP_ECUDA;
+    // (up to four blocks an SM)
+    const bool ways = (int64_t)p.m_cap * p.hq <= 4 * (int64_t)ctas;
+    const dim3 grid((unsigned)p.m_cap, (unsigned)(ways ? p.hq : (p.hq + kPxHalves - 1) / kPxHalves));
+    const cudaError_t e = ways ? launch_pdl(prefix_join_kernel<D, kPxHalves>, grid, dim3(kPxThreads), 0, stream, p, own, (int32_t)ctas)
+                               : launch_pdl(prefix_join_kernel<D, 1>, grid, dim3(kPxThreads), 0, stream, p, own, (int32_t)ctas);
+    return e == cudaSuccess ? SVP_OK : SVP_ECUDA;
 }
 
 static bool al16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
