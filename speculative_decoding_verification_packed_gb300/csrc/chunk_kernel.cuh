@@ -50,7 +50,7 @@
 #include <cfloat>
 #include <type_traits>
 
-#include "prefix_pieces.cuh"
+#include "prefix_few.cuh"
 
 namespace svp {
 
@@ -248,7 +248,8 @@ __device__ __forceinline__ void ck_store8(void *at, const uint32_t *x)
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int D, bool Q8, bool kShared>
+// kFew: blocks of 8 query rows of the requests' own blocks (kPxBeside), 0: no such blocks.
+template <int D, bool Q8, bool kShared, int kFew = 0>
 __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p)
 {
     using Cfg = ChunkCfg<D, Q8>;
@@ -327,12 +328,38 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    const ChunkShares shares = ck_shares(px_total(sums, pairs));
-    const int32_t cta = blockIdx.x;
+    int32_t cta = blockIdx.x;
+    ChunkShares shares;
+    bool few = false;
+    if constexpr (kFew > 0) {
+        // of this block's kind: the groups' or the requests'
+        const int64_t all = px_total(sums, pairs), groups = sums.prefix[kPxMost];
+        const int32_t split = px_split(all, groups, (int32_t)gridDim.x);
+        few = cta >= split;
+        shares = few ? ck_shares(all - groups, (int32_t)gridDim.x - split) : ck_shares(groups, split);
+        cta -= few ? split : 0;
+    } else {
+        shares = ck_shares(px_total(sums, pairs));
+    }
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     Piece s;
     if constexpr (kShared)
         px_bind(p, s, pairs);
+    if constexpr (kFew > 0) {
+        const int64_t groups = sums.prefix[kPxMost];
+        if (few) {
+            // (costs from the groups' on)
+            s.R = p.own_R;
+            const bool have = ck_first<1>(p, sums, s, groups + v0, groups + v1);
+            __syncthreads();
+            few_body<D, kFew>(p, smem, s, have, groups + v1, cta);
+            __syncthreads();
+            if (warp == 1)
+                tmem_dealloc(tmem, 512);
+            return;
+        }
+        s.ne = s.ng;
+    }
     const bool have0 = ck_first<NT>(p, sums, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();

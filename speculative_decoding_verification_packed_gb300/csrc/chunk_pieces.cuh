@@ -55,7 +55,11 @@ struct ChunkParams {
     // groups of requests with common first pages (prefix_pieces.cuh)
     const int32_t *cu_groups, *prefix_len;
     int32_t ng;
-    int32_t part, share_rows;         // pairs of this kernel: kPxAll, ..; tokens of a block of the group kernel
+    int32_t part, share_rows;         // pairs of this kernel: kPxAll, ..; tokens of a block of the groups'
+    int32_t own_R, own_NT;            // tokens and query tiles of a block of the requests'
+    int32_t few_ring, few_slots, few_misc;
+    float2 *few_ml;                   // as part_ml and part_o, of the blocks for requests of few rows
+    float *few_o;
     int4 *plan;                       // [grid][2 * kPxMost]
     struct PrefixRec *rec;            // [n]
     struct PrefixGroup *grp;          // [n]

@@ -1,4 +1,5 @@
-// prefix_few.cu -- svp_prefix_attn over bf16 pages: requests of few rows behind what their groups share.
+// prefix_few.cuh -- svp_prefix_attn over bf16 pages: the blocks that take requests of few rows, beside those that take
+// the groups (chunk_kernel.cuh, whose kernel this is a part of).
 //
 // Decode tokens behind a common beginning have short keys of their own, and many of them: 64 requests of 8 KV
 // heads are 512 pairs of a few tiles.  The tile kernel (chunk_kernel.cuh) pays 5 us for a pair's start and end, with
@@ -10,16 +11,15 @@
 // kernel's half tiles (128 rows of 64 elements, 128-byte swizzle) and are read by ldmatrix, V transposed; P^T
 // turns from accumulator to operand by movmatrix.  Scores, m, l and O are fp32, P is rounded to bf16 because the
 // products take 16 bits (l sums it unrounded), as in the tile kernel.  NB = 1 or 2 blocks of 8 rows.
-#include <algorithm>
+#pragma once
+
 #include <cfloat>
-#include <cstring>
 
 #include "prefix_pieces.cuh"
 
 namespace svp {
 
 constexpr int kFwWarps = 8;           // computing warps; then a K and a V loader
-constexpr int kFwThreads = 32 * (kFwWarps + 2);
 constexpr int kFwSlots = 8;           // ring slots at most: even ones hold K, odd ones V
 
 struct FewMisc {
@@ -73,20 +73,21 @@ __device__ __forceinline__ uint32_t fw_chunk(int row, int c)
     return (uint32_t)((c >> 3) * kCkSub + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
+// Share [v0, v1) of the requests' costs; every thread of the block, whose shared memory below p.few_end is free (from
+// p.off_ring on the prologue's sums are, which is why the first piece, s, is given).
 template <int D, int NB>
-__global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_constant__ ChunkParams p)
+__device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, PrefixPiece s, bool have0, int64_t v1, int32_t cta)
 {
     using Cfg = FewCfg<D, NB>;
     constexpr int KS = Cfg::KS;
-    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    FewMisc *m = reinterpret_cast<FewMisc *>(smem + p.off_misc);
+    FewMisc *m = reinterpret_cast<FewMisc *>(smem + p.few_misc);
     const uint32_t bar0 = smem_u32(m->bars);
     auto bar_full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (kFwSlots + s); };
     volatile int *abort_flag = &m->abort_flag;
-    const uint32_t nslot = (uint32_t)p.nslot;
+    const uint32_t nslot = (uint32_t)p.few_slots;
     if (tid == 0) {
         for (int s = 0; s < kFwSlots; ++s) {
             mbar_init(bar_full(s), 1);
@@ -94,23 +95,11 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
         }
         mbar_fence_init();
         m->abort_flag = 0;
-        tma_prefetch_desc(&p.tm_k);
-        tma_prefetch_desc(&p.tm_v);
     }
-    griddep_launch_dependents();
-    griddep_wait();
-    const int32_t pairs = px_prologue<1>(p, smem + p.off_ring);
-    const PrefixSums &sums = *reinterpret_cast<const PrefixSums *>(smem + p.off_ring);   // (until the loaders start)
-    const ChunkShares shares = ck_shares(px_total(sums, pairs));
-    const int32_t cta = blockIdx.x;
-    const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
-    PrefixPiece s;
-    px_bind(p, s, pairs);
-    const bool have0 = ck_first<1>(p, sums, s, v0, v1);
     fence_proxy_async_smem();             // the loads overwrite the sums
     __syncthreads();
 
-    if (warp >= kFwWarps) {
+    if (warp == kFwWarps || warp == kFwWarps + 1) {
         // ============================================================ K loader, V loader
         // Lane u looks after positions 4 u .. 4 u + 3 of a tile; the lane of a page's first positions loads the
         // page; pages that are not needed or not in the pool are loaded from past the pool (zeros).
@@ -146,7 +135,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
                 if (loads) {
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d_hint(sbase + p.off_ring + slot * Cfg::kSlot + c * kCkSub + lane * 512, tm, bar_full(slot),
+                        tma_load_4d_hint(sbase + p.few_ring + slot * Cfg::kSlot + c * kCkSub + lane * 512, tm, bar_full(slot),
                                          c * 64, 0, s.g, id, pol);
                 }
                 __syncwarp();
@@ -166,7 +155,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
                 mbar_wait(bar_full((2 * x + kv) % nslot), (x / per) & 1u, &drain);
         }
         __syncwarp();
-    } else {
+    } else if (warp < kFwWarps) {
         // ============================================================ computing warps
         const int q = lane & 3, r = lane >> 2, kb = warp * 16;
         float *red = reinterpret_cast<float *>(smem);       // [8 warps][8 NB rows][D + 8]
@@ -215,7 +204,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
                     break;
                 const int32_t k0 = t * kCkKeys + kb;        // this warp's first key
                 const bool masked = k0 + 15 > s.L + s.tb0;
-                const uint32_t kt = sbase + p.off_ring + slot * Cfg::kSlot, vt = sbase + p.off_ring + vs * Cfg::kSlot;
+                const uint32_t kt = sbase + p.few_ring + slot * Cfg::kSlot, vt = sbase + p.few_ring + vs * Cfg::kSlot;
                 // ---- S^T of keys k0 + r and k0 + r + 8 with rows 2 q and 2 q + 1, in two chains of products
                 float sc[NB][4];
                 {
@@ -379,8 +368,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
                         p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
                 } else {
                     int64_t prow = (int64_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kShortRows + rho;
-                    float *part_o = p.part_o;
-                    float2 *part_ml = p.part_ml;
+                    float *part_o = p.few_o;
+                    float2 *part_ml = p.few_ml;
                     if (all) {
                         prow = px_place(p, false, s.off + s.tb0 + tok, s.g * p.G + h);
                         part_o = p.place_o;
@@ -397,37 +386,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const __grid_
     __syncthreads();
     if (*abort_flag && tid == 0)
         set_status(p.status, SVP_DEV_TIMEOUT);
-}
-
-int chunk_ctas();
-
-template <int D, int NB>
-static svp_status few_launch(ChunkParams &p, cudaStream_t stream)
-{
-    using Cfg = FewCfg<D, NB>;
-    constexpr int kBudget = 227 * 1024;
-    const int misc = (int)(sizeof(FewMisc) + 127) / 128 * 128;
-    p.off_ring = (Cfg::kRed + 1023) / 1024 * 1024;
-    p.nslot = std::min(kFwSlots, (kBudget - p.off_ring - misc) / Cfg::kSlot) / 2 * 2;
-    if (p.nslot < 4 || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
-        return SVP_EUNSUPPORTED;
-    p.off_misc = p.off_ring + p.nslot * Cfg::kSlot;
-    static std::atomic<uint64_t> configured{0};
-    if (set_smem_limit_once(prefix_few_kernel<D, NB>, kBudget, configured) != cudaSuccess)
-        return SVP_ECUDA;
-    return launch_ctas(prefix_few_kernel<D, NB>, chunk_ctas(), kFwThreads, (size_t)(p.off_misc + misc), stream, p, true,
-                       false) == cudaSuccess
-               ? SVP_OK
-               : SVP_ECUDA;
-}
-
-// The requests of svp_prefix_attn over bf16 pages, at most kShortRows rows of a KV head each (p.R tokens).
-svp_status prefix_few_run(ChunkParams &p, int32_t d, cudaStream_t stream)
-{
-    const bool one = p.G * p.R <= 8;      // rows of one block
-    if (d == 64)
-        return one ? few_launch<64, 1>(p, stream) : few_launch<64, 2>(p, stream);
-    return one ? few_launch<128, 1>(p, stream) : few_launch<128, 2>(p, stream);
 }
 
 }  // namespace svp

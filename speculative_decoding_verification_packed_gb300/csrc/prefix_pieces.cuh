@@ -17,8 +17,9 @@ namespace svp {
 
 constexpr int kPxMost = 1024;         // requests, and groups, of a call
 
-// One kernel for all pairs, or one for the groups and another for the requests (prefix_tc.cu says when).
-enum { kPxAll = 0, kPxGroups = 1, kPxRequests = 2 };
+// One sequence of all pairs; one of the groups and one of the requests, each with blocks of its own in one kernel;
+// or a kernel for each (prefix_tc.cu says when).
+enum { kPxAll = 0, kPxBeside = 1, kPxGroups = 2, kPxRequests = 3 };
 
 // What the joining kernel needs of a request, and of its group, written by the first CTA of the kernel that has the pairs.
 struct PrefixRec {
@@ -35,6 +36,7 @@ struct PrefixPiece : ChunkPiece {     // i: place in the sequence of groups and 
     const int4 *plan;                 // this CTA's copy: (first row, rows, P, row of the block table), then (first
                                       // row, rows, tokens behind P, P)
     int32_t row, first;               // row of the block table, and the first key's position
+    int32_t R;                        // tokens of a query tile
     bool group;
 };
 
@@ -48,6 +50,11 @@ __device__ __forceinline__ int32_t ck_last(const PrefixPiece &s, int32_t tok)
 }
 __device__ __forceinline__ bool ck_kept(const PrefixPiece &s) { return s.group || s.first > 0; }
 
+__device__ __forceinline__ int32_t px_weight(int32_t nt, int32_t k, int32_t R)
+{
+    return nt == 2 ? ck_weight<2>(k, R) : ck_weight<1>(k, R);
+}
+
 // Keys of one KV head of a group of k rows, B a block: each block sees all L.
 __device__ __forceinline__ int64_t px_head_keys(int32_t L, int32_t k, int32_t B)
 {
@@ -57,7 +64,7 @@ __device__ __forceinline__ int64_t px_head_keys(int32_t L, int32_t k, int32_t B)
 template <int NT>
 __device__ __forceinline__ bool ck_set(const ChunkParams &p, PrefixPiece &s, int64_t v1, int32_t t0)
 {
-    const int32_t B = NT * p.R;
+    const int32_t B = NT * s.R;
     s.tb0 = s.b * B;
     s.ntok = min(B, s.k - s.tb0);
     s.len = s.group ? s.L : s.L + s.tb0 + s.ntok;
@@ -72,7 +79,7 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, PrefixPiece &s, int
 template <int NT>
 __device__ __forceinline__ bool px_entry(const ChunkParams &p, PrefixPiece &s, const int4 x)
 {
-    const int32_t B = NT * p.R;
+    const int32_t B = NT * s.R;
     s.group = s.i < s.ng;
     s.off = x.x;
     s.k = x.y;
@@ -82,7 +89,7 @@ __device__ __forceinline__ bool px_entry(const ChunkParams &p, PrefixPiece &s, c
     if (s.k <= 0)
         return false;
     s.nb = (s.k + B - 1) / B;
-    s.wt = ck_weight<NT>(s.k, p.R);
+    s.wt = ck_weight<NT>(s.k, s.R);
     return true;
 }
 
@@ -176,7 +183,7 @@ template <int NT>
 __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
 {
     PrefixSums &x = *static_cast<PrefixSums *>(smem);
-    const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, n = p.n, ng = p.ng;
+    const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, OB = p.own_NT * p.own_R, n = p.n, ng = p.ng;
     const bool tells = blockIdx.x == 0, has_groups = p.part != kPxRequests, has_requests = p.part != kPxGroups;
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     if (tid == 0)
@@ -267,7 +274,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 if (k > 0 && !ck_bad(p, off, x.cu[i + 1], L)) {
                     const int32_t g = grouped ? group_of(i) : -1, P = g >= 0 ? x.shared[g] : 0;
                     what = make_int4(off, k, L - P, P);
-                    cost = ck_head_keys(what.z, k, B) * ck_weight<NT>(k, p.R) * p.c.hkv;
+                    cost = ck_head_keys(what.z, k, OB) * px_weight(p.own_NT, k, p.own_R) * p.c.hkv;
                 }
             }
         }
@@ -292,14 +299,16 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
         }
     }
     const int32_t first = run.count, length = first + (has_requests ? n : 0);
-    if (tid == 0) {
+    if (tid == 0)
         x.prefix[2 * kPxMost] = run.running;
-        if (tells && has_groups)
-            p.total[0] = run.running;
-        if (tells && has_requests)
-            p.total[1] = run.running;
-    }
     __syncthreads();
+    // (the sums of kPxBeside: of both, and of the groups)
+    if (tells && tid == 0) {
+        if (has_groups)
+            p.total[0] = run.running;
+        if (has_requests)
+            p.total[1] = p.part == kPxBeside ? x.prefix[kPxMost] : run.running;
+    }
     if (tells && has_groups)
         for (int32_t i = tid; i < n; i += nt) {
             const int32_t g = grouped ? group_of(i) : -1;
@@ -327,7 +336,7 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const PrefixSums 
 {
     if (v0 >= v1)
         return false;
-    const int32_t B = NT * p.R;
+    const int32_t B = NT * s.R;
     int32_t lo = 0, hi = s.ne;
     while (hi - lo > 1) {             // last pairs with prefix <= v0 (they have a cost: v0 < total)
         const int32_t mid = (lo + hi) >> 1;
@@ -370,6 +379,16 @@ __device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, in
     s.plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     s.ne = length;
     s.ng = p.part == kPxGroups ? length : p.part == kPxRequests ? 0 : length - p.n;
+    s.R = p.part == kPxRequests ? p.own_R : p.R;
+}
+
+// kPxBeside: of `ctas` blocks, those that the groups have; the others have the requests.  all: cost of both, groups: of
+// the groups, which come first in the sums.
+__device__ __forceinline__ int32_t px_split(int64_t all, int64_t groups, int32_t ctas)
+{
+    if (groups == 0 || groups == all)
+        return groups == 0 ? 0 : ctas;
+    return max(1, min(ctas - 1, (int32_t)((groups * ctas + all / 2) / all)));
 }
 
 // Place of (row, head) of a part that one piece has all of, a group's or a request's behind one.

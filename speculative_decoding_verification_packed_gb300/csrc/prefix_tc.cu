@@ -38,7 +38,7 @@ __device__ __forceinline__ PxPieces px_pieces(const ChunkParams &p, const ChunkS
     return y;
 }
 
-// Where the requests' pieces are: the tile kernel's, beside the groups', or those of a kernel of their own.
+// Where the requests' pieces are: among the groups', or those of blocks or a kernel for few rows.
 struct PxOwn {
     int32_t few, R;                   // tokens of its query tile
     const float2 *ml;
@@ -66,6 +66,17 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
         owner = -1;
     __syncthreads();
     const int64_t total[2] = {__ldcg(p.total), __ldcg(p.total + 1)};
+    ChunkShares gs, os;                                   // the groups' and the requests'
+    int64_t obase = 0;                                    // cost before the first request
+    if (p.part == kPxBeside) {
+        const int32_t split = px_split(total[0], total[1], ctas);
+        gs = ck_shares(total[1], split);
+        os = ck_shares(total[0] - total[1], ctas - split);
+        obase = total[1];
+    } else {
+        gs = ck_shares(total[0], ctas);
+        os = ck_shares(total[1], ctas);
+    }
     for (int32_t i = tid; i < p.n; i += kPxThreads)
         if (__ldg(p.cu + i) <= row && row < __ldg(p.cu + i + 1))
             owner = i;                                    // (one, but where nothing is computed)
@@ -78,13 +89,13 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (r.k <= 0 || head >= p.hq)
         return;
     const int32_t g = head / p.G, h = head - g * p.G;
-    const PxPieces own = w.few ? px_pieces<1>(p, ck_shares(total[1], ctas), false, r.base, r.k, r.L, row - r.off, g, h, w.R)
-                               : px_pieces<NT>(p, ck_shares(total[1], ctas), false, r.base, r.k, r.L, row - r.off, g, h, w.R);
+    const PxPieces own = w.few ? px_pieces<1>(p, os, false, r.base - obase, r.k, r.L, row - r.off, g, h, w.R)
+                               : px_pieces<NT>(p, os, false, r.base, r.k, r.L, row - r.off, g, h, w.R);
     if (r.P == 0 && own.np == 1)
         return;                                           // (the output has it already)
     PxPieces grp{0, 0, 0};
     if (r.P > 0)
-        grp = px_pieces<NT>(p, ck_shares(total[0], ctas), true, gr.base, gr.k, r.P, row - gr.off, g, h, p.R);
+        grp = px_pieces<NT>(p, gs, true, gr.base, gr.k, r.P, row - gr.off, g, h, p.R);
     const int32_t np = grp.np + own.np;
     auto at = [&](int32_t q, const float2 *&ml, const float *&o) {
         const bool mine = q >= grp.np;
@@ -205,9 +216,8 @@ bool chunk_maps(ChunkParams &p, const void *q, int64_t q_stride, svp_dtype kv, i
 template <int D, bool Q8>
 bool chunk_layout(ChunkParams &p, int32_t rows, int &smem);
 svp_status chunk_short_prefix_run(ChunkParams &p, int32_t d, cudaStream_t stream);
-svp_status prefix_few_run(ChunkParams &p, int32_t d, cudaStream_t stream);
 
-constexpr int kPxFewPairs = 300;      // requests times KV heads
+constexpr int kPxFewPairs = 300;      // requests times KV heads, 8-bit pages
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -235,11 +245,34 @@ static PrefixWs prefix_ws(int32_t hq, int32_t d, int32_t m_cap)
     return w;
 }
 
-// Requests of few rows have a kernel of their own where their pairs are many: then the tile kernel's 5 us for a
-// pair's start and end cost more than a third launch.
-static bool few_requests(const ChunkParams &p, int32_t d)
+// Requests of at most kShortRows rows a KV head, d <= 128: over bf16 pages blocks of their own in the one kernel; over 8-bit
+// ones chunk_short.cu's kernel, from so many pairs on that a third launch costs less than the tile kernel's pairs.
+static bool few_rows(const ChunkParams &p, int32_t d) { return d <= 128 && (int64_t)p.G * p.w <= kShortRows; }
+
+template <int D, bool Q8, int kFew>
+static svp_status prefix_tiles(const ChunkParams &p, int smem, cudaStream_t stream)
 {
-    return d <= 128 && (int64_t)p.G * p.w <= kShortRows && (int64_t)p.n * p.c.hkv >= kPxFewPairs;
+    static std::atomic<uint64_t> configured{0};
+    if (set_smem_limit_once(chunk_tc_kernel<D, Q8, true, kFew>, 227 * 1024, configured) != cudaSuccess)
+        return SVP_ECUDA;
+    return launch_ctas(chunk_tc_kernel<D, Q8, true, kFew>, chunk_ctas(), ChunkCfg<D, Q8>::kThreads, (size_t)smem, stream, p, true,
+                       true) == cudaSuccess
+               ? SVP_OK
+               : SVP_ECUDA;
+}
+
+// The layout of few_body's shared memory, below the tile kernel's barriers, which are moved to the end.
+template <int D, int NB>
+static bool few_layout(ChunkParams &p, int &smem)
+{
+    using Cfg = FewCfg<D, NB>;
+    const int misc = smem - p.off_misc;
+    smem = 227 * 1024;
+    p.off_misc = (smem - misc) / 128 * 128;
+    p.few_ring = (Cfg::kRed + 1023) / 1024 * 1024;
+    p.few_slots = std::min(kFwSlots, (p.off_misc - p.few_ring - (int)sizeof(FewMisc)) / Cfg::kSlot) / 2 * 2;
+    p.few_misc = p.few_ring + p.few_slots * Cfg::kSlot;
+    return p.few_slots >= 4;
 }
 
 template <int D, bool Q8>
@@ -248,27 +281,44 @@ static svp_status prefix_run(ChunkParams &p, ChunkParams &few, cudaStream_t stre
     using Cfg = ChunkCfg<D, Q8>;
     int smem = 0;
     p.share_rows = Cfg::NT * p.R;
-    const bool split = few_requests(p, D);
-    p.part = split ? kPxGroups : kPxAll;
+    p.own_NT = Cfg::NT;
+    p.own_R = p.R;
+    p.part = kPxAll;
     if (!chunk_layout<D, Q8>(p, p.m_cap, smem) || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
         return SVP_EUNSUPPORTED;
-    static std::atomic<uint64_t> configured{0};
-    if (set_smem_limit_once(chunk_tc_kernel<D, Q8, true>, 227 * 1024, configured) != cudaSuccess)
-        return SVP_ECUDA;
-    const int ctas = chunk_ctas();
-    if (launch_ctas(chunk_tc_kernel<D, Q8, true>, ctas, Cfg::kThreads, (size_t)smem, stream, p, true, true) != cudaSuccess)
-        return SVP_ECUDA;
     PxOwn own{0, p.R, p.part_ml, p.part_o};
-    if (split) {
-        // (a pair of the kernel for few rows is a request's KV head: w tokens are one block)
-        few.share_rows = p.share_rows;
-        few.part = kPxRequests;
-        few.R = p.w;
-        const svp_status st = Q8 ? chunk_short_prefix_run(few, D, stream) : prefix_few_run(few, D, stream);
-        if (st != SVP_OK)
-            return st;
-        own = PxOwn{1, few.R, few.part_ml, few.part_o};
+    svp_status st;
+    if (few_rows(p, D) && (!Q8 || (int64_t)p.n * p.c.hkv >= kPxFewPairs)) {
+        // (a pair for few rows is a request's KV head: w tokens are one block)
+        p.own_NT = few.own_NT = 1;
+        p.own_R = few.own_R = p.w;
+        own = PxOwn{1, p.w, p.few_ml, p.few_o};
+        if constexpr (Q8) {
+            p.part = kPxGroups;
+            st = prefix_tiles<D, true, 0>(p, smem, stream);
+            if (st != SVP_OK)
+                return st;
+            few.share_rows = p.share_rows;
+            few.part = kPxRequests;
+            few.R = p.w;
+            few.part_ml = p.few_ml;
+            few.part_o = p.few_o;
+            st = chunk_short_prefix_run(few, D, stream);
+        } else if constexpr (D <= 128) {
+            p.part = kPxBeside;
+            const bool one = p.G * p.w <= 8;              // rows of one block of 8
+            if (!(one ? few_layout<D, 1>(p, smem) : few_layout<D, 2>(p, smem)))
+                return SVP_EUNSUPPORTED;
+            st = one ? prefix_tiles<D, false, 1>(p, smem, stream) : prefix_tiles<D, false, 2>(p, smem, stream);
+        } else {
+            return SVP_EUNSUPPORTED;                      // (never: few rows are d <= 128)
+        }
+    } else {
+        st = prefix_tiles<D, Q8, 0>(p, smem, stream);
     }
+    if (st != SVP_OK)
+        return st;
+    const int ctas = chunk_ctas();
     // (up to four blocks an SM)
     const bool ways = (int64_t)p.m_cap * p.hq <= 4 * (int64_t)ctas;
     const dim3 grid((unsigned)p.m_cap, (unsigned)(ways ? p.hq : (p.hq + kPxHalves - 1) / kPxHalves));
@@ -361,10 +411,10 @@ svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache 
     p.place_o = reinterpret_cast<float *>(b + o.o3);
     if (!chunk_maps(p, q, q_row_stride, cache->dtype, m_cap, d, std::min(p.R, m_cap), false))
         return SVP_EUNSUPPORTED;
-    ChunkParams few = p;
-    few.part_ml = reinterpret_cast<float2 *>(b + o.ml2);
-    few.part_o = reinterpret_cast<float *>(b + o.o2);
-    if (few_requests(p, d) && !chunk_maps(few, q, q_row_stride, cache->dtype, m_cap, d, 1, true))
+    p.few_ml = reinterpret_cast<float2 *>(b + o.ml2);
+    p.few_o = reinterpret_cast<float *>(b + o.o2);
+    ChunkParams few = p;                  // (for chunk_short.cu: other swizzles)
+    if (cache->dtype == SVP_E4M3 && few_rows(p, d) && !chunk_maps(few, q, q_row_stride, cache->dtype, m_cap, d, 1, true))
         return SVP_EUNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->dtype == SVP_E4M3) {
