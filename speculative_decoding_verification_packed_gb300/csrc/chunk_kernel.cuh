@@ -50,6 +50,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "chunk_short.cuh"
 #include "prefix_few.cuh"
 
 namespace svp {
@@ -248,8 +249,8 @@ __device__ __forceinline__ void ck_store8(void *at, const uint32_t *x)
 }
 
 // ------------------------------------------------------------------ the kernel
-// kFew: blocks of 8 query rows of the requests' own blocks (kPxBeside), 0: no such blocks.
-template <int D, bool Q8, bool kShared, int kFew = 0>
+// kFew: the requests, of few rows, have blocks of their own (kPxBeside).
+template <int D, bool Q8, bool kShared, bool kFew = false>
 __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p)
 {
     using Cfg = ChunkCfg<D, Q8>;
@@ -328,31 +329,45 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    int32_t cta = blockIdx.x;
-    ChunkShares shares;
-    bool few = false;
-    if constexpr (kFew > 0) {
-        // of this block's kind: the groups' or the requests'
-        const int64_t all = px_total(sums, pairs), groups = sums.prefix[kPxMost];
-        const int32_t split = px_split(all, groups, (int32_t)gridDim.x);
-        few = cta >= split;
-        shares = few ? ck_shares(all - groups, (int32_t)gridDim.x - split) : ck_shares(groups, split);
-        cta -= few ? split : 0;
-    } else {
-        shares = ck_shares(px_total(sums, pairs));
-    }
+    // kFew: of this block's kind, the groups' (the first blocks) or the requests'
+    const int32_t split = [&]() -> int32_t {
+        if constexpr (kFew)
+            return px_split(px_total(sums, pairs), sums.prefix[kPxMost], (int32_t)gridDim.x);
+        else
+            return 0;
+    }();
+    const bool few = kFew && (int32_t)blockIdx.x >= split;
+    const ChunkShares shares = [&]() -> ChunkShares {
+        if constexpr (kFew) {
+            const int64_t groups = sums.prefix[kPxMost];
+            return few ? ck_shares(px_total(sums, pairs) - groups, (int32_t)gridDim.x - split) : ck_shares(groups, split);
+        } else {
+            return ck_shares(px_total(sums, pairs));
+        }
+    }();
+    const int32_t cta = (int32_t)blockIdx.x - (few ? split : 0);
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     Piece s;
     if constexpr (kShared)
         px_bind(p, s, pairs);
-    if constexpr (kFew > 0) {
+    if constexpr (kFew) {
         const int64_t groups = sums.prefix[kPxMost];
         if (few) {
             // (costs from the groups' on)
             s.R = p.own_R;
             const bool have = ck_first<1>(p, sums, s, groups + v0, groups + v1);
             __syncthreads();
-            few_body<D, kFew>(p, smem, s, have, groups + v1, cta);
+            if constexpr (Q8) {
+                ShortMisc *sm = reinterpret_cast<ShortMisc *>(smem + p.few_misc);
+                if (tid == 0)
+                    short_init(sm);
+                fence_proxy_async_smem();     // the loads overwrite the sums
+                __syncthreads();
+                short_body<D, 1, true>(p, ShortLayout{p.few_ring, p.few_raw, p.few_slots, p.few_o, p.few_ml, &p.few_k, &p.few_v}, sm,
+                                          smem, s, have, groups + v1, cta, shares);
+            } else {
+                few_body<D>(p, smem, s, have, groups + v1, cta);
+            }
             __syncthreads();
             if (warp == 1)
                 tmem_dealloc(tmem, 512);

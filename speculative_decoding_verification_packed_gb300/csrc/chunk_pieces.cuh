@@ -55,15 +55,16 @@ struct ChunkParams {
     // groups of requests with common first pages (prefix_pieces.cuh)
     const int32_t *cu_groups, *prefix_len;
     int32_t ng;
-    int32_t part, share_rows;         // pairs of this kernel: kPxAll, ..; tokens of a block of the groups'
+    int32_t part, share_rows;         // kPxAll, kPxBeside; tokens of a block of the groups'
     int32_t own_R, own_NT;            // tokens and query tiles of a block of the requests'
-    int32_t few_ring, few_slots, few_misc;
+    CUtensorMap few_k, few_v;         // 8-bit pages as chunk_short.cuh reads them
+    int32_t few_ring, few_raw, few_slots, few_misc;
     float2 *few_ml;                   // as part_ml and part_o, of the blocks for requests of few rows
     float *few_o;
     int4 *plan;                       // [grid][2 * kPxMost]
     struct PrefixRec *rec;            // [n]
     struct PrefixGroup *grp;          // [n]
-    int64_t *total;                   // costs of the groups' kernel and of the requests'
+    int64_t *total;                   // costs of all pairs, and of the groups'
     float2 *place_ml;                 // [2][m_cap][hq]: parts of rows that one piece has all of
     float *place_o;                   // [2][m_cap][hq][d]
 };

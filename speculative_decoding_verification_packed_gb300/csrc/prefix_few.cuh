@@ -10,7 +10,7 @@
 // O in registers; they join at the end of a piece through shared memory.  K and V come by TMA as the tile
 // kernel's half tiles (128 rows of 64 elements, 128-byte swizzle) and are read by ldmatrix, V transposed; P^T
 // turns from accumulator to operand by movmatrix.  Scores, m, l and O are fp32, P is rounded to bf16 because the
-// products take 16 bits (l sums it unrounded), as in the tile kernel.  NB = 1 or 2 blocks of 8 rows.
+// products take 16 bits (l sums it unrounded), as in the tile kernel.
 #pragma once
 
 #include <cfloat>
@@ -25,14 +25,14 @@ constexpr int kFwSlots = 8;           // ring slots at most: even ones hold K, o
 struct FewMisc {
     uint64_t bars[2 * kFwSlots];
     int32_t abort_flag, pad;
-    float2 ml[kFwWarps][16];          // [warp][row of its request]
+    float2 ml[kFwWarps][kPxRows];     // [warp][row of its request]
 };
 
-template <int D, int NB>
+template <int D>
 struct FewCfg {
     static constexpr int kSlot = (D / 64) * kCkSub;
     static constexpr int KS = D / 16;
-    static constexpr int kRed = kFwWarps * 8 * NB * (D + 8) * 4;   // the warps' O, rows padded
+    static constexpr int kRed = kFwWarps * kPxRows * (D + 8) * 4;   // the warps' O, rows padded
 };
 
 // C += A B, bf16 operands, fp32 accumulators (m16n8k16).
@@ -75,10 +75,10 @@ __device__ __forceinline__ uint32_t fw_chunk(int row, int c)
 
 // Share [v0, v1) of the requests' costs; every thread of the block, whose shared memory below p.few_end is free (from
 // p.off_ring on the prologue's sums are, which is why the first piece, s, is given).
-template <int D, int NB>
+template <int D>
 __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, PrefixPiece s, bool have0, int64_t v1, int32_t cta)
 {
-    using Cfg = FewCfg<D, NB>;
+    using Cfg = FewCfg<D>;
     constexpr int KS = Cfg::KS;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -158,7 +158,7 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
     } else if (warp < kFwWarps) {
         // ============================================================ computing warps
         const int q = lane & 3, r = lane >> 2, kb = warp * 16;
-        float *red = reinterpret_cast<float *>(smem);       // [8 warps][8 NB rows][D + 8]
+        float *red = reinterpret_cast<float *>(smem);       // [8 warps][8 rows][D + 8]
         // this lane's row of the blocks that ldmatrix reads: keys kb + (0 .. 7, and + 8), chunk 0 or 1
         const int krow = kb + (lane & 15), kchunk = lane >> 4;                        // of K: blocks by key, then by d
         const int vrow = kb + (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1; // of V: by d, then by key
@@ -166,37 +166,28 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
         bool ok = true;
         for (bool have = have0; have; have = ck_next<1>(p, s, v1)) {
             const int32_t nrows = s.ntok * p.G;
-            // ---- Q: row r of each block as operands; last visible key of rows 2 q and 2 q + 1
-            uint32_t b0[NB][KS], b1[NB][KS];
-            int32_t last[NB][2];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int32_t rho = nb * 8 + r;
-                const bool live = rho < nrows;
-                const int32_t tok = live ? rho / p.G : 0, h = live ? rho - tok * p.G : 0;
+            // ---- Q: row r as operands; last visible key of rows 2 q and 2 q + 1
+            uint32_t b0[KS], b1[KS];
+            int32_t last[2];
+            {
+                const bool live = r < nrows;
+                const int32_t tok = live ? r / p.G : 0, h = live ? r - tok * p.G : 0;
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) +
                                                                          (int64_t)(s.off + s.tb0 + tok) * p.q_stride +
                                                                          (int64_t)(s.g * p.G + h) * D) + q;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    b0[nb][k] = live ? __ldg(src + 8 * k) : 0u;
-                    b1[nb][k] = live ? __ldg(src + 8 * k + 4) : 0u;
+                    b0[k] = live ? __ldg(src + 8 * k) : 0u;
+                    b1[k] = live ? __ldg(src + 8 * k + 4) : 0u;
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int32_t rx = nb * 8 + 2 * q + x;
-                    last[nb][x] = rx < nrows ? s.L + s.tb0 + rx / p.G : -1;
-                }
+                for (int x = 0; x < 2; ++x)
+                    last[x] = 2 * q + x < nrows ? s.L + s.tb0 + (2 * q + x) / p.G : -1;
             }
-            float o[NB][KS][4], mx[NB][2], l[NB][2];
+            float o[KS][4], mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                mx[nb][0] = mx[nb][1] = -INFINITY;
-                l[nb][0] = l[nb][1] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-                    o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.0f;
-            }
+            for (int j = 0; j < KS; ++j)
+                o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
             for (int32_t t = s.t0; t < s.t1 && ok; ++t) {
                 const uint32_t vs = slot + 1;               // (slots come in pairs, nslot is even)
                 ok = __all_sync(0xffffffffu, mbar_wait(bar_full(slot), phase, abort_flag));
@@ -206,78 +197,66 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
                 const bool masked = k0 + 15 > s.L + s.tb0;
                 const uint32_t kt = sbase + p.few_ring + slot * Cfg::kSlot, vt = sbase + p.few_ring + vs * Cfg::kSlot;
                 // ---- S^T of keys k0 + r and k0 + r + 8 with rows 2 q and 2 q + 1, in two chains of products
-                float sc[NB][4];
-                {
-                    float s0[NB][4], s1[NB][4];
+                float sc[4], s1[4];
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
+                for (int x = 0; x < 4; ++x)
+                    sc[x] = s1[x] = 0.0f;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            s0[nb][x] = s1[nb][x] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        uint32_t a[4];
-                        fw_ld4(kt + fw_chunk(krow, 2 * k + kchunk), a);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            fw_mma(k & 1 ? s1[nb] : s0[nb], a, b0[nb][k], b1[nb][k]);
-                    }
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            sc[nb][x] = s0[nb][x] + s1[nb][x];
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t a[4];
+                    fw_ld4(kt + fw_chunk(krow, 2 * k + kchunk), a);
+                    fw_mma(k & 1 ? s1 : sc, a, b0[k], b1[k]);
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    sc[x] += s1[x];
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_empty(slot));
                 // ---- the running maximum (moved when a score lies more than 2^8 above it) and P
-                uint32_t pb[NB][2];
+                uint32_t pb[2];
+                float top[2];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float top[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float z = sc[nb][2 * y + x] * p.scale_log2;
-                            if (masked)
-                                z = k0 + r + 8 * y <= last[nb][x] ? z : -INFINITY;
-                            sc[nb][2 * y + x] = z;
-                        }
-                        top[x] = fmaxf(sc[nb][x], sc[nb][2 + x]);
-                    }
-#pragma unroll
-                    for (int w2 = 4; w2 < 32; w2 <<= 1) {
-                        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w2));
-                        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w2));
-                    }
-                    const bool up0 = top[0] > mx[nb][0] + kCkSlack || (mx[nb][0] == -INFINITY && top[0] != -INFINITY);
-                    const bool up1 = top[1] > mx[nb][1] + kCkSlack || (mx[nb][1] == -INFINITY && top[1] != -INFINITY);
-                    if (__any_sync(0xffffffffu, up0 || up1)) {
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float mn = fmaxf(mx[nb][x], top[x]);
-                            const float alpha = mx[nb][x] == -INFINITY ? 0.0f : fast_exp2(mx[nb][x] - mn);
-                            mx[nb][x] = mn;
-                            l[nb][x] *= alpha;
-#pragma unroll
-                            for (int j = 0; j < KS; ++j) {
-                                o[nb][j][x] *= alpha;
-                                o[nb][j][2 + x] *= alpha;
-                            }
-                        }
-                    }
+                for (int x = 0; x < 2; ++x) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float pr[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            pr[x] = fast_exp2(sc[nb][2 * y + x] - (mx[nb][x] == -INFINITY ? 0.0f : mx[nb][x]));
-                            l[nb][x] += pr[x];
-                        }
-                        pb[nb][y] = fw_turn(pack_bf16x2(pr[0], pr[1]));     // row r, keys 8 y + 2 q, + 1
+                        float z = sc[2 * y + x] * p.scale_log2;
+                        if (masked)
+                            z = k0 + r + 8 * y <= last[x] ? z : -INFINITY;
+                        sc[2 * y + x] = z;
                     }
+                    top[x] = fmaxf(sc[x], sc[2 + x]);
+                }
+#pragma unroll
+                for (int w2 = 4; w2 < 32; w2 <<= 1) {
+                    top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w2));
+                    top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w2));
+                }
+                const bool up0 = top[0] > mx[0] + kCkSlack || (mx[0] == -INFINITY && top[0] != -INFINITY);
+                const bool up1 = top[1] > mx[1] + kCkSlack || (mx[1] == -INFINITY && top[1] != -INFINITY);
+                if (__any_sync(0xffffffffu, up0 || up1)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float mn = fmaxf(mx[x], top[x]);
+                        const float alpha = mx[x] == -INFINITY ? 0.0f : fast_exp2(mx[x] - mn);
+                        mx[x] = mn;
+                        l[x] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < KS; ++j) {
+                            o[j][x] *= alpha;
+                            o[j][2 + x] *= alpha;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float pr[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        pr[x] = fast_exp2(sc[2 * y + x] - (mx[x] == -INFINITY ? 0.0f : mx[x]));
+                        l[x] += pr[x];
+                    }
+                    pb[y] = fw_turn(pack_bf16x2(pr[0], pr[1]));             // row r, keys 8 y + 2 q, + 1
                 }
                 // ---- O^T += V^T P^T: keys k0 + 2 q, + 1 and + 8, + 9 in a thread
                 ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), phase, abort_flag));
@@ -302,9 +281,7 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
                         a[2] &= seen[1];
                         a[3] &= seen[1];
                     }
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        fw_mma(o[nb][j], a, pb[nb][0], pb[nb][1]);
+                    fw_mma(o[j], a, pb[0], pb[1]);
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -316,23 +293,21 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
             }
             // ---- join the warps: every warp's (m, l) and O to shared memory, then four columns of a row a thread
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int x = 0; x < 2; ++x) {
+                float z = l[x];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float z = l[nb][x];
+                for (int w2 = 4; w2 < 32; w2 <<= 1)
+                    z += __shfl_xor_sync(0xffffffffu, z, w2);
+                const int row = 2 * q + x;
+                if (r == 0)
+                    m->ml[warp][row] = make_float2(mx[x], z);
+                float *dst = red + (warp * kPxRows + row) * (D + 8) + r;
 #pragma unroll
-                    for (int w2 = 4; w2 < 32; w2 <<= 1)
-                        z += __shfl_xor_sync(0xffffffffu, z, w2);
-                    const int row = nb * 8 + 2 * q + x;
-                    if (r == 0)
-                        m->ml[warp][row] = make_float2(mx[nb][x], z);
-                    float *dst = red + (warp * 8 * NB + row) * (D + 8) + r;
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        dst[16 * j] = o[nb][j][x];
-                        dst[16 * j + 8] = o[nb][j][2 + x];
-                    }
+                for (int j = 0; j < KS; ++j) {
+                    dst[16 * j] = o[j][x];
+                    dst[16 * j + 8] = o[j][2 + x];
                 }
+            }
             if (named_bar_any(1, 32 * kFwWarps, !ok))
                 break;                                      // (all eight warps leave together)
             const bool all = s.t0 == 0 && s.t1 == s.nt, whole = all && !ck_kept(s);
@@ -352,7 +327,7 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
                         continue;                           // no visible key: whatever its O holds
                     const float w = fmaxf(fast_exp2(x.x - M), FLT_MIN);   // (more than 0: its O may be NaN)
                     L += w * x.y;
-                    const float4 v = *reinterpret_cast<const float4 *>(red + (k * 8 * NB + rho) * (D + 8) + 4 * c4);
+                    const float4 v = *reinterpret_cast<const float4 *>(red + (k * kPxRows + rho) * (D + 8) + 4 * c4);
                     acc[0] = fmaf(w, v.x, acc[0]);
                     acc[1] = fmaf(w, v.y, acc[1]);
                     acc[2] = fmaf(w, v.z, acc[2]);
@@ -367,7 +342,7 @@ __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, Pr
                     if (c4 == 0 && p.lse)
                         p.lse[orow] = (M + __log2f(L)) * 0.69314718055994531f;
                 } else {
-                    int64_t prow = (int64_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kShortRows + rho;
+                    int64_t prow = (int64_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kPxRows + rho;
                     float *part_o = p.few_o;
                     float2 *part_ml = p.few_ml;
                     if (all) {

@@ -17,9 +17,13 @@ namespace svp {
 
 constexpr int kPxMost = 1024;         // requests, and groups, of a call
 
-// One sequence of all pairs; one of the groups and one of the requests, each with blocks of its own in one kernel;
-// or a kernel for each (prefix_tc.cu says when).
-enum { kPxAll = 0, kPxBeside = 1, kPxGroups = 2, kPxRequests = 3 };
+// One sequence of all pairs, or one of the groups and one of the requests, each with blocks of its own (prefix_tc.cu
+// says when).
+enum { kPxAll = 0, kPxBeside = 1 };
+// Rows of a KV head up to which requests have blocks of their own.  One block of 8 in warp-level products; with 16 rows
+// they took 136 us where the tile kernel's pairs take 126 (64 requests of 4 tokens behind 16384, bf16; 8-bit
+// 209 and 187).
+constexpr int kPxRows = 8;
 
 // What the joining kernel needs of a request, and of its group, written by the first CTA of the kernel that has the pairs.
 struct PrefixRec {
@@ -184,7 +188,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
 {
     PrefixSums &x = *static_cast<PrefixSums *>(smem);
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, OB = p.own_NT * p.own_R, n = p.n, ng = p.ng;
-    const bool tells = blockIdx.x == 0, has_groups = p.part != kPxRequests, has_requests = p.part != kPxGroups;
+    const bool tells = blockIdx.x == 0;
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     if (tid == 0)
         x.broken = x.groups_broken = 0;
@@ -255,9 +259,9 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
     }
     __syncthreads();
     // the groups and the requests in one sequence of sums; the requests' places follow when the number of groups is known
-    const int32_t from = has_groups ? 0 : ng, to = ng + (has_requests ? n : 0);
+    const int32_t to = ng + n;
     PrefixScan run{0, 0};
-    for (int32_t e0 = from; e0 < to; e0 += nt) {
+    for (int32_t e0 = 0; e0 < to; e0 += nt) {
         const int32_t e = e0 + tid;
         int64_t cost = 0;
         int4 what = make_int4(0, 0, 0, 0);
@@ -298,18 +302,15 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 p.rec[i] = PrefixRec{what.x, what.y, what.z, what.w, before};
         }
     }
-    const int32_t first = run.count, length = first + (has_requests ? n : 0);
+    const int32_t length = run.count + n;
     if (tid == 0)
         x.prefix[2 * kPxMost] = run.running;
     __syncthreads();
-    // (the sums of kPxBeside: of both, and of the groups)
     if (tells && tid == 0) {
-        if (has_groups)
-            p.total[0] = run.running;
-        if (has_requests)
-            p.total[1] = p.part == kPxBeside ? x.prefix[kPxMost] : run.running;
+        p.total[0] = run.running;
+        p.total[1] = x.prefix[kPxMost];                   // (of the groups)
     }
-    if (tells && has_groups)
+    if (tells)
         for (int32_t i = tid; i < n; i += nt) {
             const int32_t g = grouped ? group_of(i) : -1;
             PrefixGroup gr{0, 0, 0};
@@ -378,8 +379,8 @@ __device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, in
 {
     s.plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     s.ne = length;
-    s.ng = p.part == kPxGroups ? length : p.part == kPxRequests ? 0 : length - p.n;
-    s.R = p.part == kPxRequests ? p.own_R : p.R;
+    s.ng = length - p.n;
+    s.R = p.R;
 }
 
 // kPxBeside: of `ctas` blocks, those that the groups have; the others have the requests.  all: cost of both, groups: of

@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
         os = ck_shares(total[0] - total[1], ctas - split);
         obase = total[1];
     } else {
-        gs = ck_shares(total[0], ctas);
-        os = ck_shares(total[1], ctas);
+        gs = os = ck_shares(total[0], ctas);
     }
     for (int32_t i = tid; i < p.n; i += kPxThreads)
         if (__ldg(p.cu + i) <= row && row < __ldg(p.cu + i + 1))
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
         const PxPieces &y = mine ? own : grp;
         q -= mine ? grp.np : 0;
         int64_t x = y.np == 1 ? px_place(p, !mine, row, head)
-                              : (int64_t)(q == 0 ? 2 * y.first + 1 : 2 * (y.first + q)) * (mine && w.few ? kShortRows : kPartRows) + y.pr;
+                              : (int64_t)(q == 0 ? 2 * y.first + 1 : 2 * (y.first + q)) * (mine && w.few ? kPxRows : kPartRows) + y.pr;
         ml = (y.np == 1 ? p.place_ml : mine ? w.ml : p.part_ml) + x;
         o = (y.np == 1 ? p.place_o : mine ? w.o : p.part_o) + x * D + lane * 4;
     };
@@ -215,20 +214,17 @@ bool chunk_maps(ChunkParams &p, const void *q, int64_t q_stride, svp_dtype kv, i
                 bool few);
 template <int D, bool Q8>
 bool chunk_layout(ChunkParams &p, int32_t rows, int &smem);
-svp_status chunk_short_prefix_run(ChunkParams &p, int32_t d, cudaStream_t stream);
-
-constexpr int kPxFewPairs = 300;      // requests times KV heads, 8-bit pages
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct PrefixWs {
-    size_t total, rec, grp, plan, ml, ml2, ml3, o, o2, o3, bytes;   // 2: of the kernel for few rows; 3: the rows' places
+    size_t total, rec, grp, plan, ml, ml2, ml3, o, o2, o3, bytes;   // 2: of the blocks for few rows; 3: the rows' places
 };
 
 static PrefixWs prefix_ws(int32_t hq, int32_t d, int32_t m_cap)
 {
     // partial results: two pieces a CTA, and those of whole pairs of groups and of requests behind them
-    const size_t g = (size_t)chunk_ctas(), one = 2 * g * (d == 256 ? 128 : 256), two = 2 * g * kShortRows,
+    const size_t g = (size_t)chunk_ctas(), one = 2 * g * (d == 256 ? 128 : 256), two = 2 * g * kPxRows,
                  three = 2 * (size_t)m_cap * hq, row = (size_t)d * sizeof(float);
     PrefixWs w;
     w.total = kWsHeader;
@@ -245,11 +241,10 @@ static PrefixWs prefix_ws(int32_t hq, int32_t d, int32_t m_cap)
     return w;
 }
 
-// Requests of at most kShortRows rows a KV head, d <= 128: over bf16 pages blocks of their own in the one kernel; over 8-bit
-// ones chunk_short.cu's kernel, from so many pairs on that a third launch costs less than the tile kernel's pairs.
-static bool few_rows(const ChunkParams &p, int32_t d) { return d <= 128 && (int64_t)p.G * p.w <= kShortRows; }
+// Requests of at most kPxRows rows a KV head, d <= 128, have blocks of their own.
+static bool few_rows(const ChunkParams &p, int32_t d) { return d <= 128 && (int64_t)p.G * p.w <= kPxRows; }
 
-template <int D, bool Q8, int kFew>
+template <int D, bool Q8, bool kFew>
 static svp_status prefix_tiles(const ChunkParams &p, int smem, cudaStream_t stream)
 {
     static std::atomic<uint64_t> configured{0};
@@ -261,22 +256,30 @@ static svp_status prefix_tiles(const ChunkParams &p, int smem, cudaStream_t stre
                : SVP_ECUDA;
 }
 
-// The layout of few_body's shared memory, below the tile kernel's barriers, which are moved to the end.
-template <int D, int NB>
+// Shared memory of the blocks for few rows, below the tile kernel's barriers, which are moved to the end.
+template <int D, bool Q8>
 static bool few_layout(ChunkParams &p, int &smem)
 {
-    using Cfg = FewCfg<D, NB>;
     const int misc = smem - p.off_misc;
     smem = 227 * 1024;
     p.off_misc = (smem - misc) / 128 * 128;
-    p.few_ring = (Cfg::kRed + 1023) / 1024 * 1024;
-    p.few_slots = std::min(kFwSlots, (p.off_misc - p.few_ring - (int)sizeof(FewMisc)) / Cfg::kSlot) / 2 * 2;
-    p.few_misc = p.few_ring + p.few_slots * Cfg::kSlot;
+    if constexpr (Q8) {
+        using Cfg = ShortCfg<D, 1>;
+        p.few_ring = (Cfg::kRed + 1023) / 1024 * 1024;
+        p.few_slots = std::min(kShSlots, (p.off_misc - p.few_ring - (int)sizeof(ShortMisc)) / (Cfg::kRaw + 512)) / 2 * 2;
+        p.few_raw = p.few_ring + p.few_slots * Cfg::kRaw;
+        p.few_misc = p.few_raw + p.few_slots * 512;
+    } else {
+        using Cfg = FewCfg<D>;
+        p.few_ring = (Cfg::kRed + 1023) / 1024 * 1024;
+        p.few_slots = std::min(kFwSlots, (p.off_misc - p.few_ring - (int)sizeof(FewMisc)) / Cfg::kSlot) / 2 * 2;
+        p.few_misc = p.few_ring + p.few_slots * Cfg::kSlot;
+    }
     return p.few_slots >= 4;
 }
 
 template <int D, bool Q8>
-static svp_status prefix_run(ChunkParams &p, ChunkParams &few, cudaStream_t stream)
+static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
 {
     using Cfg = ChunkCfg<D, Q8>;
     int smem = 0;
@@ -288,33 +291,21 @@ static svp_status prefix_run(ChunkParams &p, ChunkParams &few, cudaStream_t stre
         return SVP_EUNSUPPORTED;
     PxOwn own{0, p.R, p.part_ml, p.part_o};
     svp_status st;
-    if (few_rows(p, D) && (!Q8 || (int64_t)p.n * p.c.hkv >= kPxFewPairs)) {
-        // (a pair for few rows is a request's KV head: w tokens are one block)
-        p.own_NT = few.own_NT = 1;
-        p.own_R = few.own_R = p.w;
-        own = PxOwn{1, p.w, p.few_ml, p.few_o};
-        if constexpr (Q8) {
-            p.part = kPxGroups;
-            st = prefix_tiles<D, true, 0>(p, smem, stream);
-            if (st != SVP_OK)
-                return st;
-            few.share_rows = p.share_rows;
-            few.part = kPxRequests;
-            few.R = p.w;
-            few.part_ml = p.few_ml;
-            few.part_o = p.few_o;
-            st = chunk_short_prefix_run(few, D, stream);
-        } else if constexpr (D <= 128) {
+    if (few_rows(p, D)) {
+        if constexpr (D <= 128) {
+            // (a pair is a request's KV head: w tokens are one block)
             p.part = kPxBeside;
-            const bool one = p.G * p.w <= 8;              // rows of one block of 8
-            if (!(one ? few_layout<D, 1>(p, smem) : few_layout<D, 2>(p, smem)))
+            p.own_NT = 1;
+            p.own_R = p.w;
+            own = PxOwn{1, p.w, p.few_ml, p.few_o};
+            if (!few_layout<D, Q8>(p, smem))
                 return SVP_EUNSUPPORTED;
-            st = one ? prefix_tiles<D, false, 1>(p, smem, stream) : prefix_tiles<D, false, 2>(p, smem, stream);
+            st = prefix_tiles<D, Q8, true>(p, smem, stream);
         } else {
             return SVP_EUNSUPPORTED;                      // (never: few rows are d <= 128)
         }
     } else {
-        st = prefix_tiles<D, Q8, 0>(p, smem, stream);
+        st = prefix_tiles<D, Q8, false>(p, smem, stream);
     }
     if (st != SVP_OK)
         return st;
@@ -413,21 +404,26 @@ svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache 
         return SVP_EUNSUPPORTED;
     p.few_ml = reinterpret_cast<float2 *>(b + o.ml2);
     p.few_o = reinterpret_cast<float *>(b + o.o2);
-    ChunkParams few = p;                  // (for chunk_short.cu: other swizzles)
-    if (cache->dtype == SVP_E4M3 && few_rows(p, d) && !chunk_maps(few, q, q_row_stride, cache->dtype, m_cap, d, 1, true))
-        return SVP_EUNSUPPORTED;
+    if (cache->dtype == SVP_E4M3 && few_rows(p, d)) {
+        // (the pages once more, with the swizzle of chunk_short.cuh)
+        ChunkParams few = p;
+        if (!chunk_maps(few, q, q_row_stride, cache->dtype, m_cap, d, 1, true))
+            return SVP_EUNSUPPORTED;
+        p.few_k = few.tm_k;
+        p.few_v = few.tm_v;
+    }
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->dtype == SVP_E4M3) {
         switch (d) {
-        case 64: return prefix_run<64, true>(p, few, s);
-        case 128: return prefix_run<128, true>(p, few, s);
-        default: return prefix_run<256, true>(p, few, s);
+        case 64: return prefix_run<64, true>(p, s);
+        case 128: return prefix_run<128, true>(p, s);
+        default: return prefix_run<256, true>(p, s);
         }
     }
     switch (d) {
-    case 64: return prefix_run<64, false>(p, few, s);
-    case 128: return prefix_run<128, false>(p, few, s);
-    default: return prefix_run<256, false>(p, few, s);
+    case 64: return prefix_run<64, false>(p, s);
+    case 128: return prefix_run<128, false>(p, s);
+    default: return prefix_run<256, false>(p, s);
     }
 }
 
