@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     // kFew: of this block's kind, the groups' (the first blocks) or the requests'
     const int32_t split = [&]() -> int32_t {
         if constexpr (kFew)
-            return px_split(px_total(sums, pairs), sums.prefix[kPxMost], (int32_t)gridDim.x);
+            return px_split(px_total(sums, pairs), sums.prefix[kPxMost], (int64_t)sums.longs, (int32_t)gridDim.x, Q8);
         else
             return 0;
     }();

@@ -134,6 +134,7 @@ struct PrefixSums {
     int32_t lead[kPxMost];            // its first request with rows
     int32_t shared[kPxMost];          // tokens that it shares, 0: none
     int32_t gbase[kPxMost];           // its place in the sequence
+    unsigned long long longs;         // cost of the groups with two query tiles a block
     int32_t broken, groups_broken;
     int32_t cnt[32];
     int64_t tot[32];
@@ -190,8 +191,10 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, OB = p.own_NT * p.own_R, n = p.n, ng = p.ng;
     const bool tells = blockIdx.x == 0;
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
-    if (tid == 0)
+    if (tid == 0) {
         x.broken = x.groups_broken = 0;
+        x.longs = 0;
+    }
     // everything that is read, in one round trip
     for (int32_t i = tid; i <= n; i += nt) {
         x.cu[i] = __ldg(p.cu + i);
@@ -272,6 +275,8 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 if (one) {
                     what = make_int4(x.cu[x.gcu[e]], x.cu[x.gcu[e + 1]] - x.cu[x.gcu[e]], x.shared[e], x.lead[e]);
                     cost = px_head_keys(what.z, what.y, B) * ck_weight<NT>(what.y, p.R) * p.c.hkv;
+                    if (ck_weight<NT>(what.y, p.R) == kLongCost)
+                        atomicAdd(&x.longs, (unsigned long long)cost);
                 }
             } else {
                 const int32_t i = e - ng, off = x.cu[i], k = x.cu[i + 1] - off, L = x.ctx[i];
@@ -309,6 +314,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
     if (tells && tid == 0) {
         p.total[0] = run.running;
         p.total[1] = x.prefix[kPxMost];                   // (of the groups)
+        p.total[2] = (int64_t)x.longs;
     }
     if (tells)
         for (int32_t i = tid; i < n; i += nt) {
@@ -384,13 +390,15 @@ __device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, in
 }
 
 // kPxBeside: of `ctas` blocks, those that the groups have; the others have the requests.  all: cost of both, groups: of
-// the groups, which come first in the sums.  A unit of the requests' cost takes 0.66 to 0.9 times one of the groups'
-// (64 tokens, prefixes of 16384 and 4 x 20480, 0 to 1024 of their own): three quarters.
-__device__ __forceinline__ int32_t px_split(int64_t all, int64_t groups, int32_t ctas)
+// the groups, which come first in the sums, longs: of those with two query tiles a block.  In ns a unit, 64 tokens
+// behind prefixes of 16384 (two tiles) and 4 x 20480 (one), with 0 to 1024 of their own: over bf16 pages two tiles 4.0 to
+// 4.6, one 3.5, requests 2.8 to 3.1; over 8-bit ones, where tiles are widened for the groups, two 5.4 to 6.3, one 3.9,
+// requests 2.5 to 3.7.  So two tiles count 5 / 4 (8-bit 3 / 2), and requests 14 / 16 (12 / 16).
+__device__ __forceinline__ int32_t px_split(int64_t all, int64_t groups, int64_t longs, int32_t ctas, bool q8)
 {
     if (groups == 0 || groups == all)
         return groups == 0 ? 0 : ctas;
-    const int64_t a = 4 * groups, b = a + 3 * (all - groups);
+    const int64_t a = 16 * groups + (q8 ? 8 : 4) * longs, b = a + (q8 ? 12 : 14) * (all - groups);
     return max(1, min(ctas - 1, (int32_t)((a * ctas + b / 2) / b)));
 }
 

@@ -40,7 +40,7 @@ __device__ __forceinline__ PxPieces px_pieces(const ChunkParams &p, const ChunkS
 
 // Where the requests' pieces are: among the groups', or those of blocks or a kernel for few rows.
 struct PxOwn {
-    int32_t few, R;                   // tokens of its query tile
+    int32_t few, R, q8;               // tokens of its query tile; pages are 8-bit
     const float2 *ml;
     const float *o;
 };
@@ -65,11 +65,11 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (tid == 0)
         owner = -1;
     __syncthreads();
-    const int64_t total[2] = {__ldcg(p.total), __ldcg(p.total + 1)};
+    const int64_t total[3] = {__ldcg(p.total), __ldcg(p.total + 1), __ldcg(p.total + 2)};
     ChunkShares gs, os;                                   // the groups' and the requests'
     int64_t obase = 0;                                    // cost before the first request
     if (p.part == kPxBeside) {
-        const int32_t split = px_split(total[0], total[1], ctas);
+        const int32_t split = px_split(total[0], total[1], total[2], ctas, w.q8 != 0);
         gs = ck_shares(total[1], split);
         os = ck_shares(total[0] - total[1], ctas - split);
         obase = total[1];
@@ -289,7 +289,7 @@ static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
     p.part = kPxAll;
     if (!chunk_layout<D, Q8>(p, p.m_cap, smem) || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
         return SVP_EUNSUPPORTED;
-    PxOwn own{0, p.R, p.part_ml, p.part_o};
+    PxOwn own{0, p.R, 0, p.part_ml, p.part_o};
     svp_status st;
     if (few_rows(p, D)) {
         if constexpr (D <= 128) {
@@ -297,7 +297,7 @@ static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
             p.part = kPxBeside;
             p.own_NT = 1;
             p.own_R = p.w;
-            own = PxOwn{1, p.w, p.few_ml, p.few_o};
+            own = PxOwn{1, p.w, Q8, p.few_ml, p.few_o};
             if (!few_layout<D, Q8>(p, smem))
                 return SVP_EUNSUPPORTED;
             st = prefix_tiles<D, Q8, true>(p, smem, stream);
