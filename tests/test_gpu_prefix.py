@@ -7,28 +7,63 @@ import pytest
 import torch
 
 import speculative_decoding_verification_packed_gb300 as svp
-from test_gpu_cache import BF16, E4M3, F32, Pool, attend_exact, i32, pack_rows, packed, picked_rows
+from test_gpu_cache import BF16, E4M3, F32, Pool, i32, pack_rows, packed, picked_rows
 
 pytestmark = pytest.mark.gpu
 
 
-class Shared(Pool):
-    """A pool whose groups (first request, end, tokens) have their first whole pages in common: the first request's
-    that has rows.  The pages that they would have had themselves are NaN."""
+def attend_exact(pool, q, rows, ctx, scale, picks=None):
+    """test_gpu_cache.attend_exact (the same values and bounds), all heads of a row at once."""
+    hq, d = q.shape[1:]
+    G = hq // pool.hkv
+    half = 2.0 ** -24 if pool.kind == F32 else 2.0 ** -8
+    o, lse, tol, ltol = [], [], [], []
+    q = q.double().cpu().numpy()
+    first = 0
+    for i, r in enumerate(rows):
+        take = range(r) if picks is None else sorted({j for j in picks if j < r} | {r - 1} if r else set())
+        if len(take):
+            K, V = (np.ascontiguousarray(pool.rows(w, i, 0, ctx[i] + r).transpose(1, 0, 2)) for w in range(2))   # [hkv, T, d]
+        for j in take:
+            T = ctx[i] + j + 1
+            k, v = K[:, :T], V[:, :T]
+            x = q[first + j].reshape(pool.hkv, G, d)
+            s = x @ k.transpose(0, 2, 1) * scale                                                                 # [hkv, G, T]
+            ds = (d + 2) * 2.0 ** -23 * (np.abs(x) @ np.abs(k).transpose(0, 2, 1)).max(-1, keepdims=True) * scale
+            top = s.max(-1, keepdims=True)
+            p = np.exp(s - top)
+            l = p.sum(-1, keepdims=True)
+            y, A = p @ v / l, p @ np.abs(v) / l
+            rel = (0 if pool.kind == F32 else half) + 2 * ds + (T / 32 + 64) * 2.0 ** -23
+            o.append(y)
+            tol.append(rel * A + half * np.abs(y) + 1e-30)
+            lse.append(top + np.log(l))
+            ltol.append(ds + (T / 32 + 64) * 2.0 ** -23 + np.abs(lse[-1]) * 2.0 ** -22)
+        first += r
+    return (np.array(o).reshape(-1, hq, d), np.array(lse).reshape(-1, hq), np.array(tol).reshape(-1, hq, d),
+            np.array(ltol).reshape(-1, hq))
 
-    def __init__(self, rows, ctx, groups, *args, **kw):
-        super().__init__(len(rows), [a + b if a else 0 for a, b in zip(rows, ctx)], *args, **kw)
+
+class Shared(Pool):
+    """A pool whose groups (first request, end, tokens) have their first whole pages in common: the pages of the first
+    request that has rows; the others have pages of their own for the rest only."""
+
+    def __init__(self, rows, ctx, groups, hkv, d, page, *args, **kw):
+        n = len(rows)
+        total = [a + b if a else 0 for a, b in zip(rows, ctx)]
+        lead, common = list(range(n)), [0] * n
         for lo, hi, tokens in groups:
             live = [i for i in range(lo, hi) if rows[i]]
-            k = max(tokens, 0) // self.page
             for i in live[1:]:
-                for page in self.table[i, :k].tolist():
-                    for which in range(2):
-                        self.raw[which][page] = 0x7f if self.kind == E4M3 else float("nan")
-                        self.vals[which][page] = np.nan
-                        if self.kind == E4M3:
-                            self.exps[which][page] = 255
-                self.table[i, :k] = self.table[live[0], :k]
+                lead[i], common[i] = live[0], max(tokens, 0) // page
+        super().__init__(n, [t - c * page for t, c in zip(total, common)], hkv, d, page, *args, **kw)
+        own = self.table
+        self.table = torch.full((n, max([-(-t // page) for t in total] + [1])), -1, dtype=torch.int32)
+        for i in range(n):
+            k = -(-total[i] // page) - common[i]
+            self.table[i, :common[i]] = own[lead[i], :common[i]]
+            self.table[i, common[i]:common[i] + k] = own[i, :k]
+        self.lens = total
 
 
 def group_tensors(groups, n):
