@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     Sums &sums = *reinterpret_cast<Sums *>(smem + p.off_ring);
     int32_t pairs = p.n;
     if constexpr (kShared)
-        pairs = px_prologue<NT>(p, smem + p.off_ring);
+        pairs = px_prologue<NT>(p, smem + p.off_ring, kFew ? kPxBeside : kPxAll, Q8);
     else
         ck_prologue<NT>(p, sums, m->warp_tot);
     tc_fence_before();
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, Q8>::kThreads, 1) chunk_tc_kernel(
     const int64_t v0 = min(shares.total, cta * shares.share), v1 = min(shares.total, (cta + 1) * shares.share);
     Piece s;
     if constexpr (kShared)
-        px_bind(p, s, pairs);
+        px_bind(p, sums, s, pairs, kFew ? kPxBeside : kPxAll, Q8);
     if constexpr (kFew) {
         const int64_t groups = sums.prefix[kPxMost];
         if (few) {

@@ -64,7 +64,7 @@ struct ChunkParams {
     int4 *plan;                       // [grid][2 * kPxMost]
     struct PrefixRec *rec;            // [n]
     struct PrefixGroup *grp;          // [n]
-    int64_t *total;                   // costs of all pairs, of the groups', of those of two tiles
+    int64_t *total;                   // costs of all pairs, of the groups', of those of two tiles; whether there are any
     float2 *place_ml;                 // [2][m_cap][hq]: parts of rows that one piece has all of
     float *place_o;                   // [2][m_cap][hq][d]
 };

@@ -35,12 +35,28 @@ struct PrefixGroup {
     int64_t base;
 };
 
+// Costs of a key: a request's pair of one query tile, and a pair of two.  In the tile kernel a request's few tiles of its
+// own take longer than those of a long stream (64 requests of 8 rows, 64 to 2048 own tokens: 2.2 us each, where a group's
+// take 1.4, or 1.9 for two query tiles).  64 requests of 4 and of 8 rows behind 16384, us with 3 : 4, 4 : 5 and 4 : 4: bf16
+// 126 and 188, 118 and 180, 118 and 193; 8-bit 183 and 266, 174 and 259, 160 and 257.  Where nothing is shared the costs,
+// and so the pieces, are svp_chunk_attn's.
+struct PxCosts {
+    int32_t one, two;
+};
+
+__device__ __forceinline__ PxCosts px_costs(int32_t part, bool shared, bool q8)
+{
+    static_assert(kShortCost == 3 && kLongCost == 4, "px_tile_at");
+    return part == kPxAll && shared ? PxCosts{4, q8 ? 4 : 5} : PxCosts{kShortCost, kLongCost};
+}
+
 struct PrefixPiece : ChunkPiece {     // i: place in the sequence of groups and requests
     int32_t ne, ng;                   // length of the sequence, and groups in it
     const int4 *plan;                 // this CTA's copy: (first row, rows, P, row of the block table), then (first
                                       // row, rows, tokens behind P, P)
     int32_t row, first;               // row of the block table, and the first key's position
     int32_t R;                        // tokens of a query tile
+    PxCosts cost;
     bool group;
 };
 
@@ -54,9 +70,18 @@ __device__ __forceinline__ int32_t ck_last(const PrefixPiece &s, int32_t tok)
 }
 __device__ __forceinline__ bool ck_kept(const PrefixPiece &s) { return s.group || s.first > 0; }
 
-__device__ __forceinline__ int32_t px_weight(int32_t nt, int32_t k, int32_t R)
+__device__ __forceinline__ int32_t px_weight(int32_t nt, int32_t one, int32_t two, int32_t k, int32_t R)   // nt query tiles a block
 {
-    return nt == 2 ? ck_weight<2>(k, R) : ck_weight<1>(k, R);
+    return nt == 2 && k > R ? two : one;
+}
+
+__device__ __forceinline__ int32_t px_tile_at(int64_t x, int32_t wt)   // ck_tile_at for the costs 3, 4 and 5
+{
+    const int64_t s = (int64_t)kStartKeys * wt;
+    if (x <= s)
+        return 0;
+    const uint32_t y = (uint32_t)((x - s - 1) / kCkKeys);
+    return (int32_t)(wt == 3 ? y / 3u : wt == 4 ? y / 4u : y / 5u) + 1;
 }
 
 // Keys of one KV head of a group of k rows, B a block: each block sees all L.
@@ -76,7 +101,7 @@ __device__ __forceinline__ bool ck_set(const ChunkParams &p, PrefixPiece &s, int
     s.t0 = t0;
     const int32_t wt = s.wt;
     const int64_t y = v1 - s.base;
-    s.t1 = y >= (int64_t)wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, ck_tile_at(y, wt));
+    s.t1 = y >= (int64_t)wt * (kStartKeys + (int64_t)s.len) ? s.nt : min(s.nt, px_tile_at(y, wt));
     return s.t0 < s.t1;
 }
 
@@ -93,7 +118,7 @@ __device__ __forceinline__ bool px_entry(const ChunkParams &p, PrefixPiece &s, c
     if (s.k <= 0)
         return false;
     s.nb = (s.k + B - 1) / B;
-    s.wt = ck_weight<NT>(s.k, s.R);
+    s.wt = px_weight(NT, s.group ? kShortCost : s.cost.one, s.cost.two, s.k, s.R);
     return true;
 }
 
@@ -135,7 +160,7 @@ struct PrefixSums {
     int32_t shared[kPxMost];          // tokens that it shares, 0: none
     int32_t gbase[kPxMost];           // its place in the sequence
     unsigned long long longs;         // cost of the groups with two query tiles a block
-    int32_t broken, groups_broken;
+    int32_t broken, groups_broken, any_shared;
     int32_t cnt[32];
     int64_t tot[32];
 };
@@ -185,14 +210,14 @@ __device__ __forceinline__ void px_scan(PrefixSums &x, PrefixScan &run, int64_t 
 // Cost before each of the sequence's groups and requests into x->prefix, their places and sizes into x->plan and this
 // CTA's copy, and (first CTA) what the joining kernel needs.  Returns the sequence's length.
 template <int NT>
-__device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
+__device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem, int32_t part, bool q8)
 {
     PrefixSums &x = *static_cast<PrefixSums *>(smem);
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = NT * p.R, OB = p.own_NT * p.own_R, n = p.n, ng = p.ng;
     const bool tells = blockIdx.x == 0;
     int4 *plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     if (tid == 0) {
-        x.broken = x.groups_broken = 0;
+        x.broken = x.groups_broken = x.any_shared = 0;
         x.longs = 0;
     }
     // everything that is read, in one round trip
@@ -259,8 +284,11 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 P = x.len[g] >> p.c.page_shift << p.c.page_shift;
         }
         x.shared[g] = P;
+        if (P > 0)
+            x.any_shared = 1;
     }
     __syncthreads();
+    const PxCosts cs = px_costs(part, x.any_shared != 0, q8);
     // the groups and the requests in one sequence of sums; the requests' places follow when the number of groups is known
     const int32_t to = ng + n;
     PrefixScan run{0, 0};
@@ -274,8 +302,8 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 one = x.shared[e] > 0;                    // (else its bounds may be anything)
                 if (one) {
                     what = make_int4(x.cu[x.gcu[e]], x.cu[x.gcu[e + 1]] - x.cu[x.gcu[e]], x.shared[e], x.lead[e]);
-                    cost = px_head_keys(what.z, what.y, B) * ck_weight<NT>(what.y, p.R) * p.c.hkv;
-                    if (ck_weight<NT>(what.y, p.R) == kLongCost)
+                    cost = px_head_keys(what.z, what.y, B) * px_weight(NT, kShortCost, cs.two, what.y, p.R) * p.c.hkv;
+                    if (NT == 2 && what.y > p.R)
                         atomicAdd(&x.longs, (unsigned long long)cost);
                 }
             } else {
@@ -283,7 +311,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
                 if (k > 0 && !ck_bad(p, off, x.cu[i + 1], L)) {
                     const int32_t g = grouped ? group_of(i) : -1, P = g >= 0 ? x.shared[g] : 0;
                     what = make_int4(off, k, L - P, P);
-                    cost = ck_head_keys(what.z, k, OB) * px_weight(p.own_NT, k, p.own_R) * p.c.hkv;
+                    cost = ck_head_keys(what.z, k, OB) * px_weight(p.own_NT, cs.one, cs.two, k, p.own_R) * p.c.hkv;
                 }
             }
         }
@@ -315,6 +343,7 @@ __device__ __forceinline__ int32_t px_prologue(const ChunkParams &p, void *smem)
         p.total[0] = run.running;
         p.total[1] = x.prefix[kPxMost];                   // (of the groups)
         p.total[2] = (int64_t)x.longs;
+        p.total[3] = x.any_shared;
     }
     if (tells)
         for (int32_t i = tid; i < n; i += nt) {
@@ -376,13 +405,14 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const PrefixSums 
         --b;
     s.b = (int32_t)b;
     s.base = start + s.g * H + ck_before(a, slope, b) * wt;
-    const int32_t t0 = ck_tile_at(v0 - s.base, wt);
+    const int32_t t0 = px_tile_at(v0 - s.base, wt);
     const bool have = ck_set<NT>(p, s, v1, t0);
     return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
 }
 
-__device__ __forceinline__ void px_bind(const ChunkParams &p, PrefixPiece &s, int32_t length)
+__device__ __forceinline__ void px_bind(const ChunkParams &p, const PrefixSums &x, PrefixPiece &s, int32_t length, int32_t part, bool q8)
 {
+    s.cost = px_costs(part, x.any_shared != 0, q8);
     s.plan = p.plan + (int64_t)blockIdx.x * 2 * kPxMost;
     s.ne = length;
     s.ng = length - p.n;

@@ -21,12 +21,13 @@ struct PxPieces {
     int32_t first, np, pr;            // pr: the row in a CTA's partial results
 };
 
-// tok: the row among its group's, or its request's; R tokens a query tile, NT of them a block.
+// tok: the row among its group's, or its request's; R tokens a query tile, NT of them a block; one, two: costs of
+// a key of a pair of one tile, of two.
 template <int NT>
 __device__ __forceinline__ PxPieces px_pieces(const ChunkParams &p, const ChunkShares &x, bool group, int64_t base, int32_t k,
-                                              int32_t L, int32_t tok, int32_t g, int32_t h, int32_t R)
+                                              int32_t L, int32_t tok, int32_t g, int32_t h, int32_t R, int32_t one, int32_t two)
 {
-    const int32_t B = NT * R, b = tok / B, t = tok - b * B, wt = ck_weight<NT>(k, R);
+    const int32_t B = NT * R, b = tok / B, t = tok - b * B, wt = px_weight(NT, one, two, k, R);
     const int64_t H = group ? px_head_keys(L, k, B) : ck_head_keys(L, k, B);
     base += wt * (g * H + ck_before((int64_t)kStartKeys + L, group ? 0 : B, b));
     const int32_t len = group ? L : L + b * B + min(B, k - b * B), nt = (len + kCkKeys - 1) / kCkKeys;
@@ -65,7 +66,8 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (tid == 0)
         owner = -1;
     __syncthreads();
-    const int64_t total[3] = {__ldcg(p.total), __ldcg(p.total + 1), __ldcg(p.total + 2)};
+    const int64_t total[4] = {__ldcg(p.total), __ldcg(p.total + 1), __ldcg(p.total + 2), __ldcg(p.total + 3)};
+    const PxCosts cs = px_costs(p.part, total[3] != 0, w.q8 != 0);
     ChunkShares gs, os;                                   // the groups' and the requests'
     int64_t obase = 0;                                    // cost before the first request
     if (p.part == kPxBeside) {
@@ -88,13 +90,13 @@ __global__ void __launch_bounds__(kPxThreads) prefix_join_kernel(const __grid_co
     if (r.k <= 0 || head >= p.hq)
         return;
     const int32_t g = head / p.G, h = head - g * p.G;
-    const PxPieces own = w.few ? px_pieces<1>(p, os, false, r.base - obase, r.k, r.L, row - r.off, g, h, w.R)
-                               : px_pieces<NT>(p, os, false, r.base, r.k, r.L, row - r.off, g, h, w.R);
+    const PxPieces own = w.few ? px_pieces<1>(p, os, false, r.base - obase, r.k, r.L, row - r.off, g, h, w.R, cs.one, cs.two)
+                               : px_pieces<NT>(p, os, false, r.base, r.k, r.L, row - r.off, g, h, w.R, cs.one, cs.two);
     if (r.P == 0 && own.np == 1)
         return;                                           // (the output has it already)
     PxPieces grp{0, 0, 0};
     if (r.P > 0)
-        grp = px_pieces<NT>(p, gs, true, gr.base, gr.k, r.P, row - gr.off, g, h, p.R);
+        grp = px_pieces<NT>(p, gs, true, gr.base, gr.k, r.P, row - gr.off, g, h, p.R, kShortCost, cs.two);
     const int32_t np = grp.np + own.np;
     auto at = [&](int32_t q, const float2 *&ml, const float *&o) {
         const bool mine = q >= grp.np;
@@ -289,7 +291,7 @@ static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
     p.part = kPxAll;
     if (!chunk_layout<D, Q8>(p, p.m_cap, smem) || p.nslot * Cfg::kSlot < (int)sizeof(PrefixSums))
         return SVP_EUNSUPPORTED;
-    PxOwn own{0, p.R, 0, p.part_ml, p.part_o};
+    PxOwn own{0, p.R, Q8, p.part_ml, p.part_o};
     svp_status st;
     if (few_rows(p, D)) {
         if constexpr (D <= 128) {
