@@ -42,8 +42,9 @@
  *   - Kernels never trap.  Every wait inside a kernel is bounded; on expiry the kernel
  *     sets SVP_DEV_TIMEOUT in the status word and returns.
  *   - The DVL allocator, the row gathers, the verification attention, the margin /
- *     accept calls, the stochastic verifier's second pass, the cache's write and read
- *     and the chunk attention (unless the call may be a long one) are launched as
+ *     accept calls, the stochastic verifier's second pass, the cache's write and read,
+ *     the chunk attention (unless the call may be a long one), the rotary positions, the
+ *     pages' calls and the attention behind common pages are launched as
  *     programmatic dependents of the previous kernel on their stream: they may be
  *     scheduled while it finishes, but read nothing before it has completed, so the
  *     results are those of plain stream order (also inside a captured CUDA graph).

@@ -265,6 +265,48 @@ def test_compact_pools_of_any_size(num, share):
     dev.check()
 
 
+def test_pools_past_32_bits():
+    """Pages whose elements lie more than 2^31 into their pools: copied by a fork, written by rope_cache_write, moved by a
+    compaction, and read as a common beginning."""
+    pages_n, hkv, page, d = 70000, 8, 16, 256
+    pool = [torch.empty(pages_n, hkv, page, d, dtype=BF16, device="cuda") for _ in range(2)]
+    assert pool[0].numel() > 2 ** 31
+    refs = torch.ones(pages_n, dtype=torch.int32, device="cuda")        # others hold all but the pages at either end
+    refs[:8] = refs[-20:] = 0
+    table, used = torch.full((3, 8), -1, dtype=torch.int32, device="cuda"), i32([0, 0, 0])
+    refs[:8] = 1
+    p = svp.make_pages(table, used, refs, page_size=page)
+    cache = svp.make_cache(pool[0], pool[1], table)
+    svp.pages_resize(p, i32([40, 0, 0]))
+    first = pages_n - 20
+    assert table[0, :3].tolist() == [first, first + 1, first + 2]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(40, h, d, generator=g, device="cuda").to(BF16) for h in (16, hkv, hkv))
+    freq = svp.rope_frequencies(d)
+    cu, ctx = i32([0, 40, 40, 40]), i32([0, 0, 0])
+    qr, kr = svp.rope(q, k, ctx, cu, freq=freq)
+    assert torch.equal(svp.rope_cache_write(q, k, v, ctx, cu, cache=cache, freq=freq), qr)
+    svp.pages_fork(p, i32([0, 0]), i32([1, 2]), i32([40, 39]), caches=[cache])
+    assert table[1, :3].tolist() == [first, first + 1, first + 3] and table[2, :3].tolist() == [first, first + 1, first + 4]
+    for i, t in ((0, 40), (1, 40), (2, 39)):
+        at = i32([0] * (i + 1) + [t] * (3 - i))
+        a, b = svp.cache_read(None, at, cache=cache, rows=t)
+        assert torch.equal(a, kr[:t]) and torch.equal(b, v[:t])
+    # a token each, behind the two pages that they share
+    rows, one = i32([0, 1, 2, 3]), i32([39, 39, 38])
+    args = (qr[:3], one, rows)
+    out, lse = svp.prefix_attn(*args, i32([0, 3]), i32([32]), cache=cache, w=1)
+    want, wl = svp.chunk_attn(*args, cache=cache, w=1)
+    assert ((out.float() - want.float()).abs() <= 4 * 2.0 ** -8 * v.float().abs().max()).all()
+    assert ((lse - wl).abs() <= 2.0 ** -16 * (1 + wl.abs())).all()
+    refs[1:4] = 0                                                       # three others leave
+    live = i32([0])
+    svp.pages_compact(p, caches=[cache], live=live)
+    assert live.item() == 69980 + 5 - 3 and table[:, :3].max() < live.item() and p.ws.read_status() == 0
+    moved = svp.prefix_attn(*args, i32([0, 3]), i32([32]), cache=cache, w=1)
+    assert torch.equal(moved[0], out) and torch.equal(moved[1], lse)
+
+
 def test_many_requests_and_forks():
     n, cols, page = 1024, 9, 16
     m = Model(n, cols, page, 9000)
