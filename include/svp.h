@@ -612,8 +612,8 @@ svp_status svp_pages_workspace_size(const svp_pages *pages, size_t *bytes);
  * of requests and positions (refs 1).  Without enough free pages a request i is left as it was when what
  * requests 0 .. i ask for together is more than there are (SVP_DEV_NO_PAGES).
  * Left as they were too (SVP_DEV_BAD_CONTEXT): a request with used[i] outside 0 .. max_pages, a length
- * past max_pages * page_size, and one that would keep part of a page that another holds as well (refs > 1
- * before the call), as its next write would go there: give it a whole page less, or fork it instead.
+ * past max_pages * page_size, and one that would end in a part of a page of its own that another holds as well
+ * (refs > 1 before the call), as its next write would go there: give it a whole page less, or fork it instead.
  * An entry that names no page of the pool, or one whose refs is 0 already, is given back as -1 without
  * counting (SVP_DEV_BAD_CONTEXT).
  * ws     at least svp_pages_workspace_size bytes, its first 256 zeroed once by svp_workspace_init
@@ -625,6 +625,7 @@ svp_status svp_pages_resize(const svp_pages *pages, const int32_t *length, void 
  * Request dst[f], which holds no page, gets the first length[f] tokens of src[f] (0 <= f < forks;
  * int32 [forks], device): the whole pages among them are shared (refs + 1), and a part of a page at the
  * end is copied, its tokens only, to a page of its own (refs 1): the lowest free ids in the order of f.
+ * The length[f] tokens are ones that src[f] has written and will not write again.
  * caches: HOST array of the n_caches <= SVP_PAGES_MAX_CACHES caches (a model's layers) that this block
  * table serves, of one type, strides, page size and num_pages, hkv heads of d; read during the call and
  * not retained.  n_caches may be 0 (the caller copies).  The rest of block_table's row dst[f] is -1.
@@ -668,8 +669,9 @@ svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, in
  * whole call (SVP_DEV_BAD_SLOTS; nothing is written).  Groups that run backwards or leave [0, n] anywhere are
  * none (SVP_DEV_BAD_SLOTS), and a group with prefix_len < 0 or > a member's ctx_len (SVP_DEV_BAD_CONTEXT), or
  * with a member that is skipped, is not shared; its other requests then use their own entries.
- * Precision: as svp_chunk_attn's tile kernel (8-bit pages: units of a tile's largest power of two), a row's
- * two parts in fp32 until they are joined.
+ * Precision and values: as svp_chunk_attn's.  8-bit rows of a shared prefix are in units of their tile's largest power
+ * of two whatever w is, and a request's own ones unless hq / hkv * w <= 8 and d <= 128, where they are used as they
+ * are.  A row's two parts stay in fp32 until they are joined.
  */
 svp_status svp_prefix_attn_workspace_size(const svp_heads *heads, svp_dtype dtype, int32_t m_cap,
                                           size_t *bytes);

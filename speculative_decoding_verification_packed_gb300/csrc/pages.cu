@@ -236,9 +236,10 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     const uint32_t rank = cluster_rank();
     const int32_t i = threadIdx.x;
     // Block 0 looks at the requests, the others take its numbers: all agree on them (and on the number of
-    // barriers) whatever else changes the tables meanwhile.
+    // barriers) whatever else changes the tables meanwhile.  Block 1 looks at them for the last pages of those that keep
+    // their number of pages, which tells no more than a status bit and would lengthen block 0's chain of reads.
     int32_t held = 0, want = 0, bits = 0;
-    if (rank == 0 && i < p.n) {
+    if (rank <= 1 && i < p.n) {
         const int32_t len = __ldg(p.length + i);
         held = __ldcg(p.used + i);
         want = held;
@@ -251,7 +252,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
             if (want > p.max_pages) {
                 bits = SVP_DEV_BAD_CONTEXT;
                 want = held;
-            } else if (want < held && part) {
+            } else if (part && (rank == 0 ? want < held : want == held)) {
                 // the last page is kept in part: it has to be this request's alone
                 const int32_t page = __ldcg(p.table + (int64_t)i * p.max_pages + want - 1);
                 if (page >= 0 && page < p.num_pages && __ldcg(p.refs + page) > 1) {
@@ -267,7 +268,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         // (sums of up to 1024 x max_pages < 2^31: checked on the host)
         pages_scan(s, max(want - held, 0), max(held - want, 0));
     }
-    cluster_sync(rank == 0);
+    cluster_sync(rank <= 1);
     if (rank != 0) {
         // (of the requests that there are: block 0 answers for seven)
         if (i < p.n) {

@@ -37,7 +37,7 @@ class Model:
             elif length[i] >= 0:
                 w = self.pages(length[i])
                 last = self.table[i][w - 1] if 0 < w <= self.cols else -1
-                if w > self.cols or (w < u and length[i] % self.page and self.inside(last) and before[last] > 1):
+                if w > self.cols or (w <= u and length[i] % self.page and self.inside(last) and before[last] > 1):
                     self.status |= svp.DEV_BAD_CONTEXT
                     w = None
             want.append(w)
@@ -342,6 +342,24 @@ def test_shared_parts_of_pages_are_not_kept():
     svp.pages_fork(dev.pages, i32([0, 0]), i32([1, 2]), i32([64, 70]), caches=dev.caches)
     dev.check()
     for ask, bits in (([40, 0, -1], svp.DEV_BAD_CONTEXT), ([-1, -1, 0], 0), ([33, -1, -1], 0), ([32, -1, -1], 0)):
+        m.resize(ask)
+        svp.pages_resize(dev.pages, i32(ask))
+        assert m.status == bits
+        dev.check()
+
+
+def test_rewound_behind_a_fork_is_reported():
+    """A request forked at a page's end and then taken back into that page, with as many pages as before: its next
+    write would go where its forks read, which is reported as a shrinking into a shared page is."""
+    m = Model(3, 6, 16, 20)
+    dev = Device(m)
+    m.resize([64, 32, 0])
+    svp.pages_resize(dev.pages, i32([64, 32, 0]))
+    m.fork([0], [2], [64])
+    svp.pages_fork(dev.pages, i32([0]), i32([2]), i32([64]), caches=dev.caches)
+    dev.check()
+    for ask, bits in (([64, 20, 64], 0), ([60, -1, -1], svp.DEV_BAD_CONTEXT), ([-1, -1, 49], svp.DEV_BAD_CONTEXT),
+                      ([65, -1, 64], 0), ([60, -1, 0], svp.DEV_BAD_CONTEXT), ([60, -1, -1], 0), ([52, -1, 0], 0)):
         m.resize(ask)
         svp.pages_resize(dev.pages, i32(ask))
         assert m.status == bits
