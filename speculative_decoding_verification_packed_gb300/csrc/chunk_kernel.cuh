@@ -34,8 +34,9 @@
 // in range is made up by the units (above) and by P' = 2^7 at the reference.
 //
 // What bounds it.  Short pieces over bf16 pages: their bytes (64 requests x 18000 keys, 8 KV heads, d 128:
-// 674 us, 7.0 TB/s; with 8 rows each 676 us).  Over 8-bit pages: the conversion, and the shared memory
-// that it shares with the MMAs (8 rows each 649 us for half the bytes).  Prompts: the chain S -> softmax -> P V of a
+// 674 us, 7.0 TB/s; with 8 rows each 676 us).  Over 8-bit pages: the chains of the two warpgroups, 2.7 us a tile each,
+// with the conversion, and the shared memory that it shares with the MMAs, beside them (8 rows each 649 us for half the
+// bytes; 639 with 128-token pages, and 570 at d 64, with half the conversion).  Prompts: the chain S -> softmax -> P V of a
 // tile (4096 rows on 8192 keys, 32 heads: 496 to 519 us by the data, 1.32 to 1.39 PFLOP/s, 8-bit pages 641; the
 // MMAs alone 342 us; the exponentials keep their pipe busy for 29 % of it, all instructions the issue slots
 // for 32 %).

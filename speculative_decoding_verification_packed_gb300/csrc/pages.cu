@@ -10,8 +10,9 @@
 // Free pages are found by their counts (refs == 0), lowest ids first: no list of free pages has to be
 // kept consistent, and the ids in use stay low.  A warp looks at 32 pages a load; ballots rank them.
 //
-// What bounds it: for a step's few pages the chain of dependent reads and cluster barriers; for moves
-// memory.
+// What bounds it: for a step's few pages the chain of dependent reads and cluster barriers (64 requests: 8.2 us of a
+// graph's 9.7); for 54700 pages given back at once their atomics (12 of 21 us); for moves memory (924 MB in a compaction:
+// 150 us, 6.2 TB/s).
 #include <cstring>
 
 #include "svp_cache.cuh"
