@@ -491,7 +491,8 @@ svp_status svp_cache_read(const svp_cache *cache, const int32_t *start, const in
  *        cache (anything else: SVP_EUNSUPPORTED)
  * ws     at least svp_chunk_attn_workspace_size bytes (it depends on d and dtype only), its
  *        first 256 zeroed once by svp_workspace_init; every call leaves it ready for the next
- *        one of any size, head layout or type that it is large enough for.
+ *        one of any size, head layout or type that it is large enough for; 32-byte aligned with
+ *        SVP_BF16 (SVP_EINVAL otherwise)
  * 0 <= n <= 1024, hq / hkv <= 128, d = 64, 128 or 256 (SVP_EUNSUPPORTED otherwise).
  *
  * Precision.  Scores, the softmax's maximum and sum, and the output are accumulated in fp32; the
@@ -663,8 +664,8 @@ svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, in
  * cu_groups [n_groups+1], prefix_len [n_groups] int32 (device); 0 <= n_groups <= 1024
  * With an SVP_F32 cache, or without groups, the call is svp_chunk_attn (groups are not looked at).
  * ws     at least svp_prefix_attn_workspace_size bytes (it grows with m_cap), its first 256 zeroed once by
- *        svp_workspace_init; every call leaves it ready for the next one that it is large enough for; 16-byte
- *        aligned
+ *        svp_workspace_init; every call leaves it ready for the next one that it is large enough for; 32-byte
+ *        aligned with SVP_BF16 (SVP_EINVAL otherwise)
  * Device checks are svp_chunk_attn's, but cu_slots that run backwards or leave [0, m_cap] anywhere reject the
  * whole call (SVP_DEV_BAD_SLOTS; nothing is written).  Groups that run backwards or leave [0, n] anywhere are
  * none (SVP_DEV_BAD_SLOTS), and a group with prefix_len < 0 or > a member's ctx_len (SVP_DEV_BAD_CONTEXT), or

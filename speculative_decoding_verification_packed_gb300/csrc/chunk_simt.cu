@@ -189,6 +189,9 @@ svp_status svp_chunk_attn(const void *q, int64_t q_row_stride, const svp_cache *
         return SVP_OK;
     if (!q || !ctx_len || !cu_slots || !out || !al16(q) || !al16(out))
         return SVP_EINVAL;
+    // (partial results are stored 32 bytes at a time; the fp32 kernel has none)
+    if (dtype == SVP_BF16 && (reinterpret_cast<uintptr_t>(ws) & 31) != 0)
+        return SVP_EINVAL;
     if (dtype == SVP_BF16)
         return chunk_tc_launch(q, q_row_stride, cache->dtype, c, ctx_len, cu_slots, n, m_cap, w, heads->hq, heads->d,
                                scale, out, lse, ws, (cudaStream_t)stream);

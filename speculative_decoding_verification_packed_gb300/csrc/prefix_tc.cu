@@ -325,6 +325,7 @@ static svp_status prefix_run(ChunkParams &p, cudaStream_t stream)
 }
 
 static bool al16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
+static bool al32(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 31) == 0; }   // (as ck_store8 wants its parts)
 
 }  // namespace svp
 
@@ -375,7 +376,7 @@ svp_status svp_prefix_attn(const void *q, int64_t q_row_stride, const svp_cache 
         return SVP_EINVAL;
     if (!ws || ws_bytes < need)
         return SVP_EWORKSPACE;
-    if (!q || !ctx_len || !cu_slots || !cu_groups || !prefix_len || !out || !al16(q) || !al16(out) || !al16(ws))
+    if (!q || !ctx_len || !cu_slots || !cu_groups || !prefix_len || !out || !al16(q) || !al16(out) || !al32(ws))
         return SVP_EINVAL;
     const int32_t d = heads->d;
     p.ctx_len = ctx_len;
