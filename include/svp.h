@@ -633,7 +633,8 @@ svp_status svp_pages_resize(const svp_pages *pages, const int32_t *length, void 
  * Not done: a src or dst outside 0 .. n - 1, a dst that holds pages or is that of an earlier fork of the
  * call (SVP_DEV_BAD_SLOTS); a length outside 0 .. used[src] * page_size (SVP_DEV_BAD_CONTEXT); a fork when
  * forks 0 .. f together need more pages than are free (SVP_DEV_NO_PAGES).  An entry of src that names no
- * page of the pool is passed on as -1 (SVP_DEV_BAD_CONTEXT).  0 <= forks <= 1024, hkv <= 4096.
+ * page of the pool is passed on as -1 (SVP_DEV_BAD_CONTEXT), that of the part at the end too, for which no page is
+ * taken then.  0 <= forks <= 1024, hkv <= 4096.
  */
 svp_status svp_pages_fork(const svp_pages *pages, const svp_cache *caches, int32_t n_caches,
                           int32_t hkv, int32_t d, const int32_t *src, const int32_t *dst,

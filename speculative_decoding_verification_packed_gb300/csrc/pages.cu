@@ -357,7 +357,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     s.a[f] = INT32_MAX;                                   // by request: the first fork into it
     __syncthreads();
     int32_t from = 0, to = 0, whole = -1, part = 0, bits = 0;
-    bool fine = false;
+    bool fine = false, lost = false;                      // lost: the part's page is none of the pool
     if (rank == 0 && f < p.forks) {                       // (as in the resize)
         from = __ldg(p.src + f);
         to = __ldg(p.dst + f);
@@ -365,6 +365,9 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         if (from < 0 || from >= p.n || to < 0 || to >= p.n) {
             bits = SVP_DEV_BAD_SLOTS;
         } else {
+            // (the entry beside the counts: one round trip)
+            const bool row = len >= 0 && (len >> p.page_shift) < p.max_pages;
+            const int32_t page = row ? __ldcg(p.table + (int64_t)from * p.max_pages + (len >> p.page_shift)) : -1;
             const int32_t held = __ldcg(p.used + from);
             if (__ldcg(p.used + to) != 0) {
                 bits = SVP_DEV_BAD_SLOTS;
@@ -374,6 +377,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
                 fine = true;
                 whole = len >> p.page_shift;
                 part = len & ((1 << p.page_shift) - 1);
+                lost = part && (page < 0 || page >= p.num_pages);
                 atomicMin(&s.a[to], f);
             }
         }
@@ -383,7 +387,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         fine = false;
         bits = SVP_DEV_BAD_SLOTS;
     }
-    pages_scan(s, fine && part ? 1 : 0, 0);
+    pages_scan(s, fine && part && !lost ? 1 : 0, 0);
     cluster_sync(rank == 0);
     const int32_t need = cluster_load(&s.need[kPgThreads], 0);
     int32_t found = 0;
@@ -397,7 +401,9 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
         const bool got = fine && s.need[f + 1] <= found;  // (forks behind the last page that there is need it too, or a later one)
         if (fine && !got)
             bits = SVP_DEV_NO_PAGES;
-        const int32_t page = got && part ? __ldcg(p.tail + s.need[f]) : -1;
+        if (got && lost)
+            bits = SVP_DEV_BAD_CONTEXT;                   // (passed on as -1, without a page)
+        const int32_t page = got && part && !lost ? __ldcg(p.tail + s.need[f]) : -1;
         p.plan[f] = make_int4(from, to, got ? whole : -1, page);
         if (got)
             p.used[to] = whole + (part ? 1 : 0);
@@ -469,11 +475,8 @@ __global__ void __launch_bounds__(kPgCopyThreads) pages_fork_copy_kernel(const _
     if (page < 0)
         return;
     const int32_t from = row[whole], part = __ldg(p.length + f) & ((1 << p.page_shift) - 1);
-    if (from < 0 || from >= p.num_pages) {
-        if (tid == 0)
-            set_status(p.status, SVP_DEV_BAD_CONTEXT);
-        return;
-    }
+    if (from < 0 || from >= p.num_pages)
+        return;                                           // (never, but for a table that changes meanwhile)
     const int32_t x = (blockIdx.y - 1) >> 1;
     const bool v = (blockIdx.y - 1) & 1;
     pages_copy(c, v ? c.v[x] : c.k[x], from, page, part, p.page_shift);
