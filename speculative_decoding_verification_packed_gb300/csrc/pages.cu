@@ -570,8 +570,7 @@ __global__ void __launch_bounds__(kPgCopyThreads) pages_move_kernel(const __grid
     griddep_wait();
     const int32_t tid = threadIdx.x;
     const int32_t moves = p.moves[0], live = p.moves[1];
-    if (moves == 0)
-        return;
+    // (without moves too: an entry at or behind `live` is reported all the same)
     for (int32_t i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int32_t held = p.used[i];
         int32_t *row = p.table + (int64_t)i * p.max_pages;

@@ -76,3 +76,34 @@ def test_such_forks_alone_take_no_page():
     assert m.status == svp.DEV_BAD_CONTEXT and m.table[1] == m.table[2] == [0, -1, -1]
     svp.pages_fork(dev.pages, i32([0, 0]), i32([1, 2]), i32([40, 63]), caches=dev.caches)
     dev.check()
+
+
+@pytest.mark.parametrize("num", [12, 40, 8200])
+@pytest.mark.parametrize("moved", [False, True])
+@pytest.mark.parametrize("stale", [True, False])
+def test_an_entry_of_a_page_that_nobody_counts_is_reported_by_a_compaction(num, moved, stale):
+    """Whether other pages move or the pool is compact already; it stays as it is."""
+    last = num - 1
+    refs = [1, 1, 1, 0] + [0] * (num - 4)
+    table = [[0, 1, -1, -1], [2, -1, -1, -1]]
+    if moved:                              # page 1 free, page 5 in use: it moves
+        refs[1], refs[5], table[0][1] = 0, 1, 5
+    if stale:
+        table[1][1] = last
+    m = Model(2, 4, 16, num, table=table, used=[2, 2 if stale else 1], refs=refs)
+    dev = Device(m, layers=1)
+    live = i32([-5])
+    svp.pages_compact(dev.pages, caches=dev.caches, live=live)
+    assert m.compact() == live.item() == 3
+    assert m.table == [[0, 1, -1, -1], [2, last if stale else -1, -1, -1]]
+    m.status = svp.DEV_BAD_CONTEXT if stale else 0
+    dev.check()
+
+
+def test_a_pool_without_a_free_page_has_nothing_to_report():
+    m = Model(2, 3, 16, 4, table=[[3, 0, -1], [1, 2, 99]], used=[2, 3], refs=[1, 1, 1, 1])
+    dev = Device(m)
+    m.compact()
+    svp.pages_compact(dev.pages, caches=dev.caches)
+    assert m.status == 0                   # (an id that is no page's is not the compaction's affair)
+    dev.check()
