@@ -878,18 +878,25 @@ def prefix_attn_workspace_size(hq: int, hkv: int, d: int, m_cap: int, dtype=torc
     return int(nb.value)
 
 
+_prefix_ws: dict = {}
+_PREFIX_WS_LARGEST = 128 << 20    # bytes of a scratch buffer that is kept; 47 MB and 8 bytes an element of q
+
+
 def _prefix_workspace(hq: int, m_cap: int, cache: svp_cache, dtype, raw: int) -> Workspace:
-    """As _chunk_workspace; a stream's scratch grows with the calls' rows."""
+    """As _chunk_workspace, in places of its own; a stream's scratch grows with the calls' rows.  That of a call
+    of many rows is not kept: its memory goes back to torch's allocator, for later work of the same stream."""
     nb = prefix_attn_workspace_size(hq, cache.hkv, cache.d, m_cap, dtype)
     if torch._C._cuda_isCurrentStreamCapturing():
         return Workspace(nb, cache.device, zeroed=0)
-    key = (raw, cache.index, "prefix")
-    ws = _chunk_ws.get(key)
+    key = (raw, cache.index)
+    ws = _prefix_ws.get(key)
     if ws is None or ws.nbytes < nb:
-        _chunk_ws.pop(key, None)
-        while len(_chunk_ws) >= _CHUNK_WS_MOST:
-            _chunk_ws.pop(next(iter(_chunk_ws)), None)
-        ws = _chunk_ws[key] = Workspace(nb, cache.device, zeroed=256)
+        if nb > _PREFIX_WS_LARGEST:
+            return Workspace(nb, cache.device, zeroed=256)
+        _prefix_ws.pop(key, None)
+        while len(_prefix_ws) >= _CHUNK_WS_MOST:
+            _prefix_ws.pop(next(iter(_prefix_ws)), None)
+        ws = _prefix_ws[key] = Workspace(nb, cache.device, zeroed=256)
     return ws
 
 
