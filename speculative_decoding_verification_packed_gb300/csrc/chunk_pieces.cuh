@@ -15,9 +15,13 @@ constexpr int kStartKeys = 256;
 // Cost of a key with one query tile, and with two: where 3 to 4 takes 325 us on those blocks and prompts, 2 to
 // 3 takes 329 and 1 to 1 345 (the one prompt takes 146 to 147 with each).
 constexpr int kShortCost = 3, kLongCost = 4;
-// Smallest share of a CTA, more than a tile's cost: a shorter one is not worth its join.  One token over 500
-// keys takes 14.6 us, with 2048 16.6 (700 keys 14.6 and 19.0).
+// Dearest key of any call (prefix_pieces.cuh).
+constexpr int kMostCost = 5;
+// Smallest share of a CTA: a shorter one is not worth its join.  One token over 500 keys takes 14.6 us, with 2048
+// 16.6 (700 keys 14.6 and 19.0).  At least a tile's cost, so that every CTA between the first and the last of a
+// pair owns the start of a tile, i.e. has a piece of it: the joining kernels read one from each.
 constexpr int kShareCost = 640;
+static_assert(kShareCost >= kMostCost * kCkKeys, "a share without the start of a tile");
 // P stays below 2^8 times its value at the reference, but over bf16 pages in a tile that is read once: there it
 // may go on as long as a row's sum over the tile is at most 2^15 (chunk_tc.cu).
 constexpr float kCkSlack = 8.0f;
@@ -242,8 +246,8 @@ __device__ __forceinline__ bool ck_first(const ChunkParams &p, const int64_t *pr
     return have || (t0 >= s.nt && ck_next<NT>(p, s, v1));
 }
 
-// CTA c of ncta has the costs [c, c + 1) x share; ncta shares hold the total, and a share (but the last)
-// more than a tile.
+// CTA c of ncta has the costs [c, c + 1) x share; ncta shares hold the total, and a share (but the last) is a
+// tile's cost or more.
 struct ChunkShares {
     int64_t total, share;
     int32_t ncta;

@@ -73,8 +73,8 @@ __device__ __forceinline__ uint32_t fw_chunk(int row, int c)
     return (uint32_t)((c >> 3) * kCkSub + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
-// Share [v0, v1) of the requests' costs; every thread of the block, whose shared memory below p.few_end is free (from
-// p.off_ring on the prologue's sums are, which is why the first piece, s, is given).
+// Share [v0, v1) of the requests' costs; every thread of the block.  The joining buffer, the ring (p.few_ring, p.few_slots) and
+// the barriers (p.few_misc) lie below p.off_misc, where the prologue's sums were until the first piece, s, was found.
 template <int D>
 __device__ __forceinline__ void few_body(const ChunkParams &p, uint8_t *smem, PrefixPiece s, bool have0, int64_t v1, int32_t cta)
 {

@@ -46,8 +46,8 @@ struct PxCosts {
 
 __device__ __forceinline__ PxCosts px_costs(int32_t part, bool shared, bool q8)
 {
-    static_assert(kShortCost == 3 && kLongCost == 4, "px_tile_at");
-    return part == kPxAll && shared ? PxCosts{4, q8 ? 4 : 5} : PxCosts{kShortCost, kLongCost};
+    static_assert(kShortCost == 3 && kLongCost == 4 && kMostCost == 5, "px_tile_at");
+    return part == kPxAll && shared ? PxCosts{4, q8 ? 4 : kMostCost} : PxCosts{kShortCost, kLongCost};
 }
 
 struct PrefixPiece : ChunkPiece {     // i: place in the sequence of groups and requests

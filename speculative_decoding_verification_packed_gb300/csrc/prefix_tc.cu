@@ -5,7 +5,8 @@
 // So the common keys are worked on once for all rows of a group (chunk_kernel.cuh over the sequence of
 // prefix_pieces.cuh): G heads times all tokens of the group fill the 128-row tiles that a decode token alone
 // leaves empty, and the pages are read once.  Every piece, of a group or of a request behind one, leaves (O, m, l)
-// in fp32, the joining kernel below adds a row's pieces up in their order.  Requests alone are svp_chunk_attn's.
+// in fp32, the joining kernel below adds a row's pieces up in their order.  Requests alone are cut as
+// svp_chunk_attn's are, but for those of few rows, which have blocks of their own beside the groups' (prefix_few.cuh).
 //
 // What bounds it: for few rows latency (8 tokens behind 4096, bf16: 23 us, 5.3 to the shares, 9 for a piece's chain, 5 for
 // the join); else the groups' tiles (64 tokens behind 4 prefixes of 8192 to 32768, 8-bit: 105 us, 270 MB; 64 blocks of up
