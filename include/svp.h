@@ -661,7 +661,8 @@ svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, in
  * tokens of each of them lie in the same pages: the block table's rows of a group's requests (of
  * those with k_i > 0) have the same ids there, and only the first one's are read.  The whole pages of a
  * prefix are read once for 256 / (hq / hkv) rows of the group (128 / (hq / hkv) at d = 256) instead of once
- * for every request, where that is fewer times.
+ * for every request, where that is fewer times.  The call is for long prefixes: where they are short beside the
+ * requests' own contexts, for a few decode tokens over 8-bit pages and for prompt chunks svp_chunk_attn is the quicker one.
  * cu_groups [n_groups+1], prefix_len [n_groups] int32 (device); 0 <= n_groups <= 1024
  * With an SVP_F32 cache, or without groups, the call is svp_chunk_attn (groups are not looked at).
  * ws     at least svp_prefix_attn_workspace_size bytes (it grows with m_cap), its first 256 zeroed once by

@@ -904,8 +904,9 @@ def prefix_attn(q, ctx_len, cu_slots, cu_groups, prefix_len, *, cache: svp_cache
                 lse=None, want_lse: bool = True, scale: float = 0.0, ws: Optional[Workspace] = None, stream=None):
     """chunk_attn (the same arguments and results) for groups of requests that share a beginning
     (svp_prefix_attn): requests cu_groups[g]..cu_groups[g+1]-1 (int32) have their first prefix_len[g] tokens (int32)
-    in the same pages, as pages_fork leaves them, and those are read once for the group.  ws: a Workspace of
-    prefix_attn_workspace_size bytes; without one as for chunk_attn."""
+    in the same pages, as pages_fork leaves them, and those are read once for the group (chunk_attn is the quicker call
+    where they are few beside the requests' own).  ws: a Workspace of prefix_attn_workspace_size bytes; without one as
+    for chunk_attn, with scratch that grows with the calls' rows and above 128 MB is not kept."""
     n = _requests(cu_slots, cache, "cu_slots")
     other = _other_stream(stream, cache)
     if other is not None:

@@ -9,8 +9,10 @@
 // svp_chunk_attn's are, but for those of few rows, which have blocks of their own beside the groups' (prefix_few.cuh).
 //
 // What bounds it: for few rows latency (8 tokens behind 4096, bf16: 23 us, 5.3 to the shares, 9 for a piece's chain, 5 for
-// the join); else the groups' tiles (64 tokens behind 4 prefixes of 8192 to 32768, 8-bit: 105 us, 270 MB; 64 blocks of up
-// to 16 rows behind 2 prefixes, bf16: 164 us, 0.65 PFLOP/s).
+// the join); else the groups' tiles (64 tokens behind 4 prefixes of 8192 to 32768, 8-bit: 109 us, 270 MB; 64 blocks of up
+// to 16 rows behind 2 prefixes, bf16: 165 us, 0.65 PFLOP/s).  Where little is shared beside what the requests have
+// themselves, or a decode call is small, svp_chunk_attn is quicker (2 tokens behind 256, 8192 of their own: 27 us and 25; over
+// 8-bit pages 29 and 17; 8 tokens behind 4096 there 25 and 20): a group is shared by its number of blocks, not by time.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

@@ -9,13 +9,14 @@
 // shared memory, beside the lookup of their requests and pages; the first heads' data is on the way
 // then.  A group of d / 8 lanes has every few heads of one row, eight elements a lane, so that a lane's
 // sines and cosines stay in its registers from head to head (read from shared memory for each head they
-// took as long as the rows: 26000 prompt rows of 48 heads x 128 then 180 us).  The other half of a pair
+// took as long as the rows: 21100 prompt rows of 48 heads x 128 then 180 us).  The other half of a pair
 // (t, t + rot / 2) comes by a shuffle from rot / 16 lanes away, or, for a rot / 2 that is no multiple of 8,
-// element by element from memory.  All reads of a row come before its writes (one warp holds it), so
+// element by element from memory, with the sines read for every head (20000 such rows: 178 us with rot 36 or 18,
+// where 48, 64 and 128 take 88 to 90).  All reads of a row come before its writes (one warp holds it), so
 // an output may be its input.
 //
 // What bounds it: the chain cu -> context -> angle -> row for few rows (64 blocks of up to 16 rows, 11 MB: 5.0 us from
-// a graph); memory for prompts (those 519 MB: 94 us, 5.5 TB/s), with the issue slots 60% busy beside it, so that
+// a graph); memory for prompts (those 519 MB: 93 us, 5.6 TB/s), with the issue slots 57% busy beside it, so that
 // occupancy counts: with 3 blocks an SM instead of 4, and four heads in flight instead of three, the
 // blocks take 6.6 us.
 #include <cmath>
