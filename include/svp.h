@@ -617,7 +617,7 @@ svp_status svp_pages_workspace_size(const svp_pages *pages, size_t *bytes);
  * (refs > 1 before the call), as its next write would go there: give it a whole page less, or fork it instead.
  * An entry that names no page of the pool, or one whose refs is 0 already, is given back as -1 without
  * counting (SVP_DEV_BAD_CONTEXT).
- * ws     at least svp_pages_workspace_size bytes, its first 256 zeroed once by svp_workspace_init
+ * ws     at least svp_pages_workspace_size bytes, its first 256 zeroed once by svp_workspace_init; 16-byte aligned
  */
 svp_status svp_pages_resize(const svp_pages *pages, const int32_t *length, void *ws,
                             size_t ws_bytes, void *stream);
@@ -670,8 +670,8 @@ svp_status svp_pages_compact(const svp_pages *pages, const svp_cache *caches, in
  *        aligned with SVP_BF16 (SVP_EINVAL otherwise)
  * Device checks are svp_chunk_attn's, but cu_slots that run backwards or leave [0, m_cap] anywhere reject the
  * whole call (SVP_DEV_BAD_SLOTS; nothing is written).  Groups that run backwards or leave [0, n] anywhere are
- * none (SVP_DEV_BAD_SLOTS), and a group with prefix_len < 0 or > a member's ctx_len (SVP_DEV_BAD_CONTEXT), or
- * with a member that is skipped, is not shared; its other requests then use their own entries.
+ * none (SVP_DEV_BAD_SLOTS), and a group with prefix_len < 0 or > the ctx_len of a member with rows
+ * (SVP_DEV_BAD_CONTEXT), or with a member that is skipped, is not shared; its other requests then use their own entries.
  * Precision and values: as svp_chunk_attn's.  8-bit rows of a shared prefix are in units of their tile's largest power
  * of two whatever w is, and a request's own ones unless hq / hkv * w <= 8 and d <= 128, where they are used as they
  * are.  A row's two parts stay in fp32 until they are joined.
